@@ -336,3 +336,9 @@ class DepthwiseConv2d:
             self.close()
         except Exception:
             pass
+
+
+from .seq import *  # noqa: E402,F401,F403
+from .seq import __all__ as _seq_names  # noqa: E402
+
+__all__ += _seq_names

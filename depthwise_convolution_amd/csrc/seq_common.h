@@ -1,0 +1,84 @@
+// seq_common.h -- what the sequence operators' kernels share: arguments,
+// vectors of elements, packed sequences and activations.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dw_common.h"
+
+namespace dw {
+
+// N consecutive elements moved by one load or store (two of 16 bytes for 32).
+template <class X, int N>
+struct alignas(sizeof(X) * N > 16 ? 16 : sizeof(X) * N) Vec {
+    X v[N];
+};
+
+template <class DT, int N>
+__device__ __forceinline__ void load_f32(float (&out)[N], const typename DT::X *p) {
+    const Vec<typename DT::X, N> a = *(const Vec<typename DT::X, N> *)p;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = DT::widen(a.v[i]);
+}
+
+template <class DT, int N>
+__device__ __forceinline__ void store_f32(typename DT::X *p, const float (&in)[N]) {
+    Vec<typename DT::X, N> a;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a.v[i] = DT::narrow(in[i]);
+    *(Vec<typename DT::X, N> *)p = a;
+}
+
+__device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+// Packed sequences.  Wrong offsets are clamped, so that begin <= end lie in
+// [0, tokens] whatever the device array holds.
+struct Packed {
+    const int32_t *offsets;  // seqs + 1, or nullptr: one sequence of all tokens
+    int seqs, tokens;
+    __device__ __forceinline__ int begin(int s) const {
+        if (!offsets) return 0;
+        const int a = offsets[s];
+        return a < 0 ? 0 : (a > tokens ? tokens : a);
+    }
+    __device__ __forceinline__ int end(int s) const {
+        if (!offsets) return tokens;
+        const int a = begin(s), b = offsets[s + 1];
+        return b < a ? a : (b > tokens ? tokens : b);
+    }
+    // The last sequence s with offsets[s] <= t, -1 if there is none.  Of
+    // several that begin at t it is the last, so the one that may hold t.
+    __device__ __forceinline__ int find(int t) const {
+        if (!offsets) return 0;
+        int lo = -1, hi = seqs;  // offsets[lo] <= t < offsets[hi], hi past the end
+        while (hi - lo > 1) {
+            const int m = (lo + hi) >> 1;
+            if (offsets[m] <= t) lo = m; else hi = m;
+        }
+        return lo;
+    }
+};
+
+// Which rows of a step share this row's cache entry.  Rows with the same slot
+// are consecutive tokens of one sequence: the first one's workgroup takes them
+// all in order, the others' workgroups leave.
+struct SlotRows {
+    int slot;     // -1: nothing to do
+    bool shared;  // later rows have it too
+};
+__device__ __forceinline__ SlotRows slot_rows(const int32_t *slots, int n_slots, int rows, int row) {
+    if (!slots) return {row, false};
+    const int s = slots[row];
+    if (s < 0 || s >= n_slots) return {-1, false};
+    bool before = false, after = false;
+    for (int j = threadIdx.x & 63; j < rows; j += 64) {
+        const bool same = slots[j] == s;
+        before |= same && j < row;
+        after |= same && j > row;
+    }
+    if (__any(before)) return {-1, false};
+    return {s, (bool)__any(after)};
+}
+
+}  // namespace dw
