@@ -38,113 +38,12 @@
 // exponents next to a reset); decays below e^-1000 are zero either way, so g
 // is cut there and -infinity needs no case of its own.  All products and sums
 // are fp32.
-#include "seq_common.h"
-#include "seq_plan.h"
+#include "delta_common.h"
 
 namespace dw {
 namespace {
 
-constexpr int CH = 64;             // tokens a chunk
-constexpr int TRI = 10 * 256;      // floats of a lower triangle of 4x4 tiles of 16x16
-constexpr int NV = 3 * CH;         // per-chunk vectors: e^b, e^{b_last - b}, beta
-
-using f32x4 = __attribute__((ext_vector_type(4))) float;
-
-__device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-// c += A B over 16 terms: a[i] is the left operand's term 4 (l / 16) + i of row
-// l % 16, b[i] the right operand's term 4 (l / 16) + i of column l % 16
-__device__ __forceinline__ f32x4 mfma16(f32x4 a, f32x4 b, f32x4 c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = mfma4(a[i], b[i], c);
-    return c;
-}
-__device__ __forceinline__ f32x4 splat(float v) { return f32x4{v, v, v, v}; }
-__host__ __device__ constexpr int tri(int i, int j) { return (i * (i + 1) / 2 + j) * 256; }
-
-// Sizes and inputs; T, P, vectors and norms of every chunk in the workspace.
-struct Ctx {
-    Packed seq;
-    int Hk, Hv, Dk, Dv, DvP;  // DvP: Dv rounded up to 32
-    int slots;
-    float scale, eps;
-    int normalize, vec4;      // vec4: rows of q and k load 4 elements at once
-    const void *q, *k, *v;
-    int64_t ldq, ldk, ldv;
-    const float *g, *beta;
-    float *T, *P;             // slots x Hv x TRI
-    float *vecs;              // slots x Hv x NV
-};
-
-// A chunk's place.  Sequence s begins at slot begin / 64 + s: a sequence of L
-// tokens needs ceil(L / 64) slots, and no two chunks share one.
-struct Chunk {
-    int s, tok, n;  // sequence, first token, tokens (0: an unused slot)
-};
-__device__ __forceinline__ int first_slot(const Packed &p, int s) { return p.begin(s) / CH + s; }
-__device__ __forceinline__ Chunk chunk_of(const Packed &p, int slot) {
-    int lo = 0, hi = p.seqs;  // first_slot(lo) <= slot
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (first_slot(p, m) <= slot) lo = m; else hi = m;
-    }
-    const int c = slot - first_slot(p, lo), a = p.begin(lo), b = p.end(lo);
-    if (c < 0 || (int64_t)a + (int64_t)c * CH >= b) return {lo, 0, 0};
-    const int tok = a + c * CH;
-    return {lo, tok, b - tok < CH ? b - tok : CH};
-}
-
-template <class DT>
-__device__ __forceinline__ f32x4 load4(const typename DT::X *p, int valid, bool vec4) {
-    f32x4 r = splat(0.0f);
-    if (valid >= 4 && vec4) {
-        float t[4];
-        load_f32<DT, 4>(t, p);
-        r = f32x4{t[0], t[1], t[2], t[3]};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < valid) r[i] = DT::widen(p[i]);
-    }
-    return r;
-}
-
-// Rows [tok, tok + n) of q or k into LDS as unit vectors (zeros behind), four
-// threads a row; rnorm, where given, gets 1 / |row|.
-template <class DT, int DK>
-__device__ __forceinline__ void stage_unit(float (*dst)[DK + 4], const typename DT::X *src, int64_t ld, int n,
-                                           const Ctx &c, float *rnorm) {
-    const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
-    f32x4 v[DK / 16];
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < DK / 16; ++i) {
-        const int col = i * 16 + part * 4;
-        v[i] = row < n ? load4<DT>(src + (int64_t)row * ld + col, c.Dk - col, c.vec4) : splat(0.0f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sq = __builtin_fmaf(v[i][j], v[i][j], sq);
-    }
-    sq += __shfl_xor(sq, 1, 64);
-    sq += __shfl_xor(sq, 2, 64);
-    const float r = c.normalize && row < n ? 1.0f / sqrtf(sq + c.eps) : 1.0f;
-    if (rnorm && part == 0) rnorm[row] = r;
-#pragma unroll
-    for (int i = 0; i < DK / 16; ++i) *(f32x4 *)&dst[row][i * 16 + part * 4] = v[i] * r;
-}
-
-// The running sum of g over the chunk's tokens, lane i: token i (one wavefront).
-__device__ __forceinline__ double running_sum(const float *g, int Hv, int n, int lane) {
-    float x = lane < n ? g[(int64_t)lane * Hv] : 0.0f;
-    if (x < -1000.0f) x = -1000.0f;
-    double b = x;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const double o = __shfl_up(b, m, 64);
-        if (lane >= m) b += o;
-    }
-    return b;
-}
+using namespace delta;
 
 template <class DT, int DK>
 __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
@@ -159,7 +58,7 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
     const int slot = blockIdx.x / c.Hk, hk = blockIdx.x % c.Hk;
     const Chunk ch = chunk_of(c.seq, slot);
     if (ch.n == 0) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g4 = (lane >> 4) * 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4;
     stage_unit<DT, DK>(K, (const X *)c.k + ch.tok * c.ldk + (int64_t)hk * c.Dk, c.ldk, ch.n, c, nullptr);
     stage_unit<DT, DK>(Q, (const X *)c.q + ch.tok * c.ldq + (int64_t)hk * c.Dk, c.ldq, ch.n, c, nullptr);
     __syncthreads();
@@ -203,38 +102,8 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
             }
         }
         __syncthreads();
-        // wave w inverts diagonal tile w: a lane solves one column downwards
-        f32x4 Tc[4];  // column w of T, tiles w .. 3
-        {
-            const float *a = At + tri(wave, wave);
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s = i == r ? 1.0f : 0.0f;
-#pragma unroll
-                for (int j = 0; j < i; ++j) s = __builtin_fmaf(-a[i * 16 + j], x[j], s);
-                x[i] = s;
-            }
-            f32x4 d;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                d[i] = g4 == 0 ? x[i] : g4 == 4 ? x[4 + i] : g4 == 8 ? x[8 + i] : x[12 + i];
-                Td[wave * 256 + (g4 + i) * 16 + r] = d[i];
-            }
-            Tc[0] = d;
-        }
-        __syncthreads();
-        // tiles below it: T_ij = -T_ii sum_m A_im T_mj; n counts tiles below the diagonal
-#pragma unroll
-        for (int n = 1; n < 4; ++n) {
-            const int i = wave + n;
-            if (i >= 4) break;
-            f32x4 s = splat(0.0f);
-#pragma unroll
-            for (int m = 0; m < n; ++m)
-                s = mfma16(*(const f32x4 *)&At[tri(i, wave + m) + r * 16 + g4], Tc[m], s);
-            Tc[n] = mfma16(-*(const f32x4 *)&Td[i * 256 + r * 16 + g4], s, splat(0.0f));
-        }
+        f32x4 Tc[4];
+        invert(At, Td, wave, r, g4, Tc);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             if (wave + n >= 4) break;
@@ -277,7 +146,7 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
     Stage<DK> &L = *(Stage<DK> *)lds;
     const int nb = (c.Dv + 63) / 64;
     const int vb = blockIdx.x % nb, h = blockIdx.x / nb % c.Hv, s = blockIdx.x / nb / c.Hv;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g4 = (lane >> 4) * 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4;
     const int dv = vb * 64 + wave * 16 + r;
     const bool in = dv < c.Dv;
     const int a = c.seq.begin(s), b = c.seq.end(s);
@@ -387,7 +256,7 @@ __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o,
     Stage<DK> &L = *(Stage<DK> *)lds;
     const int nb = (c.Dv + 63) / 64;
     const int vb = blockIdx.x % nb, h = blockIdx.x / nb % c.Hv, s = blockIdx.x / nb / c.Hv;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g4 = (lane >> 4) * 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4;
     const int dv = vb * 64 + wave * 16 + r;
     const bool in = dv < c.Dv;
     const int a = c.seq.begin(s), b = c.seq.end(s);
@@ -533,7 +402,7 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
     const int slot = blockIdx.x / c.Hk, hk = blockIdx.x % c.Hk;
     const Chunk ch = chunk_of(c.seq, slot);
     if (ch.n == 0) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g4 = (lane >> 4) * 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4;
     const int group = c.Hv / c.Hk;
     f32x4 dQ[DK / 16], dK[DK / 16];
 #pragma unroll
@@ -756,21 +625,32 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
 int padded_keys(int Dk) { return (Dk + 63) / 64 * 64; }
 
 struct Layout {
-    size_t T, P, vecs, S0s, Us, dSs, dRs, end;  // offsets in floats
+    size_t T, P, vecs, keys, heads, S0s, Us, dSs, dRs, end;  // offsets in floats
+    size_t key_bytes, head_bytes;
 };
 Layout layout(const dwconv_delta_plan &p, int seqs, int tokens, bool backward) {
     const size_t slots = (size_t)tokens / CH + seqs, n = slots * p.Hv;
     const size_t DvP = (p.Dv + 31) / 32 * 32, DK = padded_keys(p.Dk);
+    const bool split = split_runs(p.dtype, (int)DK);
     Layout l{};
     size_t at = 0;
     auto take = [&](size_t f) {
         const size_t here = at;
-        at += (f + 63) / 64 * 64;
+        at += (f + 255) / 256 * 256;
         return here;
     };
-    l.T = take(n * TRI);
-    l.P = take(n * TRI);
-    l.vecs = take(n * NV);
+    if (split) {
+        l.key_bytes = (size_t)key_frags((int)DK, key_terms(p.dtype)) * (backward ? 4 : 3) * FRAG;
+        l.head_bytes = (size_t)(backward ? HEAD_BWD : HEAD_FWD) * FRAG;
+        l.keys = take(slots * p.Hk * l.key_bytes / 4);
+        l.heads = take(n * l.head_bytes / 4);
+    } else {
+        l.T = take(n * TRI);
+    }
+    if (!split || backward) {
+        l.P = take(n * TRI);
+        l.vecs = take(n * NV);
+    }
     if (backward) {
         l.S0s = take(n * DK * DvP);
         l.Us = take(n * CH * DvP);
@@ -782,8 +662,8 @@ Layout layout(const dwconv_delta_plan &p, int seqs, int tokens, bool backward) {
 }
 
 template <class X>
-bool rows_of_4(const void *p, int64_t ld, int d) {
-    return ((uintptr_t)p & (4 * sizeof(X) - 1)) == 0 && ld % 4 == 0 && d % 4 == 0;
+bool rows_of(int n, const void *p, int64_t ld, int d) {
+    return ((uintptr_t)p & (n * sizeof(X) - 1)) == 0 && ld % n == 0 && d % n == 0;
 }
 
 template <class DT, int DK>
@@ -796,10 +676,14 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
     c.Hk = p.Hk, c.Hv = p.Hv, c.Dk = p.Dk, c.Dv = p.Dv, c.DvP = (p.Dv + 31) / 32 * 32;
     c.slots = a.tokens / CH + a.seqs;
     c.scale = p.scale, c.eps = p.eps, c.normalize = p.normalize;
-    c.vec4 = rows_of_4<X>(a.q, a.ldq, p.Dk) && rows_of_4<X>(a.k, a.ldk, p.Dk);
+    c.vec4 = rows_of<X>(4, a.q, a.ldq, p.Dk) && rows_of<X>(4, a.k, a.ldk, p.Dk);
+    c.vec8 = rows_of<X>(8, a.q, a.ldq, p.Dk) && rows_of<X>(8, a.k, a.ldk, p.Dk);
     c.q = a.q, c.k = a.k, c.v = a.v, c.ldq = a.ldq, c.ldk = a.ldk, c.ldv = a.ldv;
     c.g = a.g, c.beta = a.beta;
     c.T = ws + l.T, c.P = ws + l.P, c.vecs = ws + l.vecs;
+    c.keys = (char *)(ws + l.keys), c.heads = (char *)(ws + l.heads);
+    c.key_bytes = (int64_t)l.key_bytes, c.head_bytes = (int64_t)l.head_bytes;
+    const bool split = split_runs(p.dtype, DK);
     const uint64_t chunks = (uint64_t)c.slots * p.Hk, walks = (uint64_t)a.seqs * p.Hv * ((p.Dv + 63) / 64);
     if (chunks >= (1u << 24) || walks >= (1u << 24)) return hipErrorInvalidConfiguration;
     const size_t keys = 2 * sizeof(float) * CH * (DK + 4);
@@ -807,30 +691,42 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
         return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
     };
     hipError_t e;
-    if (a.tokens > 0) {
+    if (a.tokens > 0 && split) {
+        if ((e = split_prepare(p.dtype, DK, c, backward, st)) != hipSuccess) return e;
+    } else if (a.tokens > 0) {
         const size_t n = keys + (TRI + 4 * 256) * sizeof(float);
         if ((e = lds((const void *)k_prepare<DT, DK>, n)) != hipSuccess) return e;
         k_prepare<DT, DK><<<(uint32_t)chunks, 256, n, st>>>(c);
     }
     if (walks == 0) return hipGetLastError();
+    if (!backward && split) return split_scan(p.dtype, DK, c, a.state_in, a.state_out, a.o, a.ldo, nullptr, nullptr, st);
     if (!backward) {
         if ((e = lds((const void *)k_scan<DT, DK, false>, sizeof(Stage<DK>))) != hipSuccess) return e;
         k_scan<DT, DK, false><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, a.state_in, a.state_out, (X *)a.o,
                                                                                a.ldo, nullptr, nullptr);
         return hipGetLastError();
     }
-    if (a.tokens > 0) {
+    if (split) {
+        if (a.tokens > 0 && (e = split_scan(p.dtype, DK, c, a.state_in, nullptr, nullptr, 0, ws + l.S0s, ws + l.Us, st)) != hipSuccess)
+            return e;
+    } else if (a.tokens > 0) {
         if ((e = lds((const void *)k_scan<DT, DK, true>, sizeof(Stage<DK>))) != hipSuccess) return e;
         k_scan<DT, DK, true><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, a.state_in, nullptr, (X *)nullptr, 0,
                                                                               ws + l.S0s, ws + l.Us);
     }
-    if ((e = lds((const void *)k_rscan<DT, DK>, sizeof(Stage<DK>))) != hipSuccess) return e;
-    k_rscan<DT, DK><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, (const X *)a.d_o, a.lddo, a.dstate_out,
-                                                                     a.dstate_in, (X *)a.dv, a.lddv, ws + l.dSs,
-                                                                     ws + l.dRs);
+    if (split) {
+        if ((e = split_rscan(p.dtype, DK, c, a.d_o, a.lddo, a.dstate_out, a.dstate_in, a.dv, a.lddv, ws + l.dSs,
+                             ws + l.dRs, st)) != hipSuccess)
+            return e;
+    } else {
+        if ((e = lds((const void *)k_rscan<DT, DK>, sizeof(Stage<DK>))) != hipSuccess) return e;
+        k_rscan<DT, DK><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, (const X *)a.d_o, a.lddo, a.dstate_out,
+                                                                         a.dstate_in, (X *)a.dv, a.lddv, ws + l.dSs,
+                                                                         ws + l.dRs);
+    }
     if (a.tokens > 0) {
         GradArgs ga{ws + l.S0s, ws + l.Us, ws + l.dSs, ws + l.dRs, a.d_o, a.lddo, a.dq, a.dk, a.lddq, a.lddk, a.dg,
-                    a.dbeta, rows_of_4<X>(a.d_o, a.lddo, p.Dv), rows_of_4<X>(a.v, a.ldv, p.Dv)};
+                    a.dbeta, rows_of<X>(4, a.d_o, a.lddo, p.Dv), rows_of<X>(4, a.v, a.ldv, p.Dv)};
         const size_t blocks = sizeof(float) * 36 * (2 * DK + CH), tiles = keys + 2 * TRI * sizeof(float);
         const size_t n = blocks > tiles ? blocks : tiles;
         if ((e = lds((const void *)k_grad<DT, DK>, n)) != hipSuccess) return e;
