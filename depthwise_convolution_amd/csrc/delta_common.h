@@ -167,16 +167,7 @@ __host__ __device__ constexpr int key_frags(int DK, int terms) { return DK / 8 *
 // bf16 values are one term, fp16 values two bf16 terms
 __host__ __device__ constexpr int key_terms(int dtype) { return dtype == DWCONV_BF16 ? 1 : 2; }
 
-// LDS of the walks: forward Q, K, K^T with P, T and the vectors; backward K,
-// K^T, Q^T with the vectors, T^T and P^T.
-__host__ __device__ constexpr int lds_fwd(int DK, int terms) { return (3 * key_frags(DK, terms) + HEAD_FWD) * FRAG; }
-__host__ __device__ constexpr int lds_bwd(int DK, int terms) {
-    return (3 * key_frags(DK, terms) + HEAD_BWD - AT_VEC) * FRAG;
-}
-// Sizes that the 16-bit products cover: both walks' operands fit LDS.
-inline bool split_runs(int dtype, int DK) {
-    return dtype != DWCONV_F32 && lds_bwd(DK, key_terms(dtype)) <= 160 * 1024;
-}
+inline bool split_runs(int dtype) { return dtype != DWCONV_F32; }
 
 // launchers (k_delta_split.hip)
 hipError_t split_prepare(int dtype, int DK, const Ctx &c, bool backward, hipStream_t st);

@@ -631,7 +631,7 @@ struct Layout {
 Layout layout(const dwconv_delta_plan &p, int seqs, int tokens, bool backward) {
     const size_t slots = (size_t)tokens / CH + seqs, n = slots * p.Hv;
     const size_t DvP = (p.Dv + 31) / 32 * 32, DK = padded_keys(p.Dk);
-    const bool split = split_runs(p.dtype, (int)DK);
+    const bool split = split_runs(p.dtype);
     Layout l{};
     size_t at = 0;
     auto take = [&](size_t f) {
@@ -683,9 +683,10 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
     c.T = ws + l.T, c.P = ws + l.P, c.vecs = ws + l.vecs;
     c.keys = (char *)(ws + l.keys), c.heads = (char *)(ws + l.heads);
     c.key_bytes = (int64_t)l.key_bytes, c.head_bytes = (int64_t)l.head_bytes;
-    const bool split = split_runs(p.dtype, DK);
+    const bool split = split_runs(p.dtype);
     const uint64_t chunks = (uint64_t)c.slots * p.Hk, walks = (uint64_t)a.seqs * p.Hv * ((p.Dv + 63) / 64);
-    if (chunks >= (1u << 24) || walks >= (1u << 24)) return hipErrorInvalidConfiguration;
+    // (the 16-bit walks have up to four workgroups for each of these)
+    if (chunks >= (1u << 24) || walks >= (1u << 22)) return hipErrorInvalidConfiguration;
     const size_t keys = 2 * sizeof(float) * CH * (DK + 4);
     auto lds = [](const void *f, size_t bytes) {
         return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);

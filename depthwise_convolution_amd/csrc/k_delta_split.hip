@@ -11,10 +11,14 @@
 // times three), six for two fp32 ones.  What only makes o (its own rounding is
 // 2^-9 or 2^-12) takes two terms: 2^-18.
 //
-// k_prepare lays all left operands out as fragments (delta_common.h) in the
-// workspace, once for all wavefronts that use them, so that a walk copies them
-// to LDS in a line, through registers that are loaded a chunk ahead, and reads
-// them without bank conflicts.
+// A workgroup walks one sequence's chunks for one head and 16 NT columns of the
+// state.  Wavefront w has tokens 16 w .. 16 w + 15 of every chunk and a quarter
+// of the state's rows, so that a chunk's chain of products (K S, T R, K^T U) is
+// a quarter as long as in one wavefront; right operands are split by the
+// wavefront that made them and pass through LDS, three barriers a chunk.  Left
+// operands each serve one wavefront: they go from the workspace, where
+// k_prepare lays them out as fragments (delta_common.h), straight to registers,
+// and a register is loaded for the next chunk as soon as it has been used.
 #include <type_traits>
 
 #include "delta_common.h"
@@ -45,6 +49,15 @@ __device__ __forceinline__ void split(f32x4 a, f32x4 b, bf16x8 (&t)[N]) {
     }
 }
 
+template <int N>
+__device__ __forceinline__ void split(f32x4 x, bf16x4 (&t)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        t[n] = __builtin_convertvector(x, bf16x4);
+        if (n + 1 < N) x -= __builtin_convertvector(t[n], f32x4);
+    }
+}
+
 template <class DT>
 struct Raw;
 template <>
@@ -69,24 +82,31 @@ struct Raw<F16> {
     }
 };
 
-// Products of NA terms times NB terms down to order `last` (term i times term j
-// has order i + j)
-template <int NA, int NB>
-__device__ __forceinline__ f32x4 mac(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], int last, f32x4 c) {
+// c += products of NA terms times NB terms down to order `last` (term i times
+// term j has order i + j), for NT neighbouring column tiles
+template <int NA, int NB, int NT>
+__device__ __forceinline__ void mac(const bf16x8 (&a)[NA], const bf16x8 (&b)[NT][NB], int last, f32x4 (&c)[NT]) {
 #pragma unroll
     for (int o = 0; o < NA + NB - 1; ++o) {
         if (o > last) break;
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-            if (o - i >= 0 && o - i < NB) c = mfma32(a[i], b[o - i], c);
+            if (o - i >= 0 && o - i < NB) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) c[t] = mfma32(a[i], b[t][o - i], c[t]);
+            }
     }
-    return c;
 }
 
-// place of block (m, kb) of a lower triangle's six (kb <= m / 2), and of an
-// upper one's (kb >= m / 2)
-__host__ __device__ constexpr int lower_block(int m, int kb) { return m < 2 ? m : 2 * (m - 1) + kb; }
-__host__ __device__ constexpr int upper_block(int m, int kb) { return m < 2 ? 2 * m + kb : 2 + m; }
+// the place of block (m, kb) among a triangle's six
+__device__ __forceinline__ int lower_block(int m, int kb) { return m < 2 ? m : 2 * (m - 1) + kb; }
+__device__ __forceinline__ int upper_block(int m, int kb) { return m < 2 ? 2 * m + kb : 2 + m; }
+// the row tile and term block of a lower triangle's six blocks (kb <= m / 2),
+// and of an upper one's (kb >= m / 2)
+__host__ __device__ constexpr int lower_m(int blk) { return blk < 2 ? blk : blk / 2 + 1; }
+__host__ __device__ constexpr int lower_kb(int blk) { return blk < 2 ? 0 : blk % 2; }
+__host__ __device__ constexpr int upper_m(int blk) { return blk < 4 ? blk / 2 : blk - 2; }
+__host__ __device__ constexpr int upper_kb(int blk) { return blk < 4 ? blk % 2 : 1; }
 
 // One chunk and key head: lengths, the triangles of its value heads, and all
 // left operands as fragments.
@@ -246,12 +266,12 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
             const float *S = what == 0 || what == 3 ? Pl : Tl;
             f32x4 x[2];
             if (what < 2) {
-                const int m = blk < 2 ? blk : blk / 2 + 1, kb = blk < 2 ? 0 : blk % 2;
+                const int m = lower_m(blk), kb = lower_kb(blk);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                     x[j] = 2 * kb + j <= m ? *(const f32x4 *)&S[tri(m, 2 * kb + j) + r * 16 + g4] : splat(0.0f);
             } else {
-                const int m = blk < 4 ? blk / 2 : blk - 2, kb = blk < 4 ? blk % 2 : 1;
+                const int m = upper_m(blk), kb = upper_kb(blk);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -269,349 +289,460 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
     }
 }
 
-// A walk's operands on their way from the workspace to LDS: the first N1
-// fragments from the key head's part, the rest from the value head's; every
-// wavefront moves every fourth.
-template <int N1, int N2>
-struct Feed {
-    static constexpr int N = N1 + N2, PER = (N + 3) / 4;
-    u32x4 v[PER];
-    __device__ __forceinline__ void load(const char *a, const char *b, int wave, int lane) {
+// A wavefront's left operands from the workspace: N fragments' terms.
+template <int N>
+__device__ __forceinline__ void fetch(bf16x8 (&w)[N], const char *p, int lane) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int f = i * 4 + wave;
-            if (f >= N) break;
-            v[i] = *(const u32x4 *)((f < N1 ? a + f * FRAG : b + (f - N1) * FRAG) + lane * 16);
-        }
+    for (int n = 0; n < N; ++n) w[n] = *(const bf16x8 *)(p + n * FRAG + lane * 16);
+}
+
+// Right operands in LDS: [block of 32 terms][column tile][term], a fragment
+// each.  A wavefront writes a tile's terms (half of a block: `half`) and reads
+// whole blocks.
+template <int NT, int TERMS>
+struct Right {
+    char *p;
+    static constexpr int bytes(int blocks) { return blocks * NT * TERMS * FRAG; }
+    __device__ __forceinline__ void put(int tile, int t, f32x4 x, int lane) const {
+        bf16x4 v[TERMS];
+        split(x, v);
+#pragma unroll
+        for (int n = 0; n < TERMS; ++n)
+            *(bf16x4 *)(p + ((tile / 2 * NT + t) * TERMS + n) * FRAG + lane * 16 + tile % 2 * 8) = v[n];
     }
-    __device__ __forceinline__ void store(char *lds, int wave, int lane) const {
+    template <int N>
+    __device__ __forceinline__ void get(int blk, bf16x8 (&v)[NT][N], int lane) const {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int f = i * 4 + wave;
-            if (f >= N) break;
-            *(u32x4 *)(lds + f * FRAG + lane * 16) = v[i];
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[t][n] = *(const bf16x8 *)(p + ((blk * NT + t) * TERMS + n) * FRAG + lane * 16);
+    }
+};
+
+// The columns of a walk: NT tiles of 16 from `first` on; a lane's column of
+// tile t is first + 16 t + lane % 16.
+template <int NT>
+struct Columns {
+    int dv[NT], at[NT];  // the column, and the column itself or the last one
+    bool in[NT];
+    __device__ __forceinline__ Columns(int first, int r, int Dv) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            dv[t] = first + 16 * t + r;
+            in[t] = dv[t] < Dv;
+            at[t] = in[t] ? dv[t] : Dv - 1;
         }
     }
 };
 
-template <int N>
-__device__ __forceinline__ void frag(bf16x8 (&t)[N], const char *lds, int first, int lane) {
+// Four tokens x NT columns of v or dO: rows clamped to the n tokens that are
+// left and values not looked at (that would wait for them); `widened` puts
+// zeros in place of what is not there.
+template <class X, int NT>
+__device__ __forceinline__ void fetch_tokens(X (&v)[NT][4], const X *p, int64_t ld, int n, int row, const Columns<NT> &cl) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) t[n] = *(const bf16x8 *)(lds + (first + n) * FRAG + lane * 16);
+    for (int i = 0; i < 4; ++i) {
+        const X *q = p + (int64_t)min(row + i, n - 1) * ld;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) v[t][i] = q[cl.at[t]];
+    }
+}
+template <class DT, int NT>
+__device__ __forceinline__ f32x4 widened(const typename DT::X (&v)[NT][4], int t, int n, int row, const Columns<NT> &cl) {
+    f32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = cl.in[t] && row + i < n ? DT::widen(v[t][i]) : 0.0f;
+    return x;
+}
+template <class DT, int NT>
+__device__ __forceinline__ void store_tokens(typename DT::X *p, int64_t ld, const f32x4 (&x)[NT], int n, int row,
+                                             const Columns<NT> &cl) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (row + i < n) {
+            typename DT::X *q = p + (int64_t)(row + i) * ld;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (cl.in[t]) q[cl.dv[t]] = DT::narrow(x[t][i]);
+        }
 }
 
-// Forward walk (as k_scan in k_delta.hip).
-template <class DT, int DK, bool SAVE>
+// A wavefront's rows of the state: tiles w T .. w T + T - 1, T = DK / 64.
+template <int DK, int NT>
+struct State {
+    static constexpr int T = DK / 64;
+    f32x4 S[T][NT];
+    __device__ __forceinline__ void load(const float *p, const Ctx &c, int wave, int g4, const Columns<NT> &cl) {
+#pragma unroll
+        for (int x = 0; x < T; ++x)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * (wave * T + x) + g4 + i;
+                    S[x][t][i] = p && cl.in[t] && row < c.Dk ? p[(int64_t)row * c.Dv + cl.dv[t]] : 0.0f;
+                }
+    }
+    __device__ __forceinline__ void store(float *p, const Ctx &c, int wave, int g4, const Columns<NT> &cl) const {
+#pragma unroll
+        for (int x = 0; x < T; ++x)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * (wave * T + x) + g4 + i;
+                    if (cl.in[t] && row < c.Dk) p[(int64_t)row * c.Dv + cl.dv[t]] = S[x][t][i];
+                }
+    }
+    // all DK rows and the columns below DvP, for the backward pass
+    __device__ __forceinline__ void keep(float *p, const Ctx &c, int wave, int g4, const Columns<NT> &cl) const {
+#pragma unroll
+        for (int x = 0; x < T; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float *q = p + (int64_t)(16 * (wave * T + x) + g4 + i) * c.DvP;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (cl.dv[t] < c.DvP) q[cl.dv[t]] = S[x][t][i];
+            }
+    }
+    __device__ __forceinline__ void put(const Right<NT, 3> &r, int wave, int lane) const {
+#pragma unroll
+        for (int x = 0; x < T; ++x)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) r.put(wave * T + x, t, S[x][t], lane);
+    }
+};
+template <int NT>
+__device__ __forceinline__ void keep_tokens(float *p, const Ctx &c, const f32x4 (&x)[NT], int row, const Columns<NT> &cl) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float *q = p + (int64_t)(row + i) * c.DvP;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (cl.dv[t] < c.DvP) q[cl.dv[t]] = x[t][i];
+    }
+}
+
+// Which walk a workgroup has.  Neighbouring workgroups (column groups of a
+// head, heads of a key head) share operands: they go to one XCD.
+struct Walk {
+    int first, h, s;
+    __device__ __forceinline__ Walk(const Ctx &c, int cols, int width) {
+        const uint32_t nb = (width + cols - 1) / cols, i = xcd_remap(blockIdx.x, gridDim.x);
+        first = (int)(i % nb) * cols;
+        h = (int)(i / nb % c.Hv);
+        s = (int)(i / nb / c.Hv);
+    }
+};
+
+// Forward walk.  SAVE: keeps each chunk's state and U for the backward pass
+// instead of making outputs.
+template <class DT, int DK, int NT, bool SAVE>
 __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, float *state_out, typename DT::X *o,
                                               int64_t ldo, float *S0s, float *Us) {
     using X = typename DT::X;
-    constexpr int NA = Raw<DT>::TERMS, NK = DK / 32, NF = DK / 8 * NA;
-    // LDS: [Q] K K^T | [P] T vectors
-    constexpr int ATK = SAVE ? 0 : NF, ATKT = ATK + NF, N1 = ATKT + NF;
-    constexpr int ATP = N1, ATT = SAVE ? N1 : N1 + NBLK * P_TERMS, ATV = ATT + NBLK * T_TERMS, N2 = ATV + VEC_FRAGS - N1;
+    constexpr int NA = Raw<DT>::TERMS, NK = DK / 32, NF = DK / 8 * NA, T = DK / 64;
     extern __shared__ char L[];
-    const int nb = (c.Dv + 63) / 64;
-    const int vb = blockIdx.x % nb, h = blockIdx.x / nb % c.Hv, s = blockIdx.x / nb / c.Hv;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4;
-    const int dv = vb * 64 + wave * 16 + r;
-    const bool in = dv < c.Dv;
-    const int a = c.seq.begin(s), b = c.seq.end(s);
-    const int64_t st = ((int64_t)s * c.Hv + h) * c.Dk * c.Dv + dv;
-    f32x4 S[DK / 16];
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 16 * t + g4 + i;
-            S[t][i] = state_in && in && row < c.Dk ? state_in[st + (int64_t)row * c.Dv] : 0.0f;
-        }
-    const int slot0 = first_slot(c.seq, s), nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
-    const char *keys = c.keys + ((int64_t)slot0 * c.Hk + hk) * c.key_bytes + (SAVE ? NF * FRAG : 0);
-    const char *heads = c.heads + ((int64_t)slot0 * c.Hv + h) * c.head_bytes + (SAVE ? AT_T * FRAG : 0);
-    const X *pv = (const X *)c.v + (int64_t)a * c.ldv + (int64_t)h * c.Dv + dv;
-    Feed<N1, N2> feed;
-    X vn[16];
-    auto ahead = [&](int k) {
-        feed.load(keys + (int64_t)k * c.Hk * c.key_bytes, heads + (int64_t)k * c.Hv * c.head_bytes, wave, lane);
-        const int n = b - a - k * CH;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * m + g4 + i;
-                vn[4 * m + i] = in && t < n ? pv[((int64_t)k * CH + t) * c.ldv] : (X)0;
-            }
-    };
-    if (nc > 0) ahead(0);
-    for (int k = 0; k < nc; ++k) {
-        const int n = b - a - k * CH;  // tokens left
-        __syncthreads();
-        feed.store(L, wave, lane);
-        f32x4 x[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[m][i] = DT::widen(vn[4 * m + i]);
-        if (k + 1 < nc) ahead(k + 1);
-        const int64_t at = (int64_t)(slot0 + k) * c.Hv + h;
-        if (SAVE && dv < c.DvP) {
-            float *d = S0s + at * DK * c.DvP + dv;
-#pragma unroll
-            for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[(int64_t)(16 * t + g4 + i) * c.DvP] = S[t][i];
-        }
-        __syncthreads();
-        const float *vec = (const float *)(L + ATV * FRAG);
-        auto v4 = [&](int which, int m) { return *(const f32x4 *)&vec[which * CH + 16 * m + g4]; };
-        f32x4 ks[4], os[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) ks[m] = os[m] = splat(0.0f);
+    const Right<NT, 3> SB{L}, RB{SB.p + SB.bytes(NK)}, EB{RB.p + RB.bytes(2)};
+    const Right<NT, 2> UB{EB.p + EB.bytes(2)};
+    const Walk wk(c, 16 * NT, SAVE ? c.DvP : c.Dv);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
+              g4 = (lane >> 4) * 4;
+    const int h = wk.h, row = 16 * wave + g4;  // this lane's tokens: row .. row + 3
+    const Columns<NT> cl(wk.first, r, c.Dv);
+    const int a = c.seq.begin(wk.s), b = c.seq.end(wk.s);
+    const int64_t st = ((int64_t)wk.s * c.Hv + h) * c.Dk * c.Dv;
+    State<DK, NT> S;
+    S.load(state_in ? state_in + st : nullptr, c, wave, g4, cl);
+    const int slot0 = first_slot(c.seq, wk.s), nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
+    const X *pv = (const X *)c.v + (int64_t)a * c.ldv + (int64_t)h * c.Dv;
+    X *po = SAVE ? nullptr : o + (int64_t)a * ldo + (int64_t)h * c.Dv;
+    // operands of the chunk at hand
+    bf16x8 wK[NK][NA], wQ[SAVE ? 1 : NK][NA], wT[2][T_TERMS], wP[2][P_TERMS], wKT[T][2][NA];
+    f32x4 ek, rk, beta, eq;
+    float el;
+    X vn[NT][4];
+    auto keys_of = [&](int k) { return c.keys + ((int64_t)(slot0 + k) * c.Hk + hk) * c.key_bytes; };
+    auto head_of = [&](int k) { return c.heads + ((int64_t)(slot0 + k) * c.Hv + h) * c.head_bytes; };
+    auto fetch_rows = [&](int k) {  // what the first products need
+        const char *p = keys_of(k);
+        fetch_tokens<X, NT>(vn, pv + (int64_t)k * CH * c.ldv, c.ldv, b - a - k * CH, row, cl);
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-            bf16x8 t[3], w[NA];
-            split(S[2 * kb], S[2 * kb + 1], t);
+            fetch(wK[kb], p + (NF + (wave * NK + kb) * NA) * FRAG, lane);
+            if (!SAVE) fetch(wQ[kb], p + (wave * NK + kb) * NA * FRAG, lane);
+        }
+        const float *v = (const float *)(head_of(k) + AT_VEC * FRAG);
+        ek = *(const f32x4 *)(v + V_EK * CH + row);
+        beta = *(const f32x4 *)(v + V_BETA * CH + row);
+        if (!SAVE) eq = *(const f32x4 *)(v + V_EQ * CH + row);
+    };
+    auto fetch_T = [&](int k) {
+        const char *p = head_of(k);
+        fetch(wT[0], p + (AT_T + lower_block(wave, 0) * T_TERMS) * FRAG, lane);
+        if (wave >= 2) fetch(wT[1], p + (AT_T + lower_block(wave, 1) * T_TERMS) * FRAG, lane);
+        rk = *(const f32x4 *)((const float *)(p + AT_VEC * FRAG) + V_RK * CH + row);
+    };
+    auto fetch_KT = [&](int k) {
+        const char *p = keys_of(k) + 2 * NF * FRAG;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                frag(w, L, ATK + (m * NK + kb) * NA, lane);
-                ks[m] = mac(w, t, 2, ks[m]);
-                if (!SAVE) {
-                    frag(w, L, (m * NK + kb) * NA, lane);
-                    os[m] = mac(w, t, 1, os[m]);
-                }
+        for (int x = 0; x < T; ++x)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) fetch(wKT[x][kb], p + (2 * (wave * T + x) + kb) * NA * FRAG, lane);
+        el = ((const float *)(head_of(k) + AT_VEC * FRAG))[V_EB * CH + CH - 1];
+    };
+    auto fetch_P = [&](int k) {
+        const char *p = head_of(k);
+        fetch(wP[0], p + (AT_P + lower_block(wave, 0) * P_TERMS) * FRAG, lane);
+        if (wave >= 2) fetch(wP[1], p + (AT_P + lower_block(wave, 1) * P_TERMS) * FRAG, lane);
+    };
+    if (nc > 0) {
+        fetch_rows(0);
+        fetch_T(0);
+        fetch_KT(0);
+        if (!SAVE) fetch_P(0);
+        S.put(SB, wave, lane);
+    }
+    for (int k = 0; k < nc; ++k) {
+        const int n = b - a - k * CH, next = k + 1 < nc ? k + 1 : k;  // tokens left; the last chunk is fetched again
+        const int64_t at = (int64_t)(slot0 + k) * c.Hv + h;
+        __syncthreads();
+        if (SAVE) S.keep(S0s + at * DK * c.DvP, c, wave, g4, cl);
+        // R = beta (V - e^b K S)
+        f32x4 ks[NT], os[NT], u[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) ks[t] = os[t] = u[t] = splat(0.0f);
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            bf16x8 s[NT][3];
+            SB.get(kb, s, lane);
+            mac(wK[kb], s, 2, ks);
+            if (!SAVE) mac(wQ[kb], s, 1, os);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            RB.put(wave, t, beta * (widened<DT, NT>(vn, t, n, row, cl) - ek * ks[t]), lane);
+            if (!SAVE) os[t] *= eq;
+        }
+        fetch_rows(next);
+        __syncthreads();
+        // U = T R
+        {
+            bf16x8 x[NT][3];
+            RB.get(0, x, lane);
+            mac(wT[0], x, 2, u);
+            if (wave >= 2) {
+                RB.get(1, x, lane);
+                mac(wT[1], x, 2, u);
             }
         }
-        // R = beta (V - e^b K S), then U = T R
-        bf16x8 rt[2][3];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = v4(V_BETA, m) * (x[m] - v4(V_EK, m) * ks[m]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) split(x[2 * q], x[2 * q + 1], rt[q]);
-        f32x4 u[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            u[m] = splat(0.0f);
-#pragma unroll
-            for (int kb = 0; kb <= m / 2; ++kb) {
-                bf16x8 w[T_TERMS];
-                frag(w, L, ATT + lower_block(m, kb) * T_TERMS, lane);
-                u[m] = mac(w, rt[kb], 2, u[m]);
-            }
+        for (int t = 0; t < NT; ++t) {
+            EB.put(wave, t, u[t] * rk, lane);
+            if (!SAVE) UB.put(wave, t, u[t], lane);
         }
-        if (SAVE) {
-            if (dv < c.DvP) {
-                float *d = Us + at * CH * c.DvP + dv;
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) d[(int64_t)(16 * m + g4 + i) * c.DvP] = u[m][i];
-            }
-        } else {
-            bf16x8 ut[2][2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) split(u[2 * q], u[2 * q + 1], ut[q]);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                f32x4 y = v4(V_EQ, m) * os[m];
-#pragma unroll
-                for (int kb = 0; kb <= m / 2; ++kb) {
-                    bf16x8 w[P_TERMS];
-                    frag(w, L, ATP + lower_block(m, kb) * P_TERMS, lane);
-                    y = mac(w, ut[kb], 1, y);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 16 * m + g4 + i;
-                    if (in && t < n) o[(a + k * CH + t) * ldo + (int64_t)h * c.Dv + dv] = DT::narrow(y[i]);
-                }
-            }
-        }
+        fetch_T(next);
+        if (SAVE) keep_tokens<NT>(Us + at * CH * c.DvP, c, u, row, cl);
+        __syncthreads();
         // S = e^{b_last} S + K^T (e^{b_last - b} U)
-        const float el = vec[V_EB * CH + CH - 1];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) u[m] *= v4(V_RK, m);
+        for (int x = 0; x < T; ++x)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) split(u[2 * q], u[2 * q + 1], rt[q]);
+            for (int t = 0; t < NT; ++t) S.S[x][t] *= el;
 #pragma unroll
-        for (int t = 0; t < DK / 16; ++t) {
-            f32x4 y = S[t] * el;
+        for (int kb = 0; kb < 2; ++kb) {
+            bf16x8 e[NT][3];
+            EB.get(kb, e, lane);
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                bf16x8 w[NA];
-                frag(w, L, ATKT + (2 * t + kb) * NA, lane);
-                y = mac(w, rt[kb], 2, y);
+            for (int x = 0; x < T; ++x) mac(wKT[x][kb], e, 2, S.S[x]);
+        }
+        fetch_KT(next);
+        S.put(SB, wave, lane);
+        // O = scale e^b (Q S0) + P U
+        if (!SAVE) {
+            bf16x8 x[NT][2];
+            UB.get(0, x, lane);
+            mac(wP[0], x, 1, os);
+            if (wave >= 2) {
+                UB.get(1, x, lane);
+                mac(wP[1], x, 1, os);
             }
-            S[t] = y;
+            fetch_P(next);
+            store_tokens<DT, NT>(po + (int64_t)k * CH * ldo, ldo, os, n, row, cl);
         }
     }
-    if (state_out && in) {
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 16 * t + g4 + i;
-                if (row < c.Dk) state_out[st + (int64_t)row * c.Dv] = S[t][i];
-            }
-    }
+    if (state_out) S.store(state_out + st, c, wave, g4, cl);
 }
 
-// Backward walk (as k_rscan in k_delta.hip).
-template <class DT, int DK>
+// Backward walk.
+template <class DT, int DK, int NT>
 __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o, int64_t lddo, const float *dstate_out,
                                                float *dstate_in, typename DT::X *dvo, int64_t lddv, float *dSs,
                                                float *dRs) {
     using X = typename DT::X;
-    constexpr int NA = Raw<DT>::TERMS, NK = DK / 32, NF = DK / 8 * NA;
-    // LDS: K K^T Q^T | vectors T^T P^T
-    constexpr int ATKT = NF, ATQT = 2 * NF, N1 = 3 * NF, ATV = N1, ATTT = ATV + VEC_FRAGS,
-                  ATPT = ATTT + NBLK * T_TERMS, N2 = ATPT + NBLK * T_TERMS - N1;
+    constexpr int NA = Raw<DT>::TERMS, NK = DK / 32, NF = DK / 8 * NA, T = DK / 64;
     extern __shared__ char L[];
-    const int nb = (c.Dv + 63) / 64;
-    const int vb = blockIdx.x % nb, h = blockIdx.x / nb % c.Hv, s = blockIdx.x / nb / c.Hv;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4;
-    const int dv = vb * 64 + wave * 16 + r;
-    const bool in = dv < c.Dv;
-    const int a = c.seq.begin(s), b = c.seq.end(s);
-    const int64_t st = ((int64_t)s * c.Hv + h) * c.Dk * c.Dv + dv;
-    f32x4 S[DK / 16];
-#pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 16 * t + g4 + i;
-            S[t][i] = dstate_out && in && row < c.Dk ? dstate_out[st + (int64_t)row * c.Dv] : 0.0f;
-        }
-    const int slot0 = first_slot(c.seq, s), nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
-    const char *keys = c.keys + ((int64_t)slot0 * c.Hk + hk) * c.key_bytes + NF * FRAG;
-    const char *heads = c.heads + ((int64_t)slot0 * c.Hv + h) * c.head_bytes + AT_VEC * FRAG;
-    const X *pd = d_o + (int64_t)a * lddo + (int64_t)h * c.Dv + dv;
-    Feed<N1, N2> feed;
-    X dn[16];
-    auto ahead = [&](int k) {
-        feed.load(keys + (int64_t)k * c.Hk * c.key_bytes, heads + (int64_t)k * c.Hv * c.head_bytes, wave, lane);
-        const int n = b - a - k * CH;
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * m + g4 + i;
-                dn[4 * m + i] = in && t < n ? pd[((int64_t)k * CH + t) * lddo] : (X)0;
-            }
+    const Right<NT, 3> SB{L}, XB{SB.p + SB.bytes(NK)}, QB{XB.p + XB.bytes(2)}, ZB{QB.p + QB.bytes(2)};
+    const Right<NT, NA> OB{ZB.p + ZB.bytes(2)};
+    const Walk wk(c, 16 * NT, c.DvP);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
+              g4 = (lane >> 4) * 4;
+    const int h = wk.h, row = 16 * wave + g4;
+    const Columns<NT> cl(wk.first, r, c.Dv);
+    const int a = c.seq.begin(wk.s), b = c.seq.end(wk.s);
+    const int64_t st = ((int64_t)wk.s * c.Hv + h) * c.Dk * c.Dv;
+    State<DK, NT> S;
+    S.load(dstate_out ? dstate_out + st : nullptr, c, wave, g4, cl);
+    const int slot0 = first_slot(c.seq, wk.s), nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
+    const X *pd = d_o + (int64_t)a * lddo + (int64_t)h * c.Dv;
+    X *pv = dvo + (int64_t)a * lddv + (int64_t)h * c.Dv;
+    bf16x8 wK[NK][NA], wPT[2][T_TERMS], wTT[2][T_TERMS], wKT[T][2][NA], wQT[T][2][NA];
+    f32x4 ek, rk, beta, eq;
+    float el;
+    X dn[NT][4];
+    auto keys_of = [&](int k) { return c.keys + ((int64_t)(slot0 + k) * c.Hk + hk) * c.key_bytes; };
+    auto head_of = [&](int k) { return c.heads + ((int64_t)(slot0 + k) * c.Hv + h) * c.head_bytes; };
+    auto fetch_tokens_of = [&](int k) {
+        fetch_tokens<X, NT>(dn, pd + (int64_t)k * CH * lddo, lddo, b - a - k * CH, row, cl);
+        eq = *(const f32x4 *)((const float *)(head_of(k) + AT_VEC * FRAG) + V_EQ * CH + row);
     };
-    if (nc > 0) ahead(nc - 1);
-    for (int k = nc - 1; k >= 0; --k) {
-        const int n = b - a - k * CH;
-        __syncthreads();
-        feed.store(L, wave, lane);
-        f32x4 dO[4];
+    auto fetch_rows = [&](int k) {
+        const char *p = keys_of(k) + NF * FRAG, *q = head_of(k);
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int kb = 0; kb < NK; ++kb) fetch(wK[kb], p + (wave * NK + kb) * NA * FRAG, lane);
+        fetch(wPT[1], q + (AT_PT + upper_block(wave, 1) * T_TERMS) * FRAG, lane);
+        if (wave < 2) fetch(wPT[0], q + (AT_PT + upper_block(wave, 0) * T_TERMS) * FRAG, lane);
+        rk = *(const f32x4 *)((const float *)(q + AT_VEC * FRAG) + V_RK * CH + row);
+    };
+    auto fetch_T = [&](int k) {
+        const char *q = head_of(k);
+        const float *v = (const float *)(q + AT_VEC * FRAG);
+        fetch(wTT[1], q + (AT_TT + upper_block(wave, 1) * T_TERMS) * FRAG, lane);
+        if (wave < 2) fetch(wTT[0], q + (AT_TT + upper_block(wave, 0) * T_TERMS) * FRAG, lane);
+        beta = *(const f32x4 *)(v + V_BETA * CH + row);
+        ek = *(const f32x4 *)(v + V_EK * CH + row);
+    };
+    auto fetch_columns = [&](int k, bool q) {
+        const char *p = keys_of(k) + (q ? 3 : 2) * NF * FRAG;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dO[m][i] = DT::widen(dn[4 * m + i]);
-        if (k > 0) ahead(k - 1);
-        const int64_t at = (int64_t)(slot0 + k) * c.Hv + h;
-        if (dv < c.DvP) {
-            float *d = dSs + at * DK * c.DvP + dv;
+        for (int x = 0; x < T; ++x)
 #pragma unroll
-            for (int t = 0; t < DK / 16; ++t)
+            for (int kb = 0; kb < 2; ++kb)
+                fetch(q ? wQT[x][kb] : wKT[x][kb], p + (2 * (wave * T + x) + kb) * NA * FRAG, lane);
+        if (q) el = ((const float *)(head_of(k) + AT_VEC * FRAG))[V_EB * CH + CH - 1];
+    };
+    // dO's terms (exact) and those of scale e^b dO, for all wavefronts
+    auto put_tokens = [&](int k) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) d[(int64_t)(16 * t + g4 + i) * c.DvP] = S[t][i];
+        for (int t = 0; t < NT; ++t) {
+            const f32x4 x = widened<DT, NT>(dn, t, b - a - k * CH, row, cl);
+            OB.put(wave, t, x, lane);
+            QB.put(wave, t, x * eq, lane);
         }
+    };
+    if (nc > 0) {
+        fetch_tokens_of(nc - 1);
+        fetch_rows(nc - 1);
+        fetch_T(nc - 1);
+        fetch_columns(nc - 1, true);
+        fetch_columns(nc - 1, false);
+        put_tokens(nc - 1);
+        fetch_tokens_of(nc > 1 ? nc - 2 : 0);
+        S.put(SB, wave, lane);
+    }
+    for (int k = nc - 1; k >= 0; --k) {
+        const int n = b - a - k * CH, next = k > 0 ? k - 1 : 0;
+        const int64_t at = (int64_t)(slot0 + k) * c.Hv + h;
         __syncthreads();
-        const float *vec = (const float *)(L + ATV * FRAG);
-        auto v4 = [&](int which, int m) { return *(const f32x4 *)&vec[which * CH + 16 * m + g4]; };
-        // dU = e^{b_last - b} (K dS) + P^T dO; dO's terms are exact
-        f32x4 x[4];
+        S.keep(dSs + at * DK * c.DvP, c, wave, g4, cl);
+        // dU = e^{b_last - b} (K dS) + P^T dO
+        f32x4 x[NT], dR[NT];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = splat(0.0f);
+        for (int t = 0; t < NT; ++t) x[t] = dR[t] = splat(0.0f);
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-            bf16x8 t[3], w[NA];
-            split(S[2 * kb], S[2 * kb + 1], t);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                frag(w, L, (m * NK + kb) * NA, lane);
-                x[m] = mac(w, t, 2, x[m]);
-            }
+            bf16x8 s[NT][3];
+            SB.get(kb, s, lane);
+            mac(wK[kb], s, 2, x);
         }
-        bf16x8 ot[2][NA], rt[2][3];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) split(dO[2 * q], dO[2 * q + 1], ot[q]);
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            x[m] *= v4(V_RK, m);
-#pragma unroll
-            for (int kb = m / 2; kb < 2; ++kb) {
-                bf16x8 w[T_TERMS];
-                frag(w, L, ATPT + upper_block(m, kb) * T_TERMS, lane);
-                x[m] = mac(w, ot[kb], 2, x[m]);
+        for (int t = 0; t < NT; ++t) x[t] *= rk;
+        {
+            bf16x8 y[NT][NA];
+            OB.get(1, y, lane);
+            mac(wPT[1], y, 2, x);
+            if (wave < 2) {
+                OB.get(0, y, lane);
+                mac(wPT[0], y, 2, x);
             }
         }
 #pragma unroll
-        for (int q = 0; q < 2; ++q) split(x[2 * q], x[2 * q + 1], rt[q]);
-        f32x4 dR[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            dR[m] = splat(0.0f);
-#pragma unroll
-            for (int kb = m / 2; kb < 2; ++kb) {
-                bf16x8 w[T_TERMS];
-                frag(w, L, ATTT + upper_block(m, kb) * T_TERMS, lane);
-                dR[m] = mac(w, rt[kb], 2, dR[m]);
-            }
-            const f32x4 y = dR[m] * v4(V_BETA, m);
-            float *d = dRs + at * CH * c.DvP + dv;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * m + g4 + i;
-                if (dv < c.DvP) d[(int64_t)t * c.DvP] = dR[m][i];
-                if (in && t < n) dvo[(a + k * CH + t) * lddv + (int64_t)h * c.Dv + dv] = DT::narrow(y[i]);
+        for (int t = 0; t < NT; ++t) XB.put(wave, t, x[t], lane);
+        fetch_rows(next);
+        __syncthreads();
+        // dR = T^T dU, dV = beta dR; the part of dS that needs no dR
+        {
+            bf16x8 y[NT][3];
+            XB.get(1, y, lane);
+            mac(wTT[1], y, 2, dR);
+            if (wave < 2) {
+                XB.get(0, y, lane);
+                mac(wTT[0], y, 2, dR);
             }
         }
+        f32x4 y[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            y[t] = beta * dR[t];
+            ZB.put(wave, t, -ek * y[t], lane);
+        }
+        fetch_T(next);
+#pragma unroll
+        for (int z = 0; z < T; ++z)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) S.S[z][t] *= el;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            bf16x8 e[NT][3];
+            QB.get(kb, e, lane);
+#pragma unroll
+            for (int z = 0; z < T; ++z) mac(wQT[z][kb], e, 2, S.S[z]);
+        }
+        fetch_columns(next, true);
+        keep_tokens<NT>(dRs + at * CH * c.DvP, c, dR, row, cl);
+        store_tokens<DT, NT>(pv + (int64_t)k * CH * lddv, lddv, y, n, row, cl);
+        __syncthreads();
         // dS = e^{b_last} dS + Q^T (scale e^b dO) - K^T (e^b beta dR)
-        const float el = vec[V_EB * CH + CH - 1];
-        bf16x8 qt[2][3];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            dO[m] *= v4(V_EQ, m);
-            dR[m] *= -v4(V_EK, m) * v4(V_BETA, m);
+        for (int kb = 0; kb < 2; ++kb) {
+            bf16x8 e[NT][3];
+            ZB.get(kb, e, lane);
+#pragma unroll
+            for (int z = 0; z < T; ++z) mac(wKT[z][kb], e, 2, S.S[z]);
         }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            split(dO[2 * q], dO[2 * q + 1], qt[q]);
-            split(dR[2 * q], dR[2 * q + 1], rt[q]);
-        }
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t) {
-            f32x4 y = S[t] * el;
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                bf16x8 w[NA];
-                frag(w, L, ATQT + (2 * t + kb) * NA, lane);
-                y = mac(w, qt[kb], 2, y);
-                frag(w, L, ATKT + (2 * t + kb) * NA, lane);
-                y = mac(w, rt[kb], 2, y);
-            }
-            S[t] = y;
-        }
+        fetch_columns(next, false);
+        S.put(SB, wave, lane);
+        put_tokens(next);
+        fetch_tokens_of(next > 0 ? next - 1 : 0);
     }
-    if (dstate_in && in) {
-#pragma unroll
-        for (int t = 0; t < DK / 16; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 16 * t + g4 + i;
-                if (row < c.Dk) dstate_in[st + (int64_t)row * c.Dv] = S[t][i];
-            }
-    }
+    if (dstate_in) S.store(dstate_in + st, c, wave, g4, cl);
 }
+
+// Columns of the state a workgroup walks: 32, or 16 where that leaves CUs
+// without a walk.
+int walk_tiles(const Ctx &c) { return (int64_t)c.seq.seqs * c.Hv * ((c.Dv + 31) / 32) < 256 ? 1 : 2; }
+
+template <int NT>
+size_t lds_scan(int DK) { return (size_t)(DK / 32 + 2 + 2) * NT * 3 * FRAG + (size_t)2 * NT * 2 * FRAG; }
+template <int NT>
+size_t lds_rscan(int DK, int terms) { return (size_t)(DK / 32 + 6) * NT * 3 * FRAG + (size_t)2 * NT * terms * FRAG; }
 
 hipError_t lds_room(const void *f, size_t bytes) {
     return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-// Calls f with the type and the padded key size; sizes that split_runs leaves
-// out never come here.
+// Calls f with the type and the padded key size.
 template <class F>
 hipError_t pick(int dtype, int DK, F f) {
     if (dtype == DWCONV_BF16) {
@@ -622,7 +753,12 @@ hipError_t pick(int dtype, int DK, F f) {
             default: return f(BF16{}, std::integral_constant<int, 256>{});
         }
     }
-    return DK == 64 ? f(F16{}, std::integral_constant<int, 64>{}) : f(F16{}, std::integral_constant<int, 128>{});
+    switch (DK) {
+        case 64: return f(F16{}, std::integral_constant<int, 64>{});
+        case 128: return f(F16{}, std::integral_constant<int, 128>{});
+        case 192: return f(F16{}, std::integral_constant<int, 192>{});
+        default: return f(F16{}, std::integral_constant<int, 256>{});
+    }
 }
 
 }  // namespace
@@ -649,9 +785,11 @@ hipError_t split_scan(int dtype, int DK_, const Ctx &c, const float *state_in, f
         using DT = decltype(dt);
         using X = typename DT::X;
         constexpr int DK = decltype(dk)::value;
-        const uint32_t blocks = (uint32_t)((int64_t)c.seq.seqs * c.Hv * ((c.Dv + 63) / 64));
-        const size_t n = lds_fwd(DK, Raw<DT>::TERMS);
-        auto f = S0s ? k_scan<DT, DK, true> : k_scan<DT, DK, false>;
+        const int nt = walk_tiles(c);
+        const uint32_t blocks = (uint32_t)((int64_t)c.seq.seqs * c.Hv * (((S0s ? c.DvP : c.Dv) + 16 * nt - 1) / (16 * nt)));
+        const size_t n = nt == 1 ? lds_scan<1>(DK) : lds_scan<2>(DK);
+        auto f = nt == 1 ? (S0s ? k_scan<DT, DK, 1, true> : k_scan<DT, DK, 1, false>)
+                         : (S0s ? k_scan<DT, DK, 2, true> : k_scan<DT, DK, 2, false>);
         hipError_t e = lds_room((const void *)f, n);
         if (e != hipSuccess) return e;
         f<<<blocks, 256, n, st>>>(c, state_in, state_out, (X *)o, ldo, S0s, Us);
@@ -665,11 +803,13 @@ hipError_t split_rscan(int dtype, int DK_, const Ctx &c, const void *d_o, int64_
         using DT = decltype(dt);
         using X = typename DT::X;
         constexpr int DK = decltype(dk)::value;
-        const uint32_t blocks = (uint32_t)((int64_t)c.seq.seqs * c.Hv * ((c.Dv + 63) / 64));
-        const size_t n = lds_bwd(DK, Raw<DT>::TERMS);
-        hipError_t e = lds_room((const void *)k_rscan<DT, DK>, n);
+        const int nt = walk_tiles(c);
+        const uint32_t blocks = (uint32_t)((int64_t)c.seq.seqs * c.Hv * (c.DvP / (16 * nt)));
+        const size_t n = nt == 1 ? lds_rscan<1>(DK, Raw<DT>::TERMS) : lds_rscan<2>(DK, Raw<DT>::TERMS);
+        auto f = nt == 1 ? k_rscan<DT, DK, 1> : k_rscan<DT, DK, 2>;
+        hipError_t e = lds_room((const void *)f, n);
         if (e != hipSuccess) return e;
-        k_rscan<DT, DK><<<blocks, 256, n, st>>>(c, (const X *)d_o, lddo, dstate_out, dstate_in, (X *)dv, lddv, dSs, dRs);
+        f<<<blocks, 256, n, st>>>(c, (const X *)d_o, lddo, dstate_out, dstate_in, (X *)dv, lddv, dSs, dRs);
         return hipGetLastError();
     });
 }
