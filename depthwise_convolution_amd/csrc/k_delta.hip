@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = 16 * m + g4 + i;
-                    if (in && t < ch.n) o[(ch.tok + t) * ldo + (int64_t)h * c.Dv + dv] = DT::narrow(x[i]);
+                    if (in && t < ch.n) o[(ch.tok + t) * ldo + (int64_t)h * c.Dv + dv] = rounded<DT>(x[i]);
                 }
             }
         }
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o,
             for (int i = 0; i < 4; ++i) {
                 const int t = 16 * m + g4 + i;
                 if (dv < c.DvP) d[(int64_t)t * c.DvP] = x[i];
-                if (in && t < ch.n) dvo[(ch.tok + t) * lddv + (int64_t)h * c.Dv + dv] = DT::narrow(y[i]);
+                if (in && t < ch.n) dvo[(ch.tok + t) * lddv + (int64_t)h * c.Dv + dv] = rounded<DT>(y[i]);
             }
         }
         const float el = L.eb[CH - 1];
@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
             const int x = 16 * wave + g4 + i, y = 16 * t + r;
             if (x >= ch.n || y >= c.Dk) continue;
             const float q = rq[x] * (dQ[t][i] - Q[x][y] * uq[i]), k = rk[x] * (dK[t][i] - K[x][y] * uk[i]);
-            ((X *)ga.dq)[(ch.tok + x) * ga.lddq + (int64_t)hk * c.Dk + y] = DT::narrow(q);
-            ((X *)ga.dk)[(ch.tok + x) * ga.lddk + (int64_t)hk * c.Dk + y] = DT::narrow(k);
+            ((X *)ga.dq)[(ch.tok + x) * ga.lddq + (int64_t)hk * c.Dk + y] = rounded<DT>(q);
+            ((X *)ga.dk)[(ch.tok + x) * ga.lddk + (int64_t)hk * c.Dk + y] = rounded<DT>(k);
         }
 }
 

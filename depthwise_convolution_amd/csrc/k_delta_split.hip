@@ -29,34 +29,50 @@ namespace {
 using namespace delta;
 
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
-using bf16x4 = __attribute__((ext_vector_type(4))) __bf16;
 using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
 using f32x8 = __attribute__((ext_vector_type(8))) float;
 using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
+using u32x2 = __attribute__((ext_vector_type(2))) uint32_t;
 
 __device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// x = t[0] + t[1] + ... : each the nearest bf16 of what is left
+using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
+using f32x2 = __attribute__((ext_vector_type(2))) float;
+
+// a and b split into N bf16 terms, each the nearest of what is left, in pairs.
+// (On the words: conversions of single values would be made a second time.)
+template <int N>
+__device__ __forceinline__ void split(float a, float b, uint32_t (&t)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        t[n] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+        if (n + 1 < N) {
+            a -= __uint_as_float(t[n] << 16);
+            b -= __uint_as_float(t[n] & 0xffff0000u);
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void split(f32x4 x, u32x2 (&t)[N]) {
+    uint32_t lo[N], hi[N];
+    split(x[0], x[1], lo);
+    split(x[2], x[3], hi);
+#pragma unroll
+    for (int n = 0; n < N; ++n) t[n] = u32x2{lo[n], hi[n]};
+}
 template <int N>
 __device__ __forceinline__ void split(f32x4 a, f32x4 b, bf16x8 (&t)[N]) {
-    f32x8 x = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    u32x2 lo[N], hi[N];
+    split(a, lo);
+    split(b, hi);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        t[n] = __builtin_convertvector(x, bf16x8);
-        if (n + 1 < N) x -= __builtin_convertvector(t[n], f32x8);
-    }
+    for (int n = 0; n < N; ++n) t[n] = __builtin_bit_cast(bf16x8, (u32x4{lo[n][0], lo[n][1], hi[n][0], hi[n][1]}));
 }
 
-template <int N>
-__device__ __forceinline__ void split(f32x4 x, bf16x4 (&t)[N]) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        t[n] = __builtin_convertvector(x, bf16x4);
-        if (n + 1 < N) x -= __builtin_convertvector(t[n], f32x4);
-    }
-}
+// Keeps loads in front of the products that hide them.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
 template <class DT>
 struct Raw;
@@ -292,8 +308,9 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
 // A wavefront's left operands from the workspace: N fragments' terms.
 template <int N>
 __device__ __forceinline__ void fetch(bf16x8 (&w)[N], const char *p, int lane) {
+    const uint32_t off = (uint32_t)lane * 16;
 #pragma unroll
-    for (int n = 0; n < N; ++n) w[n] = *(const bf16x8 *)(p + n * FRAG + lane * 16);
+    for (int n = 0; n < N; ++n) w[n] = *(const bf16x8 *)(p + n * FRAG + off);
 }
 
 // Right operands in LDS: [block of 32 terms][column tile][term], a fragment
@@ -304,11 +321,11 @@ struct Right {
     char *p;
     static constexpr int bytes(int blocks) { return blocks * NT * TERMS * FRAG; }
     __device__ __forceinline__ void put(int tile, int t, f32x4 x, int lane) const {
-        bf16x4 v[TERMS];
+        u32x2 v[TERMS];
         split(x, v);
 #pragma unroll
         for (int n = 0; n < TERMS; ++n)
-            *(bf16x4 *)(p + ((tile / 2 * NT + t) * TERMS + n) * FRAG + lane * 16 + tile % 2 * 8) = v[n];
+            *(u32x2 *)(p + ((tile / 2 * NT + t) * TERMS + n) * FRAG + lane * 16 + tile % 2 * 8) = v[n];
     }
     template <int N>
     __device__ __forceinline__ void get(int blk, bf16x8 (&v)[NT][N], int lane) const {
@@ -335,16 +352,33 @@ struct Columns {
     }
 };
 
-// Four tokens x NT columns of v or dO: rows clamped to the n tokens that are
-// left and values not looked at (that would wait for them); `widened` puts
-// zeros in place of what is not there.
+// Four tokens (row .. row + 3, row = row0 + g4 of a chunk at p) x NT columns of
+// v or dO.  Loads are clamped to the n tokens that are left and not looked at
+// (that would wait for them); `widened` puts zeros in place of what is not
+// there.  Whole chunks take addresses of a uniform part and a 32-bit one.
+struct Rows {
+    int64_t ld;
+    uint32_t lane;  // elements from the wavefront's first row to the lane's
+    bool narrow;    // lane parts fit 32 bits
+    __device__ __forceinline__ Rows(int64_t ld, int g4) : ld(ld), lane((uint32_t)ld * g4), narrow(ld < (1 << 26)) {}
+};
 template <class X, int NT>
-__device__ __forceinline__ void fetch_tokens(X (&v)[NT][4], const X *p, int64_t ld, int n, int row, const Columns<NT> &cl) {
+__device__ __forceinline__ void fetch_tokens(X (&v)[NT][4], const X *p, const Rows &R, int n, int row0, int g4,
+                                             const Columns<NT> &cl) {
+    if (n >= CH && R.narrow) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const X *q = p + (int64_t)min(row + i, n - 1) * ld;
+        for (int i = 0; i < 4; ++i) {
+            const X *q = p + (row0 + i) * R.ld;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) v[t][i] = q[cl.at[t]];
+            for (int t = 0; t < NT; ++t) v[t][i] = q[R.lane + (uint32_t)cl.at[t]];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const X *q = p + min(row0 + g4 + i, n - 1) * R.ld;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) v[t][i] = q[cl.at[t]];
+        }
     }
 }
 template <class DT, int NT>
@@ -355,16 +389,26 @@ __device__ __forceinline__ f32x4 widened(const typename DT::X (&v)[NT][4], int t
     return x;
 }
 template <class DT, int NT>
-__device__ __forceinline__ void store_tokens(typename DT::X *p, int64_t ld, const f32x4 (&x)[NT], int n, int row,
-                                             const Columns<NT> &cl) {
+__device__ __forceinline__ void store_tokens(typename DT::X *p, const Rows &R, const f32x4 (&x)[NT], int n, int row0,
+                                             int g4, const Columns<NT> &cl) {
+    if (n >= CH && R.narrow) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (row + i < n) {
-            typename DT::X *q = p + (int64_t)(row + i) * ld;
+        for (int t = 0; t < NT; ++t)
+            if (cl.in[t]) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (cl.in[t]) q[cl.dv[t]] = DT::narrow(x[t][i]);
-        }
+                for (int i = 0; i < 4; ++i)
+                    (p + (row0 + i) * R.ld)[R.lane + (uint32_t)cl.dv[t]] = rounded<DT>(x[t][i]);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row0 + g4 + i < n) {
+                typename DT::X *q = p + (row0 + g4 + i) * R.ld;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (cl.in[t]) q[cl.dv[t]] = rounded<DT>(x[t][i]);
+            }
+    }
 }
 
 // A wavefront's rows of the state: tiles w T .. w T + T - 1, T = DK / 64.
@@ -394,17 +438,16 @@ struct State {
                     if (cl.in[t] && row < c.Dk) p[(int64_t)row * c.Dv + cl.dv[t]] = S[x][t][i];
                 }
     }
-    // all DK rows and the columns below DvP, for the backward pass
+    // all DK rows of all DvP columns, for the backward pass
     __device__ __forceinline__ void keep(float *p, const Ctx &c, int wave, int g4, const Columns<NT> &cl) const {
+        const uint32_t lane = g4 * c.DvP;
 #pragma unroll
-        for (int x = 0; x < T; ++x)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float *q = p + (int64_t)(16 * (wave * T + x) + g4 + i) * c.DvP;
+            for (int x = 0; x < T; ++x)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    if (cl.dv[t] < c.DvP) q[cl.dv[t]] = S[x][t][i];
-            }
+                for (int i = 0; i < 4; ++i)
+                    (p + (16 * (wave * T + x) + i) * c.DvP)[lane + (uint32_t)cl.dv[t]] = S[x][t][i];
     }
     __device__ __forceinline__ void put(const Right<NT, 3> &r, int wave, int lane) const {
 #pragma unroll
@@ -414,32 +457,44 @@ struct State {
     }
 };
 template <int NT>
-__device__ __forceinline__ void keep_tokens(float *p, const Ctx &c, const f32x4 (&x)[NT], int row, const Columns<NT> &cl) {
+__device__ __forceinline__ void keep_tokens(float *p, const Ctx &c, const f32x4 (&x)[NT], int row0, int g4,
+                                            const Columns<NT> &cl) {
+    const uint32_t lane = g4 * c.DvP;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float *q = p + (int64_t)(row + i) * c.DvP;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (cl.dv[t] < c.DvP) q[cl.dv[t]] = x[t][i];
-    }
+        for (int i = 0; i < 4; ++i) (p + (row0 + i) * c.DvP)[lane + (uint32_t)cl.dv[t]] = x[t][i];
 }
 
-// Which walk a workgroup has.  Neighbouring workgroups (column groups of a
-// head, heads of a key head) share operands: they go to one XCD.
+// Which walk a workgroup has.  The column groups of the value heads of one key
+// head and sequence (a unit) share operands: they go to one XCD, one behind the
+// other; units go round the XCDs, so that each gets its share of every
+// sequence.  `width`: columns walked (the backward pass also fills the padded
+// ones).  A grid that the XCDs do not divide has workgroups without a walk.
 struct Walk {
     int first, h, s;
     __device__ __forceinline__ Walk(const Ctx &c, int cols, int width) {
-        const uint32_t nb = (width + cols - 1) / cols, i = xcd_remap(blockIdx.x, gridDim.x);
+        const uint32_t nb = (width + cols - 1) / cols, group = c.Hv / c.Hk, per = nb * group;
+        const uint32_t j = blockIdx.x / 8, unit = j / per * 8 + blockIdx.x % 8, i = j % per;
         first = (int)(i % nb) * cols;
-        h = (int)(i / nb % c.Hv);
-        s = (int)(i / nb / c.Hv);
+        h = (int)(unit % c.Hk * group + i / nb);
+        s = (int)(unit / c.Hk);
+    }
+    static uint32_t blocks(const Ctx &c, int cols, int width) {
+        const int64_t units = (int64_t)c.seq.seqs * c.Hk, per = (int64_t)((width + cols - 1) / cols) * (c.Hv / c.Hk);
+        return (uint32_t)((units + 7) / 8 * 8 * per);
     }
 };
+
+// Two workgroups a CU where their registers allow it (a wavefront that may have
+// more than 256 also keeps results in accumulation registers and moves them).
+template <class DT, int DK, int NT>
+constexpr int walks_a_cu() { return DK * Raw<DT>::TERMS * NT <= 256 ? 2 : 1; }
 
 // Forward walk.  SAVE: keeps each chunk's state and U for the backward pass
 // instead of making outputs.
 template <class DT, int DK, int NT, bool SAVE>
-__global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, float *state_out, typename DT::X *o,
+__global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c, const float *state_in, float *state_out, typename DT::X *o,
                                               int64_t ldo, float *S0s, float *Us) {
     using X = typename DT::X;
     constexpr int NA = Raw<DT>::TERMS, NK = DK / 32, NF = DK / 8 * NA, T = DK / 64;
@@ -447,15 +502,17 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
     const Right<NT, 3> SB{L}, RB{SB.p + SB.bytes(NK)}, EB{RB.p + RB.bytes(2)};
     const Right<NT, 2> UB{EB.p + EB.bytes(2)};
     const Walk wk(c, 16 * NT, SAVE ? c.DvP : c.Dv);
+    if (wk.s >= c.seq.seqs) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
               g4 = (lane >> 4) * 4;
     const int h = wk.h, row = 16 * wave + g4;  // this lane's tokens: row .. row + 3
     const Columns<NT> cl(wk.first, r, c.Dv);
-    const int a = c.seq.begin(wk.s), b = c.seq.end(wk.s);
+    const Rows rv(c.ldv, g4), ro(ldo, g4);
+    const int a = uniform(c.seq.begin(wk.s)), b = uniform(c.seq.end(wk.s));
     const int64_t st = ((int64_t)wk.s * c.Hv + h) * c.Dk * c.Dv;
     State<DK, NT> S;
     S.load(state_in ? state_in + st : nullptr, c, wave, g4, cl);
-    const int slot0 = first_slot(c.seq, wk.s), nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
+    const int slot0 = a / CH + wk.s, nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
     const X *pv = (const X *)c.v + (int64_t)a * c.ldv + (int64_t)h * c.Dv;
     X *po = SAVE ? nullptr : o + (int64_t)a * ldo + (int64_t)h * c.Dv;
     // operands of the chunk at hand
@@ -467,7 +524,7 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
     auto head_of = [&](int k) { return c.heads + ((int64_t)(slot0 + k) * c.Hv + h) * c.head_bytes; };
     auto fetch_rows = [&](int k) {  // what the first products need
         const char *p = keys_of(k);
-        fetch_tokens<X, NT>(vn, pv + (int64_t)k * CH * c.ldv, c.ldv, b - a - k * CH, row, cl);
+        fetch_tokens<X, NT>(vn, pv + (int64_t)k * CH * c.ldv, rv, b - a - k * CH, 16 * wave, g4, cl);
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
             fetch(wK[kb], p + (NF + (wave * NK + kb) * NA) * FRAG, lane);
@@ -510,66 +567,63 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
         __syncthreads();
         if (SAVE) S.keep(S0s + at * DK * c.DvP, c, wave, g4, cl);
         // R = beta (V - e^b K S)
-        f32x4 ks[NT], os[NT], u[NT];
+        f32x4 ks[NT], y[NT], u[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) ks[t] = os[t] = u[t] = splat(0.0f);
+        for (int t = 0; t < NT; ++t) ks[t] = y[t] = u[t] = splat(0.0f);
+        bf16x8 s[2][NT][3];
+        SB.get(0, s[0], lane);
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-            bf16x8 s[NT][3];
-            SB.get(kb, s, lane);
-            mac(wK[kb], s, 2, ks);
-            if (!SAVE) mac(wQ[kb], s, 1, os);
+            if (kb + 1 < NK) SB.get(kb + 1, s[(kb + 1) & 1], lane);
+            fence();
+            mac(wK[kb], s[kb & 1], 2, ks);
+            if (!SAVE) mac(wQ[kb], s[kb & 1], 1, y);
+            fence();
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             RB.put(wave, t, beta * (widened<DT, NT>(vn, t, n, row, cl) - ek * ks[t]), lane);
-            if (!SAVE) os[t] *= eq;
+            if (!SAVE) y[t] *= eq;
         }
         fetch_rows(next);
         __syncthreads();
         // U = T R
-        {
-            bf16x8 x[NT][3];
-            RB.get(0, x, lane);
-            mac(wT[0], x, 2, u);
-            if (wave >= 2) {
-                RB.get(1, x, lane);
-                mac(wT[1], x, 2, u);
-            }
-        }
+        RB.get(0, s[0], lane);
+        RB.get(1, s[1], lane);
+        fence();
+        mac(wT[0], s[0], 2, u);
+        if (wave >= 2) mac(wT[1], s[1], 2, u);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             EB.put(wave, t, u[t] * rk, lane);
             if (!SAVE) UB.put(wave, t, u[t], lane);
         }
         fetch_T(next);
-        if (SAVE) keep_tokens<NT>(Us + at * CH * c.DvP, c, u, row, cl);
+        if (SAVE) keep_tokens<NT>(Us + at * CH * c.DvP, c, u, 16 * wave, g4, cl);
         __syncthreads();
         // S = e^{b_last} S + K^T (e^{b_last - b} U)
+        EB.get(0, s[0], lane);
+        EB.get(1, s[1], lane);
+        fence();
 #pragma unroll
         for (int x = 0; x < T; ++x)
 #pragma unroll
             for (int t = 0; t < NT; ++t) S.S[x][t] *= el;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            bf16x8 e[NT][3];
-            EB.get(kb, e, lane);
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int x = 0; x < T; ++x) mac(wKT[x][kb], e, 2, S.S[x]);
-        }
+            for (int x = 0; x < T; ++x) mac(wKT[x][kb], s[kb], 2, S.S[x]);
         fetch_KT(next);
         S.put(SB, wave, lane);
         // O = scale e^b (Q S0) + P U
         if (!SAVE) {
-            bf16x8 x[NT][2];
-            UB.get(0, x, lane);
-            mac(wP[0], x, 1, os);
-            if (wave >= 2) {
-                UB.get(1, x, lane);
-                mac(wP[1], x, 1, os);
-            }
+            bf16x8 x[2][NT][2];
+            UB.get(0, x[0], lane);
+            UB.get(1, x[1], lane);
+            mac(wP[0], x[0], 1, y);
+            if (wave >= 2) mac(wP[1], x[1], 1, y);
             fetch_P(next);
-            store_tokens<DT, NT>(po + (int64_t)k * CH * ldo, ldo, os, n, row, cl);
+            store_tokens<DT, NT>(po + (int64_t)k * CH * ldo, ro, y, n, 16 * wave, g4, cl);
         }
     }
     if (state_out) S.store(state_out + st, c, wave, g4, cl);
@@ -577,7 +631,7 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
 
 // Backward walk.
 template <class DT, int DK, int NT>
-__global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o, int64_t lddo, const float *dstate_out,
+__global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c, const typename DT::X *d_o, int64_t lddo, const float *dstate_out,
                                                float *dstate_in, typename DT::X *dvo, int64_t lddv, float *dSs,
                                                float *dRs) {
     using X = typename DT::X;
@@ -586,15 +640,17 @@ __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o,
     const Right<NT, 3> SB{L}, XB{SB.p + SB.bytes(NK)}, QB{XB.p + XB.bytes(2)}, ZB{QB.p + QB.bytes(2)};
     const Right<NT, NA> OB{ZB.p + ZB.bytes(2)};
     const Walk wk(c, 16 * NT, c.DvP);
+    if (wk.s >= c.seq.seqs) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
               g4 = (lane >> 4) * 4;
     const int h = wk.h, row = 16 * wave + g4;
     const Columns<NT> cl(wk.first, r, c.Dv);
-    const int a = c.seq.begin(wk.s), b = c.seq.end(wk.s);
+    const Rows rd(lddo, g4), rv(lddv, g4);
+    const int a = uniform(c.seq.begin(wk.s)), b = uniform(c.seq.end(wk.s));
     const int64_t st = ((int64_t)wk.s * c.Hv + h) * c.Dk * c.Dv;
     State<DK, NT> S;
     S.load(dstate_out ? dstate_out + st : nullptr, c, wave, g4, cl);
-    const int slot0 = first_slot(c.seq, wk.s), nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
+    const int slot0 = a / CH + wk.s, nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
     const X *pd = d_o + (int64_t)a * lddo + (int64_t)h * c.Dv;
     X *pv = dvo + (int64_t)a * lddv + (int64_t)h * c.Dv;
     bf16x8 wK[NK][NA], wPT[2][T_TERMS], wTT[2][T_TERMS], wKT[T][2][NA], wQT[T][2][NA];
@@ -604,7 +660,7 @@ __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o,
     auto keys_of = [&](int k) { return c.keys + ((int64_t)(slot0 + k) * c.Hk + hk) * c.key_bytes; };
     auto head_of = [&](int k) { return c.heads + ((int64_t)(slot0 + k) * c.Hv + h) * c.head_bytes; };
     auto fetch_tokens_of = [&](int k) {
-        fetch_tokens<X, NT>(dn, pd + (int64_t)k * CH * lddo, lddo, b - a - k * CH, row, cl);
+        fetch_tokens<X, NT>(dn, pd + (int64_t)k * CH * lddo, rd, b - a - k * CH, 16 * wave, g4, cl);
         eq = *(const f32x4 *)((const float *)(head_of(k) + AT_VEC * FRAG) + V_EQ * CH + row);
     };
     auto fetch_rows = [&](int k) {
@@ -657,41 +713,40 @@ __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o,
         __syncthreads();
         S.keep(dSs + at * DK * c.DvP, c, wave, g4, cl);
         // dU = e^{b_last - b} (K dS) + P^T dO
-        f32x4 x[NT], dR[NT];
+        f32x4 x[NT], y[NT], dR[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) x[t] = dR[t] = splat(0.0f);
+        bf16x8 s[2][NT][3], ot[2][NT][NA];
+        SB.get(0, s[0], lane);
 #pragma unroll
         for (int kb = 0; kb < NK; ++kb) {
-            bf16x8 s[NT][3];
-            SB.get(kb, s, lane);
-            mac(wK[kb], s, 2, x);
+            if (kb + 1 < NK) {
+                SB.get(kb + 1, s[(kb + 1) & 1], lane);
+            } else {
+                OB.get(0, ot[0], lane);
+                OB.get(1, ot[1], lane);
+            }
+            fence();
+            mac(wK[kb], s[kb & 1], 2, x);
+            fence();
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) x[t] *= rk;
-        {
-            bf16x8 y[NT][NA];
-            OB.get(1, y, lane);
-            mac(wPT[1], y, 2, x);
-            if (wave < 2) {
-                OB.get(0, y, lane);
-                mac(wPT[0], y, 2, x);
-            }
-        }
+        mac(wPT[1], ot[1], 2, x);
+        if (wave < 2) mac(wPT[0], ot[0], 2, x);
 #pragma unroll
         for (int t = 0; t < NT; ++t) XB.put(wave, t, x[t], lane);
         fetch_rows(next);
         __syncthreads();
         // dR = T^T dU, dV = beta dR; the part of dS that needs no dR
-        {
-            bf16x8 y[NT][3];
-            XB.get(1, y, lane);
-            mac(wTT[1], y, 2, dR);
-            if (wave < 2) {
-                XB.get(0, y, lane);
-                mac(wTT[0], y, 2, dR);
-            }
-        }
-        f32x4 y[NT];
+        XB.get(0, s[0], lane);
+        XB.get(1, s[1], lane);
+        fence();
+        mac(wTT[1], s[1], 2, dR);
+        if (wave < 2) mac(wTT[0], s[0], 2, dR);
+        QB.get(0, s[0], lane);
+        QB.get(1, s[1], lane);
+        fence();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             y[t] = beta * dR[t];
@@ -703,24 +758,21 @@ __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o,
 #pragma unroll
             for (int t = 0; t < NT; ++t) S.S[z][t] *= el;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            bf16x8 e[NT][3];
-            QB.get(kb, e, lane);
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int z = 0; z < T; ++z) mac(wQT[z][kb], e, 2, S.S[z]);
-        }
+            for (int z = 0; z < T; ++z) mac(wQT[z][kb], s[kb], 2, S.S[z]);
         fetch_columns(next, true);
-        keep_tokens<NT>(dRs + at * CH * c.DvP, c, dR, row, cl);
-        store_tokens<DT, NT>(pv + (int64_t)k * CH * lddv, lddv, y, n, row, cl);
+        keep_tokens<NT>(dRs + at * CH * c.DvP, c, dR, 16 * wave, g4, cl);
+        store_tokens<DT, NT>(pv + (int64_t)k * CH * lddv, rv, y, n, 16 * wave, g4, cl);
         __syncthreads();
         // dS = e^{b_last} dS + Q^T (scale e^b dO) - K^T (e^b beta dR)
+        ZB.get(0, s[0], lane);
+        ZB.get(1, s[1], lane);
+        fence();
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            bf16x8 e[NT][3];
-            ZB.get(kb, e, lane);
+        for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int z = 0; z < T; ++z) mac(wKT[z][kb], e, 2, S.S[z]);
-        }
+            for (int z = 0; z < T; ++z) mac(wKT[z][kb], s[kb], 2, S.S[z]);
         fetch_columns(next, false);
         S.put(SB, wave, lane);
         put_tokens(next);
@@ -786,7 +838,7 @@ hipError_t split_scan(int dtype, int DK_, const Ctx &c, const float *state_in, f
         using X = typename DT::X;
         constexpr int DK = decltype(dk)::value;
         const int nt = walk_tiles(c);
-        const uint32_t blocks = (uint32_t)((int64_t)c.seq.seqs * c.Hv * (((S0s ? c.DvP : c.Dv) + 16 * nt - 1) / (16 * nt)));
+        const uint32_t blocks = Walk::blocks(c, 16 * nt, S0s ? c.DvP : c.Dv);
         const size_t n = nt == 1 ? lds_scan<1>(DK) : lds_scan<2>(DK);
         auto f = nt == 1 ? (S0s ? k_scan<DT, DK, 1, true> : k_scan<DT, DK, 1, false>)
                          : (S0s ? k_scan<DT, DK, 2, true> : k_scan<DT, DK, 2, false>);
@@ -804,7 +856,7 @@ hipError_t split_rscan(int dtype, int DK_, const Ctx &c, const void *d_o, int64_
         using X = typename DT::X;
         constexpr int DK = decltype(dk)::value;
         const int nt = walk_tiles(c);
-        const uint32_t blocks = (uint32_t)((int64_t)c.seq.seqs * c.Hv * (c.DvP / (16 * nt)));
+        const uint32_t blocks = Walk::blocks(c, 16 * nt, c.DvP);
         const size_t n = nt == 1 ? lds_rscan<1>(DK, Raw<DT>::TERMS) : lds_rscan<2>(DK, Raw<DT>::TERMS);
         auto f = nt == 1 ? k_rscan<DT, DK, 1> : k_rscan<DT, DK, 2>;
         hipError_t e = lds_room((const void *)f, n);

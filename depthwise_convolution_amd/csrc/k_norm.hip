@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(256) k_gate_sum(const float *part, int64_t gro
     const float *p = part + i / D * segs * D + i % D;
     float s = 0.0f;
     for (int k = 0; k < segs; ++k) s += p[(int64_t)k * D];
-    out[i] = DT::narrow(s);
+    out[i] = rounded<DT>(s);
 }
 
 // Lanes a row and channels a lane.  Short rows share a wavefront; a lane has 8

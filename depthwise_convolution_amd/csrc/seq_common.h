@@ -22,11 +22,25 @@ __device__ __forceinline__ void load_f32(float (&out)[N], const typename DT::X *
     for (int i = 0; i < N; ++i) out[i] = DT::widen(a.v[i]);
 }
 
+// fp32 to the storage type, to nearest even.  bf16 by the conversion instruction
+// (NaN stays NaN); the other types as everywhere.
+template <class DT>
+__device__ __forceinline__ typename DT::X rounded(float v) {
+    return DT::narrow(v);
+}
+template <>
+__device__ __forceinline__ uint16_t rounded<BF16>(float v) {
+    return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// a value that is the same in all lanes, in a scalar register
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 template <class DT, int N>
 __device__ __forceinline__ void store_f32(typename DT::X *p, const float (&in)[N]) {
     Vec<typename DT::X, N> a;
 #pragma unroll
-    for (int i = 0; i < N; ++i) a.v[i] = DT::narrow(in[i]);
+    for (int i = 0; i < N; ++i) a.v[i] = rounded<DT>(in[i]);
     *(Vec<typename DT::X, N> *)p = a;
 }
 
