@@ -42,6 +42,7 @@ struct Ctx {
     // operands of the 16-bit products, in fragments: a slot's key head (Q, K,
     // K^T and, backward, Q^T) and value head
     char *keys, *heads;
+    double *sums;             // slots x Hv x CH: b, backward
     int64_t key_bytes, head_bytes;
     int vec8;                 // rows of q and k load 8 elements at once
 };
@@ -160,8 +161,8 @@ constexpr int AT_P = 0, AT_T = AT_P + NBLK * P_TERMS, AT_VEC = AT_T + NBLK * T_T
               HEAD_FWD = AT_VEC + VEC_FRAGS, AT_TT = HEAD_FWD, AT_PT = AT_TT + NBLK * T_TERMS,
               HEAD_BWD = AT_PT + NBLK * T_TERMS;
 // vectors of a chunk, 64 floats each: e^b / |k|, e^{b_last - b} / |k|, beta,
-// scale e^b / |q|, e^b
-enum { V_EK, V_RK, V_BETA, V_EQ, V_EB };
+// scale e^b / |q|, e^b and, backward, e^{b_last - b}, 1 / |k|, 1 / |q|
+enum { V_EK, V_RK, V_BETA, V_EQ, V_EB, V_ER, V_NK, V_NQ };
 
 __host__ __device__ constexpr int key_frags(int DK, int terms) { return DK / 8 * terms; }  // one matrix
 // bf16 values are one term, fp16 values two bf16 terms
@@ -169,7 +170,28 @@ __host__ __device__ constexpr int key_terms(int dtype) { return dtype == DWCONV_
 
 inline bool split_runs(int dtype) { return dtype != DWCONV_F32; }
 
-// launchers (k_delta_split.hip)
+// What the gradients of q, k, g and beta need: each chunk's states and U, dS, dR.
+struct GradArgs {
+    const float *S0s, *Us, *dSs, *dRs;
+    const void *d_o;
+    int64_t lddo;
+    void *dq, *dk;
+    int64_t lddq, lddk;
+    float *dg, *dbeta;
+    int vec_o, vec_v;  // rows of d_o and v load 4 (fp32) or 8 elements at once
+};
+
+// sum over the 16 lanes that share rows
+__device__ __forceinline__ f32x4 sum16(f32x4 v) {
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], m, 64);
+    return v;
+}
+
+// launchers (k_delta_split.hip, k_delta_grad.hip)
+hipError_t split_grad(int dtype, int DK, const Ctx &c, const GradArgs &ga, hipStream_t st);
 hipError_t split_prepare(int dtype, int DK, const Ctx &c, bool backward, hipStream_t st);
 hipError_t split_scan(int dtype, int DK, const Ctx &c, const float *state_in, float *state_out, void *o, int64_t ldo,
                       float *S0s, float *Us, hipStream_t st);

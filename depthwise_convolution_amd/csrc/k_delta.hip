@@ -362,25 +362,6 @@ __global__ void __launch_bounds__(256) k_rscan(Ctx c, const typename DT::X *d_o,
     }
 }
 
-struct GradArgs {
-    const float *S0s, *Us, *dSs, *dRs;
-    const void *d_o;
-    int64_t lddo;
-    void *dq, *dk;
-    int64_t lddq, lddk;
-    float *dg, *dbeta;
-    int vec_o, vec_v;  // rows of d_o and v load 4 elements at once
-};
-
-// sum over the 16 lanes that share rows
-__device__ __forceinline__ f32x4 sum16(f32x4 v) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], m, 64);
-    return v;
-}
-
 // A workgroup: one chunk and one key head, its value heads one after the other
 // (their shares of dQ and dK add up in registers).  Wave w has tokens 16 w ..
 // 16 w + 15.
@@ -625,7 +606,7 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
 int padded_keys(int Dk) { return (Dk + 63) / 64 * 64; }
 
 struct Layout {
-    size_t T, P, vecs, keys, heads, S0s, Us, dSs, dRs, end;  // offsets in floats
+    size_t T, P, vecs, keys, heads, sums, S0s, Us, dSs, dRs, end;  // offsets in floats
     size_t key_bytes, head_bytes;
 };
 Layout layout(const dwconv_delta_plan &p, int seqs, int tokens, bool backward) {
@@ -647,10 +628,9 @@ Layout layout(const dwconv_delta_plan &p, int seqs, int tokens, bool backward) {
     } else {
         l.T = take(n * TRI);
     }
-    if (!split || backward) {
-        l.P = take(n * TRI);
-        l.vecs = take(n * NV);
-    }
+    if (!split || backward) l.P = take(n * TRI);
+    if (!split) l.vecs = take(n * NV);
+    if (split && backward) l.sums = take(n * CH * 2);
     if (backward) {
         l.S0s = take(n * DK * DvP);
         l.Us = take(n * CH * DvP);
@@ -681,7 +661,7 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
     c.q = a.q, c.k = a.k, c.v = a.v, c.ldq = a.ldq, c.ldk = a.ldk, c.ldv = a.ldv;
     c.g = a.g, c.beta = a.beta;
     c.T = ws + l.T, c.P = ws + l.P, c.vecs = ws + l.vecs;
-    c.keys = (char *)(ws + l.keys), c.heads = (char *)(ws + l.heads);
+    c.keys = (char *)(ws + l.keys), c.heads = (char *)(ws + l.heads), c.sums = (double *)(ws + l.sums);
     c.key_bytes = (int64_t)l.key_bytes, c.head_bytes = (int64_t)l.head_bytes;
     const bool split = split_runs(p.dtype);
     const uint64_t chunks = (uint64_t)c.slots * p.Hk, walks = (uint64_t)a.seqs * p.Hv * ((p.Dv + 63) / 64);
@@ -726,8 +706,10 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
                                                                          ws + l.dRs);
     }
     if (a.tokens > 0) {
+        const int vec = split ? 8 : 4;
         GradArgs ga{ws + l.S0s, ws + l.Us, ws + l.dSs, ws + l.dRs, a.d_o, a.lddo, a.dq, a.dk, a.lddq, a.lddk, a.dg,
-                    a.dbeta, rows_of<X>(4, a.d_o, a.lddo, p.Dv), rows_of<X>(4, a.v, a.ldv, p.Dv)};
+                    a.dbeta, rows_of<X>(vec, a.d_o, a.lddo, p.Dv), rows_of<X>(vec, a.v, a.ldv, p.Dv)};
+        if (split) return split_grad(p.dtype, DK, c, ga, st);
         const size_t blocks = sizeof(float) * 36 * (2 * DK + CH), tiles = keys + 2 * TRI * sizeof(float);
         const size_t n = blocks > tiles ? blocks : tiles;
         if ((e = lds((const void *)k_grad<DT, DK>, n)) != hipSuccess) return e;

@@ -1,0 +1,369 @@
+// k_delta_grad.hip -- the gated delta rule's gradients of q, k, g and beta for
+// bf16 and fp16 data, on the 16-bit matrix cores (the algebra is in
+// k_delta.hip, the terms in delta_split.h).
+//
+// A workgroup has one chunk and one key head; its value heads come one after
+// the other and their shares of dQ and dK add up in registers.  Wavefront w has
+// tokens 16 w .. 16 w + 15.  Per value head, first the sums over the state's
+// columns, 32 at a time: the rows of S0 and dS, split into terms by one
+// wavefront each, and U pass through LDS; dO, dR and U rows are left operands
+// that a lane loads as they lie.  Then the sums over tokens: E and M = beta dA D
+// go through LDS once as left operands by rows and once, in terms, by columns;
+// their right operands are the fragments of K^T and Q^T in the workspace, which
+// also hold a lane's own elements of k and q in the result layout.
+//
+// Bound: 2900 products of 16x16x32 a head and chunk at Dk = Dv = 128 (11.6
+// thousand cycles of a CU) against 128 KB of states read.
+#include "delta_split.h"
+
+namespace dw {
+namespace {
+
+using namespace delta;
+
+template <int NA, int NB>
+__device__ __forceinline__ void mac1(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], int last, f32x4 &c) {
+#pragma unroll
+    for (int o = 0; o < NA + NB - 1; ++o) {
+        if (o > last) break;
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (o - i >= 0 && o - i < NB) c = mfma32(a[i], b[o - i], c);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void put_frag(char *p, const bf16x8 (&t)[N], int lane) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) *(bf16x8 *)(p + n * FRAG + lane * 16) = t[n];
+}
+template <int N>
+__device__ __forceinline__ void get_frag(bf16x8 (&t)[N], const char *p, int lane) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) t[n] = *(const bf16x8 *)(p + n * FRAG + lane * 16);
+}
+
+// Eight elements of a row of v or dO, zeros past `valid`.
+template <class X>
+__device__ __forceinline__ Vec<X, 8> load8(const X *p, int valid, bool vec) {
+    Vec<X, 8> r;
+    if (valid >= 8 && vec) return *(const Vec<X, 8> *)p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = i < valid ? p[i] : (X)0;
+    return r;
+}
+
+// A lane's four elements k[token 16 w + g4 + i][channel 16 t + lane % 16], half
+// of a fragment of K^T (Q^T).
+template <int NA>
+__device__ __forceinline__ f32x4 own_elements(const char *kt, int t, int wave, int lane) {
+    f32x4 x = splat(0.0f);
+#pragma unroll
+    for (int n = 0; n < NA; ++n) {
+        const u32x2 v = *(const u32x2 *)(kt + ((2 * t + wave / 2) * NA + n) * FRAG + (uint32_t)lane * 16 + wave % 2 * 8);
+        x += f32x4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
+                   __uint_as_float(v[1] & 0xffff0000u)};
+    }
+    return x;
+}
+
+constexpr int PITCH = 20;  // of a 16x16 tile that is written by columns and read by rows
+constexpr int WAVE_TILES = 2 * 4 * 16 * PITCH * 4;  // bytes of a wavefront's tiles of E and M
+__host__ __device__ constexpr int lds_blocks(int DK) { return (2 * DK / 16 + 4) * 3 * FRAG; }
+constexpr int LDS_TILES = 4 * WAVE_TILES + 2 * Right<4, 3>::bytes(2);
+
+template <class DT, int DK>
+__global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
+    using X = typename DT::X;
+    using R = Raw<DT>;
+    constexpr int NA = R::TERMS, NT = DK / 16, T = DK / 64, NF = DK / 8 * NA, NK = DK / 32;
+    extern __shared__ char L[];
+    char *SF = L, *DF = SF + NT * 3 * FRAG, *UF = DF + NT * 3 * FRAG;
+    __shared__ float db[CH], dbe[CH], a2[CH], colP[4][CH], colA[4][CH], dots[4];
+    const int slot = blockIdx.x / c.Hk, hk = blockIdx.x % c.Hk;
+    const Chunk found = chunk_of(c.seq, slot);
+    const int n = uniform(found.n), tok = uniform(found.tok);
+    if (n == 0) return;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4, g8 = 2 * g4;
+    const int row = 16 * wave + g4;      // result layout: tokens row .. row + 3
+    const int mine = 16 * wave + r;      // left operands: the lane's token
+    float *ET = (float *)(L + wave * WAVE_TILES), *MT = ET + 4 * 16 * PITCH;
+    const Right<4, 3> ER{L + 4 * WAVE_TILES}, MR{ER.p + ER.bytes(2)};
+    const char *keys = c.keys + ((int64_t)slot * c.Hk + hk) * c.key_bytes;
+    const char *rows_k = keys + NF * FRAG, *kt = keys + 2 * NF * FRAG, *qt = keys + 3 * NF * FRAG;
+    const int group = c.Hv / c.Hk;
+    f32x4 dQ[NT], dK[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) dQ[t] = dK[t] = splat(0.0f);
+    for (int h = hk * group; h < (hk + 1) * group; ++h) {
+        const int64_t at = (int64_t)slot * c.Hv + h;
+        f32x4 X1[NT], X2[NT], X3[NT], dP[4], dA[4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) X1[t] = X2[t] = X3[t] = splat(0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dP[j] = dA[j] = splat(0.0f);
+        float rv = 0.0f, sd = 0.0f;  // dR . V of token `mine`; <S0, dS>
+        // ---- sums over the state's columns
+        f32x4 s0[T][2], ds[T][2], ur[2], dr[2];
+        Vec<X, 8> od, vv;
+        auto ahead = [&](int col) {
+            const uint32_t off = r * c.DvP + g8;
+#pragma unroll
+            for (int x = 0; x < T; ++x) {
+                const int64_t p = (at * DK + 16 * (wave * T + x)) * c.DvP + col;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    s0[x][j] = *(const f32x4 *)(ga.S0s + p + off + 4 * j);
+                    ds[x][j] = *(const f32x4 *)(ga.dSs + p + off + 4 * j);
+                }
+            }
+            const int64_t p = (at * CH + 16 * wave) * c.DvP + col;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                ur[j] = *(const f32x4 *)(ga.Us + p + off + 4 * j);
+                dr[j] = *(const f32x4 *)(ga.dRs + p + off + 4 * j);
+            }
+            const int x = col + g8, token = tok + min(mine, n - 1), valid = mine < n ? c.Dv - x : 0;
+            od = load8<X>((const X *)ga.d_o + token * ga.lddo + (int64_t)h * c.Dv + x, valid, ga.vec_o);
+            vv = load8<X>((const X *)c.v + token * c.ldv + (int64_t)h * c.Dv + x, valid, ga.vec_v);
+        };
+        ahead(0);
+        for (int col = 0; col < c.DvP; col += 32) {
+            __syncthreads();
+            bf16x8 ot[NA], ut[3], rt[3];
+            R::terms(__builtin_bit_cast(typename R::V8, od), ot);
+            split(ur[0], ur[1], ut);
+            split(dr[0], dr[1], rt);
+            put_frag(UF + wave * 3 * FRAG, ut, lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) rv = __builtin_fmaf(dr[j / 4][j % 4], DT::widen(vv.v[j]), rv);
+#pragma unroll
+            for (int x = 0; x < T; ++x) {
+                bf16x8 t[3];
+                split(s0[x][0], s0[x][1], t);
+                put_frag(SF + (wave * T + x) * 3 * FRAG, t, lane);
+                split(ds[x][0], ds[x][1], t);
+                put_frag(DF + (wave * T + x) * 3 * FRAG, t, lane);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sd = __builtin_fmaf(s0[x][j / 4][j % 4], ds[x][j / 4][j % 4], sd);
+            }
+            if (col + 32 < c.DvP) ahead(col + 32);
+            __syncthreads();
+            bf16x8 st[2][3], dt[2][3];
+            get_frag(st[0], SF, lane);
+            get_frag(dt[0], DF, lane);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t + 1 < NT) {
+                    get_frag(st[(t + 1) & 1], SF + (t + 1) * 3 * FRAG, lane);
+                    get_frag(dt[(t + 1) & 1], DF + (t + 1) * 3 * FRAG, lane);
+                }
+                fence();
+                mac1(rt, st[t & 1], 2, X3[t]);
+                mac1(ut, dt[t & 1], 2, X2[t]);
+                mac1(ot, st[t & 1], 2, X1[t]);
+                fence();
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j > wave) continue;
+                bf16x8 u[3];
+                get_frag(u, UF + j * 3 * FRAG, lane);
+                mac1(ot, u, 2, dP[j]);
+                mac1(rt, u, 2, dA[j]);  // of the other sign
+            }
+        }
+        // ---- sums over tokens
+        const float *vec = (const float *)(c.heads + at * c.head_bytes + AT_VEC * FRAG);
+        auto rows4 = [&](int which) { return *(const f32x4 *)(vec + which * CH + row); };
+        const f32x4 eb = rows4(V_EB), er = rows4(V_ER), be = rows4(V_BETA), nk = rows4(V_NK), nq = rows4(V_NQ);
+        const double *bs = c.sums + at * CH;
+        double br[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) br[i] = bs[row + i];
+        f32x4 s1 = splat(0.0f), s2 = splat(0.0f), s3 = splat(0.0f);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const f32x4 kr = own_elements<NA>(kt, t, wave, lane), qr = own_elements<NA>(qt, t, wave, lane);
+            s1 += qr * X1[t];
+            s2 += kr * X2[t];
+            s3 += kr * X3[t];
+            dQ[t] += c.scale * eb * X1[t];
+            dK[t] += er * X2[t] - eb * be * X3[t];
+            fence();
+        }
+        s1 = sum16(s1) * eb * nq * c.scale;
+        s2 = sum16(s2) * er * nk;
+        s3 = sum16(s3) * eb * nk;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) sd += __shfl_xor(sd, m, 64);
+        rv += __shfl_xor(rv, 16, 64);
+        rv += __shfl_xor(rv, 32, 64);
+        __syncthreads();  // the blocks have been read: tiles take their place
+        if (lane == 0) dots[wave] = sd;
+        if (lane < 16) dbe[mine] = rv;
+        bf16x8 kw[NK][NA];
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) fetch(kw[kb], rows_k + (wave * NK + kb) * NA * FRAG, lane);
+        f32x4 rowP = splat(0.0f), rowA = splat(0.0f), rowB = splat(0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float cp = 0.0f, ca = 0.0f;
+            f32x4 e = splat(0.0f), m = splat(0.0f);
+            if (j <= wave) {
+                f32x4 kk = splat(0.0f);
+#pragma unroll
+                for (int kb = 0; kb < NK; ++kb) {
+                    bf16x8 x[NA];
+                    fetch(x, rows_k + (j * NK + kb) * NA * FRAG, lane);
+                    mac1(kw[kb], x, 2, kk);
+                }
+                const int y = 16 * j + r;
+                const float nky = vec[V_NK * CH + y];
+                const double by = bs[y];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = row + i;
+                    const float d = x >= y ? expf((float)(br[i] - by)) : 0.0f;
+                    const float p = x >= y ? dP[j][i] * c.P[at * TRI + tri(wave, j) + (g4 + i) * 16 + r] : 0.0f;
+                    const float a = x > y ? -dA[j][i] * d : 0.0f;
+                    const float ak = x > y ? a * (nk[i] * nky * kk[i]) : 0.0f;
+                    e[i] = x >= y ? c.scale * dP[j][i] * d : 0.0f;
+                    m[i] = be[i] * a;
+                    rowP[i] += p;
+                    rowB[i] += ak;
+                    rowA[i] += be[i] * ak;
+                    cp += p;
+                    ca += be[i] * ak;
+                    ET[(j * 16 + g4 + i) * PITCH + r] = e[i] * nky;
+                    MT[(j * 16 + g4 + i) * PITCH + r] = m[i] * nky;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ET[(j * 16 + g4 + i) * PITCH + r] = MT[(j * 16 + g4 + i) * PITCH + r] = 0.0f;
+            }
+            ER.put(wave, j, e * nq, lane);
+            MR.put(wave, j, m * nk, lane);
+            cp += __shfl_xor(cp, 16, 64);
+            cp += __shfl_xor(cp, 32, 64);
+            ca += __shfl_xor(ca, 16, 64);
+            ca += __shfl_xor(ca, 32, 64);
+            if (lane < 16) {
+                colP[wave][16 * j + r] = cp;
+                colA[wave][16 * j + r] = ca;
+            }
+        }
+        rowP = sum16(rowP);
+        rowA = sum16(rowA);
+        rowB = sum16(rowB);
+        if (r == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                db[row + i] = s1[i] + rowP[i] + rowA[i] - be[i] * s3[i] - s2[i];
+                a2[row + i] = s2[i];
+                dbe[row + i] += rowB[i] - s3[i];
+            }
+        }
+        __syncthreads();
+        if (wave == 0) {
+            float x = db[lane];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) x -= colP[w][lane] + colA[w][lane];
+            double all = a2[lane];
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m, 64);
+            double y = x;
+            if (lane == 63) y += all + (double)vec[V_EB * CH + CH - 1] * ((dots[0] + dots[1]) + (dots[2] + dots[3]));
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const double z = __shfl_down(y, m, 64);
+                if (lane + m < 64) y += z;
+            }
+            if (lane < n) {
+                ga.dg[((int64_t)tok + lane) * c.Hv + h] = (float)y;
+                ga.dbeta[((int64_t)tok + lane) * c.Hv + h] = dbe[lane];
+            }
+        }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            bf16x8 er3[3], mr3[3], et3[3], mt3[3];
+            const bool low = kb <= wave / 2, high = kb >= wave / 2;  // E K and M K; E^T Q and M^T K
+            {
+                const float *pe = ET + (2 * kb * 16 + r) * PITCH + g4, *pm = MT + (2 * kb * 16 + r) * PITCH + g4;
+                split(*(const f32x4 *)pe, *(const f32x4 *)(pe + 16 * PITCH), er3);
+                split(*(const f32x4 *)pm, *(const f32x4 *)(pm + 16 * PITCH), mr3);
+            }
+            get_frag(et3, ER.p + (kb * 4 + wave) * 3 * FRAG, lane);
+            get_frag(mt3, MR.p + (kb * 4 + wave) * 3 * FRAG, lane);
+            bf16x8 fk[2][NA], fq[2][NA];
+            fetch(fk[0], kt + kb * NA * FRAG, lane);
+            fetch(fq[0], qt + kb * NA * FRAG, lane);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                if (t + 1 < NT) {
+                    fetch(fk[(t + 1) & 1], kt + (2 * (t + 1) + kb) * NA * FRAG, lane);
+                    fetch(fq[(t + 1) & 1], qt + (2 * (t + 1) + kb) * NA * FRAG, lane);
+                }
+                fence();
+                if (low) {
+                    mac1(er3, fk[t & 1], 2, dQ[t]);
+                    mac1(mr3, fk[t & 1], 2, dK[t]);
+                }
+                if (high) {
+                    mac1(et3, fq[t & 1], 2, dK[t]);
+                    mac1(mt3, fk[t & 1], 2, dK[t]);
+                }
+                fence();
+            }
+        }
+    }
+    // from the unit vectors to q and k: d - u (u . d), over the length
+    const float *vec = (const float *)(c.heads + ((int64_t)slot * c.Hv + hk * group) * c.head_bytes + AT_VEC * FRAG);
+    const f32x4 nk = *(const f32x4 *)(vec + V_NK * CH + row), nq = *(const f32x4 *)(vec + V_NQ * CH + row);
+    f32x4 uq = splat(0.0f), uk = splat(0.0f);
+    if (c.normalize) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            uq += dQ[t] * own_elements<NA>(qt, t, wave, lane);
+            uk += dK[t] * own_elements<NA>(kt, t, wave, lane);
+            fence();
+        }
+        uq = sum16(uq) * nq * nq;
+        uk = sum16(uk) * nk * nk;
+    }
+    asm volatile("" ::: "memory");  // the elements are read again, not kept
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const f32x4 q = nq * (dQ[t] - uq * own_elements<NA>(qt, t, wave, lane));
+        const f32x4 k = nk * (dK[t] - uk * own_elements<NA>(kt, t, wave, lane));
+        const int y = 16 * t + r;
+        if (y < c.Dk) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (row + i < n) {
+                    ((X *)ga.dq)[(tok + row + i) * ga.lddq + (int64_t)hk * c.Dk + y] = rounded<DT>(q[i]);
+                    ((X *)ga.dk)[(tok + row + i) * ga.lddk + (int64_t)hk * c.Dk + y] = rounded<DT>(k[i]);
+                }
+        }
+        fence();
+    }
+}
+
+}  // namespace
+
+namespace delta {
+
+hipError_t split_grad(int dtype, int DK_, const Ctx &c, const GradArgs &ga, hipStream_t st) {
+    return pick(dtype, DK_, [&](auto dt, auto dk) {
+        using DT = decltype(dt);
+        constexpr int DK = decltype(dk)::value;
+        const size_t n = lds_blocks(DK) > LDS_TILES ? lds_blocks(DK) : LDS_TILES;
+        hipError_t e = lds_room((const void *)k_grad<DT, DK>, n);
+        if (e != hipSuccess) return e;
+        k_grad<DT, DK><<<(uint32_t)((int64_t)c.slots * c.Hk), 256, n, st>>>(c, ga);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace delta
+}  // namespace dw

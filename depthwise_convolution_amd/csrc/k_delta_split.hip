@@ -19,115 +19,23 @@
 // operands each serve one wavefront: they go from the workspace, where
 // k_prepare lays them out as fragments (delta_common.h), straight to registers,
 // and a register is loaded for the next chunk as soon as it has been used.
-#include <type_traits>
-
-#include "delta_common.h"
+#include "delta_split.h"
 
 namespace dw {
 namespace {
 
 using namespace delta;
 
-using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
-using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
-using f32x8 = __attribute__((ext_vector_type(8))) float;
-using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
-using u32x2 = __attribute__((ext_vector_type(2))) uint32_t;
-
-__device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
-using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
-using f32x2 = __attribute__((ext_vector_type(2))) float;
-
-// a and b split into N bf16 terms, each the nearest of what is left, in pairs.
-// (On the words: conversions of single values would be made a second time.)
-template <int N>
-__device__ __forceinline__ void split(float a, float b, uint32_t (&t)[N]) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        t[n] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
-        if (n + 1 < N) {
-            a -= __uint_as_float(t[n] << 16);
-            b -= __uint_as_float(t[n] & 0xffff0000u);
-        }
-    }
-}
-template <int N>
-__device__ __forceinline__ void split(f32x4 x, u32x2 (&t)[N]) {
-    uint32_t lo[N], hi[N];
-    split(x[0], x[1], lo);
-    split(x[2], x[3], hi);
-#pragma unroll
-    for (int n = 0; n < N; ++n) t[n] = u32x2{lo[n], hi[n]};
-}
-template <int N>
-__device__ __forceinline__ void split(f32x4 a, f32x4 b, bf16x8 (&t)[N]) {
-    u32x2 lo[N], hi[N];
-    split(a, lo);
-    split(b, hi);
-#pragma unroll
-    for (int n = 0; n < N; ++n) t[n] = __builtin_bit_cast(bf16x8, (u32x4{lo[n][0], lo[n][1], hi[n][0], hi[n][1]}));
-}
-
-// Keeps loads in front of the products that hide them.
-__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
-
-template <class DT>
-struct Raw;
-template <>
-struct Raw<BF16> {
-    static constexpr int TERMS = 1;
-    using V8 = bf16x8;
-    static __device__ __forceinline__ f32x4 mfma(V8 a, V8 b, f32x4 c) { return mfma32(a, b, c); }
-    static __device__ __forceinline__ void terms(V8 x, bf16x8 (&t)[1]) { t[0] = x; }
-};
-template <>
-struct Raw<F16> {
-    static constexpr int TERMS = 2;
-    using V8 = f16x8;
-    static __device__ __forceinline__ f32x4 mfma(V8 a, V8 b, f32x4 c) {
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-    }
-    // 11 bits: the nearest bf16 leaves at most 3, exactly
-    static __device__ __forceinline__ void terms(V8 x, bf16x8 (&t)[2]) {
-        const f32x8 f = __builtin_convertvector(x, f32x8);
-        t[0] = __builtin_convertvector(f, bf16x8);
-        t[1] = __builtin_convertvector(f - __builtin_convertvector(t[0], f32x8), bf16x8);
-    }
-};
-
-// c += products of NA terms times NB terms down to order `last` (term i times
-// term j has order i + j), for NT neighbouring column tiles
-template <int NA, int NB, int NT>
-__device__ __forceinline__ void mac(const bf16x8 (&a)[NA], const bf16x8 (&b)[NT][NB], int last, f32x4 (&c)[NT]) {
-#pragma unroll
-    for (int o = 0; o < NA + NB - 1; ++o) {
-        if (o > last) break;
-#pragma unroll
-        for (int i = 0; i < NA; ++i)
-            if (o - i >= 0 && o - i < NB) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) c[t] = mfma32(a[i], b[t][o - i], c[t]);
-            }
-    }
-}
-
-// the place of block (m, kb) among a triangle's six
-__device__ __forceinline__ int lower_block(int m, int kb) { return m < 2 ? m : 2 * (m - 1) + kb; }
-__device__ __forceinline__ int upper_block(int m, int kb) { return m < 2 ? 2 * m + kb : 2 + m; }
-// the row tile and term block of a lower triangle's six blocks (kb <= m / 2),
-// and of an upper one's (kb >= m / 2)
-__host__ __device__ constexpr int lower_m(int blk) { return blk < 2 ? blk : blk / 2 + 1; }
-__host__ __device__ constexpr int lower_kb(int blk) { return blk < 2 ? 0 : blk % 2; }
-__host__ __device__ constexpr int upper_m(int blk) { return blk < 4 ? blk / 2 : blk - 2; }
-__host__ __device__ constexpr int upper_kb(int blk) { return blk < 4 ? blk % 2 : 1; }
-
 // One chunk and key head: lengths, the triangles of its value heads, and all
 // left operands as fragments.
+// (LDS: the rows of q and k, later the triangles.)
+template <int DK>
+constexpr size_t lds_prepare() {
+    constexpr size_t rows = 2 * CH * (DK + 8) * 2, triangles = (2 * TRI + 4 * 256) * sizeof(float);
+    return rows > triangles ? rows : triangles;
+}
 template <class DT, int DK, bool BACK>
-__global__ void __launch_bounds__(256) k_prepare(Ctx c) {
+__global__ void __launch_bounds__(256, (DK <= 128 ? 3 : 2)) k_prepare(Ctx c) {
     using X = typename DT::X;
     using R = Raw<DT>;
     using V8 = typename R::V8;
@@ -135,9 +43,9 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
     extern __shared__ char lds_raw[];
     X(*K)[PITCH] = (X(*)[PITCH])lds_raw;
     X(*Q)[PITCH] = K + CH;
-    float *At = (float *)(Q + CH), *Pl = At + TRI, *Tl = Pl + TRI, *Td = Tl + TRI;
-    __shared__ double b[CH];
-    __shared__ float beta[CH], rk[CH], rq[CH];
+    float *At = (float *)lds_raw, *Pl = At + TRI, *Tl = At, *Td = Pl + TRI;  // T takes A's place
+    __shared__ double b[4][CH];
+    __shared__ float beta[4][CH], rk[CH], rq[CH];
     const int slot = blockIdx.x / c.Hk, hk = blockIdx.x % c.Hk;
     const Chunk ch = chunk_of(c.seq, slot);
     if (ch.n == 0) return;
@@ -199,8 +107,9 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
     {
         constexpr int NF = DK / 8;
         char *base = c.keys + ((int64_t)slot * c.Hk + hk) * c.key_bytes;
-        for (int f = wave; f < (BACK ? 4 : 3) * NF; f += 4) {
-            const int mat = f / NF, i = f % NF;
+#pragma unroll
+        for (int f4 = 0; f4 < (BACK ? 4 : 3) * NF; f4 += 4) {
+            const int f = f4 + wave, mat = f4 / NF, i = f % NF;
             V8 x;
             if (mat < 2) {  // rows 16 m, terms 32 kb
                 const X(*S)[PITCH] = mat == 0 ? Q : K;
@@ -227,42 +136,47 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
             for (int n = 0; n < NA; ++n) *(bf16x8 *)(base + (int64_t)(f * NA + n) * FRAG + lane * 16) = terms[n];
         }
     }
-    const int group = c.Hv / c.Hk;
-    for (int h = hk * group; h < (hk + 1) * group; ++h) {
+    const int group = c.Hv / c.Hk, h0 = hk * group;
+    for (int n = 0; n < group; ++n) {
+        const int h = h0 + n;
         const int64_t at = (int64_t)slot * c.Hv + h;
         char *base = c.heads + at * c.head_bytes;
-        __syncthreads();  // the previous head's values have been read
-        if (wave == 0) {
-            const double x = running_sum(c.g + (int64_t)ch.tok * c.Hv + h, c.Hv, ch.n, lane);
-            const double last = __shfl(x, 63, 64);
-            const float be = lane < ch.n ? c.beta[((int64_t)ch.tok + lane) * c.Hv + h] : 0.0f;
-            const float eb = expf((float)x), er = expf((float)(last - x));
-            b[lane] = x;
-            beta[lane] = be;
-            float *v = (float *)(base + AT_VEC * FRAG);
-            v[V_EK * CH + lane] = eb * rk[lane];
-            v[V_RK * CH + lane] = er * rk[lane];
-            v[V_BETA * CH + lane] = be;
-            v[V_EQ * CH + lane] = c.scale * eb * rq[lane];
-            v[V_EB * CH + lane] = eb;
-            if (BACK) {
-                float *u = c.vecs + at * NV;
-                u[lane] = eb;
-                u[CH + lane] = er;
-                u[2 * CH + lane] = be;
+        const int w = n & 3;
+        __syncthreads();  // rows, or the previous head's values, have been read
+        if (w == 0) {     // the vectors of four heads, one a wavefront
+            const int hw = h + wave;
+            if (n + wave < group) {
+                const float be = lane < ch.n ? c.beta[((int64_t)ch.tok + lane) * c.Hv + hw] : 0.0f;
+                const double x = running_sum(c.g + (int64_t)ch.tok * c.Hv + hw, c.Hv, ch.n, lane);
+                const double last = __shfl(x, 63, 64);
+                const float eb = expf((float)x), er = expf((float)(last - x));
+                b[wave][lane] = x;
+                beta[wave][lane] = be;
+                float *v = (float *)(base + wave * c.head_bytes + AT_VEC * FRAG);
+                v[V_EK * CH + lane] = eb * rk[lane];
+                v[V_RK * CH + lane] = er * rk[lane];
+                v[V_BETA * CH + lane] = be;
+                v[V_EQ * CH + lane] = c.scale * eb * rq[lane];
+                v[V_EB * CH + lane] = eb;
+                if (BACK) {
+                    v[V_ER * CH + lane] = er;
+                    v[V_NK * CH + lane] = rk[lane];
+                    v[V_NQ * CH + lane] = rq[lane];
+                    c.sums[(at + wave) * CH + lane] = x;
+                }
             }
+            __syncthreads();
         }
-        __syncthreads();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (j > wave) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = 16 * wave + g4 + i, col = 16 * j + r;
-                const float d = row >= col ? expf((float)(b[row] - b[col])) : 0.0f;
+                const float d = row >= col ? expf((float)(b[w][row] - b[w][col])) : 0.0f;
                 const float p = row >= col ? c.scale * d * (rq[row] * rk[col] * qk[j][i]) : 0.0f;
                 const int e = tri(wave, j) + (g4 + i) * 16 + r;
-                At[e] = row > col ? beta[row] * d * (rk[row] * rk[col] * kk[j][i]) : 0.0f;
+                At[e] = row > col ? beta[w][row] * d * (rk[row] * rk[col] * kk[j][i]) : 0.0f;
                 Pl[e] = p;
                 if (BACK) c.P[at * TRI + e] = p;
             }
@@ -270,6 +184,7 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
         __syncthreads();
         f32x4 Tc[4];
         invert(At, Td, wave, r, g4, Tc);
+        __syncthreads();
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             if (wave + n >= 4) break;
@@ -277,8 +192,9 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
             for (int i = 0; i < 4; ++i) Tl[tri(wave + n, wave) + (g4 + i) * 16 + r] = Tc[n][i];
         }
         __syncthreads();
-        for (int f = wave; f < (BACK ? 4 : 2) * NBLK; f += 4) {
-            const int what = f / NBLK, blk = f % NBLK;  // P, T, T^T, P^T
+#pragma unroll
+        for (int f4 = 0; f4 < (BACK ? 4 : 2) * NBLK; f4 += 4) {
+            const int f = f4 + wave, what = f / NBLK, blk = f % NBLK;  // P, T, T^T, P^T
             const float *S = what == 0 || what == 3 ? Pl : Tl;
             f32x4 x[2];
             if (what < 2) {
@@ -304,37 +220,6 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
         }
     }
 }
-
-// A wavefront's left operands from the workspace: N fragments' terms.
-template <int N>
-__device__ __forceinline__ void fetch(bf16x8 (&w)[N], const char *p, int lane) {
-    const uint32_t off = (uint32_t)lane * 16;
-#pragma unroll
-    for (int n = 0; n < N; ++n) w[n] = *(const bf16x8 *)(p + n * FRAG + off);
-}
-
-// Right operands in LDS: [block of 32 terms][column tile][term], a fragment
-// each.  A wavefront writes a tile's terms (half of a block: `half`) and reads
-// whole blocks.
-template <int NT, int TERMS>
-struct Right {
-    char *p;
-    static constexpr int bytes(int blocks) { return blocks * NT * TERMS * FRAG; }
-    __device__ __forceinline__ void put(int tile, int t, f32x4 x, int lane) const {
-        u32x2 v[TERMS];
-        split(x, v);
-#pragma unroll
-        for (int n = 0; n < TERMS; ++n)
-            *(u32x2 *)(p + ((tile / 2 * NT + t) * TERMS + n) * FRAG + lane * 16 + tile % 2 * 8) = v[n];
-    }
-    template <int N>
-    __device__ __forceinline__ void get(int blk, bf16x8 (&v)[NT][N], int lane) const {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int n = 0; n < N; ++n) v[t][n] = *(const bf16x8 *)(p + ((blk * NT + t) * TERMS + n) * FRAG + lane * 16);
-    }
-};
 
 // The columns of a walk: NT tiles of 16 from `first` on; a lane's column of
 // tile t is first + 16 t + lane % 16.
@@ -790,29 +675,6 @@ size_t lds_scan(int DK) { return (size_t)(DK / 32 + 2 + 2) * NT * 3 * FRAG + (si
 template <int NT>
 size_t lds_rscan(int DK, int terms) { return (size_t)(DK / 32 + 6) * NT * 3 * FRAG + (size_t)2 * NT * terms * FRAG; }
 
-hipError_t lds_room(const void *f, size_t bytes) {
-    return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
-// Calls f with the type and the padded key size.
-template <class F>
-hipError_t pick(int dtype, int DK, F f) {
-    if (dtype == DWCONV_BF16) {
-        switch (DK) {
-            case 64: return f(BF16{}, std::integral_constant<int, 64>{});
-            case 128: return f(BF16{}, std::integral_constant<int, 128>{});
-            case 192: return f(BF16{}, std::integral_constant<int, 192>{});
-            default: return f(BF16{}, std::integral_constant<int, 256>{});
-        }
-    }
-    switch (DK) {
-        case 64: return f(F16{}, std::integral_constant<int, 64>{});
-        case 128: return f(F16{}, std::integral_constant<int, 128>{});
-        case 192: return f(F16{}, std::integral_constant<int, 192>{});
-        default: return f(F16{}, std::integral_constant<int, 256>{});
-    }
-}
-
 }  // namespace
 
 namespace delta {
@@ -821,7 +683,7 @@ hipError_t split_prepare(int dtype, int DK_, const Ctx &c, bool backward, hipStr
     return pick(dtype, DK_, [&](auto dt, auto dk) {
         using DT = decltype(dt);
         constexpr int DK = decltype(dk)::value;
-        const size_t n = 2 * CH * (DK + 8) * 2 + (3 * TRI + 4 * 256) * sizeof(float);
+        const size_t n = lds_prepare<DK>();
         const uint32_t blocks = (uint32_t)((int64_t)c.slots * c.Hk);
         auto f = backward ? k_prepare<DT, DK, true> : k_prepare<DT, DK, false>;
         hipError_t e = lds_room((const void *)f, n);
