@@ -628,8 +628,10 @@ Layout layout(const dwconv_delta_plan &p, int seqs, int tokens, bool backward) {
     } else {
         l.T = take(n * TRI);
     }
-    if (!split || backward) l.P = take(n * TRI);
-    if (!split) l.vecs = take(n * NV);
+    if (!split) {
+        l.P = take(n * TRI);
+        l.vecs = take(n * NV);
+    }
     if (split && backward) l.sums = take(n * CH * 2);
     if (backward) {
         l.S0s = take(n * DK * DvP);

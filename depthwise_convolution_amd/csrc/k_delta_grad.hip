@@ -3,8 +3,10 @@
 // k_delta.hip, the terms in delta_split.h).
 //
 // A workgroup has one chunk and one key head; its value heads come one after
-// the other and their shares of dQ and dK add up in registers.  Wavefront w has
-// tokens 16 w .. 16 w + 15.  Per value head, first the sums over the state's
+// the other and their shares of dQ and dK add up in registers.  Wavefronts w
+// and w + 4 have tokens 16 w .. 16 w + 15, the first half of the channels of q
+// and k and the second (one wavefront's sums for all channels need more
+// registers than two wavefronts on a SIMD have).  Per value head, first the sums over the state's
 // columns, 32 at a time: the rows of S0 and dS, split into terms by one
 // wavefront each, and U pass through LDS; dO, dR and U rows are left operands
 // that a lane loads as they lie.  Then the sums over tokens: E and M = beta dA D
@@ -43,13 +45,17 @@ __device__ __forceinline__ void get_frag(bf16x8 (&t)[N], const char *p, int lane
     for (int n = 0; n < N; ++n) t[n] = *(const bf16x8 *)(p + n * FRAG + lane * 16);
 }
 
-// Eight elements of a row of v or dO, zeros past `valid`.
-template <class X>
-__device__ __forceinline__ Vec<X, 8> load8(const X *p, int valid, bool vec) {
-    Vec<X, 8> r;
-    if (valid >= 8 && vec) return *(const Vec<X, 8> *)p;
+// Eight 16-bit elements of a row of v or dO, zeros past `valid`.
+__device__ __forceinline__ u32x4 load8(const void *p, int valid, bool vec) {
+    u32x4 r = {0, 0, 0, 0};
+    if (valid >= 8 && vec) {
+        r = *(const u32x4 *)p;
+    } else {
+        const uint16_t *q = (const uint16_t *)p;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = i < valid ? p[i] : (X)0;
+        for (int i = 0; i < 8; ++i)
+            if (i < valid) r[i / 2] |= (uint32_t)q[i] << (i % 2 * 16);
+    }
     return r;
 }
 
@@ -69,22 +75,26 @@ __device__ __forceinline__ f32x4 own_elements(const char *kt, int t, int wave, i
 
 constexpr int PITCH = 20;  // of a 16x16 tile that is written by columns and read by rows
 constexpr int WAVE_TILES = 2 * 4 * 16 * PITCH * 4;  // bytes of a wavefront's tiles of E and M
-__host__ __device__ constexpr int lds_blocks(int DK) { return (2 * DK / 16 + 4) * 3 * FRAG; }
+__host__ __device__ constexpr int lds_blocks(int DK) { return (2 * DK / 16 + 8) * 3 * FRAG; }
 constexpr int LDS_TILES = 4 * WAVE_TILES + 2 * Right<4, 3>::bytes(2);
+// columns' blocks, later tiles; the tiles of Q K^T and K K^T lie behind
+__host__ __device__ constexpr int lds_work(int DK) { return lds_blocks(DK) > LDS_TILES ? lds_blocks(DK) : LDS_TILES; }
+constexpr int LDS_KQ = 8 * 4 * FRAG;
 
 template <class DT, int DK>
-__global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
+__global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
     using X = typename DT::X;
     using R = Raw<DT>;
-    constexpr int NA = R::TERMS, NT = DK / 16, T = DK / 64, NF = DK / 8 * NA, NK = DK / 32;
+    constexpr int NA = R::TERMS, NT = DK / 16, NH = NT / 2, T = (NT + 7) / 8, NF = DK / 8 * NA, NK = DK / 32;
     extern __shared__ char L[];
-    char *SF = L, *DF = SF + NT * 3 * FRAG, *UF = DF + NT * 3 * FRAG;
-    __shared__ float db[CH], dbe[CH], a2[CH], colP[4][CH], colA[4][CH], dots[4];
+    char *SF = L, *DF = SF + NT * 3 * FRAG, *UF = DF + NT * 3 * FRAG, *RF = UF + 4 * 3 * FRAG;
+    // by halves: rows of db, dbeta and of the S1 term, column sums, q and k dots
+    __shared__ __align__(16) float db[2][CH], dbe[2][CH], a2[2][CH], cols[2][4][CH], rvs[CH], uqs[2][CH], uks[2][CH], dots[8];
     const int slot = blockIdx.x / c.Hk, hk = blockIdx.x % c.Hk;
     const Chunk found = chunk_of(c.seq, slot);
     const int n = uniform(found.n), tok = uniform(found.tok);
     if (n == 0) return;
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = lane & 15, g4 = (lane >> 4) * 4, g8 = 2 * g4;
+    const int lane = threadIdx.x & 63, wave8 = uniform(threadIdx.x >> 6), wave = wave8 & 3, half = wave8 >> 2, t0 = half * NH, r = lane & 15, g4 = (lane >> 4) * 4, g8 = 2 * g4;
     const int row = 16 * wave + g4;      // result layout: tokens row .. row + 3
     const int mine = 16 * wave + r;      // left operands: the lane's token
     float *ET = (float *)(L + wave * WAVE_TILES), *MT = ET + 4 * 16 * PITCH;
@@ -92,25 +102,53 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
     const char *keys = c.keys + ((int64_t)slot * c.Hk + hk) * c.key_bytes;
     const char *rows_k = keys + NF * FRAG, *kt = keys + 2 * NF * FRAG, *qt = keys + 3 * NF * FRAG;
     const int group = c.Hv / c.Hk;
-    f32x4 dQ[NT], dK[NT];
+    f32x4 dQ[NH], dK[NH];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) dQ[t] = dK[t] = splat(0.0f);
+    for (int t = 0; t < NH; ++t) dQ[t] = dK[t] = splat(0.0f);
+    // the wavefront's tiles of Q K^T (first half) or K K^T, of the unit vectors,
+    // kept in LDS for all value heads
+    f32x4 *const KQ = (f32x4 *)(L + lds_work(DK)) + wave8 * 4 * 64 + lane;
+    {
+        const float *vec = (const float *)(c.heads + ((int64_t)slot * c.Hv + hk * group) * c.head_bytes + AT_VEC * FRAG);
+        const f32x4 nr = *(const f32x4 *)(vec + (half ? V_NK : V_NQ) * CH + row);
+        f32x4 kq[4];
+        float nky[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            kq[j] = splat(0.0f);
+            nky[j] = vec[V_NK * CH + 16 * j + r];
+        }
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) {
+            bf16x8 z[NA], x[4][NA];
+            fetch(z, (half ? rows_k : keys) + (wave * NK + kb) * NA * FRAG, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= wave) fetch(x[j], rows_k + (j * NK + kb) * NA * FRAG, lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j <= wave) mac1(z, x[j], 2, kq[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) KQ[j * 64] = kq[j] * nr * nky[j];
+    }
     for (int h = hk * group; h < (hk + 1) * group; ++h) {
         const int64_t at = (int64_t)slot * c.Hv + h;
-        f32x4 X1[NT], X2[NT], X3[NT], dP[4], dA[4];
+        f32x4 X1[NH], X2[NH], X3[NH], dD[4];  // dD: tiles of dP (first half) or -dA
 #pragma unroll
-        for (int t = 0; t < NT; ++t) X1[t] = X2[t] = X3[t] = splat(0.0f);
+        for (int t = 0; t < NH; ++t) X1[t] = X2[t] = X3[t] = splat(0.0f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dP[j] = dA[j] = splat(0.0f);
+        for (int j = 0; j < 4; ++j) dD[j] = splat(0.0f);
         float rv = 0.0f, sd = 0.0f;  // dR . V of token `mine`; <S0, dS>
         // ---- sums over the state's columns
-        f32x4 s0[T][2], ds[T][2], ur[2], dr[2];
-        Vec<X, 8> od, vv;
+        f32x4 s0[T][2], ds[T][2], ud[2];  // ud: U (first half) or dR
+        u32x4 od, vv;
         auto ahead = [&](int col) {
             const uint32_t off = r * c.DvP + g8;
 #pragma unroll
             for (int x = 0; x < T; ++x) {
-                const int64_t p = (at * DK + 16 * (wave * T + x)) * c.DvP + col;
+                const int y = min(wave8 + 8 * x, NT - 1);  // (4 and 12 tiles leave wavefronts without one)
+                const int64_t p = (at * DK + 16 * y) * c.DvP + col;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     s0[x][j] = *(const f32x4 *)(ga.S0s + p + off + 4 * j);
@@ -120,48 +158,47 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
             const int64_t p = (at * CH + 16 * wave) * c.DvP + col;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                ur[j] = *(const f32x4 *)(ga.Us + p + off + 4 * j);
-                dr[j] = *(const f32x4 *)(ga.dRs + p + off + 4 * j);
+                ud[j] = *(const f32x4 *)((half ? ga.dRs : ga.Us) + p + off + 4 * j);
             }
             const int x = col + g8, token = tok + min(mine, n - 1), valid = mine < n ? c.Dv - x : 0;
-            od = load8<X>((const X *)ga.d_o + token * ga.lddo + (int64_t)h * c.Dv + x, valid, ga.vec_o);
-            vv = load8<X>((const X *)c.v + token * c.ldv + (int64_t)h * c.Dv + x, valid, ga.vec_v);
+            od = load8((const X *)ga.d_o + token * ga.lddo + (int64_t)h * c.Dv + x, valid, ga.vec_o);
+            vv = load8((const X *)c.v + token * c.ldv + (int64_t)h * c.Dv + x, valid, ga.vec_v);
         };
         ahead(0);
         for (int col = 0; col < c.DvP; col += 32) {
             __syncthreads();
             bf16x8 ot[NA], ut[3], rt[3];
             R::terms(__builtin_bit_cast(typename R::V8, od), ot);
-            split(ur[0], ur[1], ut);
-            split(dr[0], dr[1], rt);
-            put_frag(UF + wave * 3 * FRAG, ut, lane);
+            split(ud[0], ud[1], ut);
+            put_frag((half ? RF : UF) + wave * 3 * FRAG, ut, lane);
+            if (half)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) rv = __builtin_fmaf(dr[j / 4][j % 4], DT::widen(vv.v[j]), rv);
+                for (int j = 0; j < 8; ++j)
+                    rv = __builtin_fmaf(ud[j / 4][j % 4], DT::widen(__builtin_bit_cast(X, (uint16_t)(vv[j / 2] >> (j % 2 * 16)))), rv);
 #pragma unroll
             for (int x = 0; x < T; ++x) {
+                const int y = wave8 + 8 * x;
+                if (y >= NT) break;
                 bf16x8 t[3];
                 split(s0[x][0], s0[x][1], t);
-                put_frag(SF + (wave * T + x) * 3 * FRAG, t, lane);
+                put_frag(SF + y * 3 * FRAG, t, lane);
                 split(ds[x][0], ds[x][1], t);
-                put_frag(DF + (wave * T + x) * 3 * FRAG, t, lane);
+                put_frag(DF + y * 3 * FRAG, t, lane);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sd = __builtin_fmaf(s0[x][j / 4][j % 4], ds[x][j / 4][j % 4], sd);
             }
             if (col + 32 < c.DvP) ahead(col + 32);
             __syncthreads();
-            bf16x8 st[2][3], dt[2][3];
-            get_frag(st[0], SF, lane);
-            get_frag(dt[0], DF, lane);
+            get_frag(ut, UF + wave * 3 * FRAG, lane);
+            get_frag(rt, RF + wave * 3 * FRAG, lane);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t + 1 < NT) {
-                    get_frag(st[(t + 1) & 1], SF + (t + 1) * 3 * FRAG, lane);
-                    get_frag(dt[(t + 1) & 1], DF + (t + 1) * 3 * FRAG, lane);
-                }
-                fence();
-                mac1(rt, st[t & 1], 2, X3[t]);
-                mac1(ut, dt[t & 1], 2, X2[t]);
-                mac1(ot, st[t & 1], 2, X1[t]);
+            for (int t = 0; t < NH; ++t) {
+                bf16x8 st[3], dt[3];
+                get_frag(st, SF + (t0 + t) * 3 * FRAG, lane);
+                get_frag(dt, DF + (t0 + t) * 3 * FRAG, lane);
+                mac1(rt, st, 2, X3[t]);
+                mac1(ot, st, 2, X1[t]);
+                mac1(ut, dt, 2, X2[t]);
                 fence();
             }
 #pragma unroll
@@ -169,8 +206,8 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
                 if (j > wave) continue;
                 bf16x8 u[3];
                 get_frag(u, UF + j * 3 * FRAG, lane);
-                mac1(ot, u, 2, dP[j]);
-                mac1(rt, u, 2, dA[j]);  // of the other sign
+                if (half) mac1(rt, u, 2, dD[j]);
+                else mac1(ot, u, 2, dD[j]);
             }
         }
         // ---- sums over tokens
@@ -181,16 +218,22 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
         double br[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) br[i] = bs[row + i];
+        double by[4];
+        float nky[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            by[j] = bs[16 * j + r];
+            nky[j] = vec[V_NK * CH + 16 * j + r];
+        }
         f32x4 s1 = splat(0.0f), s2 = splat(0.0f), s3 = splat(0.0f);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const f32x4 kr = own_elements<NA>(kt, t, wave, lane), qr = own_elements<NA>(qt, t, wave, lane);
+        for (int t = 0; t < NH; ++t) {
+            const f32x4 kr = own_elements<NA>(kt, t0 + t, wave, lane), qr = own_elements<NA>(qt, t0 + t, wave, lane);
             s1 += qr * X1[t];
             s2 += kr * X2[t];
             s3 += kr * X3[t];
             dQ[t] += c.scale * eb * X1[t];
             dK[t] += er * X2[t] - eb * be * X3[t];
-            fence();
         }
         s1 = sum16(s1) * eb * nq * c.scale;
         s2 = sum16(s2) * er * nk;
@@ -200,80 +243,66 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
         rv += __shfl_xor(rv, 16, 64);
         rv += __shfl_xor(rv, 32, 64);
         __syncthreads();  // the blocks have been read: tiles take their place
-        if (lane == 0) dots[wave] = sd;
-        if (lane < 16) dbe[mine] = rv;
-        bf16x8 kw[NK][NA];
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) fetch(kw[kb], rows_k + (wave * NK + kb) * NA * FRAG, lane);
-        f32x4 rowP = splat(0.0f), rowA = splat(0.0f), rowB = splat(0.0f);
+        if (lane == 0) dots[wave8] = sd;
+        if (half && lane < 16) rvs[mine] = rv;
+        // the first half makes E from dP, the second M from dA
+        f32x4 rowD = splat(0.0f), rowB = splat(0.0f);
+        float *tile = half ? MT : ET;
+        const f32x4 left = half ? nk : nq;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float cp = 0.0f, ca = 0.0f;
-            f32x4 e = splat(0.0f), m = splat(0.0f);
+            float cd = 0.0f;
+            f32x4 e = splat(0.0f);
             if (j <= wave) {
-                f32x4 kk = splat(0.0f);
-#pragma unroll
-                for (int kb = 0; kb < NK; ++kb) {
-                    bf16x8 x[NA];
-                    fetch(x, rows_k + (j * NK + kb) * NA * FRAG, lane);
-                    mac1(kw[kb], x, 2, kk);
-                }
                 const int y = 16 * j + r;
-                const float nky = vec[V_NK * CH + y];
-                const double by = bs[y];
+                const f32x4 kq = KQ[j * 64];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int x = row + i;
-                    const float d = x >= y ? expf((float)(br[i] - by)) : 0.0f;
-                    const float p = x >= y ? dP[j][i] * c.P[at * TRI + tri(wave, j) + (g4 + i) * 16 + r] : 0.0f;
-                    const float a = x > y ? -dA[j][i] * d : 0.0f;
-                    const float ak = x > y ? a * (nk[i] * nky * kk[i]) : 0.0f;
-                    e[i] = x >= y ? c.scale * dP[j][i] * d : 0.0f;
-                    m[i] = be[i] * a;
-                    rowP[i] += p;
-                    rowB[i] += ak;
-                    rowA[i] += be[i] * ak;
-                    cp += p;
-                    ca += be[i] * ak;
-                    ET[(j * 16 + g4 + i) * PITCH + r] = e[i] * nky;
-                    MT[(j * 16 + g4 + i) * PITCH + r] = m[i] * nky;
+                    const float d = __expf((float)(br[i] - by[j]));
+                    const float x = half ? -dD[j][i] * d : c.scale * dD[j][i] * d;
+                    const bool in = half ? row + i > y : row + i >= y;
+                    const float z = in ? x : 0.0f, zk = in ? x * kq[i] : 0.0f;
+                    e[i] = half ? be[i] * z : z;
+                    rowB[i] += zk;
+                    rowD[i] += half ? be[i] * zk : zk;
+                    cd += half ? be[i] * zk : zk;
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tile[(j * 16 + g4 + i) * PITCH + r] = e[i] * nky[j];
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ET[(j * 16 + g4 + i) * PITCH + r] = MT[(j * 16 + g4 + i) * PITCH + r] = 0.0f;
+                for (int i = 0; i < 4; ++i) tile[(j * 16 + g4 + i) * PITCH + r] = 0.0f;
             }
-            ER.put(wave, j, e * nq, lane);
-            MR.put(wave, j, m * nk, lane);
-            cp += __shfl_xor(cp, 16, 64);
-            cp += __shfl_xor(cp, 32, 64);
-            ca += __shfl_xor(ca, 16, 64);
-            ca += __shfl_xor(ca, 32, 64);
-            if (lane < 16) {
-                colP[wave][16 * j + r] = cp;
-                colA[wave][16 * j + r] = ca;
-            }
+            (half ? MR : ER).put(wave, j, e * left, lane);
+            cd += __shfl_xor(cd, 16, 64);
+            cd += __shfl_xor(cd, 32, 64);
+            if (lane < 16) cols[half][wave][16 * j + r] = cd;
         }
-        rowP = sum16(rowP);
-        rowA = sum16(rowA);
+        rowD = sum16(rowD);
         rowB = sum16(rowB);
         if (r == 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                db[row + i] = s1[i] + rowP[i] + rowA[i] - be[i] * s3[i] - s2[i];
-                a2[row + i] = s2[i];
-                dbe[row + i] += rowB[i] - s3[i];
+                db[half][row + i] = s1[i] + rowD[i] - be[i] * s3[i] - s2[i];
+                a2[half][row + i] = s2[i];
+                dbe[half][row + i] = (half ? rowB[i] : 0.0f) - s3[i];
             }
         }
         __syncthreads();
-        if (wave == 0) {
-            float x = db[lane];
+        if (wave8 == 0) {
+            float x = db[0][lane] + db[1][lane];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) x -= colP[w][lane] + colA[w][lane];
-            double all = a2[lane];
+            for (int w = 0; w < 4; ++w) x -= cols[0][w][lane] + cols[1][w][lane];
+            double all = a2[0][lane] + a2[1][lane];
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) all += __shfl_xor(all, m, 64);
             double y = x;
-            if (lane == 63) y += all + (double)vec[V_EB * CH + CH - 1] * ((dots[0] + dots[1]) + (dots[2] + dots[3]));
+            if (lane == 63) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) sum += dots[w];
+                y += all + (double)vec[V_EB * CH + CH - 1] * sum;
+            }
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
                 const double z = __shfl_down(y, m, 64);
@@ -281,7 +310,7 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
             }
             if (lane < n) {
                 ga.dg[((int64_t)tok + lane) * c.Hv + h] = (float)y;
-                ga.dbeta[((int64_t)tok + lane) * c.Hv + h] = dbe[lane];
+                ga.dbeta[((int64_t)tok + lane) * c.Hv + h] = dbe[0][lane] + dbe[1][lane] + rvs[lane];
             }
         }
 #pragma unroll
@@ -295,25 +324,25 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
             }
             get_frag(et3, ER.p + (kb * 4 + wave) * 3 * FRAG, lane);
             get_frag(mt3, MR.p + (kb * 4 + wave) * 3 * FRAG, lane);
-            bf16x8 fk[2][NA], fq[2][NA];
-            fetch(fk[0], kt + kb * NA * FRAG, lane);
-            fetch(fq[0], qt + kb * NA * FRAG, lane);
+            bf16x8 fk[NH][NA], fq[NH][NA];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t + 1 < NT) {
-                    fetch(fk[(t + 1) & 1], kt + (2 * (t + 1) + kb) * NA * FRAG, lane);
-                    fetch(fq[(t + 1) & 1], qt + (2 * (t + 1) + kb) * NA * FRAG, lane);
+            for (int t = 0; t < NH; ++t) {
+                fetch(fk[t], kt + (2 * (t0 + t) + kb) * NA * FRAG, lane);
+                fetch(fq[t], qt + (2 * (t0 + t) + kb) * NA * FRAG, lane);
+            }
+            if (low) {
+#pragma unroll
+                for (int t = 0; t < NH; ++t) {
+                    mac1(er3, fk[t], 2, dQ[t]);
+                    mac1(mr3, fk[t], 2, dK[t]);
                 }
-                fence();
-                if (low) {
-                    mac1(er3, fk[t & 1], 2, dQ[t]);
-                    mac1(mr3, fk[t & 1], 2, dK[t]);
+            }
+            if (high) {
+#pragma unroll
+                for (int t = 0; t < NH; ++t) {
+                    mac1(et3, fq[t], 2, dK[t]);
+                    mac1(mt3, fk[t], 2, dK[t]);
                 }
-                if (high) {
-                    mac1(et3, fq[t & 1], 2, dK[t]);
-                    mac1(mt3, fk[t & 1], 2, dK[t]);
-                }
-                fence();
             }
         }
     }
@@ -323,20 +352,28 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
     f32x4 uq = splat(0.0f), uk = splat(0.0f);
     if (c.normalize) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            uq += dQ[t] * own_elements<NA>(qt, t, wave, lane);
-            uk += dK[t] * own_elements<NA>(kt, t, wave, lane);
-            fence();
+        for (int t = 0; t < NH; ++t) {
+            uq += dQ[t] * own_elements<NA>(qt, t0 + t, wave, lane);
+            uk += dK[t] * own_elements<NA>(kt, t0 + t, wave, lane);
         }
         uq = sum16(uq) * nq * nq;
         uk = sum16(uk) * nk * nk;
-    }
-    asm volatile("" ::: "memory");  // the elements are read again, not kept
+        if (r == 0) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const f32x4 q = nq * (dQ[t] - uq * own_elements<NA>(qt, t, wave, lane));
-        const f32x4 k = nk * (dK[t] - uk * own_elements<NA>(kt, t, wave, lane));
-        const int y = 16 * t + r;
+            for (int i = 0; i < 4; ++i) {
+                uqs[half][row + i] = uq[i];
+                uks[half][row + i] = uk[i];
+            }
+        }
+        __syncthreads();
+        uq = *(const f32x4 *)&uqs[0][row] + *(const f32x4 *)&uqs[1][row];
+        uk = *(const f32x4 *)&uks[0][row] + *(const f32x4 *)&uks[1][row];
+    }
+#pragma unroll
+    for (int t = 0; t < NH; ++t) {
+        const f32x4 q = nq * (dQ[t] - uq * own_elements<NA>(qt, t0 + t, wave, lane));
+        const f32x4 k = nk * (dK[t] - uk * own_elements<NA>(kt, t0 + t, wave, lane));
+        const int y = 16 * (t0 + t) + r;
         if (y < c.Dk) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -345,7 +382,6 @@ __global__ void __launch_bounds__(256) k_grad(Ctx c, GradArgs ga) {
                     ((X *)ga.dk)[(tok + row + i) * ga.lddk + (int64_t)hk * c.Dk + y] = rounded<DT>(k[i]);
                 }
         }
-        fence();
     }
 }
 
@@ -357,10 +393,10 @@ hipError_t split_grad(int dtype, int DK_, const Ctx &c, const GradArgs &ga, hipS
     return pick(dtype, DK_, [&](auto dt, auto dk) {
         using DT = decltype(dt);
         constexpr int DK = decltype(dk)::value;
-        const size_t n = lds_blocks(DK) > LDS_TILES ? lds_blocks(DK) : LDS_TILES;
+        const size_t n = lds_work(DK) + LDS_KQ;
         hipError_t e = lds_room((const void *)k_grad<DT, DK>, n);
         if (e != hipSuccess) return e;
-        k_grad<DT, DK><<<(uint32_t)((int64_t)c.slots * c.Hk), 256, n, st>>>(c, ga);
+        k_grad<DT, DK><<<(uint32_t)((int64_t)c.slots * c.Hk), 512, n, st>>>(c, ga);
         return hipGetLastError();
     });
 }

@@ -178,7 +178,6 @@ __global__ void __launch_bounds__(256, (DK <= 128 ? 3 : 2)) k_prepare(Ctx c) {
                 const int e = tri(wave, j) + (g4 + i) * 16 + r;
                 At[e] = row > col ? beta[w][row] * d * (rk[row] * rk[col] * kk[j][i]) : 0.0f;
                 Pl[e] = p;
-                if (BACK) c.P[at * TRI + e] = p;
             }
         }
         __syncthreads();
