@@ -183,11 +183,7 @@ struct GradArgs {
 
 // sum over the 16 lanes that share rows
 __device__ __forceinline__ f32x4 sum16(f32x4 v) {
-#pragma unroll
-    for (int m = 1; m < 16; m <<= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], m, 64);
-    return v;
+    return f32x4{sum_row16(v[0]), sum_row16(v[1]), sum_row16(v[2]), sum_row16(v[3])};
 }
 
 // launchers (k_delta_split.hip, k_delta_grad.hip)

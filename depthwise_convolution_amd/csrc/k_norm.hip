@@ -21,22 +21,46 @@ struct Opt {
     float eps, inv_d;
 };
 
-// sum over the TPR lanes of a row; every lane gets it
+// Sums over the TPR lanes of a row; every lane gets them.  Rows of more than a
+// wavefront exchange through LDS, in two places by turns: by the time a place
+// is written again all lanes have passed the barrier behind the other one's
+// write, and so have read it.
 template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float *sh) {
+struct RowSum {
+    float *sh;  // 2 x 2 x 16
+    int turn = 0;
+    __device__ __forceinline__ RowSum(float *sh) : sh(sh) {}
+    __device__ __forceinline__ void two(float &a, float &b) {
+        if (TPR == 16) {
+            a = sum_row16(a);
+            b = sum_row16(b);
+            return;
+        }
+        a = sum_wave(a);
+        b = sum_wave(b);
+        if (TPR > 64) {
+            constexpr int W = TPR / 64;
+            float *p = sh + turn * 32;
+            turn ^= 1;
+            if ((threadIdx.x & 63) == 0) {
+                p[threadIdx.x >> 6] = a;
+                p[16 + (threadIdx.x >> 6)] = b;
+            }
+            __syncthreads();
+            a = b = 0.0f;
 #pragma unroll
-    for (int m = 1; m < (TPR < 64 ? TPR : 64); m <<= 1) v += __shfl_xor(v, m, 64);
-    if (TPR > 64) {
-        constexpr int W = TPR / 64;
-        __syncthreads();  // the previous sum has been read
-        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < W; ++i) v += sh[i];
+            for (int i = 0; i < W; ++i) {
+                a += p[i];
+                b += p[16 + i];
+            }
+        }
     }
-    return v;
-}
+    __device__ __forceinline__ float one(float a) {
+        float b = 0.0f;
+        two(a, b);
+        return a;
+    }
+};
 
 __device__ __forceinline__ float gate_value(float g, int act) {
     if (act == DWCONV_SEQ_ACT_NONE) return g;
@@ -49,27 +73,32 @@ __device__ __forceinline__ float gate_slope(float g, int act) {
     return act == DWCONV_SEQ_ACT_SILU ? p * (1.0f + g * (1.0f - p)) : p * (1.0f - p);
 }
 
-// A lane's E channels: NV vectors of VEC, TPR vectors apart.
+// A lane's E channels: NV vectors of VEC, TPR vectors apart.  Vectors past D
+// are read as the row's first one (no branch around a load) and count as zeros.
 template <class DT, int VEC, int TPR, int E>
 struct Lane {
+    using X = typename DT::X;
     static constexpr int NV = E / VEC;
+    struct Raw {
+        Vec<X, VEC> v[NV];
+    };
     int D, lane;
     __device__ __forceinline__ int channel(int n) const { return (n * TPR + lane) * VEC; }
-    __device__ __forceinline__ void load(float (&v)[E], const typename DT::X *p) const {
+    __device__ __forceinline__ bool inside(int e) const { return channel(e / VEC) < D; }
+    __device__ __forceinline__ void fetch(Raw &r, const X *p) const {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            float part[VEC];
-            if (channel(n) < D) {
-                load_f32<DT, VEC>(part, p + channel(n));
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) part[i] = 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[n * VEC + i] = part[i];
-        }
+        for (int n = 0; n < NV; ++n) r.v[n] = *(const Vec<X, VEC> *)(p + (channel(n) < D ? channel(n) : 0));
     }
-    __device__ __forceinline__ void store(typename DT::X *p, const float (&v)[E]) const {
+    __device__ __forceinline__ void widen(float (&v)[E], const Raw &r) const {
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = inside(i) ? DT::widen(r.v[i / VEC].v[i % VEC]) : 0.0f;
+    }
+    __device__ __forceinline__ void load(float (&v)[E], const X *p) const {
+        Raw r;
+        fetch(r, p);
+        widen(v, r);
+    }
+    __device__ __forceinline__ void store(X *p, const float (&v)[E]) const {
 #pragma unroll
         for (int n = 0; n < NV; ++n)
             if (channel(n) < D) {
@@ -79,26 +108,25 @@ struct Lane {
                 store_f32<DT, VEC>(p + channel(n), part);
             }
     }
-    __device__ __forceinline__ bool inside(int e) const { return channel(e / VEC) < D; }
 };
 
 // Statistics of a norm: v becomes (v - mean) r (the unit row), r is returned.
 // Channels past D stay zero.
-template <class L, int TPR, int E>
-__device__ __forceinline__ float unit_row(float (&v)[E], const L &ln, const Opt &o, int kind, float *sh) {
+template <int TPR, class L, int E>
+__device__ __forceinline__ float unit_row(float (&v)[E], const L &ln, const Opt &o, int kind, RowSum<TPR> &sum) {
     if (kind == DWCONV_NORM_NONE) return 1.0f;
     if (kind == DWCONV_NORM_LAYER) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < E; ++i) s += v[i];
-        const float mean = row_sum<TPR>(s, sh) * o.inv_d;
+        const float mean = sum.one(s) * o.inv_d;
 #pragma unroll
         for (int i = 0; i < E; ++i) v[i] = ln.inside(i) ? v[i] - mean : 0.0f;
     }
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) q = __builtin_fmaf(v[i], v[i], q);
-    const float r = 1.0f / sqrtf(row_sum<TPR>(q, sh) * o.inv_d + o.eps);
+    const float r = 1.0f / sqrtf(sum.one(q) * o.inv_d + o.eps);
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] *= r;
     return r;
@@ -107,17 +135,17 @@ __device__ __forceinline__ float unit_row(float (&v)[E], const L &ln, const Opt 
 // d becomes the gradient of the norm's input: d holds the gradient of the unit
 // row (already times w), u the unit row.
 template <int TPR, int E>
-__device__ __forceinline__ void norm_back(float (&d)[E], const float (&u)[E], float r, const Opt &o, int kind, float *sh) {
+__device__ __forceinline__ void norm_back(float (&d)[E], const float (&u)[E], float r, const Opt &o, int kind, RowSum<TPR> &sum) {
     if (kind == DWCONV_NORM_NONE) return;
     float a = 0.0f, m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) a = __builtin_fmaf(d[i], u[i], a);
-    a = row_sum<TPR>(a, sh) * o.inv_d;
-    if (kind == DWCONV_NORM_LAYER) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) m += d[i];
-        m = row_sum<TPR>(m, sh) * o.inv_d;
+    for (int i = 0; i < E; ++i) {
+        a = __builtin_fmaf(d[i], u[i], a);
+        m += d[i];
     }
+    sum.two(a, m);
+    a *= o.inv_d;
+    m = kind == DWCONV_NORM_LAYER ? m * o.inv_d : 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) d[i] = r * (d[i] - m - u[i] * a);
 }
@@ -126,7 +154,8 @@ template <class DT, int VEC, int TPR, int E>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
     k_fwd(Opt o, const typename DT::X *po, const typename DT::X *pres, const typename DT::X *pgate, const float *scale,
           const float *wa, const float *ba, const float *wb, const float *bb, typename DT::X *ph, typename DT::X *py) {
-    __shared__ float sh[16];
+    __shared__ float sh[64];
+    RowSum<TPR> sum(sh);
     constexpr int RPB = TPR > 256 ? 1 : 256 / TPR;
     using L = Lane<DT, VEC, TPR, E>;
     using LF = Lane<F32, VEC, TPR, E>;
@@ -135,9 +164,14 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
     const int64_t row0 = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     const bool live = row0 < o.rows;
     const int64_t at = (live ? row0 : o.rows - 1) * o.D;  // idle lanes follow the last row
+    // the row's tensors at once, then the parameters
+    typename L::Raw ro, rg, rr;
+    ln.fetch(ro, po + at);
+    if (pgate) ln.fetch(rg, pgate + (live ? row0 : o.rows - 1) / o.per * o.D);
+    if (pres) ln.fetch(rr, pres + at);
     float v[E], t[E];
-    ln.load(v, po + at);
-    unit_row<L, TPR, E>(v, ln, o, o.after, sh);
+    ln.widen(v, ro);
+    unit_row(v, ln, o, o.after, sum);
     if (o.after != DWCONV_NORM_NONE) {
         lf.load(t, wa);
 #pragma unroll
@@ -149,7 +183,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
         }
     }
     if (pgate) {
-        ln.load(t, pgate + (live ? row0 : o.rows - 1) / o.per * o.D);
+        ln.widen(t, rg);
 #pragma unroll
         for (int i = 0; i < E; ++i) v[i] *= gate_value(t[i], o.act);
     }
@@ -159,13 +193,13 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
         for (int i = 0; i < E; ++i) v[i] *= t[i];
     }
     if (pres) {
-        ln.load(t, pres + at);
+        ln.widen(t, rr);
 #pragma unroll
         for (int i = 0; i < E; ++i) v[i] += t[i];
     }
     if (ph && live) ln.store(ph + at, v);
     if (o.before == DWCONV_NORM_NONE) return;
-    unit_row<L, TPR, E>(v, ln, o, o.before, sh);
+    unit_row(v, ln, o, o.before, sum);
     lf.load(t, wb);
 #pragma unroll
     for (int i = 0; i < E; ++i) v[i] *= t[i];
@@ -199,33 +233,60 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
           const float *scale, const float *wa, const float *ba, const float *wb, Grad gr) {
     using X = typename DT::X;
     constexpr int RPB = TPR > 256 ? 1 : 256 / TPR;
+    // workgroups of 1024 lanes have 128 registers a lane: they read parameters
+    // again for each row and take its tensors when it is its turn
+    constexpr bool AHEAD = TPR <= 512;
     using L = Lane<DT, VEC, TPR, E>;
     using LF = Lane<F32, VEC, TPR, E>;
-    __shared__ float sh[16];
+    __shared__ float sh[64];
     __shared__ float join[RPB > 1 ? 256 * E : 1];
+    RowSum<TPR> rs(sh);
     const L ln{o.D, (int)threadIdx.x % TPR};
     const LF lf{o.D, (int)threadIdx.x % TPR};
     const int sub = threadIdx.x / TPR;
     const bool shared_gate = pgate && o.per > 1;
-    const bool affine = o.after == DWCONV_NORM_LAYER && ba;
+    if (o.after != DWCONV_NORM_LAYER) ba = nullptr;
+    if (o.after == DWCONV_NORM_NONE) wa = nullptr;
+    if (o.before == DWCONV_NORM_NONE) wb = nullptr;
     float sum[5][E], gsum[E];
 #pragma unroll
     for (int j = 0; j < 5; ++j)
 #pragma unroll
         for (int i = 0; i < E; ++i) sum[j][i] = 0.0f;
+    // parameters (scale, w_after, b_after, w_before), where they are given
+    float par[AHEAD ? 4 : 1][E];
+    auto param = [&](int k) { return k == 0 ? scale : k == 1 ? wa : k == 2 ? ba : wb; };
+    if (AHEAD) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (param(k)) lf.load(par[AHEAD ? k : 0], param(k));
+    }
+    auto get = [&](int k) -> const float(&)[E] {
+        if (!AHEAD) lf.load(par[0], param(k));
+        return par[AHEAD ? k : 0];
+    };
     // the sum over the workgroup's row lanes, in lane order; lanes of the first
     // row have it
     auto joined = [&](float (&v)[E]) {
         if (RPB == 1) return;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < E; ++i) join[threadIdx.x * E + i] = v[i];
+        for (int i = 0; i < E; ++i) join[i * 256 + threadIdx.x] = v[i];
         __syncthreads();
         if (sub == 0) {
-            for (int r = 1; r < RPB; ++r)
 #pragma unroll
-                for (int i = 0; i < E; ++i) v[i] += join[(r * TPR + threadIdx.x) * E + i];
+            for (int i = 0; i < E; ++i)
+                for (int r = 1; r < RPB; ++r) v[i] += join[i * 256 + r * TPR + threadIdx.x];
         }
+    };
+    typename L::Raw ro, rr, rh, ry, rg;
+    auto take = [&](int64_t row) {
+        const int64_t at = row * o.D;
+        ln.fetch(ro, po + at);
+        if (pres && wb) ln.fetch(rr, pres + at);
+        if (gr.dh) ln.fetch(rh, (const X *)gr.dh + at);
+        if (wb) ln.fetch(ry, (const X *)gr.dy + at);
+        if (pgate && !shared_gate) ln.fetch(rg, pgate + row / o.per * o.D);
     };
     const int64_t first = deal.segs > 1 ? blockIdx.x / deal.segs : (int64_t)blockIdx.x * deal.chunk;
     const int seg = deal.segs > 1 ? blockIdx.x % deal.segs : 0;
@@ -237,54 +298,60 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
         const int64_t r1 = r0 + deal.seg_rows < g1 ? r0 + deal.seg_rows : g1;
 #pragma unroll
         for (int i = 0; i < E; ++i) gsum[i] = 0.0f;
+        if (r0 < r1) {
+            if (AHEAD) take(r0 + sub < r1 ? r0 + sub : r1 - 1);
+            if (shared_gate) ln.fetch(rg, pgate + grp * o.D);
+        }
         for (int64_t base = r0; base < r1; base += RPB) {
             const bool live = base + sub < r1;
             const int64_t row = live ? base + sub : r1 - 1;
             const int64_t at = row * o.D;
-            float ua[E], n[E], a[E], t[E], h[E], d[E], w[E];
-            // forward values
-            ln.load(ua, po + at);
-            const float ra = unit_row<L, TPR, E>(ua, ln, o, o.after, sh);
+            float ua[E], t[E], h[E], d[E], dy[E], a[E];
+            if (!AHEAD) take(row);
+            ln.widen(ua, ro);
+            if (pgate) ln.widen(a, rg);
 #pragma unroll
-            for (int i = 0; i < E; ++i) n[i] = ua[i];
-            if (o.after != DWCONV_NORM_NONE) {
-                lf.load(w, wa);
-#pragma unroll
-                for (int i = 0; i < E; ++i) n[i] *= w[i];
-                if (affine) {
-                    lf.load(w, ba);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) n[i] += w[i];
-                }
+            for (int i = 0; i < E; ++i) d[i] = dy[i] = h[i] = 0.0f;
+            if (gr.dh) ln.widen(d, rh);
+            if (wb) {
+                ln.widen(dy, ry);
+                if (pres) ln.widen(h, rr);
             }
+            if (AHEAD && base + RPB < r1) take(base + RPB + sub < r1 ? base + RPB + sub : r1 - 1);
+            // forward values: t = N_after(o) act(gate)
+            const float ra = unit_row(ua, ln, o, o.after, rs);
+#pragma unroll
+            for (int i = 0; i < E; ++i) t[i] = ua[i];
+            if (wa) {
+                const float(&w)[E] = get(1);
+#pragma unroll
+                for (int i = 0; i < E; ++i) t[i] *= w[i];
+            }
+            if (ba) {
+                const float(&w)[E] = get(2);
+#pragma unroll
+                for (int i = 0; i < E; ++i) t[i] += w[i];
+            }
+            float slope[E];  // N_after(o) act'(gate)
             if (pgate) {
-                ln.load(a, pgate + row / o.per * o.D);
-            }
 #pragma unroll
-            for (int i = 0; i < E; ++i) t[i] = pgate ? n[i] * gate_value(a[i], o.act) : n[i];
+                for (int i = 0; i < E; ++i) {
+                    slope[i] = t[i] * gate_slope(a[i], o.act);
+                    a[i] = gate_value(a[i], o.act);
+                    t[i] *= a[i];
+                }
+            }
             // gradient of h
-            if (gr.dh) {
-                ln.load(d, (const X *)gr.dh + at);
-            } else {
-#pragma unroll
-                for (int i = 0; i < E; ++i) d[i] = 0.0f;
-            }
-            if (o.before != DWCONV_NORM_NONE) {
-                float dy[E];
-#pragma unroll
-                for (int i = 0; i < E; ++i) h[i] = t[i];
+            if (wb) {
                 if (scale) {
-                    lf.load(w, scale);
+                    const float(&w)[E] = get(0);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) h[i] *= w[i];
-                }
-                if (pres) {
-                    ln.load(w, pres + at);
+                    for (int i = 0; i < E; ++i) h[i] = __builtin_fmaf(t[i], w[i], h[i]);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < E; ++i) h[i] += w[i];
+                    for (int i = 0; i < E; ++i) h[i] += t[i];
                 }
-                const float rb = unit_row<L, TPR, E>(h, ln, o, o.before, sh);
-                ln.load(dy, (const X *)gr.dy + at);
+                const float rb = unit_row(h, ln, o, o.before, rs);
                 if (live) {
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
@@ -292,17 +359,17 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
                         sum[4][i] += dy[i];
                     }
                 }
-                lf.load(w, wb);
+                const float(&w)[E] = get(3);
 #pragma unroll
                 for (int i = 0; i < E; ++i) dy[i] *= w[i];
-                norm_back<TPR, E>(dy, h, rb, o, o.before, sh);
+                norm_back(dy, h, rb, o, o.before, rs);
 #pragma unroll
                 for (int i = 0; i < E; ++i) d[i] += dy[i];
             }
             if (gr.dres && live) ln.store((X *)gr.dres + at, d);
             // through scale and gate
             if (scale) {
-                lf.load(w, scale);
+                const float(&w)[E] = get(0);
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
                     if (live) sum[0][i] = __builtin_fmaf(d[i], t[i], sum[0][i]);
@@ -312,14 +379,14 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
             if (pgate) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    w[i] = d[i] * n[i] * gate_slope(a[i], o.act);
-                    d[i] *= gate_value(a[i], o.act);
-                    if (live) gsum[i] += w[i];
+                    slope[i] *= d[i];
+                    d[i] *= a[i];
+                    if (live) gsum[i] += slope[i];
                 }
-                if (!shared_gate && gr.dgate && live) ln.store((X *)gr.dgate + at, w);
+                if (!shared_gate && gr.dgate && live) ln.store((X *)gr.dgate + at, slope);
             }
             // through the norm after the block
-            if (o.after != DWCONV_NORM_NONE) {
+            if (wa) {
                 if (live) {
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
@@ -327,10 +394,10 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
                         sum[2][i] += d[i];
                     }
                 }
-                lf.load(w, wa);
+                const float(&w)[E] = get(1);
 #pragma unroll
                 for (int i = 0; i < E; ++i) d[i] *= w[i];
-                norm_back<TPR, E>(d, ua, ra, o, o.after, sh);
+                norm_back(d, ua, ra, o, o.after, rs);
             }
             if (gr.d_o && live) ln.store((X *)gr.d_o + at, d);
         }
@@ -356,15 +423,40 @@ struct Params {
 };
 
 // Column sums of the workgroups' partial sums: 64 columns a workgroup, wave w
-// takes every 16th row from w on, the 16 sums are added in order.
-__global__ void __launch_bounds__(1024) k_sum(const float *part, int64_t blocks, int D, Params p) {
+// takes every 16th row from w on (four rows at a time), the 16 sums are added in
+// order.  Workgroups behind `param_blocks` sum the pieces of shared gates.
+template <class DT>
+__global__ void __launch_bounds__(1024) k_sum(const float *part, int64_t blocks, int D, Params p, uint32_t param_blocks,
+                                              const float *gates, int64_t groups, int segs, typename DT::X *dgate) {
+    if (blockIdx.x >= param_blocks) {
+        const int64_t i = (int64_t)(blockIdx.x - param_blocks) * 1024 + threadIdx.x;
+        if (i >= groups * D) return;
+        const float *q = gates + i / D * segs * D + i % D;
+        float s = 0.0f;
+        int k = 0;
+        for (; k + 4 <= segs; k += 4) {
+            const float a = q[(int64_t)k * D], b = q[(int64_t)(k + 1) * D], c = q[(int64_t)(k + 2) * D],
+                        d = q[(int64_t)(k + 3) * D];
+            s += (a + b) + (c + d);
+        }
+        for (; k < segs; ++k) s += q[(int64_t)k * D];
+        dgate[i] = rounded<DT>(s);
+        return;
+    }
     __shared__ float sh[16][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t col = (int64_t)blockIdx.x * 64 + lane, n = 5 * (int64_t)D;
-    float s = 0.0f;
-    if (col < n && p.out[col / D])
-        for (int64_t b = wave; b < blocks; b += 16) s += part[b * n + col];
-    sh[wave][lane] = s;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (col < n && p.out[col / D]) {
+        const float *q = part + col;
+        int64_t b = wave;
+        for (; b + 48 < blocks; b += 64) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] += q[(b + 16 * i) * n];
+        }
+        for (; b < blocks; b += 16) s[0] += q[b * n];
+    }
+    sh[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
     if (wave || col >= n || !p.out[col / D]) return;
     float r = 0.0f;
@@ -373,25 +465,15 @@ __global__ void __launch_bounds__(1024) k_sum(const float *part, int64_t blocks,
     p.out[col / D][col % D] = r;
 }
 
-template <class DT>
-__global__ void __launch_bounds__(256) k_gate_sum(const float *part, int64_t groups, int segs, int D, typename DT::X *out) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= groups * D) return;
-    const float *p = part + i / D * segs * D + i % D;
-    float s = 0.0f;
-    for (int k = 0; k < segs; ++k) s += p[(int64_t)k * D];
-    out[i] = rounded<DT>(s);
-}
+// Lanes a row of the backward pass, 8 channels each (their arrays and sums stay
+// in registers; 16 only for rows of more than 8192); the forward pass takes 16
+// channels a lane where that saves lanes.
+int lanes_of(int D) { return D <= 128 ? 16 : D <= 512 ? 64 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024; }
 
-// Lanes a row and channels a lane.  Short rows share a wavefront; a lane has 8
-// channels (five arrays and five sums of them stay in registers), 16 only for
-// the longest rows.
-int lanes_of(int D) { return D <= 128 ? 16 : D <= 512 ? 64 : D <= 2048 ? 256 : 1024; }
-
-// About 2048 workgroups of 256 lanes fill the chip twice over; each has at
-// least 4 rows a lane group to walk, so that its sums are worth writing.
+// Workgroups that fill the chip about twice, each with rows enough for its sums
+// to be worth writing.
 Deal deal_of(int D, int rows, int per) {
-    const int tpr = lanes_of(D), rpb = tpr >= 256 ? 1 : 256 / tpr, target = tpr > 256 ? 512 : 2048;
+    const int tpr = lanes_of(D), rpb = tpr >= 256 ? 1 : 256 / tpr, target = tpr > 256 ? 512 : 1024;
     Deal d{};
     d.rows_in = per > 1 ? per : (rows > 0 ? rows : 1);
     d.groups = ((int64_t)rows + d.rows_in - 1) / d.rows_in;
@@ -409,12 +491,12 @@ Deal deal_of(int D, int rows, int per) {
     return d;
 }
 
-template <class DT, int VEC, int TPR, int E>
-hipError_t launch(bool back, const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
+template <bool BACK, class DT, int VEC, int TPR, int E>
+hipError_t launch(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
     using X = typename DT::X;
     const Opt o{p.D, a.rows, a.per, p.after, p.before, p.act, p.eps, 1.0f / (float)p.D};
     constexpr int RPB = TPR > 256 ? 1 : 256 / TPR, BLOCK = TPR > 256 ? TPR : 256;
-    if (!back) {
+    if constexpr (!BACK) {
         const uint32_t blocks = (uint32_t)(((int64_t)a.rows + RPB - 1) / RPB);
         if ((uint64_t)blocks * BLOCK >= (1ull << 32)) return hipErrorInvalidConfiguration;
         if (blocks)
@@ -422,59 +504,67 @@ hipError_t launch(bool back, const dwconv_norm_plan &p, const NormArgs &a, hipSt
                                                              a.scale, a.w_after, a.b_after, a.w_before, a.b_before,
                                                              (X *)a.h, (X *)a.y);
         return hipGetLastError();
-    }
-    const Deal d = deal_of(p.D, a.rows, a.per);
-    const Grad gr{a.dh, a.dy, a.d_o, a.dresidual, a.dgate, a.workspace, a.workspace + (int64_t)d.blocks * 5 * p.D};
-    if (d.blocks)
-        k_bwd<DT, VEC, TPR, E><<<d.blocks, BLOCK, 0, st>>>(o, d, (const X *)a.o, (const X *)a.residual,
-                                                           (const X *)a.gate, a.scale, a.w_after, a.b_after,
-                                                           a.w_before, gr);
-    if (a.gate && a.dgate && a.per > 1 && d.segs > 1)
-        k_gate_sum<DT><<<(uint32_t)((d.groups * p.D + 255) / 256), 256, 0, st>>>(gr.gate_part, d.groups, d.segs, p.D,
-                                                                                 (X *)a.dgate);
-    const Params out{{a.dscale, a.dw_after, a.db_after, a.dw_before, a.db_before}};
-    if (a.dscale || a.dw_after || a.db_after || a.dw_before || a.db_before)
-        k_sum<<<(uint32_t)((5 * (int64_t)p.D + 63) / 64), 1024, 0, st>>>(gr.part, d.blocks, p.D, out);
-    return hipGetLastError();
-}
-
-template <class DT, int VEC>
-hipError_t pick_row(bool back, const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
-    switch (lanes_of(p.D)) {
-        case 16: return launch<DT, VEC, 16, 8>(back, p, a, st);
-        case 64: return launch<DT, VEC, 64, 8>(back, p, a, st);
-        case 256: return launch<DT, VEC, 256, 8>(back, p, a, st);
-        default:
-            return p.D <= 8192 ? launch<DT, VEC, 1024, 8>(back, p, a, st) : launch<DT, VEC, 1024, 16>(back, p, a, st);
+    } else {
+        const Deal d = deal_of(p.D, a.rows, a.per);
+        const Grad gr{a.dh, a.dy, a.d_o, a.dresidual, a.dgate, a.workspace, a.workspace + (int64_t)d.blocks * 5 * p.D};
+        if (d.blocks)
+            k_bwd<DT, VEC, TPR, E><<<d.blocks, BLOCK, 0, st>>>(o, d, (const X *)a.o, (const X *)a.residual,
+                                                               (const X *)a.gate, a.scale, a.w_after, a.b_after,
+                                                               a.w_before, gr);
+        const Params out{{a.dscale, a.dw_after, a.db_after, a.dw_before, a.db_before}};
+        const bool any = a.dscale || a.dw_after || a.db_after || a.dw_before || a.db_before;
+        const uint32_t pb = any ? (uint32_t)((5 * (int64_t)p.D + 63) / 64) : 0;
+        const uint32_t gb = a.gate && a.dgate && a.per > 1 && d.segs > 1 ? (uint32_t)((d.groups * p.D + 1023) / 1024) : 0;
+        if (pb + gb)
+            k_sum<DT><<<pb + gb, 1024, 0, st>>>(gr.part, d.blocks, p.D, out, pb, gr.gate_part, d.groups, d.segs,
+                                                (X *)a.dgate);
+        return hipGetLastError();
     }
 }
 
-template <class DT>
-hipError_t pick_vec(bool back, const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
+template <bool BACK, class DT, int VEC>
+hipError_t pick_row(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
+    const int D = p.D;
+    if (D <= 128) return launch<BACK, DT, VEC, 16, 8>(p, a, st);
+    if (D <= 512) return launch<BACK, DT, VEC, 64, 8>(p, a, st);
+    if constexpr (BACK) {
+        if (D <= 2048) return launch<true, DT, VEC, 256, 8>(p, a, st);
+        if (D <= 4096) return launch<true, DT, VEC, 512, 8>(p, a, st);
+    } else {
+        if (D <= 1024) return launch<false, DT, VEC, 64, 16>(p, a, st);
+        if (D <= 2048) return launch<false, DT, VEC, 256, 8>(p, a, st);
+        if (D <= 4096) return launch<false, DT, VEC, 256, 16>(p, a, st);
+    }
+    return D <= 8192 ? launch<BACK, DT, VEC, 1024, 8>(p, a, st) : launch<BACK, DT, VEC, 1024, 16>(p, a, st);
+}
+
+template <bool BACK, class DT>
+hipError_t pick_vec(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
     constexpr int V = 16 / (int)sizeof(typename DT::X);
     const void *ptrs[] = {a.o, a.residual, a.gate, a.scale, a.w_after, a.b_after, a.w_before, a.b_before, a.h, a.y,
                           a.dh, a.dy, a.d_o, a.dresidual, a.dgate, a.workspace};
     uintptr_t bits = 0;
     for (const void *q : ptrs) bits |= (uintptr_t)q;
-    return (bits & 15) == 0 && p.D % V == 0 ? pick_row<DT, V>(back, p, a, st) : pick_row<DT, 1>(back, p, a, st);
+    return (bits & 15) == 0 && p.D % V == 0 ? pick_row<BACK, DT, V>(p, a, st) : pick_row<BACK, DT, 1>(p, a, st);
 }
 
-hipError_t pick(bool back, const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
+template <bool BACK>
+hipError_t pick(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) {
     switch (p.dtype) {
-        case DWCONV_F32: return pick_vec<F32>(back, p, a, st);
-        case DWCONV_F16: return pick_vec<F16>(back, p, a, st);
-        default: return pick_vec<BF16>(back, p, a, st);
+        case DWCONV_F32: return pick_vec<BACK, F32>(p, a, st);
+        case DWCONV_F16: return pick_vec<BACK, F16>(p, a, st);
+        default: return pick_vec<BACK, BF16>(p, a, st);
     }
 }
 
 }  // namespace
 
-hipError_t norm_fwd(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) { return pick(false, p, a, st); }
-hipError_t norm_bwd(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) { return pick(true, p, a, st); }
+hipError_t norm_fwd(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) { return pick<false>(p, a, st); }
+hipError_t norm_bwd(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st) { return pick<true>(p, a, st); }
 
 size_t norm_bwd_bytes(const dwconv_norm_plan &p, int rows, int per) {
     const Deal d = deal_of(p.D, rows, per);
-    return ((size_t)d.blocks * 5 + (d.segs > 1 ? (size_t)d.groups * d.segs : 0)) * p.D * sizeof(float);
+    return ((size_t)d.blocks * 5 + (per > 1 && d.segs > 1 ? (size_t)d.groups * d.segs : 0)) * p.D * sizeof(float);
 }
 
 }  // namespace dw

@@ -46,6 +46,22 @@ __device__ __forceinline__ void store_f32(typename DT::X *p, const float (&in)[N
 
 __device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + __expf(-z)); }
 
+// v plus the value n lanes round in each row of 16 (one instruction).
+template <int N>
+__device__ __forceinline__ float add_ror(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + N, 0xf, 0xf, true));
+}
+// sum over each row of 16 lanes, in all of them
+__device__ __forceinline__ float sum_row16(float v) { return add_ror<1>(add_ror<2>(add_ror<4>(add_ror<8>(v)))); }
+// sum over the wavefront, in all lanes
+__device__ __forceinline__ float sum_wave(float v) {
+    const int x = __builtin_bit_cast(int, sum_row16(v));
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 64; i += 16) s += __builtin_bit_cast(float, __builtin_amdgcn_readlane(x, i));
+    return s;
+}
+
 // Packed sequences.  Wrong offsets are clamped, so that begin <= end lie in
 // [0, tokens] whatever the device array holds.
 struct Packed {
