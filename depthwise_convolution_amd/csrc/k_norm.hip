@@ -62,15 +62,15 @@ struct RowSum {
     }
 };
 
-__device__ __forceinline__ float gate_value(float g, int act) {
-    if (act == DWCONV_SEQ_ACT_NONE) return g;
-    const float p = sigmoid_f32(g);
-    return act == DWCONV_SEQ_ACT_SILU ? g * p : p;
+// act(g), and act'(g) in `slope`
+__device__ __forceinline__ float gate_value(float g, int act, float &slope) {
+    const float p = sigmoid_f32(g), q = p * (1.0f - p);
+    slope = act == DWCONV_SEQ_ACT_NONE ? 1.0f : act == DWCONV_SEQ_ACT_SILU ? __builtin_fmaf(g, q, p) : q;
+    return act == DWCONV_SEQ_ACT_NONE ? g : act == DWCONV_SEQ_ACT_SILU ? g * p : p;
 }
-__device__ __forceinline__ float gate_slope(float g, int act) {
-    if (act == DWCONV_SEQ_ACT_NONE) return 1.0f;
-    const float p = sigmoid_f32(g);
-    return act == DWCONV_SEQ_ACT_SILU ? p * (1.0f + g * (1.0f - p)) : p * (1.0f - p);
+__device__ __forceinline__ float gate_value(float g, int act) {
+    float slope;
+    return gate_value(g, act, slope);
 }
 
 // A lane's E channels: NV vectors of VEC, TPR vectors apart.  Vectors past D
@@ -288,6 +288,13 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
         if (wb) ln.fetch(ry, (const X *)gr.dy + at);
         if (pgate && !shared_gate) ln.fetch(rg, pgate + row / o.per * o.D);
     };
+    // act(gate) and its slope, of a row or of all rows of a shared gate
+    float a[E], slope[E];
+    auto gates = [&] {
+        ln.widen(a, rg);
+#pragma unroll
+        for (int i = 0; i < E; ++i) a[i] = gate_value(a[i], o.act, slope[i]);
+    };
     const int64_t first = deal.segs > 1 ? blockIdx.x / deal.segs : (int64_t)blockIdx.x * deal.chunk;
     const int seg = deal.segs > 1 ? blockIdx.x % deal.segs : 0;
     const int64_t last = first + deal.chunk < deal.groups ? first + deal.chunk : deal.groups;
@@ -300,16 +307,19 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
         for (int i = 0; i < E; ++i) gsum[i] = 0.0f;
         if (r0 < r1) {
             if (AHEAD) take(r0 + sub < r1 ? r0 + sub : r1 - 1);
-            if (shared_gate) ln.fetch(rg, pgate + grp * o.D);
+            if (shared_gate) {
+                ln.fetch(rg, pgate + grp * o.D);
+                gates();
+            }
         }
         for (int64_t base = r0; base < r1; base += RPB) {
             const bool live = base + sub < r1;
             const int64_t row = live ? base + sub : r1 - 1;
             const int64_t at = row * o.D;
-            float ua[E], t[E], h[E], d[E], dy[E], a[E];
+            float ua[E], t[E], h[E], d[E], dy[E];
             if (!AHEAD) take(row);
             ln.widen(ua, ro);
-            if (pgate) ln.widen(a, rg);
+            if (pgate && !shared_gate) gates();
 #pragma unroll
             for (int i = 0; i < E; ++i) d[i] = dy[i] = h[i] = 0.0f;
             if (gr.dh) ln.widen(d, rh);
@@ -332,12 +342,11 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
 #pragma unroll
                 for (int i = 0; i < E; ++i) t[i] += w[i];
             }
-            float slope[E];  // N_after(o) act'(gate)
+            float dgate[E];
             if (pgate) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    slope[i] = t[i] * gate_slope(a[i], o.act);
-                    a[i] = gate_value(a[i], o.act);
+                    dgate[i] = t[i] * slope[i];
                     t[i] *= a[i];
                 }
             }
@@ -379,11 +388,11 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
             if (pgate) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    slope[i] *= d[i];
+                    dgate[i] *= d[i];
                     d[i] *= a[i];
-                    if (live) gsum[i] += slope[i];
+                    if (live) gsum[i] += dgate[i];
                 }
-                if (!shared_gate && gr.dgate && live) ln.store((X *)gr.dgate + at, slope);
+                if (!shared_gate && gr.dgate && live) ln.store((X *)gr.dgate + at, dgate);
             }
             // through the norm after the block
             if (wa) {

@@ -44,7 +44,8 @@ __device__ __forceinline__ void store_f32(typename DT::X *p, const float (&in)[N
     *(Vec<typename DT::X, N> *)p = a;
 }
 
-__device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// off by a few units of 2^-24 (reciprocal: one, exp2 of a rounded product: |z|)
+__device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // v plus the value n lanes round in each row of 16 (one instruction).
 template <int N>
