@@ -406,14 +406,15 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
     X vn[NT][4];
     auto keys_of = [&](int k) { return c.keys + ((int64_t)(slot0 + k) * c.Hk + hk) * c.key_bytes; };
     auto head_of = [&](int k) { return c.heads + ((int64_t)(slot0 + k) * c.Hv + h) * c.head_bytes; };
-    auto fetch_rows = [&](int k) {  // what the first products need
+    // (fetches stand between the products, a few at a time: a wavefront that
+    // issues many at once waits for the load path, which its neighbours share)
+    auto fetch_row = [&](int k, int kb) {  // what the first products need
         const char *p = keys_of(k);
+        fetch(wK[kb], p + (NF + (wave * NK + kb) * NA) * FRAG, lane);
+        if (!SAVE) fetch(wQ[kb], p + (wave * NK + kb) * NA * FRAG, lane);
+    };
+    auto fetch_V = [&](int k) {
         fetch_tokens<X, NT>(vn, pv + (int64_t)k * CH * c.ldv, rv, b - a - k * CH, 16 * wave, g4, cl);
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) {
-            fetch(wK[kb], p + (NF + (wave * NK + kb) * NA) * FRAG, lane);
-            if (!SAVE) fetch(wQ[kb], p + (wave * NK + kb) * NA * FRAG, lane);
-        }
         const float *v = (const float *)(head_of(k) + AT_VEC * FRAG);
         ek = *(const f32x4 *)(v + V_EK * CH + row);
         beta = *(const f32x4 *)(v + V_BETA * CH + row);
@@ -425,13 +426,11 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
         if (wave >= 2) fetch(wT[1], p + (AT_T + lower_block(wave, 1) * T_TERMS) * FRAG, lane);
         rk = *(const f32x4 *)((const float *)(p + AT_VEC * FRAG) + V_RK * CH + row);
     };
-    auto fetch_KT = [&](int k) {
+    auto fetch_KT = [&](int k, int kb) {
         const char *p = keys_of(k) + 2 * NF * FRAG;
 #pragma unroll
-        for (int x = 0; x < T; ++x)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) fetch(wKT[x][kb], p + (2 * (wave * T + x) + kb) * NA * FRAG, lane);
-        el = ((const float *)(head_of(k) + AT_VEC * FRAG))[V_EB * CH + CH - 1];
+        for (int x = 0; x < T; ++x) fetch(wKT[x][kb], p + (2 * (wave * T + x) + kb) * NA * FRAG, lane);
+        if (kb) el = ((const float *)(head_of(k) + AT_VEC * FRAG))[V_EB * CH + CH - 1];
     };
     auto fetch_P = [&](int k) {
         const char *p = head_of(k);
@@ -439,9 +438,12 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
         if (wave >= 2) fetch(wP[1], p + (AT_P + lower_block(wave, 1) * P_TERMS) * FRAG, lane);
     };
     if (nc > 0) {
-        fetch_rows(0);
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) fetch_row(0, kb);
+        fetch_V(0);
         fetch_T(0);
-        fetch_KT(0);
+        fetch_KT(0, 0);
+        fetch_KT(0, 1);
         if (!SAVE) fetch_P(0);
         S.put(SB, wave, lane);
     }
@@ -462,6 +464,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
             fence();
             mac(wK[kb], s[kb & 1], 2, ks);
             if (!SAVE) mac(wQ[kb], s[kb & 1], 1, y);
+            fetch_row(next, kb);
             fence();
         }
 #pragma unroll
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
             RB.put(wave, t, beta * (widened<DT, NT>(vn, t, n, row, cl) - ek * ks[t]), lane);
             if (!SAVE) y[t] *= eq;
         }
-        fetch_rows(next);
+        fetch_V(next);
         __syncthreads();
         // U = T R
         RB.get(0, s[0], lane);
@@ -477,12 +480,13 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
         fence();
         mac(wT[0], s[0], 2, u);
         if (wave >= 2) mac(wT[1], s[1], 2, u);
+        const f32x4 rk_now = rk;
+        fetch_T(next);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            EB.put(wave, t, u[t] * rk, lane);
+            EB.put(wave, t, u[t] * rk_now, lane);
             if (!SAVE) UB.put(wave, t, u[t], lane);
         }
-        fetch_T(next);
         if (SAVE) keep_tokens<NT>(Us + at * CH * c.DvP, c, u, 16 * wave, g4, cl);
         __syncthreads();
         // S = e^{b_last} S + K^T (e^{b_last - b} U)
@@ -494,10 +498,11 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
 #pragma unroll
             for (int t = 0; t < NT; ++t) S.S[x][t] *= el;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int x = 0; x < T; ++x) mac(wKT[x][kb], s[kb], 2, S.S[x]);
-        fetch_KT(next);
+            fetch_KT(next, kb);
+        }
         S.put(SB, wave, lane);
         // O = scale e^b (Q S0) + P U
         if (!SAVE) {
@@ -547,10 +552,9 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
         fetch_tokens<X, NT>(dn, pd + (int64_t)k * CH * lddo, rd, b - a - k * CH, 16 * wave, g4, cl);
         eq = *(const f32x4 *)((const float *)(head_of(k) + AT_VEC * FRAG) + V_EQ * CH + row);
     };
-    auto fetch_rows = [&](int k) {
-        const char *p = keys_of(k) + NF * FRAG, *q = head_of(k);
-#pragma unroll
-        for (int kb = 0; kb < NK; ++kb) fetch(wK[kb], p + (wave * NK + kb) * NA * FRAG, lane);
+    auto fetch_row = [&](int k, int kb) { fetch(wK[kb], keys_of(k) + (NF + (wave * NK + kb) * NA) * FRAG, lane); };
+    auto fetch_P = [&](int k) {
+        const char *q = head_of(k);
         fetch(wPT[1], q + (AT_PT + upper_block(wave, 1) * T_TERMS) * FRAG, lane);
         if (wave < 2) fetch(wPT[0], q + (AT_PT + upper_block(wave, 0) * T_TERMS) * FRAG, lane);
         rk = *(const f32x4 *)((const float *)(q + AT_VEC * FRAG) + V_RK * CH + row);
@@ -563,14 +567,11 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
         beta = *(const f32x4 *)(v + V_BETA * CH + row);
         ek = *(const f32x4 *)(v + V_EK * CH + row);
     };
-    auto fetch_columns = [&](int k, bool q) {
+    auto fetch_columns = [&](int k, int kb, bool q) {
         const char *p = keys_of(k) + (q ? 3 : 2) * NF * FRAG;
 #pragma unroll
-        for (int x = 0; x < T; ++x)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
-                fetch(q ? wQT[x][kb] : wKT[x][kb], p + (2 * (wave * T + x) + kb) * NA * FRAG, lane);
-        if (q) el = ((const float *)(head_of(k) + AT_VEC * FRAG))[V_EB * CH + CH - 1];
+        for (int x = 0; x < T; ++x) fetch(q ? wQT[x][kb] : wKT[x][kb], p + (2 * (wave * T + x) + kb) * NA * FRAG, lane);
+        if (q && kb) el = ((const float *)(head_of(k) + AT_VEC * FRAG))[V_EB * CH + CH - 1];
     };
     // dO's terms (exact) and those of scale e^b dO, for all wavefronts
     auto put_tokens = [&](int k) {
@@ -583,10 +584,15 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
     };
     if (nc > 0) {
         fetch_tokens_of(nc - 1);
-        fetch_rows(nc - 1);
+#pragma unroll
+        for (int kb = 0; kb < NK; ++kb) fetch_row(nc - 1, kb);
+        fetch_P(nc - 1);
         fetch_T(nc - 1);
-        fetch_columns(nc - 1, true);
-        fetch_columns(nc - 1, false);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            fetch_columns(nc - 1, kb, true);
+            fetch_columns(nc - 1, kb, false);
+        }
         put_tokens(nc - 1);
         fetch_tokens_of(nc > 1 ? nc - 2 : 0);
         S.put(SB, wave, lane);
@@ -612,15 +618,16 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
             }
             fence();
             mac(wK[kb], s[kb & 1], 2, x);
+            fetch_row(next, kb);
             fence();
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) x[t] *= rk;
         mac(wPT[1], ot[1], 2, x);
         if (wave < 2) mac(wPT[0], ot[0], 2, x);
+        fetch_P(next);
 #pragma unroll
         for (int t = 0; t < NT; ++t) XB.put(wave, t, x[t], lane);
-        fetch_rows(next);
         __syncthreads();
         // dR = T^T dU, dV = beta dR; the part of dS that needs no dR
         XB.get(0, s[0], lane);
@@ -628,24 +635,26 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
         fence();
         mac(wTT[1], s[1], 2, dR);
         if (wave < 2) mac(wTT[0], s[0], 2, dR);
+        const f32x4 beta_now = beta, ek_now = ek;
+        fetch_T(next);
         QB.get(0, s[0], lane);
         QB.get(1, s[1], lane);
         fence();
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            y[t] = beta * dR[t];
-            ZB.put(wave, t, -ek * y[t], lane);
+            y[t] = beta_now * dR[t];
+            ZB.put(wave, t, -ek_now * y[t], lane);
         }
-        fetch_T(next);
 #pragma unroll
         for (int z = 0; z < T; ++z)
 #pragma unroll
             for (int t = 0; t < NT; ++t) S.S[z][t] *= el;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int z = 0; z < T; ++z) mac(wQT[z][kb], s[kb], 2, S.S[z]);
-        fetch_columns(next, true);
+            fetch_columns(next, kb, true);
+        }
         keep_tokens<NT>(dRs + at * CH * c.DvP, c, dR, 16 * wave, g4, cl);
         store_tokens<DT, NT>(pv + (int64_t)k * CH * lddv, rv, y, n, 16 * wave, g4, cl);
         __syncthreads();
@@ -654,10 +663,11 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
         ZB.get(1, s[1], lane);
         fence();
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+        for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
             for (int z = 0; z < T; ++z) mac(wKT[z][kb], s[kb], 2, S.S[z]);
-        fetch_columns(next, false);
+            fetch_columns(next, kb, false);
+        }
         S.put(SB, wave, lane);
         put_tokens(next);
         fetch_tokens_of(next > 0 ? next - 1 : 0);
