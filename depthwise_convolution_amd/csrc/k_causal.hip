@@ -168,6 +168,47 @@ __device__ __forceinline__ float silu_slope(float z) {
     return p * (1.0f + z * (1.0f - p));
 }
 
+// dstate_in: ext row e < K-1 gets shares from tokens 0 .. e, and is row e - L
+// of the state behind a sequence of L <= e tokens.
+template <class DT, int VEC, int K>
+__device__ __forceinline__ void state_gradient(const Geo &G, uint64_t i, const typename DT::X *x, int64_t ldx,
+                                               const typename DT::X *w, const float *bias,
+                                               const typename DT::X *state_in, const typename DT::X *dy, int64_t lddy,
+                                               const typename DT::X *dstate_out, typename DT::X *dstate_in, int silu) {
+    const Packed &P = G.seq;
+    const uint64_t row = i / G.ncv;
+    if (row >= (uint64_t)P.seqs * (K - 1)) return;
+    const int s = (int)(row / (K - 1)), e = (int)(row % (K - 1)), c = (int)(i % G.ncv) * VEC;
+    const int a = P.begin(s), L = P.end(s) - a;
+    const typename DT::X *st = state_in ? state_in + (int64_t)s * (K - 1) * G.C + c : nullptr;
+    float sum[VEC];
+    if (dstate_out && e >= L)
+        load_f32<DT, VEC>(sum, dstate_out + ((int64_t)s * (K - 1) + (e - L)) * G.C + c);
+    else
+        zero<DT, VEC>(sum);
+    for (int t = 0; t <= e && t < L; ++t) {
+        float win[K][VEC], z[VEC], d[VEC], wt[VEC];
+        fill_window<DT, VEC, K>(win, x + c, ldx, st, G.C, a, a + t);
+        load_f32<DT, VEC>(win[K - 1], x + c + (int64_t)(a + t) * ldx);
+        load_f32<DT, VEC>(d, dy + c + (int64_t)(a + t) * lddy);
+        if (silu) {
+            if (bias) load_f32<F32, VEC>(z, bias + c); else zero<DT, VEC>(z);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                load_f32<DT, VEC>(wt, w + (int64_t)k * G.C + c);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) z[j] = __builtin_fmaf(wt[j], win[k][j], z[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) d[j] *= silu_slope(z[j]);
+        }
+        load_f32<DT, VEC>(wt, w + (int64_t)(e - t) * G.C + c);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) sum[j] = __builtin_fmaf(wt[j], d[j], sum[j]);
+    }
+    store_f32<DT, VEC>(dstate_in + (int64_t)row * G.C + c, sum);
+}
+
 // dx, and this run's sums for dw and dbias.  Token t's dz = dy act'(z) goes to
 // the K rows of ext that z read; acc[k] holds the row K-1-k tokens back, which
 // is complete once token t has given its share.  The run continues K-1 tokens
@@ -177,9 +218,14 @@ __global__ void __launch_bounds__(256) k_bwd(Geo G, const typename DT::X *x, int
                                              const float *bias, const typename DT::X *state_in,
                                              const typename DT::X *dy, int64_t lddy,
                                              const typename DT::X *dstate_out, typename DT::X *dx, int64_t lddx,
-                                             float *part, int silu) {
+                                             typename DT::X *dstate_in, float *part, int silu) {
     using X = typename DT::X;
     const Packed &P = G.seq;
+    if (blockIdx.x >= G.main_blocks) {
+        state_gradient<DT, VEC, K>(G, (uint64_t)(blockIdx.x - G.main_blocks) * 256 + threadIdx.x, x, ldx, w, bias,
+                                   state_in, dy, lddy, dstate_out, dstate_in, silu);
+        return;
+    }
     const uint64_t idx = (uint64_t)xcd_remap(blockIdx.x, G.main_blocks) * 256 + threadIdx.x;
     const uint64_t tile = idx / G.ncv;
     const int c = (int)(idx % G.ncv) * VEC;
@@ -303,49 +349,6 @@ __global__ void __launch_bounds__(256) k_bwd(Geo G, const typename DT::X *x, int
     store_f32<F32, VEC>(o + (int64_t)K * G.C, gb);
 }
 
-// dstate_in: ext row e < K-1 gets shares from tokens 0 .. e, and is row e - L
-// of the state behind a sequence of L <= e tokens.
-template <class DT, int VEC, int K>
-__global__ void __launch_bounds__(256) k_dstate(Geo G, const typename DT::X *x, int64_t ldx,
-                                                const typename DT::X *w, const float *bias,
-                                                const typename DT::X *state_in, const typename DT::X *dy,
-                                                int64_t lddy, const typename DT::X *dstate_out,
-                                                typename DT::X *dstate_in, int silu) {
-    const Packed &P = G.seq;
-    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    const uint64_t row = i / G.ncv;
-    if (row >= (uint64_t)P.seqs * (K - 1)) return;
-    const int s = (int)(row / (K - 1)), e = (int)(row % (K - 1)), c = (int)(i % G.ncv) * VEC;
-    const int a = P.begin(s), L = P.end(s) - a;
-    const typename DT::X *st = state_in ? state_in + (int64_t)s * (K - 1) * G.C + c : nullptr;
-    float sum[VEC];
-    if (dstate_out && e >= L)
-        load_f32<DT, VEC>(sum, dstate_out + ((int64_t)s * (K - 1) + (e - L)) * G.C + c);
-    else
-        zero<DT, VEC>(sum);
-    for (int t = 0; t <= e && t < L; ++t) {
-        float win[K][VEC], z[VEC], d[VEC], wt[VEC];
-        fill_window<DT, VEC, K>(win, x + c, ldx, st, G.C, a, a + t);
-        load_f32<DT, VEC>(win[K - 1], x + c + (int64_t)(a + t) * ldx);
-        load_f32<DT, VEC>(d, dy + c + (int64_t)(a + t) * lddy);
-        if (silu) {
-            if (bias) load_f32<F32, VEC>(z, bias + c); else zero<DT, VEC>(z);
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                load_f32<DT, VEC>(wt, w + (int64_t)k * G.C + c);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) z[j] = __builtin_fmaf(wt[j], win[k][j], z[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) d[j] *= silu_slope(z[j]);
-        }
-        load_f32<DT, VEC>(wt, w + (int64_t)(e - t) * G.C + c);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] = __builtin_fmaf(wt[j], d[j], sum[j]);
-    }
-    store_f32<DT, VEC>(dstate_in + (int64_t)row * G.C + c, sum);
-}
-
 // Sum of the runs' rows: 64 columns a workgroup, four waves take every fourth
 // run and their sums are added in wave order.
 __global__ void __launch_bounds__(256) k_sum(const float *part, int64_t runs, int C, int K, float *dw, float *dbias) {
@@ -436,17 +439,12 @@ hipError_t bwd(const dwconv_causal_plan &p, const CausalArgs &a, hipStream_t st)
     const uint64_t tiles = ((uint64_t)a.tokens + G.TT - 1) / G.TT;
     const uint64_t blocks = blocks_of(tiles * G.ncv);
     const uint64_t sb = a.dstate_in ? blocks_of((uint64_t)a.seqs * (K - 1) * G.ncv) : 0;
-    if (too_many(blocks) || too_many(sb)) return hipErrorInvalidConfiguration;
+    if (too_many(blocks + sb)) return hipErrorInvalidConfiguration;
     G.main_blocks = (uint32_t)blocks;
-    if (blocks)
-        k_bwd<DT, VEC, K><<<G.main_blocks, 256, 0, st>>>(G, (const X *)a.x, a.ldx, (const X *)a.w, a.bias,
-                                                         (const X *)a.state_in, (const X *)a.dy, a.lddy,
-                                                         (const X *)a.dstate_out, (X *)a.dx, a.lddx, a.workspace,
-                                                         silu);
-    if (sb)
-        k_dstate<DT, VEC, K><<<(uint32_t)sb, 256, 0, st>>>(G, (const X *)a.x, a.ldx, (const X *)a.w, a.bias,
-                                                 (const X *)a.state_in, (const X *)a.dy, a.lddy,
-                                                 (const X *)a.dstate_out, (X *)a.dstate_in, silu);
+    if (blocks + sb)
+        k_bwd<DT, VEC, K><<<(uint32_t)(blocks + sb), 256, 0, st>>>(
+            G, (const X *)a.x, a.ldx, (const X *)a.w, a.bias, (const X *)a.state_in, (const X *)a.dy, a.lddy,
+            (const X *)a.dstate_out, (X *)a.dx, a.lddx, (X *)a.dstate_in, a.workspace, silu);
     const uint32_t cols = (uint32_t)(((uint64_t)(K + 1) * p.C + 63) / 64);
     k_sum<<<cols, 256, 0, st>>>(a.workspace, (int64_t)tiles, p.C, K, a.dw, a.dbias);
     return hipGetLastError();
