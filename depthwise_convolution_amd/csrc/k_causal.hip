@@ -14,7 +14,9 @@
 namespace dw {
 namespace {
 
-constexpr int U = 4;  // tokens in flight
+// Tokens in flight: single elements (rows that are not aligned) need more to
+// keep as many bytes on their way.
+__host__ __device__ constexpr int in_flight(int vec) { return vec == 1 ? 8 : 4; }
 
 struct Geo {
     Packed seq;
@@ -51,6 +53,7 @@ __global__ void __launch_bounds__(256) k_fwd(Geo G, const typename DT::X *x, int
                                              const float *bias, const typename DT::X *state_in,
                                              typename DT::X *state_out, typename DT::X *y, int64_t ldy, int silu) {
     using X = typename DT::X;
+    constexpr int U = in_flight(VEC);
     const Packed &P = G.seq;
     if (blockIdx.x >= G.main_blocks) {  // the last K-1 rows of every sequence
         const uint64_t i = (uint64_t)(blockIdx.x - G.main_blocks) * 256 + threadIdx.x;
@@ -220,6 +223,7 @@ __global__ void __launch_bounds__(256) k_bwd(Geo G, const typename DT::X *x, int
                                              const typename DT::X *dstate_out, typename DT::X *dx, int64_t lddx,
                                              typename DT::X *dstate_in, float *part, int silu) {
     using X = typename DT::X;
+    constexpr int U = in_flight(VEC);
     const Packed &P = G.seq;
     if (blockIdx.x >= G.main_blocks) {
         state_gradient<DT, VEC, K>(G, (uint64_t)(blockIdx.x - G.main_blocks) * 256 + threadIdx.x, x, ldx, w, bias,
