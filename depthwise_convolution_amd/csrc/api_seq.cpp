@@ -33,7 +33,11 @@ bool slots_ok(const int32_t *slots, int n_slots, int rows) {
     return rows >= 0 && n_slots >= 0 && at(slots, 4) && (slots || rows <= n_slots);
 }
 
-dwconv_status_t status(hipError_t e) { return e == hipSuccess ? DWCONV_OK : DWCONV_ERR_HIP; }
+// launchers say hipErrorInvalidConfiguration before a grid that passes its limit
+dwconv_status_t status(hipError_t e) {
+    return e == hipSuccess ? DWCONV_OK
+           : e == hipErrorInvalidConfiguration ? DWCONV_ERR_UNSUPPORTED : DWCONV_ERR_HIP;
+}
 
 template <class P>
 dwconv_status_t make(P **out, const P &v) {

@@ -36,8 +36,13 @@
 //
 // b is summed in 64 bits (a difference of two far sums would lose the small
 // exponents next to a reset); decays below e^-1000 are zero either way, so g
-// is cut there and -infinity needs no case of its own.  All products and sums
-// are fp32.
+// is cut there and -infinity needs no case of its own.
+//
+// The kernels of this file do all products on the fp32 matrix cores and serve
+// fp32 data; bf16 and fp16 data take the same steps in k_delta_split.hip and
+// k_delta_grad.hip.
+#include <type_traits>
+
 #include "delta_common.h"
 
 namespace dw {
@@ -651,6 +656,7 @@ bool rows_of(int n, const void *p, int64_t ld, int d) {
 template <class DT, int DK>
 hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hipStream_t st) {
     using X = typename DT::X;
+    if (a.seqs == 0) return hipSuccess;
     const Layout l = layout(p, a.seqs, a.tokens, backward);
     float *ws = (float *)a.workspace;
     Ctx c{};
@@ -665,59 +671,58 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
     c.T = ws + l.T, c.P = ws + l.P, c.vecs = ws + l.vecs;
     c.keys = (char *)(ws + l.keys), c.heads = (char *)(ws + l.heads), c.sums = (double *)(ws + l.sums);
     c.key_bytes = (int64_t)l.key_bytes, c.head_bytes = (int64_t)l.head_bytes;
-    const bool split = split_runs(p.dtype);
     const uint64_t chunks = (uint64_t)c.slots * p.Hk, walks = (uint64_t)a.seqs * p.Hv * ((p.Dv + 63) / 64);
-    // (the 16-bit walks have up to four workgroups for each of these)
-    if (chunks >= (1u << 24) || walks >= (1u << 22)) return hipErrorInvalidConfiguration;
-    const size_t keys = 2 * sizeof(float) * CH * (DK + 4);
-    auto lds = [](const void *f, size_t bytes) {
-        return hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    };
-    hipError_t e;
-    if (a.tokens > 0 && split) {
-        if ((e = split_prepare(p.dtype, DK, c, backward, st)) != hipSuccess) return e;
-    } else if (a.tokens > 0) {
-        const size_t n = keys + (TRI + 4 * 256) * sizeof(float);
-        if ((e = lds((const void *)k_prepare<DT, DK>, n)) != hipSuccess) return e;
-        k_prepare<DT, DK><<<(uint32_t)chunks, 256, n, st>>>(c);
-    }
-    if (walks == 0) return hipGetLastError();
-    if (!backward && split) return split_scan(p.dtype, DK, c, a.state_in, a.state_out, a.o, a.ldo, nullptr, nullptr, st);
-    if (!backward) {
-        if ((e = lds((const void *)k_scan<DT, DK, false>, sizeof(Stage<DK>))) != hipSuccess) return e;
-        k_scan<DT, DK, false><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, a.state_in, a.state_out, (X *)a.o,
-                                                                               a.ldo, nullptr, nullptr);
-        return hipGetLastError();
-    }
-    if (split) {
-        if (a.tokens > 0 && (e = split_scan(p.dtype, DK, c, a.state_in, nullptr, nullptr, 0, ws + l.S0s, ws + l.Us, st)) != hipSuccess)
+    // a grid holds fewer than 2^32 lanes (the 16-bit walks have up to four
+    // workgroups for each of these, and their grids are rounded up)
+    if (chunks >= (1u << 23) || walks >= (1u << 21)) return hipErrorInvalidConfiguration;
+    const int vec = std::is_same<DT, F32>::value ? 4 : 8;
+    const GradArgs ga{ws + l.S0s, ws + l.Us, ws + l.dSs, ws + l.dRs, a.d_o, a.lddo, a.dq, a.dk, a.lddq, a.lddk, a.dg,
+                      a.dbeta, rows_of<X>(vec, a.d_o, a.lddo, p.Dv), rows_of<X>(vec, a.v, a.ldv, p.Dv)};
+    hipError_t e = hipSuccess;
+    auto ok = [&](hipError_t x) { return (e = x) == hipSuccess; };
+    if constexpr (!std::is_same<DT, F32>::value) {
+        if (a.tokens > 0 && !ok(split_prepare(p.dtype, DK, c, backward, st))) return e;
+        if (!backward) return split_scan(p.dtype, DK, c, a.state_in, a.state_out, a.o, a.ldo, nullptr, nullptr, st);
+        if (a.tokens > 0 &&
+            !ok(split_scan(p.dtype, DK, c, a.state_in, nullptr, nullptr, 0, ws + l.S0s, ws + l.Us, st)))
             return e;
-    } else if (a.tokens > 0) {
-        if ((e = lds((const void *)k_scan<DT, DK, true>, sizeof(Stage<DK>))) != hipSuccess) return e;
-        k_scan<DT, DK, true><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, a.state_in, nullptr, (X *)nullptr, 0,
-                                                                              ws + l.S0s, ws + l.Us);
-    }
-    if (split) {
-        if ((e = split_rscan(p.dtype, DK, c, a.d_o, a.lddo, a.dstate_out, a.dstate_in, a.dv, a.lddv, ws + l.dSs,
-                             ws + l.dRs, st)) != hipSuccess)
+        if (!ok(split_rscan(p.dtype, DK, c, a.d_o, a.lddo, a.dstate_out, a.dstate_in, a.dv, a.lddv, ws + l.dSs,
+                            ws + l.dRs, st)))
             return e;
+        return a.tokens > 0 ? split_grad(p.dtype, DK, c, ga, st) : hipSuccess;
     } else {
-        if ((e = lds((const void *)k_rscan<DT, DK>, sizeof(Stage<DK>))) != hipSuccess) return e;
+        const size_t keys = 2 * sizeof(float) * CH * (DK + 4);
+        auto lds = [&](const void *f, size_t bytes) {
+            return ok(hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+        };
+        if (a.tokens > 0) {
+            const size_t n = keys + (TRI + 4 * 256) * sizeof(float);
+            if (!lds((const void *)k_prepare<DT, DK>, n)) return e;
+            k_prepare<DT, DK><<<(uint32_t)chunks, 256, n, st>>>(c);
+        }
+        if (!backward) {
+            if (!lds((const void *)k_scan<DT, DK, false>, sizeof(Stage<DK>))) return e;
+            k_scan<DT, DK, false><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, a.state_in, a.state_out,
+                                                                                   (X *)a.o, a.ldo, nullptr, nullptr);
+            return hipGetLastError();
+        }
+        if (a.tokens > 0) {
+            if (!lds((const void *)k_scan<DT, DK, true>, sizeof(Stage<DK>))) return e;
+            k_scan<DT, DK, true><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(
+                c, a.state_in, nullptr, (X *)nullptr, 0, ws + l.S0s, ws + l.Us);
+        }
+        if (!lds((const void *)k_rscan<DT, DK>, sizeof(Stage<DK>))) return e;
         k_rscan<DT, DK><<<(uint32_t)walks, 256, sizeof(Stage<DK>), st>>>(c, (const X *)a.d_o, a.lddo, a.dstate_out,
                                                                          a.dstate_in, (X *)a.dv, a.lddv, ws + l.dSs,
                                                                          ws + l.dRs);
+        if (a.tokens > 0) {
+            const size_t blocks = sizeof(float) * 36 * (2 * DK + CH), tiles = keys + 2 * TRI * sizeof(float);
+            const size_t n = blocks > tiles ? blocks : tiles;
+            if (!lds((const void *)k_grad<DT, DK>, n)) return e;
+            k_grad<DT, DK><<<(uint32_t)chunks, 256, n, st>>>(c, ga);
+        }
+        return hipGetLastError();
     }
-    if (a.tokens > 0) {
-        const int vec = split ? 8 : 4;
-        GradArgs ga{ws + l.S0s, ws + l.Us, ws + l.dSs, ws + l.dRs, a.d_o, a.lddo, a.dq, a.dk, a.lddq, a.lddk, a.dg,
-                    a.dbeta, rows_of<X>(vec, a.d_o, a.lddo, p.Dv), rows_of<X>(vec, a.v, a.ldv, p.Dv)};
-        if (split) return split_grad(p.dtype, DK, c, ga, st);
-        const size_t blocks = sizeof(float) * 36 * (2 * DK + CH), tiles = keys + 2 * TRI * sizeof(float);
-        const size_t n = blocks > tiles ? blocks : tiles;
-        if ((e = lds((const void *)k_grad<DT, DK>, n)) != hipSuccess) return e;
-        k_grad<DT, DK><<<(uint32_t)chunks, 256, n, st>>>(c, ga);
-    }
-    return hipGetLastError();
 }
 
 template <class DT>

@@ -484,7 +484,7 @@ int lanes_of(int D) { return D <= 128 ? 16 : D <= 512 ? 64 : D <= 2048 ? 256 : D
 Deal deal_of(int D, int rows, int per) {
     const int tpr = lanes_of(D), rpb = tpr >= 256 ? 1 : 256 / tpr, target = tpr > 256 ? 512 : 1024;
     Deal d{};
-    d.rows_in = per > 1 ? per : (rows > 0 ? rows : 1);
+    d.rows_in = per > 1 && per < rows ? per : (rows > 0 ? rows : 1);
     d.groups = ((int64_t)rows + d.rows_in - 1) / d.rows_in;
     d.chunk = 1;
     d.segs = 1;
@@ -494,8 +494,8 @@ Deal deal_of(int D, int rows, int per) {
         const int64_t want = (target + d.groups - 1) / d.groups, most = ((int64_t)d.rows_in + 4 * rpb - 1) / (4 * rpb);
         d.segs = (int)(want < most ? want : most);
     }
-    d.seg_rows = (d.rows_in + d.segs - 1) / d.segs;
-    d.segs = (d.rows_in + d.seg_rows - 1) / d.seg_rows;
+    d.seg_rows = (int)(((int64_t)d.rows_in + d.segs - 1) / d.segs);
+    d.segs = (int)(((int64_t)d.rows_in + d.seg_rows - 1) / d.seg_rows);
     d.blocks = (uint32_t)(d.segs > 1 ? d.groups * d.segs : (d.groups + d.chunk - 1) / d.chunk);
     return d;
 }

@@ -12,8 +12,8 @@
  * Tokens of several sequences lie one behind the other.  `offsets` holds
  * seqs + 1 int32 device values: sequence s is tokens offsets[s] ..
  * offsets[s+1]-1; they rise, start at 0 and end at or below `tokens`.  A
- * sequence may be empty.  Tokens behind the last sequence are neither read
- * nor are their outputs written.  offsets == NULL: one sequence of all tokens
+ * sequence may be empty.  What tokens behind the last sequence hold does not
+ * matter, and their outputs are left as they were.  offsets == NULL: one sequence of all tokens
  * (seqs must be 1).  The offsets are device data that the host does not see:
  * the kernels clamp them to [0, tokens], so wrong ones give wrong results but
  * no access out of bounds.
@@ -33,6 +33,11 @@
  * current device, as do all pointers.  Outputs must not overlap inputs unless
  * stated.  Every sum is formed in a fixed order without atomics: the same call
  * gives the same bits.
+ *
+ * A call whose grid would pass 2^32 lanes returns DWCONV_ERR_UNSUPPORTED: for
+ * the delta rule 2^29 tokens x key heads or 2^21 sequences x value heads x 64
+ * columns of the state, for a step 2^24 rows x value heads or x 256 vectors of
+ * channels.
  *
  * float (fp32) everywhere: biases, scales, norm weights, decays, write
  * strengths, matrix states and the gradients of all of these.  Sums and
@@ -156,7 +161,8 @@ dwconv_status_t dwconv_delta_step(dwconv_delta_t h, const void *q, int64_t ldq, 
                                   int rows, void *o, int64_t ldo, hipStream_t stream);
 
 /* Gradients for d_o (as o) and dstate_out (as state_out; NULL: zeros) of the
- * forward pass from the same inputs (its intermediates are computed again):
+ * forward pass from the same inputs (its intermediates are computed again);
+ * dstate_in may be dstate_out itself:
  * dq, dk, dv (as q, k, v, token strides lddq, lddk, lddv; a shared key head's
  * gradient is the sum over its value heads), dg and dbeta (as g, beta) and
  * dstate_in (as state_in) or NULL. */

@@ -88,6 +88,8 @@ CONV = [  # fmt, C, K, lens, act, state, extra channels of a wider token, offset
     ("f16", 64, 6, [130], "silu", False, 5, 3),
     ("f32", 1024, 4, [300, 1, 2, 3, 400], "silu", True, 0, 0),
     ("bf16", 1, 7, [40, 6], "silu", True, 0, 0),
+    ("f16", 72, 4, [1, 2, 0, 3, 1] * 40, "silu", True, 0, 0),
+    ("bf16", 8, 3, [5000], "silu", False, 0, 0),
 ]
 
 
@@ -262,8 +264,14 @@ DELTA = [  # fmt, Hk, Hv, Dk, Dv, lens, state, gates, normalize
     ("bf16", 3, 3, 64, 1, [128, 129], False, "mixed", True),
     ("f32", 1, 1, 1, 2, [70], True, "plain", False),
     ("f16", 2, 2, 64, 48, [80, 5], True, "plain", False),
+    ("bf16", 1, 6, 64, 40, [65, 2], True, "mixed", True),      # more value heads than wavefronts
+    ("f32", 1, 5, 40, 24, [67], True, "mixed", True),
+    ("bf16", 2, 18, 32, 20, [130], False, "plain", True),
+    ("f16", 1, 2, 130, 300, [64, 64], True, "mixed", True),
+    ("bf16", 1, 2, 24, 33, [1, 2, 0, 3] * 12, True, "mixed", True),
+    ("f32", 1, 1, 256, 70, [65], True, "plain", True),
 ]
-IDS = [f"{c[0]}-{c[1]}x{c[2]}-{c[3]}x{c[4]}-{'+'.join(map(str, c[5]))}" for c in DELTA]
+IDS = [f"{c[0]}-{c[1]}x{c[2]}-{c[3]}x{c[4]}-{'+'.join(map(str, c[5][:4]))}" for c in DELTA]
 
 
 def delta_check(got, want, half, n, size, what, chain=1):
@@ -600,6 +608,91 @@ def test_norm_rows_of_zeros_and_infinities():
     ok = torch.tensor([0, 1, 2, 4, 5], device=DEV)
     assert torch.isfinite(h[ok]).all() and torch.isfinite(y[ok]).all() and (h[0] == 0).all() and (y[2] == 0).all()
     assert torch.isnan(h[3]).any()
+
+
+@pytest.mark.parametrize("fmt", ["f32", "f16", "bf16"])
+def test_norm_of_unaligned_rows_and_large_gate_groups(fmt):
+    """Dense tensors that begin one element into their storage give the bits of
+    aligned ones where the sums are formed alike (single elements against
+    vectors: the same lanes hold other channels, so within rounding), and a gate
+    row may serve more rows than there are."""
+    D, rows = 192, 50
+    case = (fmt, rows, D, "layer", "rms", "silu", 2 ** 31 - 1, True, True)
+    d = norm_data(case)
+    plan = dw.BlockNorm(D, fmt, after="layer", before="rms")
+    dy = rand(rows, D, seed=3, dtype=fmt)
+
+    def shifted(t):
+        if t is None:
+            return None
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        buf[1:] = t.reshape(-1).to(DEV)
+        return buf[1:].view(t.shape)
+
+    out = []
+    for move in (up, shifted):
+        args = {n: move(d[n]) for n in PARAMS}
+        h, y = plan(move(d["o"]), rows_per_gate=2 ** 31 - 1, **args)
+        g = plan.backward(move(d["o"]), move(dy), move(dy), rows_per_gate=2 ** 31 - 1, **args)
+        out.append([h, y] + list(g))
+    for a, b in zip(*out):
+        assert (a is None) == (b is None)
+        if a is not None:
+            assert rel(a.cpu(), b.double().cpu()) <= 2 * HALF[a.dtype] + 1e-5
+
+
+def test_no_sequences():
+    """Offsets of no sequence at all: nothing is written but sums of nothing."""
+    off = torch.zeros(1, dtype=torch.int32, device=DEV)
+    T, C = 130, 32
+    x, w, b, _ = (up(t) for t in conv_data("bf16", C, 4, [T], False))
+    conv = dw.CausalDepthwiseConv1d(C, 4, "bf16")
+    y = torch.full((T, C), 7.0, dtype=torch.bfloat16, device=DEV)
+    conv(x, w, b, offsets=off, y=y)
+    dx, dw_, db, _ = conv.backward(x, w, x, b, offsets=off, dx=y)
+    assert (y == 7.0).all() and not dw_.any() and not db.any()
+    for fmt in ("f32", "bf16"):
+        q, k, v, g, beta, _ = (up(t) for t in delta_data(fmt, 1, 2, 32, 32, [T], False))
+        rule = dw.GatedDeltaRule(1, 2, 32, 32, fmt)
+        o = torch.full((T, 2, 32), 7.0, dtype=v.dtype, device=DEV)
+        rule(q, k, v, g, beta, offsets=off, o=o)
+        rule.backward(q, k, v, g, beta, v, offsets=off, dv=o)
+        assert (o == 7.0).all()
+
+
+@pytest.mark.parametrize("fmt,Dk,Dv", [("bf16", 128, 64), ("f16", 64, 64), ("f32", 64, 64)])
+def test_long_sequence_in_pieces(fmt, Dk, Dv):
+    """A long sequence in one call and in three with the state carried over, at
+    borders that no chunk ends on: the same values within fp32 rounding."""
+    T, cuts = 6001, [0, 1234, 1235, 6001]
+    q, k, v, g, beta, s = (up(t) for t in delta_data(fmt, 1, 2, Dk, Dv, [T], True, gates="plain"))
+    g *= 0.05  # slow decay: the state carries far
+    rule = dw.GatedDeltaRule(1, 2, Dk, Dv, fmt)
+    end, state = torch.empty_like(s), s.clone()
+    whole = rule(q, k, v, g, beta, state_in=s, state_out=end)
+    parts = [rule(*(t[a:b] for t in (q, k, v, g, beta)), state_in=state, state_out=state) for a, b in zip(cuts, cuts[1:])]
+    tol = 24 * math.sqrt(Dk + 64) * U
+    assert rel(torch.cat(parts).cpu(), whole.double().cpu()) <= 2 * HALF[v.dtype] + tol
+    assert rel(state.cpu(), end.double().cpu()) <= tol
+
+
+def test_two_streams_at_once():
+    """One plan on two streams, a workspace for each call."""
+    rule = dw.GatedDeltaRule(2, 4, 64, 64, "bf16")
+    sets = [[up(t) for t in delta_data("bf16", 2, 4, 64, 64, [300, 77], True, seed=s)] for s in (0, 100)]
+    off = offsets_of([300, 77])
+    do = up(rand(377, 4, 64, seed=5, dtype="bf16"))
+    want = [rule.backward(*t[:5], do, offsets=off, state_in=t[5]) for t in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = []
+        for st, t in zip(streams, sets):
+            st.wait_stream(torch.cuda.current_stream())
+            got.append(rule.backward(*t[:5], do, offsets=off, state_in=t[5], stream=st))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 # ---------------------------------------------------------------------------

@@ -242,3 +242,23 @@ def test_workspaces_cover_every_partition():
                     assert n % (4 * D) == 0 and (n > 0) == (rows > 0)
         finally:
             dw.dwconv_norm_destroy(p)
+
+
+def test_grids_past_their_limit_are_unsupported():
+    """Refused before anything is launched, whatever the pointers."""
+    P = [PTR + (i << 16) for i in range(12)]
+
+    def unsupported(call, *args):
+        with pytest.raises(dw.DwconvError) as e:
+            call(*args)
+        assert e.value.status == 2
+
+    h = dw.dwconv_causal_create(8, 4, "bf16", "silu")
+    unsupported(dw.dwconv_causal_step, h, P[0], 8, P[1], None, P[2], P[3], 5, 1 << 24, P[4], 8, None)
+    dw.dwconv_causal_destroy(h)
+    h = dw.dwconv_delta_create(1, 64, 8, 8, "bf16", 1.0, True, 1e-6)
+    unsupported(dw.dwconv_delta_step, h, P[0], 8, P[1], 8, P[2], 512, P[3], P[4], P[5], P[6], 5, 1 << 18, P[7], 512,
+                None)
+    unsupported(dw.dwconv_delta_fwd, h, P[0], 8, P[1], 8, P[2], 512, P[3], P[4], P[5], 1 << 16, 64, None, None, P[6],
+                512, P[7], None)
+    dw.dwconv_delta_destroy(h)
