@@ -161,11 +161,10 @@ dwconv_status_t dwconv_delta_step(dwconv_delta_t h, const void *q, int64_t ldq, 
                                   int rows, void *o, int64_t ldo, hipStream_t stream);
 
 /* Gradients for d_o (as o) and dstate_out (as state_out; NULL: zeros) of the
- * forward pass from the same inputs (its intermediates are computed again);
- * dstate_in may be dstate_out itself:
+ * forward pass from the same inputs (its intermediates are computed again):
  * dq, dk, dv (as q, k, v, token strides lddq, lddk, lddv; a shared key head's
  * gradient is the sum over its value heads), dg and dbeta (as g, beta) and
- * dstate_in (as state_in) or NULL. */
+ * dstate_in (as state_in; it may be dstate_out itself) or NULL. */
 dwconv_status_t dwconv_delta_bwd(dwconv_delta_t h, const void *q, int64_t ldq, const void *k,
                                  int64_t ldk, const void *v, int64_t ldv, const float *g,
                                  const float *beta, const int32_t *offsets, int seqs, int tokens,
