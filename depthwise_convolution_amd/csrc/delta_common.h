@@ -119,15 +119,27 @@ __device__ __forceinline__ double running_sum(const float *g, int Hv, int n, int
 // Column `wave` of T = (1 + A)^-1, tiles wave .. 3, from A's lower tiles in LDS
 // (four wavefronts; Td: room for the diagonal tiles' inverses).
 __device__ __forceinline__ void invert(const float *At, float *Td, int wave, int r, int g4, f32x4 (&Tc)[4]) {
-    // wave w inverts diagonal tile w: a lane solves one column downwards
+    // wave w inverts diagonal tile w: a lane solves one column downwards, two
+    // rows of the tile read at a time (and no more: registers)
     const float *a = At + tri(wave, wave);
     float x[16];
+    x[0] = r == 0 ? 1.0f : 0.0f;
+    x[1] = __builtin_fmaf(-a[16], x[0], r == 1 ? 1.0f : 0.0f);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float s = i == r ? 1.0f : 0.0f;
+    for (int b = 2; b < 16; b += 2) {
+        f32x4 v[2][4];
+        asm volatile("" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < i; ++j) s = __builtin_fmaf(-a[i * 16 + j], x[j], s);
-        x[i] = s;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j <= b / 4; ++j) v[i][j] = *(const f32x4 *)(a + (b + i) * 16 + 4 * j);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float s = b + i == r ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < b + i; ++j) s = __builtin_fmaf(-v[i][j / 4][j % 4], x[j], s);
+            x[b + i] = s;
+        }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -94,9 +94,8 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
     const Chunk found = chunk_of(c.seq, slot);
     const int n = uniform(found.n), tok = uniform(found.tok);
     if (n == 0) return;
-    const int lane = threadIdx.x & 63, wave8 = uniform(threadIdx.x >> 6), wave = wave8 & 3, half = wave8 >> 2, t0 = half * NH, r = lane & 15, g4 = (lane >> 4) * 4, g8 = 2 * g4;
-    const int row = 16 * wave + g4;      // result layout: tokens row .. row + 3
-    const int mine = 16 * wave + r;      // left operands: the lane's token
+    const int lane = threadIdx.x & 63, wave8 = uniform(threadIdx.x >> 6), wave = wave8 & 3, half = wave8 >> 2, t0 = half * NH, r = lane & 15, g4 = (lane >> 4) * 4;
+    const int row = 16 * wave + g4;  // result layout: tokens row .. row + 3
     float *ET = (float *)(L + wave * WAVE_TILES), *MT = ET + 4 * 16 * PITCH;
     const Right<4, 3> ER{L + 4 * WAVE_TILES}, MR{ER.p + ER.bytes(2)};
     const char *keys = c.keys + ((int64_t)slot * c.Hk + hk) * c.key_bytes;
@@ -133,6 +132,12 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
         for (int j = 0; j < 4; ++j) KQ[j * 64] = kq[j] * nr * nky[j];
     }
     for (int h = hk * group; h < (hk + 1) * group; ++h) {
+        // made anew for each head: kept over the loop, the addresses that follow
+        // from these would take a third of the registers
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int r = lane & 15, g4 = (lane >> 4) * 4, g8 = 2 * g4, row = 16 * wave + g4;
+        const int mine = 16 * wave + r;  // left operands: the lane's token
         const int64_t at = (int64_t)slot * c.Hv + h;
         f32x4 X1[NH], X2[NH], X3[NH], dD[4];  // dD: tiles of dP (first half) or -dA
 #pragma unroll

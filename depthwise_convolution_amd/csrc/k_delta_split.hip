@@ -138,6 +138,11 @@ __global__ void __launch_bounds__(256, (DK <= 128 ? 3 : 2)) k_prepare(Ctx c) {
     }
     const int group = c.Hv / c.Hk, h0 = hk * group;
     for (int n = 0; n < group; ++n) {
+        // made anew for each head: kept over the loop, the addresses and
+        // comparisons that follow from these would take the registers
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int r = lane & 15, g4 = (lane >> 4) * 4;
         const int h = h0 + n;
         const int64_t at = (int64_t)slot * c.Hv + h;
         char *base = c.heads + at * c.head_bytes;
