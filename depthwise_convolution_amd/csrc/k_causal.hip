@@ -380,10 +380,15 @@ __global__ void __launch_bounds__(256) k_sum(const float *part, int64_t runs, in
 
 // Tokens a lane walks: long runs spend less on the rows around them (and on
 // the run's sums in the backward pass); short ones give the chip enough waves.
-int run_tokens(int tokens, int C, int vec) {
+// bf16, K = 4, runs of 8 and of 64 tokens: forward 128 and 122 us at 16384
+// tokens x 8192 channels, 12 and 33 us at 4096 x 2048; backward with its sums
+// 200 and 102 us at 8192 x 8192, 35 and 62 us at 4096 x 2048.  The backward
+// pass, which writes sums for every run, stops at half the lanes (4096 x 2048,
+// runs of 8, 16 and 32 tokens: 35, 31 and 39 us; forward 12, 13 and 20 us).
+int run_tokens(int tokens, int C, int vec, bool back) {
     int tt = 64;
-    const int64_t ncv = (C + vec - 1) / vec;
-    while (tt > 8 && (int64_t)((tokens + tt - 1) / tt) * ncv < 131072) tt /= 2;
+    const int64_t ncv = (C + vec - 1) / vec, lanes = back ? 65536 : 131072;
+    while (tt > 8 && (int64_t)((tokens + tt - 1) / tt) * ncv < lanes) tt /= 2;
     return tt;
 }
 
@@ -408,7 +413,7 @@ bool too_many(uint64_t blocks) { return blocks >= (1u << 24); }
 template <class DT, int VEC, int K>
 hipError_t fwd(const dwconv_causal_plan &p, const CausalArgs &a, hipStream_t st) {
     using X = typename DT::X;
-    Geo G{{a.offsets, a.seqs, a.tokens}, p.C, run_tokens(a.tokens, p.C, VEC), (uint32_t)(p.C / VEC), 0};
+    Geo G{{a.offsets, a.seqs, a.tokens}, p.C, run_tokens(a.tokens, p.C, VEC, false), (uint32_t)(p.C / VEC), 0};
     const uint64_t tiles = ((uint64_t)a.tokens + G.TT - 1) / G.TT;
     const uint64_t blocks = blocks_of(tiles * G.ncv);
     const uint64_t extra = a.state_out ? blocks_of((uint64_t)a.seqs * (K - 1) * G.ncv) : 0;
@@ -439,7 +444,7 @@ hipError_t bwd(const dwconv_causal_plan &p, const CausalArgs &a, hipStream_t st)
     const int silu = p.act == DWCONV_SEQ_ACT_SILU;
     // the run length of the widest vectors, whatever width runs: the
     // workspace's size does not depend on alignment
-    Geo G{{a.offsets, a.seqs, a.tokens}, p.C, run_tokens(a.tokens, p.C, vec_of(p)), (uint32_t)(p.C / VEC), 0};
+    Geo G{{a.offsets, a.seqs, a.tokens}, p.C, run_tokens(a.tokens, p.C, vec_of(p), true), (uint32_t)(p.C / VEC), 0};
     const uint64_t tiles = ((uint64_t)a.tokens + G.TT - 1) / G.TT;
     const uint64_t blocks = blocks_of(tiles * G.ncv);
     const uint64_t sb = a.dstate_in ? blocks_of((uint64_t)a.seqs * (K - 1) * G.ncv) : 0;
@@ -503,7 +508,7 @@ hipError_t causal_step(const dwconv_causal_plan &p, const CausalArgs &a, hipStre
 hipError_t causal_bwd(const dwconv_causal_plan &p, const CausalArgs &a, hipStream_t st) { return pick(BWD, p, a, st); }
 
 size_t causal_bwd_bytes(const dwconv_causal_plan &p, int tokens) {
-    const int tt = run_tokens(tokens, p.C, vec_of(p));
+    const int tt = run_tokens(tokens, p.C, vec_of(p), true);
     return ((size_t)tokens + tt - 1) / tt * (size_t)(p.K + 1) * p.C * sizeof(float);
 }
 

@@ -680,9 +680,11 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
     if (dstate_in) S.store(dstate_in + st, c, wave, g4, cl);
 }
 
-// Columns of the state a workgroup walks: 32, or 16 where that leaves CUs
-// without a walk.
-int walk_tiles(const Ctx &c) { return (int64_t)c.seq.seqs * c.Hv * ((c.Dv + 31) / 32) < 256 ? 1 : 2; }
+// Columns of the state a workgroup walks: 32, or 16 where a CU would have no
+// second walk to fill its waits.  8192 bf16 tokens, 32 heads of 128 x 128, k_scan
+// with 16 columns against 32: one sequence (128 walks of 32 columns) 273 and
+// 369 us, two 216 and 238, three 229 and 200, five 234 and 197.
+int walk_tiles(const Ctx &c) { return (int64_t)c.seq.seqs * c.Hv * ((c.Dv + 31) / 32) <= 256 ? 1 : 2; }
 
 template <int NT>
 size_t lds_scan(int DK) { return (size_t)(DK / 32 + 2 + 2) * NT * 3 * FRAG + (size_t)2 * NT * 2 * FRAG; }
