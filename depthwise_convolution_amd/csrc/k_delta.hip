@@ -41,6 +41,11 @@
 // The kernels of this file do all products on the fp32 matrix cores and serve
 // fp32 data; bf16 and fp16 data take the same steps in k_delta_split.hip and
 // k_delta_grad.hip.
+//
+// Bound by fp32 matrix products (the walks: one wavefront's chain of them).
+// Measured, fp32, heads of 128 x 128: 8192 tokens, 16 key and 32 value heads,
+// five sequences: k_prepare 169 us, k_scan 658; gradients of 4096 tokens, 8 and
+// 16 heads, four sequences: k_prepare 57, k_scan 225, k_rscan 300, k_grad 418.
 #include <type_traits>
 
 #include "delta_common.h"

@@ -6,16 +6,21 @@
 // the other and their shares of dQ and dK add up in registers.  Wavefronts w
 // and w + 4 have tokens 16 w .. 16 w + 15, the first half of the channels of q
 // and k and the second (one wavefront's sums for all channels need more
-// registers than two wavefronts on a SIMD have).  Per value head, first the sums over the state's
-// columns, 32 at a time: the rows of S0 and dS, split into terms by one
-// wavefront each, and U pass through LDS; dO, dR and U rows are left operands
-// that a lane loads as they lie.  Then the sums over tokens: E and M = beta dA D
-// go through LDS once as left operands by rows and once, in terms, by columns;
-// their right operands are the fragments of K^T and Q^T in the workspace, which
-// also hold a lane's own elements of k and q in the result layout.
+// registers than two wavefronts on a SIMD have).  Per value head, first the
+// sums over the state's columns, 32 at a time: the rows of S0 and dS, split into
+// terms by one wavefront each, and U pass through LDS; dO, dR and U rows are
+// left operands that a lane loads as they lie.  Then the sums over tokens: E and
+// M = beta dA D go through LDS once as left operands by rows and once, in terms,
+// by columns; their right operands are the fragments of K^T and Q^T in the
+// workspace, which also hold a lane's own elements of k and q in the result
+// layout.
 //
-// Bound: 2900 products of 16x16x32 a head and chunk at Dk = Dv = 128 (11.6
-// thousand cycles of a CU) against 128 KB of states read.
+// 2900 products of 16x16x32 a head and chunk at Dk = Dv = 128 (11.6 thousand
+// cycles of a CU) against 128 KB of states read.  Measured, bf16, 4096 tokens in
+// four sequences, 8 key and 16 value heads: 164 us, some 65 thousand cycles a head
+// and chunk: bound by waits for loads and barriers with two wavefronts a SIMD,
+// and by whole rounds of workgroups, one a CU (here 528: one sequence's 512 take
+// 114 us, 520 take 153, 768 take 166).
 #include "delta_split.h"
 
 namespace dw {
@@ -131,12 +136,44 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) KQ[j * 64] = kq[j] * nr * nky[j];
     }
+    // Operands of a head's next 32 columns.  The next head's first ones are on their
+    // way while the sums over tokens run (167 -> 164 us at the sizes above), where there
+    // are registers for it: keys of more than 128 channels would spill.
+    constexpr bool AHEAD = T == 1;
+    f32x4 s0[T][2], ds[T][2], ud[2];  // ud: U (first half) or dR
+    u32x4 od, vv;
+    auto ahead = [&](int h, int col) {
+        const int64_t at = (int64_t)slot * c.Hv + h;
+        int lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        const int r = lane & 15, g8 = (lane >> 4) * 8, mine = 16 * wave + r;
+        const uint32_t off = r * c.DvP + g8;
+#pragma unroll
+        for (int x = 0; x < T; ++x) {
+            const int y = min(wave8 + 8 * x, NT - 1);  // (4 and 12 tiles leave wavefronts without one)
+            const int64_t p = (at * DK + 16 * y) * c.DvP + col;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                s0[x][j] = *(const f32x4 *)(ga.S0s + p + off + 4 * j);
+                ds[x][j] = *(const f32x4 *)(ga.dSs + p + off + 4 * j);
+            }
+        }
+        const int64_t p = (at * CH + 16 * wave) * c.DvP + col;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            ud[j] = *(const f32x4 *)((half ? ga.dRs : ga.Us) + p + off + 4 * j);
+        }
+        const int x = col + g8, token = tok + min(mine, n - 1), valid = mine < n ? c.Dv - x : 0;
+        od = load8((const X *)ga.d_o + token * ga.lddo + (int64_t)h * c.Dv + x, valid, ga.vec_o);
+        vv = load8((const X *)c.v + token * c.ldv + (int64_t)h * c.Dv + x, valid, ga.vec_v);
+    };
+    if (AHEAD) ahead(hk * group, 0);
     for (int h = hk * group; h < (hk + 1) * group; ++h) {
         // made anew for each head: kept over the loop, the addresses that follow
         // from these would take a third of the registers
         int lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
-        const int r = lane & 15, g4 = (lane >> 4) * 4, g8 = 2 * g4, row = 16 * wave + g4;
+        const int r = lane & 15, g4 = (lane >> 4) * 4, row = 16 * wave + g4;
         const int mine = 16 * wave + r;  // left operands: the lane's token
         const int64_t at = (int64_t)slot * c.Hv + h;
         f32x4 X1[NH], X2[NH], X3[NH], dD[4];  // dD: tiles of dP (first half) or -dA
@@ -146,30 +183,7 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
         for (int j = 0; j < 4; ++j) dD[j] = splat(0.0f);
         float rv = 0.0f, sd = 0.0f;  // dR . V of token `mine`; <S0, dS>
         // ---- sums over the state's columns
-        f32x4 s0[T][2], ds[T][2], ud[2];  // ud: U (first half) or dR
-        u32x4 od, vv;
-        auto ahead = [&](int col) {
-            const uint32_t off = r * c.DvP + g8;
-#pragma unroll
-            for (int x = 0; x < T; ++x) {
-                const int y = min(wave8 + 8 * x, NT - 1);  // (4 and 12 tiles leave wavefronts without one)
-                const int64_t p = (at * DK + 16 * y) * c.DvP + col;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    s0[x][j] = *(const f32x4 *)(ga.S0s + p + off + 4 * j);
-                    ds[x][j] = *(const f32x4 *)(ga.dSs + p + off + 4 * j);
-                }
-            }
-            const int64_t p = (at * CH + 16 * wave) * c.DvP + col;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ud[j] = *(const f32x4 *)((half ? ga.dRs : ga.Us) + p + off + 4 * j);
-            }
-            const int x = col + g8, token = tok + min(mine, n - 1), valid = mine < n ? c.Dv - x : 0;
-            od = load8((const X *)ga.d_o + token * ga.lddo + (int64_t)h * c.Dv + x, valid, ga.vec_o);
-            vv = load8((const X *)c.v + token * c.ldv + (int64_t)h * c.Dv + x, valid, ga.vec_v);
-        };
-        ahead(0);
+        if (!AHEAD) ahead(h, 0);
         for (int col = 0; col < c.DvP; col += 32) {
             __syncthreads();
             bf16x8 ot[NA], ut[3], rt[3];
@@ -192,7 +206,7 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sd = __builtin_fmaf(s0[x][j / 4][j % 4], ds[x][j / 4][j % 4], sd);
             }
-            if (col + 32 < c.DvP) ahead(col + 32);
+            if (col + 32 < c.DvP) ahead(h, col + 32);
             __syncthreads();
             get_frag(ut, UF + wave * 3 * FRAG, lane);
             get_frag(rt, RF + wave * 3 * FRAG, lane);
@@ -247,6 +261,7 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
         for (int m = 1; m < 64; m <<= 1) sd += __shfl_xor(sd, m, 64);
         rv += __shfl_xor(rv, 16, 64);
         rv += __shfl_xor(rv, 32, 64);
+        if (AHEAD && h + 1 < (hk + 1) * group) ahead(h + 1, 0);
         __syncthreads();  // the blocks have been read: tiles take their place
         if (lane == 0) dots[wave8] = sd;
         if (half && lane < 16) rvs[mine] = rv;

