@@ -336,6 +336,20 @@ def test_delta_backward(case):
         assert ds is None
 
 
+# Heads x sequences x columns enough for the walks of 32 columns (more than 256 of
+# them), at every padded key size; the last walk of a head has few columns.
+MANY = [(fmt, 1, 3, Dk, 70, [1, 66, 0, 130, 64] * 6, True, gates, True)
+        for fmt, Dk, gates in [("bf16", 40, "mixed"), ("bf16", 128, "plain"), ("bf16", 192, "mixed"), ("bf16", 250, "plain"),
+                               ("f16", 64, "plain"), ("f16", 100, "mixed"), ("f16", 130, "plain"), ("f16", 256, "mixed")]]
+MANY += [("bf16", 2, 8, 96, 33, [65] * 17, False, "mixed", True), ("f32", 1, 3, 72, 70, [1, 66, 0, 130] * 6, True, "mixed", True)]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"{c[0]}-{c[1]}x{c[2]}-{c[3]}x{c[4]}-{len(c[5])}")
+def test_delta_of_many_sequences(case):
+    test_delta_forward(case)
+    test_delta_backward(case)
+
+
 def test_delta_gradient_matches_differences():
     """The kernels' gradient along a direction against their own forward
     pass's differences (fp32: a step of 2^-8 leaves about 2^-16 of curvature
