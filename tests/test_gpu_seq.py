@@ -149,6 +149,15 @@ def test_conv_backward(case):
         assert ds is None
 
 
+# wide enough for runs of 64 tokens, in vectors and in single elements
+@pytest.mark.parametrize("case", [("f32", 8000, 5, [1500, 690, 1, 9], "silu", True, 0, 0),
+                                  ("bf16", 4001, 3, [1100, 0, 1030, 70], "silu", True, 0, 0)],
+                         ids=lambda c: f"{c[0]}-C{c[1]}-K{c[2]}")
+def test_conv_of_long_runs(case):
+    test_conv_forward(case)
+    test_conv_backward(case)
+
+
 def test_conv_one_sequence_without_offsets_and_no_tokens():
     x, w, b, _ = conv_data("f16", 32, 4, [50], False)
     plan = dw.CausalDepthwiseConv1d(32, 4, "f16", act="none")
