@@ -168,10 +168,10 @@ __device__ __forceinline__ void invert(const float *At, float *Td, int wave, int
 // ---------------------------------------------------------------------------
 constexpr int FRAG = 1024;
 constexpr int NBLK = 6;         // blocks of 16 x 32 that a 64 x 64 triangle touches
-constexpr int P_TERMS = 2, T_TERMS = 3;
-constexpr int AT_P = 0, AT_T = AT_P + NBLK * P_TERMS, AT_VEC = AT_T + NBLK * T_TERMS, VEC_FRAGS = 2,
-              HEAD_FWD = AT_VEC + VEC_FRAGS, AT_TT = HEAD_FWD, AT_PT = AT_TT + NBLK * T_TERMS,
-              HEAD_BWD = AT_PT + NBLK * T_TERMS;
+constexpr int TRI_TERMS = 3;    // of T and P
+constexpr int AT_P = 0, AT_T = AT_P + NBLK * TRI_TERMS, AT_VEC = AT_T + NBLK * TRI_TERMS, VEC_FRAGS = 2,
+              HEAD_FWD = AT_VEC + VEC_FRAGS, AT_TT = HEAD_FWD, AT_PT = AT_TT + NBLK * TRI_TERMS,
+              HEAD_BWD = AT_PT + NBLK * TRI_TERMS;
 // vectors of a chunk, 64 floats each: e^b / |k|, e^{b_last - b} / |k|, beta,
 // scale e^b / |q|, e^b and, backward, e^{b_last - b}, 1 / |k|, 1 / |q|
 enum { V_EK, V_RK, V_BETA, V_EQ, V_EB, V_ER, V_NK, V_NQ };

@@ -8,8 +8,8 @@
 // bf16 is one term, fp16 exactly two.  Lengths and decays are factored out of
 // q and k as vectors over tokens.  Products of terms below 2^-24 of the whole
 // are left out: three products for a bf16 operand times a state (one term
-// times three), six for two fp32 ones.  What only makes o (its own rounding is
-// 2^-9 or 2^-12) takes two terms: 2^-18.
+// times three), six for two fp32 ones.  What makes o is no exception: Q S0 and
+// P U can cancel, and their errors stay.
 //
 // A workgroup walks one sequence's chunks for one head and 16 NT columns of the
 // state.  Wavefront w has tokens 16 w .. 16 w + 15 of every chunk and a quarter
@@ -224,13 +224,12 @@ __global__ void __launch_bounds__(256, (DK <= 128 ? 3 : 2)) k_prepare(Ctx c) {
                     for (int i = 0; i < 4; ++i)
                         x[j][i] = 2 * kb + j >= m ? S[tri(2 * kb + j, m) + (g4 + i) * 16 + r] : 0.0f;
             }
-            bf16x8 t[T_TERMS];
+            bf16x8 t[TRI_TERMS];
             split(x[0], x[1], t);
             const int first = what == 0 ? AT_P : what == 1 ? AT_T : what == 2 ? AT_TT : AT_PT;
-            const int terms = what == 0 ? P_TERMS : T_TERMS;
 #pragma unroll
-            for (int n = 0; n < T_TERMS; ++n)
-                if (n < terms) *(bf16x8 *)(base + (int64_t)(first + blk * terms + n) * FRAG + lane * 16) = t[n];
+            for (int n = 0; n < TRI_TERMS; ++n)
+                *(bf16x8 *)(base + (int64_t)(first + blk * TRI_TERMS + n) * FRAG + lane * 16) = t[n];
         }
     }
 }
@@ -398,8 +397,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
     using X = typename DT::X;
     constexpr int NA = Raw<DT>::TERMS, NK = DK / 32, NF = DK / 8 * NA, T = DK / 64;
     extern __shared__ char L[];
-    const Right<NT, 3> SB{L}, RB{SB.p + SB.bytes(NK)}, EB{RB.p + RB.bytes(2)};
-    const Right<NT, 2> UB{EB.p + EB.bytes(2)};
+    const Right<NT, 3> SB{L}, RB{SB.p + SB.bytes(NK)}, EB{RB.p + RB.bytes(2)}, UB{EB.p + EB.bytes(2)};
     const Walk wk(c, 16 * NT, SAVE ? c.DvP : c.Dv);
     if (wk.s >= c.seq.seqs) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
@@ -415,7 +413,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
     const X *pv = (const X *)c.v + (int64_t)a * c.ldv + (int64_t)h * c.Dv;
     X *po = SAVE ? nullptr : o + (int64_t)a * ldo + (int64_t)h * c.Dv;
     // operands of the chunk at hand
-    bf16x8 wK[NK][NA], wQ[SAVE ? 1 : NK][NA], wT[2][T_TERMS], wP[2][P_TERMS], wKT[T][2][NA];
+    bf16x8 wK[NK][NA], wQ[SAVE ? 1 : NK][NA], wT[2][TRI_TERMS], wP[2][TRI_TERMS], wKT[T][2][NA];
     f32x4 ek, rk, beta, eq;
     float el;
     X vn[NT][4];
@@ -437,8 +435,8 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
     };
     auto fetch_T = [&](int k) {
         const char *p = head_of(k);
-        fetch(wT[0], p + (AT_T + lower_block(wave, 0) * T_TERMS) * FRAG, lane);
-        if (wave >= 2) fetch(wT[1], p + (AT_T + lower_block(wave, 1) * T_TERMS) * FRAG, lane);
+        fetch(wT[0], p + (AT_T + lower_block(wave, 0) * TRI_TERMS) * FRAG, lane);
+        if (wave >= 2) fetch(wT[1], p + (AT_T + lower_block(wave, 1) * TRI_TERMS) * FRAG, lane);
         rk = *(const f32x4 *)((const float *)(p + AT_VEC * FRAG) + V_RK * CH + row);
     };
     auto fetch_KT = [&](int k, int kb) {
@@ -447,10 +445,12 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
         for (int x = 0; x < T; ++x) fetch(wKT[x][kb], p + (2 * (wave * T + x) + kb) * NA * FRAG, lane);
         if (kb) el = ((const float *)(head_of(k) + AT_VEC * FRAG))[V_EB * CH + CH - 1];
     };
+    // (P is fetched in its own chunk, behind the first products: three terms of it kept
+    // from the chunk before spill; 8192 tokens, 32 heads of 128, bf16: 252 and 284 us a call)
     auto fetch_P = [&](int k) {
         const char *p = head_of(k);
-        fetch(wP[0], p + (AT_P + lower_block(wave, 0) * P_TERMS) * FRAG, lane);
-        if (wave >= 2) fetch(wP[1], p + (AT_P + lower_block(wave, 1) * P_TERMS) * FRAG, lane);
+        fetch(wP[0], p + (AT_P + lower_block(wave, 0) * TRI_TERMS) * FRAG, lane);
+        if (wave >= 2) fetch(wP[1], p + (AT_P + lower_block(wave, 1) * TRI_TERMS) * FRAG, lane);
     };
     if (nc > 0) {
 #pragma unroll
@@ -459,7 +459,6 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
         fetch_T(0);
         fetch_KT(0, 0);
         fetch_KT(0, 1);
-        if (!SAVE) fetch_P(0);
         S.put(SB, wave, lane);
     }
     for (int k = 0; k < nc; ++k) {
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
             if (kb + 1 < NK) SB.get(kb + 1, s[(kb + 1) & 1], lane);
             fence();
             mac(wK[kb], s[kb & 1], 2, ks);
-            if (!SAVE) mac(wQ[kb], s[kb & 1], 1, y);
+            if (!SAVE) mac(wQ[kb], s[kb & 1], 2, y);
             fetch_row(next, kb);
             fence();
         }
@@ -502,6 +501,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
             EB.put(wave, t, u[t] * rk_now, lane);
             if (!SAVE) UB.put(wave, t, u[t], lane);
         }
+        if (!SAVE) fetch_P(k);
         if (SAVE) keep_tokens<NT>(Us + at * CH * c.DvP, c, u, 16 * wave, g4, cl);
         __syncthreads();
         // S = e^{b_last} S + K^T (e^{b_last - b} U)
@@ -521,12 +521,10 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
         S.put(SB, wave, lane);
         // O = scale e^b (Q S0) + P U
         if (!SAVE) {
-            bf16x8 x[2][NT][2];
-            UB.get(0, x[0], lane);
-            UB.get(1, x[1], lane);
-            mac(wP[0], x[0], 1, y);
-            if (wave >= 2) mac(wP[1], x[1], 1, y);
-            fetch_P(next);
+            UB.get(0, s[0], lane);
+            UB.get(1, s[1], lane);
+            mac(wP[0], s[0], 2, y);
+            if (wave >= 2) mac(wP[1], s[1], 2, y);
             store_tokens<DT, NT>(po + (int64_t)k * CH * ldo, ro, y, n, 16 * wave, g4, cl);
         }
     }
@@ -557,7 +555,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
     const int slot0 = a / CH + wk.s, nc = (b - a + CH - 1) / CH, hk = h / (c.Hv / c.Hk);
     const X *pd = d_o + (int64_t)a * lddo + (int64_t)h * c.Dv;
     X *pv = dvo + (int64_t)a * lddv + (int64_t)h * c.Dv;
-    bf16x8 wK[NK][NA], wPT[2][T_TERMS], wTT[2][T_TERMS], wKT[T][2][NA], wQT[T][2][NA];
+    bf16x8 wK[NK][NA], wPT[2][TRI_TERMS], wTT[2][TRI_TERMS], wKT[T][2][NA], wQT[T][2][NA];
     f32x4 ek, rk, beta, eq;
     float el;
     X dn[NT][4];
@@ -570,15 +568,15 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
     auto fetch_row = [&](int k, int kb) { fetch(wK[kb], keys_of(k) + (NF + (wave * NK + kb) * NA) * FRAG, lane); };
     auto fetch_P = [&](int k) {
         const char *q = head_of(k);
-        fetch(wPT[1], q + (AT_PT + upper_block(wave, 1) * T_TERMS) * FRAG, lane);
-        if (wave < 2) fetch(wPT[0], q + (AT_PT + upper_block(wave, 0) * T_TERMS) * FRAG, lane);
+        fetch(wPT[1], q + (AT_PT + upper_block(wave, 1) * TRI_TERMS) * FRAG, lane);
+        if (wave < 2) fetch(wPT[0], q + (AT_PT + upper_block(wave, 0) * TRI_TERMS) * FRAG, lane);
         rk = *(const f32x4 *)((const float *)(q + AT_VEC * FRAG) + V_RK * CH + row);
     };
     auto fetch_T = [&](int k) {
         const char *q = head_of(k);
         const float *v = (const float *)(q + AT_VEC * FRAG);
-        fetch(wTT[1], q + (AT_TT + upper_block(wave, 1) * T_TERMS) * FRAG, lane);
-        if (wave < 2) fetch(wTT[0], q + (AT_TT + upper_block(wave, 0) * T_TERMS) * FRAG, lane);
+        fetch(wTT[1], q + (AT_TT + upper_block(wave, 1) * TRI_TERMS) * FRAG, lane);
+        if (wave < 2) fetch(wTT[0], q + (AT_TT + upper_block(wave, 0) * TRI_TERMS) * FRAG, lane);
         beta = *(const f32x4 *)(v + V_BETA * CH + row);
         ek = *(const f32x4 *)(v + V_EK * CH + row);
     };
@@ -697,7 +695,7 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
 int walk_tiles(const Ctx &c) { return (int64_t)c.seq.seqs * c.Hv * ((c.Dv + 31) / 32) <= 256 ? 1 : 2; }
 
 template <int NT>
-size_t lds_scan(int DK) { return (size_t)(DK / 32 + 2 + 2) * NT * 3 * FRAG + (size_t)2 * NT * 2 * FRAG; }
+size_t lds_scan(int DK) { return (size_t)(DK / 32 + 6) * NT * 3 * FRAG; }
 template <int NT>
 size_t lds_rscan(int DK, int terms) { return (size_t)(DK / 32 + 6) * NT * 3 * FRAG + (size_t)2 * NT * terms * FRAG; }
 
