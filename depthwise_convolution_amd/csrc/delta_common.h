@@ -116,6 +116,60 @@ __device__ __forceinline__ double running_sum(const float *g, int Hv, int n, int
     return b;
 }
 
+// NaN or infinite: x * 0 is not 0.
+__device__ __forceinline__ bool no_number(float x) { return !(x * 0.0f == 0.0f); }
+
+// Rows of A and R that hold NaN or infinity.  A matrix product multiplies them
+// with the zeros above the diagonal of T and P as well, which would carry them to
+// the tokens before; the definition is causal.  So the forward walks take such
+// values out of the operands and make the results of their own and all later
+// tokens of the column NaN instead (the state behind the chunk becomes NaN by its
+// own product).  Looking for them takes 2 to 5 % of a walk (8192 tokens of 32
+// heads, bf16, five sequences: 206 and 197 us).
+//
+// take_out_rows: z has 0 times the sum of this lane's elements of A, rows 16 w +
+// g4 + i, which the lane has written to At.  Rows that hold NaN or infinity
+// become zeros, and beta of their tokens NaN, which makes R NaN in all columns.
+__device__ __forceinline__ void take_out_rows(float z, float *At, float *beta, int wave, int r, int g4) {
+    if (!__any(z != 0.0f)) return;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        float s = 0.0f;
+        for (int j = 0; j <= wave; ++j) s = __builtin_fmaf(At[tri(wave, j) + (g4 + i) * 16 + r], 0.0f, s);
+        if (sum_row16(s) == 0.0f) continue;
+        for (int j = 0; j <= wave; ++j) At[tri(wave, j) + (g4 + i) * 16 + r] = 0.0f;
+        if (r == 0) beta[16 * wave + g4 + i] = __builtin_nanf("");
+    }
+}
+// First token of each column among N tiles of a wavefront's R (tile n: tokens
+// row + 16 n ..), CH: none; the values are replaced by zeros.
+template <int N>
+__device__ __forceinline__ int take_out(f32x4 (&x)[N], int row) {
+    int f = CH;
+#pragma unroll
+    for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+        for (int i = 3; i >= 0; --i)
+            if (no_number(x[n][i])) f = row + 16 * n + i, x[n][i] = 0.0f;
+    f = min(f, __shfl_xor(f, 16, 64));
+    return min(f, __shfl_xor(f, 32, 64));
+}
+template <int N>
+__device__ __forceinline__ bool any_no_number(const f32x4 (&x)[N]) {
+    float z = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z = __builtin_fmaf(x[n][i], 0.0f, z);
+    return __any(z != 0.0f);
+}
+// tokens row + i from `first` on
+__device__ __forceinline__ void put_from(f32x4 &x, int row, int first, float value) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (row + i >= first) x[i] = value;
+}
+
 // Column `wave` of T = (1 + A)^-1, tiles wave .. 3, from A's lower tiles in LDS
 // (four wavefronts; Td: room for the diagonal tiles' inverses).
 __device__ __forceinline__ void invert(const float *At, float *Td, int wave, int r, int g4, f32x4 (&Tc)[4]) {

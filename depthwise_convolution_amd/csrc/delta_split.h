@@ -27,6 +27,8 @@ using f32x2 = __attribute__((ext_vector_type(2))) float;
 // (On the words: conversions of single values would be made a second time.)
 template <int N>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&t)[N]) {
+// a product is rounded before it is split, so that the same value has the same terms everywhere
+#pragma clang fp contract(off)
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         t[n] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));

@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
             v[2 * CH + lane] = be;
         }
         __syncthreads();
+        float z = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (j > wave) continue;
@@ -108,9 +109,12 @@ __global__ void __launch_bounds__(256) k_prepare(Ctx c) {
                 const int row = 16 * wave + g4 + i, col = 16 * j + r;
                 const float d = row >= col ? expf((float)(b[row] - b[col])) : 0.0f;
                 c.P[at * TRI + tri(wave, j) + (g4 + i) * 16 + r] = row >= col ? c.scale * d * qk[j][i] : 0.0f;
-                At[tri(wave, j) + (g4 + i) * 16 + r] = row > col ? beta[row] * d * kk[j][i] : 0.0f;
+                const float a = row > col ? beta[row] * d * kk[j][i] : 0.0f;
+                At[tri(wave, j) + (g4 + i) * 16 + r] = a;
+                z = __builtin_fmaf(a, 0.0f, z);
             }
         }
+        take_out_rows(z, At, c.vecs + at * NV + 2 * CH, wave, r, g4);
         __syncthreads();
         f32x4 Tc[4];
         invert(At, Td, wave, r, g4, Tc);
@@ -198,11 +202,15 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
             for (int t = 0; t < DK / 16; ++t) x = mfma16(*(const f32x4 *)&L.K[16 * m + r][16 * t + g4], S[t], x);
             R[m] = *(const f32x4 *)&L.beta[16 * m + g4] * (V[m] - *(const f32x4 *)&L.eb[16 * m + g4] * x);
         }
+        // the column's first token that is no number
+        const bool mend = !SAVE && any_no_number(R);
+        const int first = mend ? take_out(R, g4) : CH;
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             f32x4 x = splat(0.0f);
 #pragma unroll
             for (int j = 0; j <= m; ++j) x = mfma16(*(const f32x4 *)&L.T[tri(m, j) + r * 16 + g4], R[j], x);
+            if (mend) put_from(x, 16 * m + g4, first, 0.0f);
             Uc[m] = x;
         }
         if (SAVE) {
@@ -222,6 +230,7 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
                 x = x * *(const f32x4 *)&L.eb[16 * m + g4] * c.scale;
 #pragma unroll
                 for (int j = 0; j <= m; ++j) x = mfma16(*(const f32x4 *)&L.P[tri(m, j) + r * 16 + g4], Uc[j], x);
+                if (mend) put_from(x, 16 * m + g4, first, __builtin_nanf(""));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = 16 * m + g4 + i;
@@ -231,7 +240,10 @@ __global__ void __launch_bounds__(256) k_scan(Ctx c, const float *state_in, floa
         }
         const float el = L.eb[CH - 1];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) Uc[m] *= *(const f32x4 *)&L.er[16 * m + g4];
+        for (int m = 0; m < 4; ++m) {
+            Uc[m] *= *(const f32x4 *)&L.er[16 * m + g4];
+            if (mend) put_from(Uc[m], 16 * m + g4, first, __builtin_nanf(""));
+        }
 #pragma unroll
         for (int t = 0; t < DK / 16; ++t) {
             f32x4 x = S[t] * el;

@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(256, (DK <= 128 ? 3 : 2)) k_prepare(Ctx c) {
             }
             __syncthreads();
         }
+        float z = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (j > wave) continue;
@@ -191,10 +192,13 @@ __global__ void __launch_bounds__(256, (DK <= 128 ? 3 : 2)) k_prepare(Ctx c) {
                 const float d = row >= col ? expf((float)(b[w][row] - b[w][col])) : 0.0f;
                 const float p = row >= col ? c.scale * d * (rq[row] * rk[col] * qk[j][i]) : 0.0f;
                 const int e = tri(wave, j) + (g4 + i) * 16 + r;
-                At[e] = row > col ? beta[w][row] * d * (rk[row] * rk[col] * kk[j][i]) : 0.0f;
+                const float a = row > col ? beta[w][row] * d * (rk[row] * rk[col] * kk[j][i]) : 0.0f;
+                At[e] = a;
+                z = __builtin_fmaf(a, 0.0f, z);
                 Pl[e] = p;
             }
         }
+        take_out_rows(z, At, (float *)(base + AT_VEC * FRAG) + V_BETA * CH, wave, r, g4);
         __syncthreads();
         f32x4 Tc[4];
         invert(At, Td, wave, r, g4, Tc);
@@ -400,9 +404,13 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
     const Right<NT, 3> SB{L}, RB{SB.p + SB.bytes(NK)}, EB{RB.p + RB.bytes(2)}, UB{EB.p + EB.bytes(2)};
     const Walk wk(c, 16 * NT, SAVE ? c.DvP : c.Dv);
     if (wk.s >= c.seq.seqs) return;
+    // each column's first token that is no number, CH: none.  A column stays spoiled:
+    // its state is NaN behind the chunk, so all of R in the next one
+    __shared__ int spoiled[16 * NT];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
               g4 = (lane >> 4) * 4;
     const int h = wk.h, row = 16 * wave + g4;  // this lane's tokens: row .. row + 3
+    if (!SAVE && threadIdx.x < 16 * NT) spoiled[threadIdx.x] = CH;
     const Columns<NT> cl(wk.first, r, c.Dv);
     const Rows rv(c.ldv, g4), ro(ldo, g4);
     const int a = uniform(c.seq.begin(wk.s)), b = uniform(c.seq.end(wk.s));
@@ -481,16 +489,34 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
             fetch_row(next, kb);
             fence();
         }
+        f32x4 R[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            RB.put(wave, t, beta * (widened<DT, NT>(vn, t, n, row, cl) - ek * ks[t]), lane);
+            R[t] = beta * (widened<DT, NT>(vn, t, n, row, cl) - ek * ks[t]);
             if (!SAVE) y[t] *= eq;
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) RB.put(wave, t, R[t], lane);
         fetch_V(next);
+        // (the paths that hardly any chunk takes stand apart, at the barriers: the
+        // compiler keeps them out of the way of the others' registers)
+        if (!SAVE && __builtin_expect(any_no_number(R), 0)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (no_number(R[t][i])) atomicMin(&spoiled[16 * t + r], row + i), R[t][i] = 0.0f;
+                RB.put(wave, t, R[t], lane);
+            }
+        }
         __syncthreads();
         // U = T R
         RB.get(0, s[0], lane);
         RB.get(1, s[1], lane);
+        int from[NT];
+        bool some = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) from[t] = SAVE ? CH : spoiled[16 * t + r];
         fence();
         mac(wT[0], s[0], 2, u);
         if (wave >= 2) mac(wT[1], s[1], 2, u);
@@ -502,6 +528,20 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_scan(Ctx c,
             if (!SAVE) UB.put(wave, t, u[t], lane);
         }
         if (!SAVE) fetch_P(k);
+        if (!SAVE) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) some |= from[t] < CH;
+            if (__builtin_expect(__any(some), 0)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (row + 3 < from[t]) continue;
+                    put_from(u[t], row, from[t], 0.0f);
+                    put_from(y[t], row, from[t], __builtin_nanf(""));
+                    UB.put(wave, t, u[t], lane);
+                    EB.put(wave, t, splat(__builtin_nanf("")), lane);
+                }
+            }
+        }
         if (SAVE) keep_tokens<NT>(Us + at * CH * c.DvP, c, u, 16 * wave, g4, cl);
         __syncthreads();
         // S = e^{b_last} S + K^T (e^{b_last - b} U)
