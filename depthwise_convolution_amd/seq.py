@@ -75,7 +75,20 @@ def _call(name, *args):
         raise DwconvError(rc, name)
 
 
+_INT = 2 ** 31 - 1
+
+
+def _n(name, v):
+    """A count as the C ABI's int, which ctypes would silently cut to 32 bits."""
+    if v > _INT or v < ~_INT:
+        raise ValueError(f"{name}: {v} is more than the library counts ({_INT})")
+    return v
+
+
 def _create(name, *args):
+    for v in args:
+        if isinstance(v, int):
+            _n(name, v)
     h = _H()
     _call(name, ctypes.byref(h), *args)
     return h.value
@@ -106,23 +119,24 @@ def dwconv_causal_destroy(h):
 
 
 def dwconv_causal_fwd(h, x, ldx, w, bias, offsets, seqs, tokens, state_in, state_out, y, ldy, stream):
-    _call("dwconv_causal_fwd", h, _p(x), ldx, _p(w), _p(bias), _p(offsets), seqs, tokens, _p(state_in),
-          _p(state_out), _p(y), ldy, stream)
+    _call("dwconv_causal_fwd", h, _p(x), ldx, _p(w), _p(bias), _p(offsets), _n("seqs", seqs), _n("tokens", tokens),
+          _p(state_in), _p(state_out), _p(y), ldy, stream)
 
 
 def dwconv_causal_step(h, x, ldx, w, bias, state, slots, n_slots, rows, y, ldy, stream):
-    _call("dwconv_causal_step", h, _p(x), ldx, _p(w), _p(bias), _p(state), _p(slots), n_slots, rows, _p(y), ldy,
-          stream)
+    _call("dwconv_causal_step", h, _p(x), ldx, _p(w), _p(bias), _p(state), _p(slots), _n("n_slots", n_slots),
+          _n("rows", rows), _p(y), ldy, stream)
 
 
 def dwconv_causal_bwd_workspace(h, tokens) -> int:
-    return _bytes("dwconv_causal_bwd_workspace", h, tokens)
+    return _bytes("dwconv_causal_bwd_workspace", h, _n("tokens", tokens))
 
 
 def dwconv_causal_bwd(h, x, ldx, w, bias, offsets, seqs, tokens, state_in, dy, lddy, dstate_out, dx, lddx, dw, dbias,
                       dstate_in, workspace, stream):
-    _call("dwconv_causal_bwd", h, _p(x), ldx, _p(w), _p(bias), _p(offsets), seqs, tokens, _p(state_in), _p(dy), lddy,
-          _p(dstate_out), _p(dx), lddx, _p(dw), _p(dbias), _p(dstate_in), _p(workspace), stream)
+    _call("dwconv_causal_bwd", h, _p(x), ldx, _p(w), _p(bias), _p(offsets), _n("seqs", seqs), _n("tokens", tokens),
+          _p(state_in), _p(dy), lddy, _p(dstate_out), _p(dx), lddx, _p(dw), _p(dbias), _p(dstate_in), _p(workspace),
+          stream)
 
 
 def dwconv_delta_create(Hk, Hv, Dk, Dv, dtype, scale, normalize, eps):
@@ -135,24 +149,24 @@ def dwconv_delta_destroy(h):
 
 
 def dwconv_delta_workspace(h, seqs, tokens, backward) -> int:
-    return _bytes("dwconv_delta_workspace", h, seqs, tokens, int(backward))
+    return _bytes("dwconv_delta_workspace", h, _n("seqs", seqs), _n("tokens", tokens), int(backward))
 
 
 def dwconv_delta_fwd(h, q, ldq, k, ldk, v, ldv, g, beta, offsets, seqs, tokens, state_in, state_out, o, ldo,
                      workspace, stream):
-    _call("dwconv_delta_fwd", h, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), _p(beta), _p(offsets), seqs, tokens,
-          _p(state_in), _p(state_out), _p(o), ldo, _p(workspace), stream)
+    _call("dwconv_delta_fwd", h, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), _p(beta), _p(offsets), _n("seqs", seqs),
+          _n("tokens", tokens), _p(state_in), _p(state_out), _p(o), ldo, _p(workspace), stream)
 
 
 def dwconv_delta_step(h, q, ldq, k, ldk, v, ldv, g, beta, state, slots, n_slots, rows, o, ldo, stream):
-    _call("dwconv_delta_step", h, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), _p(beta), _p(state), _p(slots), n_slots,
-          rows, _p(o), ldo, stream)
+    _call("dwconv_delta_step", h, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), _p(beta), _p(state), _p(slots),
+          _n("n_slots", n_slots), _n("rows", rows), _p(o), ldo, stream)
 
 
 def dwconv_delta_bwd(h, q, ldq, k, ldk, v, ldv, g, beta, offsets, seqs, tokens, state_in, d_o, lddo, dstate_out, dq,
                      lddq, dk, lddk, dv, lddv, dg, dbeta, dstate_in, workspace, stream):
-    _call("dwconv_delta_bwd", h, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), _p(beta), _p(offsets), seqs, tokens,
-          _p(state_in), _p(d_o), lddo, _p(dstate_out), _p(dq), lddq, _p(dk), lddk, _p(dv), lddv, _p(dg), _p(dbeta),
+    _call("dwconv_delta_bwd", h, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), _p(beta), _p(offsets), _n("seqs", seqs),
+          _n("tokens", tokens), _p(state_in), _p(d_o), lddo, _p(dstate_out), _p(dq), lddq, _p(dk), lddk, _p(dv), lddv, _p(dg), _p(dbeta),
           _p(dstate_in), _p(workspace), stream)
 
 
@@ -168,18 +182,18 @@ def dwconv_norm_destroy(p):
 
 def dwconv_norm_fwd(p, rows, o, residual, gate, rows_per_gate, scale, w_after, b_after, w_before, b_before, h, y,
                     stream):
-    _call("dwconv_norm_fwd", p, rows, _p(o), _p(residual), _p(gate), rows_per_gate, _p(scale), _p(w_after),
-          _p(b_after), _p(w_before), _p(b_before), _p(h), _p(y), stream)
+    _call("dwconv_norm_fwd", p, _n("rows", rows), _p(o), _p(residual), _p(gate), _n("rows_per_gate", rows_per_gate),
+          _p(scale), _p(w_after), _p(b_after), _p(w_before), _p(b_before), _p(h), _p(y), stream)
 
 
 def dwconv_norm_bwd_workspace(p, rows, rows_per_gate) -> int:
-    return _bytes("dwconv_norm_bwd_workspace", p, rows, rows_per_gate)
+    return _bytes("dwconv_norm_bwd_workspace", p, _n("rows", rows), _n("rows_per_gate", rows_per_gate))
 
 
 def dwconv_norm_bwd(p, rows, o, residual, gate, rows_per_gate, scale, w_after, b_after, w_before, b_before, dh, dy,
                     d_o, dresidual, dgate, dscale, dw_after, db_after, dw_before, db_before, workspace, stream):
-    _call("dwconv_norm_bwd", p, rows, _p(o), _p(residual), _p(gate), rows_per_gate, _p(scale), _p(w_after),
-          _p(b_after), _p(w_before), _p(b_before), _p(dh), _p(dy), _p(d_o), _p(dresidual), _p(dgate), _p(dscale),
+    _call("dwconv_norm_bwd", p, _n("rows", rows), _p(o), _p(residual), _p(gate), _n("rows_per_gate", rows_per_gate),
+          _p(scale), _p(w_after), _p(b_after), _p(w_before), _p(b_before), _p(dh), _p(dy), _p(d_o), _p(dresidual), _p(dgate), _p(dscale),
           _p(dw_after), _p(db_after), _p(dw_before), _p(db_before), _p(workspace), stream)
 
 
@@ -217,10 +231,11 @@ def _sequences(offsets, dev):
     if offsets.dim() != 1 or offsets.numel() < 1:
         raise ValueError("offsets: one dimension, one value more than there are sequences")
     _dense("offsets", offsets, (offsets.numel(),), torch.int32, dev)
-    return offsets.numel() - 1
+    return _n("offsets", offsets.numel() - 1)
 
 
 def _slots(slots, rows, n_slots, dev):
+    _n("state", n_slots)
     if slots is None:
         if rows > n_slots:
             raise ValueError(f"{rows} rows without slots need as many cache entries, got {n_slots}")
@@ -299,7 +314,7 @@ class CausalDepthwiseConv1d(_Plan):
         dev, dt = self._device("x", x), self.dtype
         if x.dim() != 2:
             raise ValueError("x: tokens x channels")
-        n, seqs = x.shape[0], _sequences(offsets, dev)
+        n, seqs = _n("x", x.shape[0]), _sequences(offsets, dev)
         _dense("w", w, (self.K, self.C), dt, dev)
         if bias is not None:
             _dense("bias", bias, (self.C,), torch.float32, dev)
@@ -395,7 +410,7 @@ class GatedDeltaRule(_Plan):
 
     def _common(self, q, k, v, g, beta):
         dev, dt = self._device("q", q), self.dtype
-        n = q.shape[0]
+        n = _n("q", q.shape[0])
         lds = (_tokens("q", q, (n, self.Hk, self.Dk), dt, dev), _tokens("k", k, (n, self.Hk, self.Dk), dt, dev),
                _tokens("v", v, (n, self.Hv, self.Dv), dt, dev))
         _dense("g", g, (n, self.Hv), torch.float32, dev)
@@ -503,10 +518,10 @@ class BlockNorm(_Plan):
             raise ValueError(f"o: rows of {D} channels")
         shape = tuple(o.shape)
         _dense("o", o, shape, self.dtype, dev)
-        rows = o.numel() // D
+        rows = _n("o", o.numel() // D)
         if residual is not None:
             _dense("residual", residual, shape, self.dtype, dev)
-        if per < 1:
+        if _n("rows_per_gate", per) < 1:
             raise ValueError("rows_per_gate: at least 1")
         if gate is not None:
             if gate.numel() != -(-rows // per) * D:

@@ -1,0 +1,83 @@
+"""What the sequence operators' binding refuses before the library is called.
+CPU only: no test here launches a kernel."""
+import pytest
+import torch
+
+import depthwise_convolution_amd as dw
+from depthwise_convolution_amd import seq
+
+BIG = 2 ** 32 + 5  # a 32-bit int keeps 5 of it
+
+
+def meta(*shape, dtype=torch.float32):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+@pytest.fixture
+def any_device(monkeypatch):
+    """Tensors without memory stand in for the GPU's: what is checked comes
+    before anything is allocated or launched."""
+    monkeypatch.setattr(seq._Plan, "_device", lambda self, name, t: t.device)
+
+
+def past_int(call, *args, **kwargs):
+    with pytest.raises(ValueError, match="2147483647"):
+        call(*args, **kwargs)
+
+
+def test_counts_past_32_bits_are_refused_by_the_functions():
+    h = dw.dwconv_causal_create(8, 4, "f32", "none")
+    P = [1 << 20 | i << 12 for i in range(16)]
+    past_int(dw.dwconv_causal_fwd, h, P[0], 8, P[1], None, P[2], BIG, 10, None, None, P[3], 8, None)
+    past_int(dw.dwconv_causal_fwd, h, P[0], 8, P[1], None, P[2], 2, BIG, None, None, P[3], 8, None)
+    past_int(dw.dwconv_causal_step, h, P[0], 8, P[1], None, P[2], P[3], BIG, 3, P[4], 8, None)
+    past_int(dw.dwconv_causal_step, h, P[0], 8, P[1], None, P[2], P[3], 5, BIG, P[4], 8, None)
+    past_int(dw.dwconv_causal_bwd_workspace, h, BIG)
+    past_int(dw.dwconv_causal_bwd, h, P[0], 8, P[1], None, P[2], 2, BIG, None, P[3], 8, None, P[4], 8, P[5], None, None,
+             P[6], None)
+    dw.dwconv_causal_destroy(h)
+    h = dw.dwconv_delta_create(1, 1, 8, 8, "f32", 1.0, True, 1e-6)
+    past_int(dw.dwconv_delta_workspace, h, BIG, 10, False)
+    past_int(dw.dwconv_delta_workspace, h, 1, BIG, True)
+    past_int(dw.dwconv_delta_fwd, h, P[0], 8, P[1], 8, P[2], 8, P[3], P[4], P[5], 2, BIG, None, None, P[6], 8, P[7], None)
+    past_int(dw.dwconv_delta_step, h, P[0], 8, P[1], 8, P[2], 8, P[3], P[4], P[5], P[6], 5, BIG, P[7], 8, None)
+    past_int(dw.dwconv_delta_bwd, h, P[0], 8, P[1], 8, P[2], 8, P[3], P[4], P[5], BIG, 10, None, P[6], 8, None, P[7], 8,
+             P[8], 8, P[9], 8, P[10], P[11], None, P[12], None)
+    dw.dwconv_delta_destroy(h)
+    p = dw.dwconv_norm_create(8, "f32", "none", "none", "none", 0.0)
+    past_int(dw.dwconv_norm_fwd, p, BIG, P[0], None, None, 1, None, None, None, None, None, P[1], None, None)
+    past_int(dw.dwconv_norm_fwd, p, 6, P[0], None, P[2], BIG, None, None, None, None, None, P[1], None, None)
+    past_int(dw.dwconv_norm_bwd_workspace, p, BIG, 1)
+    past_int(dw.dwconv_norm_bwd_workspace, p, 1, BIG)
+    past_int(dw.dwconv_norm_bwd, p, BIG, P[0], *[None] * 2, 1, *[None] * 5, P[1], None, P[2], *[None] * 7, P[3], None)
+    dw.dwconv_norm_destroy(p)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: dw.dwconv_causal_create(BIG, 4, "f32", "none"), lambda: dw.dwconv_causal_create(8, 2 ** 32 + 4, "f32", "none"),
+    lambda: dw.GatedDeltaRule(1, BIG, 8, 8), lambda: dw.GatedDeltaRule(1, 1, 2 ** 32 + 8, 8),
+    lambda: dw.BlockNorm(BIG, "bf16"), lambda: dw.BlockNorm(8, "bf16", after=2 ** 32),
+    lambda: dw.dwconv_delta_create(1, 1, 8, 8, 2 ** 32, 1.0, True, 1e-6),
+])
+def test_plans_past_32_bits_are_refused(call):
+    past_int(call)
+
+
+def test_counts_past_32_bits_are_refused_by_the_classes(any_device):
+    x, w = meta(BIG, 8), meta(4, 8)
+    conv = dw.CausalDepthwiseConv1d(8, 4, "f32")
+    past_int(conv, x, w)
+    past_int(conv, meta(5, 8), w, offsets=meta(BIG, dtype=torch.int32))
+    past_int(conv.backward, x, w, x)
+    past_int(conv.step, x, w, None, state=meta(BIG, 3, 8))
+    past_int(conv.step, meta(5, 8), w, None, state=meta(BIG, 3, 8))
+    rule = dw.GatedDeltaRule(1, 1, 8, 8, "f32")
+    q, g = meta(BIG, 1, 8), meta(BIG, 1)
+    past_int(rule, q, q, q, g, g)
+    past_int(rule.backward, q, q, q, g, g, q)
+    past_int(rule.step, q, q, q, g, g, state=meta(8, 1, 8, 8))
+    past_int(rule.step, q[:5], q[:5], q[:5], g[:5], g[:5], state=meta(BIG, 1, 8, 8))
+    norm = dw.BlockNorm(8, "f32")
+    past_int(norm, x, w_after=meta(8), w_before=meta(8))
+    past_int(norm.backward, x, x, x, w_after=meta(8), w_before=meta(8))
+    past_int(norm, x[:6], gate=x[:1], rows_per_gate=BIG, w_after=meta(8), w_before=meta(8))
