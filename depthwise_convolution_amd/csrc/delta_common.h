@@ -254,6 +254,7 @@ __device__ __forceinline__ f32x4 sum16(f32x4 v) {
 
 // launchers (k_delta_split.hip, k_delta_grad.hip)
 hipError_t split_grad(int dtype, int DK, const Ctx &c, const GradArgs &ga, hipStream_t st);
+uint64_t split_blocks(const Ctx &c, bool backward);  // workgroups of the walks
 hipError_t split_prepare(int dtype, int DK, const Ctx &c, bool backward, hipStream_t st);
 hipError_t split_scan(int dtype, int DK, const Ctx &c, const float *state_in, float *state_out, void *o, int64_t ldo,
                       float *S0s, float *Us, hipStream_t st);

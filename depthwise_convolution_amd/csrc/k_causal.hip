@@ -453,14 +453,14 @@ hipError_t bwd(const dwconv_causal_plan &p, const CausalArgs &a, hipStream_t st)
     const uint64_t tiles = ((uint64_t)a.tokens + G.TT - 1) / G.TT;
     const uint64_t blocks = blocks_of(tiles * G.ncv);
     const uint64_t sb = a.dstate_in ? blocks_of((uint64_t)a.seqs * (K - 1) * G.ncv) : 0;
-    if (too_many(blocks + sb)) return hipErrorInvalidConfiguration;
+    const uint64_t cols = ((uint64_t)(K + 1) * p.C + 63) / 64;
+    if (too_many(blocks + sb) || too_many(cols)) return hipErrorInvalidConfiguration;
     G.main_blocks = (uint32_t)blocks;
     if (blocks + sb)
         k_bwd<DT, VEC, K><<<(uint32_t)(blocks + sb), 256, 0, st>>>(
             G, (const X *)a.x, a.ldx, (const X *)a.w, a.bias, (const X *)a.state_in, (const X *)a.dy, a.lddy,
             (const X *)a.dstate_out, (X *)a.dx, a.lddx, (X *)a.dstate_in, a.workspace, silu);
-    const uint32_t cols = (uint32_t)(((uint64_t)(K + 1) * p.C + 63) / 64);
-    k_sum<<<cols, 256, 0, st>>>(a.workspace, (int64_t)tiles, p.C, K, a.dw, a.dbias);
+    k_sum<<<(uint32_t)cols, 256, 0, st>>>(a.workspace, (int64_t)tiles, p.C, K, a.dw, a.dbias);
     return hipGetLastError();
 }
 

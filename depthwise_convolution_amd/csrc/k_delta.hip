@@ -689,9 +689,10 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
     c.keys = (char *)(ws + l.keys), c.heads = (char *)(ws + l.heads), c.sums = (double *)(ws + l.sums);
     c.key_bytes = (int64_t)l.key_bytes, c.head_bytes = (int64_t)l.head_bytes;
     const uint64_t chunks = (uint64_t)c.slots * p.Hk, walks = (uint64_t)a.seqs * p.Hv * ((p.Dv + 63) / 64);
-    // a grid holds fewer than 2^32 lanes (the 16-bit walks have up to four
-    // workgroups for each of these, and their grids are rounded up)
+    // a grid holds fewer than 2^32 lanes; the 16-bit walks' grid is rounded up (eight
+    // times at most), so it is looked at as it will be, before anything is launched
     if (chunks >= (1u << 23) || walks >= (1u << 21)) return hipErrorInvalidConfiguration;
+    if (split_runs(p.dtype) && split_blocks(c, backward) >= (1u << 24)) return hipErrorInvalidConfiguration;
     const int vec = std::is_same<DT, F32>::value ? 4 : 8;
     const GradArgs ga{ws + l.S0s, ws + l.Us, ws + l.dSs, ws + l.dRs, a.d_o, a.lddo, a.dq, a.dk, a.lddq, a.lddk, a.dg,
                       a.dbeta, rows_of<X>(vec, a.d_o, a.lddo, p.Dv), rows_of<X>(vec, a.v, a.ldv, p.Dv)};

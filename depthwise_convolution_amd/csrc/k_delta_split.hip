@@ -382,9 +382,9 @@ struct Walk {
         h = (int)(unit % c.Hk * group + i / nb);
         s = (int)(unit / c.Hk);
     }
-    static uint32_t blocks(const Ctx &c, int cols, int width) {
-        const int64_t units = (int64_t)c.seq.seqs * c.Hk, per = (int64_t)((width + cols - 1) / cols) * (c.Hv / c.Hk);
-        return (uint32_t)((units + 7) / 8 * 8 * per);
+    static uint64_t blocks(const Ctx &c, int cols, int width) {
+        const uint64_t units = (uint64_t)c.seq.seqs * c.Hk, per = (uint64_t)((width + cols - 1) / cols) * (c.Hv / c.Hk);
+        return (units + 7) / 8 * 8 * per;
     }
 };
 
@@ -743,6 +743,10 @@ size_t lds_rscan(int DK, int terms) { return (size_t)(DK / 32 + 6) * NT * 3 * FR
 
 namespace delta {
 
+uint64_t split_blocks(const Ctx &c, bool backward) {
+    return Walk::blocks(c, 16 * walk_tiles(c), backward ? c.DvP : c.Dv);
+}
+
 hipError_t split_prepare(int dtype, int DK_, const Ctx &c, bool backward, hipStream_t st) {
     return pick(dtype, DK_, [&](auto dt, auto dk) {
         using DT = decltype(dt);
@@ -764,7 +768,7 @@ hipError_t split_scan(int dtype, int DK_, const Ctx &c, const float *state_in, f
         using X = typename DT::X;
         constexpr int DK = decltype(dk)::value;
         const int nt = walk_tiles(c);
-        const uint32_t blocks = Walk::blocks(c, 16 * nt, S0s ? c.DvP : c.Dv);
+        const uint32_t blocks = (uint32_t)Walk::blocks(c, 16 * nt, S0s ? c.DvP : c.Dv);
         const size_t n = nt == 1 ? lds_scan<1>(DK) : lds_scan<2>(DK);
         auto f = nt == 1 ? (S0s ? k_scan<DT, DK, 1, true> : k_scan<DT, DK, 1, false>)
                          : (S0s ? k_scan<DT, DK, 2, true> : k_scan<DT, DK, 2, false>);
@@ -782,7 +786,7 @@ hipError_t split_rscan(int dtype, int DK_, const Ctx &c, const void *d_o, int64_
         using X = typename DT::X;
         constexpr int DK = decltype(dk)::value;
         const int nt = walk_tiles(c);
-        const uint32_t blocks = Walk::blocks(c, 16 * nt, c.DvP);
+        const uint32_t blocks = (uint32_t)Walk::blocks(c, 16 * nt, c.DvP);
         const size_t n = nt == 1 ? lds_rscan<1>(DK, Raw<DT>::TERMS) : lds_rscan<2>(DK, Raw<DT>::TERMS);
         auto f = nt == 1 ? k_rscan<DT, DK, 1> : k_rscan<DT, DK, 2>;
         hipError_t e = lds_room((const void *)f, n);

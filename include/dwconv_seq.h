@@ -34,10 +34,18 @@
  * stated.  Every sum is formed in a fixed order without atomics: the same call
  * gives the same bits.
  *
- * A call whose grid would pass 2^32 lanes returns DWCONV_ERR_UNSUPPORTED: for
- * the delta rule 2^29 tokens x key heads or 2^21 sequences x value heads x 64
- * columns of the state, for a step 2^24 rows x value heads or x 256 vectors of
- * channels.
+ * A call whose grid would pass 2^32 lanes returns DWCONV_ERR_UNSUPPORTED before
+ * anything is launched:
+ *   convolution  2^24 workgroups of 256 lanes, a lane a vector of channels (16
+ *                bytes, 8 for K > 4, one element where rows are not aligned) of up
+ *                to 64 tokens, in a step of one row; gradients also 2^30 (K + 1) x C
+ *   delta rule   2^23 (tokens / 64 + sequences) x key heads, or 2^21 sequences x
+ *                value heads x ceil(Dv / 64); bf16 and fp16 also 2^24 sequences x
+ *                key heads (rounded up to a multiple of 8) x value heads a key head
+ *                x ceil(Dv / 32)
+ *   its step     2^24 rows x value heads x ceil(Dv / 128), with Dv / 32 where rows
+ *                are not aligned to four elements
+ *   norms        2^32 lanes, 16 to 1024 a row
  *
  * float (fp32) everywhere: biases, scales, norm weights, decays, write
  * strengths, matrix states and the gradients of all of these.  Sums and

@@ -81,3 +81,33 @@ def test_counts_past_32_bits_are_refused_by_the_classes(any_device):
     past_int(norm, x, w_after=meta(8), w_before=meta(8))
     past_int(norm.backward, x, x, x, w_after=meta(8), w_before=meta(8))
     past_int(norm, x[:6], gate=x[:1], rows_per_gate=BIG, w_after=meta(8), w_before=meta(8))
+
+
+def test_grids_are_refused_before_anything_is_launched():
+    """Where the last kernel's grid is the one that passes the limit, the call says
+    so as it does for the others (here, without a GPU, a launch is another error)."""
+    P = [1 << 20 | i << 16 for i in range(16)]
+
+    def unsupported(call, *args):
+        with pytest.raises(dw.DwconvError) as e:
+            call(*args)
+        assert e.value.status == 2
+
+    # one unit of 65536 heads x 62 groups of columns, rounded up to eight units
+    h = dw.dwconv_delta_create(1, 65536, 8, 1984, "bf16", 1.0, True, 1e-6)
+    wide = 65536 * 1984
+    unsupported(dw.dwconv_delta_fwd, h, P[0], 8, P[1], 8, P[2], wide, P[3], P[4], None, 1, 64, None, None, P[5], wide,
+                P[6], None)
+    unsupported(dw.dwconv_delta_bwd, h, P[0], 8, P[1], 8, P[2], wide, P[3], P[4], None, 1, 64, None, P[5], wide, None,
+                P[6], 8, P[7], 8, P[8], wide, P[9], P[10], None, P[11], None)
+    dw.dwconv_delta_destroy(h)
+    # the sums of 5 x 2^29 columns
+    h = dw.dwconv_causal_create(1 << 29, 4, "bf16", "none")
+    unsupported(dw.dwconv_causal_bwd, h, P[0], 1 << 29, P[1], None, None, 1, 1, None, P[2], 1 << 29, None, P[3], 1 << 29,
+                P[4], None, None, P[5], None)
+    dw.dwconv_causal_destroy(h)
+    # a step's groups of columns count as its rows and heads do
+    h = dw.dwconv_delta_create(1, 64, 8, 4096, "bf16", 1.0, True, 1e-6)
+    unsupported(dw.dwconv_delta_step, h, P[0], 8, P[1], 8, P[2], 64 * 4096, P[3], P[4], P[5], P[6], 5, 1 << 13, P[7],
+                64 * 4096, None)
+    dw.dwconv_delta_destroy(h)
