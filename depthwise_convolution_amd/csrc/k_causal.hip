@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) k_fwd(Geo G, const typename DT::X *x, int
                 z[i] = bi[i];
 #pragma unroll
                 for (int k = 0; k < K; ++k) z[i] = __builtin_fmaf(wt[k][i], win[k][i], z[i]);
-                if (silu) z[i] *= sigmoid_f32(z[i]);
+                if (silu) z[i] *= sigmoid_f32<DT>(z[i]);
 #pragma unroll
                 for (int k = 0; k + 1 < K; ++k) win[k][i] = win[k + 1][i];
             }
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(256) k_step(int C, uint32_t ncv, uint32_t cblo
             z[e] = bi[e];
 #pragma unroll
             for (int k = 0; k < K; ++k) z[e] = __builtin_fmaf(wt[k][e], win[k][e], z[e]);
-            if (silu) z[e] *= sigmoid_f32(z[e]);
+            if (silu) z[e] *= sigmoid_f32<DT>(z[e]);
 #pragma unroll
             for (int k = 0; k + 1 < K; ++k) win[k][e] = win[k + 1][e];
         }
@@ -171,9 +171,11 @@ __global__ void __launch_bounds__(256) k_step(int C, uint32_t ncv, uint32_t cblo
     for (int j = 0; j + 1 < K; ++j) store_f32<DT, VEC>(st + (int64_t)j * C, win[j]);
 }
 
+template <class DT>
 __device__ __forceinline__ float silu_slope(float z) {
-    const float p = sigmoid_f32(z);
-    return p * (1.0f + z * (1.0f - p));
+    float q;
+    const float p = sigmoid_f32<DT>(z, q);
+    return p * (1.0f + z * q);
 }
 
 // dstate_in: ext row e < K-1 gets shares from tokens 0 .. e, and is row e - L
@@ -208,7 +210,7 @@ __device__ __forceinline__ void state_gradient(const Geo &G, uint64_t i, const t
                 for (int j = 0; j < VEC; ++j) z[j] = __builtin_fmaf(wt[j], win[k][j], z[j]);
             }
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) d[j] *= silu_slope(z[j]);
+            for (int j = 0; j < VEC; ++j) d[j] *= silu_slope<DT>(z[j]);
         }
         load_f32<DT, VEC>(wt, w + (int64_t)(e - t) * G.C + c);
 #pragma unroll
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(256) k_bwd(Geo G, const typename DT::X *x, int
                         float z = bi[i];
 #pragma unroll
                         for (int k = 0; k < K; ++k) z = __builtin_fmaf(wt[k][i], win[k][i], z);
-                        d *= silu_slope(z);
+                        d *= silu_slope<DT>(z);
                     }
 #pragma unroll
                     for (int k = 0; k < K; ++k) acc[k][i] = __builtin_fmaf(wt[k][i], d, acc[k][i]);

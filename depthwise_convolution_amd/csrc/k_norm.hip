@@ -68,14 +68,17 @@ struct RowSum {
 };
 
 // act(g), and act'(g) in `slope`
+template <class DT>
 __device__ __forceinline__ float gate_value(float g, int act, float &slope) {
-    const float p = sigmoid_f32(g), q = p * (1.0f - p);
+    float rest;
+    const float p = sigmoid_f32<DT>(g, rest), q = p * rest;
     slope = act == DWCONV_SEQ_ACT_NONE ? 1.0f : act == DWCONV_SEQ_ACT_SILU ? __builtin_fmaf(g, q, p) : q;
     return act == DWCONV_SEQ_ACT_NONE ? g : act == DWCONV_SEQ_ACT_SILU ? g * p : p;
 }
+template <class DT>
 __device__ __forceinline__ float gate_value(float g, int act) {
     float slope;
-    return gate_value(g, act, slope);
+    return gate_value<DT>(g, act, slope);
 }
 
 // A lane's E channels: NV vectors of VEC, TPR vectors apart.  Vectors past D
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
     if (pgate) {
         ln.widen(t, rg);
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] *= gate_value(t[i], o.act);
+        for (int i = 0; i < E; ++i) v[i] *= gate_value<DT>(t[i], o.act);
     }
     if (scale) {
         lf.load(t, scale);
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
     auto gates = [&] {
         ln.widen(a, rg);
 #pragma unroll
-        for (int i = 0; i < E; ++i) a[i] = gate_value(a[i], o.act, slope[i]);
+        for (int i = 0; i < E; ++i) a[i] = gate_value<DT>(a[i], o.act, slope[i]);
     };
     const int64_t first = deal.segs > 1 ? blockIdx.x / deal.segs : (int64_t)blockIdx.x * deal.chunk;
     const int seg = deal.segs > 1 ? blockIdx.x % deal.segs : 0;

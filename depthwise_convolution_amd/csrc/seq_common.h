@@ -44,8 +44,36 @@ __device__ __forceinline__ void store_f32(typename DT::X *p, const float (&in)[N
     *(Vec<typename DT::X, N> *)p = a;
 }
 
-// off by a few units of 2^-24 (reciprocal: one, exp2 of a rounded product: |z|)
-__device__ __forceinline__ float sigmoid_f32(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
+// sigmoid(z), and 1 - sigmoid(z) in `rest`.
+// 16-bit data: the reciprocal (one unit of 2^-23) and exp2 of a rounded product (|z|
+// units of 2^-24, so at most 2^-17 of itself, of which half a step is 2^-9 or 2^-12).
+template <class DT>
+__device__ __forceinline__ float sigmoid_f32(float z, float &rest) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+    rest = 1.0f - p;
+    return p;
+}
+// fp32 data: both off by at most 8 units of 2^-24 of themselves wherever they are
+// normal numbers.  They come from t = e^-|z| <= 1: no overflow, no difference of near
+// values.  t is 2^-h for the rounded h = |z| / ln 2, times 1 - r for what the rounding
+// left, r = |z| - h ln 2.  Beyond 200 t is 0 (an infinite |z| would make r NaN).
+// For 16-bit data as well it would cost (bf16, before and after) causal gradients of
+// 8192 x 8192 93.7 and 100.5 us, gated norms of 262144 x 128 35.5 and 38.0 us.
+template <>
+__device__ __forceinline__ float sigmoid_f32<F32>(float z, float &rest) {
+    const float m = __builtin_fabsf(z), a = m > 200.0f ? 200.0f : m, h = a * 1.44269504f;
+    const float r = __builtin_fmaf(h, 1.90465421e-9f, __builtin_fmaf(h, -0.693147182f, a));
+    float t = __builtin_amdgcn_exp2f(-h);
+    t = __builtin_fmaf(t, -r, t);
+    const float s = __builtin_amdgcn_rcpf(1.0f + t);
+    rest = z < 0.0f ? s : t * s;
+    return z < 0.0f ? t * s : s;
+}
+template <class DT>
+__device__ __forceinline__ float sigmoid_f32(float z) {
+    float rest;
+    return sigmoid_f32<DT>(z, rest);
+}
 
 // v plus the value n lanes round in each row of 16 (one instruction).
 template <int N>

@@ -90,3 +90,73 @@ def test_delta_forward_is_causal_for_what_is_no_number(fmt, Hk, Hv, Dk, Dv, lens
         if name != "q":
             ends[0, heads, :, cols] = True
         assert torch.equal(end[~ends], clean_end[~ends]) and not torch.isfinite(end[ends]).any()
+
+
+# ---------------------------------------------------------------------------
+# activations far from zero
+# ---------------------------------------------------------------------------
+def far_values(n):
+    """fp32 values from -85 to 85 (their sigmoids are normal fp32 numbers), and the
+    two signs of zero."""
+    z = torch.linspace(-85, 85, n - 2, dtype=torch.float64) + 0.37 * torch.sin(torch.arange(n - 2, dtype=torch.float64))
+    return torch.cat([z.clamp(-85, 85), torch.tensor([0.0, -0.0], dtype=torch.float64)]).float()
+
+
+def within(got, want, tol, what):
+    bad = (got.double().cpu() - want).abs() > tol
+    i = int((((got.double().cpu() - want).abs() / tol.clamp_min(1e-300))).argmax())
+    print(f"{what}: worst {float((got.double().cpu() - want).abs().flatten()[i] / tol.flatten()[i]):.2f} of the bound", flush=True)
+    assert not bad.any(), what
+
+
+# e^-|z| is off by an instruction of one unit in the last place (2 U) and two
+# roundings, 1 + e^-|z| by one, the reciprocal by 2 U and a product by one: 8 U
+# relative for the sigmoid and for its distance to 1, rounded up to 10; silu is a
+# product more: 12.  The slope p (1 + z q) has 10 U of p, 10 of q, two products and
+# a sum: 24 U of p (1 + |z| q).
+SIG, SILU, SLOPE = 10 * ref.U, 12 * ref.U, 24 * ref.U
+
+
+def test_silu_of_far_values_in_the_convolution():
+    C, T = 64, 4096
+    z = far_values(C * T).view(T, C)
+    conv = dw.CausalDepthwiseConv1d(C, 2, "f32", act="silu")
+    w = torch.stack([torch.zeros(C), torch.ones(C)])  # z is x itself
+    p, q = torch.sigmoid(z.double()), torch.sigmoid(-z.double())
+    want, slope = z.double() * p, p * (1 + z.double() * q)
+    y = conv(up(z), up(w))
+    within(y, want, SILU * want.abs(), "forward")
+    state = torch.zeros(T, 1, C, device=DEV)
+    within(conv.step(up(z), up(w), None, state=state), want, SILU * want.abs(), "step")
+    dx, _, _, _ = conv.backward(up(z), up(w), torch.ones(T, C, device=DEV))
+    within(dx, slope, SLOPE * p * (1 + z.double().abs() * q), "slope")
+    special = torch.tensor([[INF, NAN, -INF, -200.0, 200.0, -1e30, 0.0, -0.0]])
+    got = dw.CausalDepthwiseConv1d(8, 2, "f32", act="silu")(up(special), up(w[:, :8].contiguous()))[0].cpu()
+    assert got[0] == INF and got[1:3].isnan().all() and (got[[3, 5, 6, 7]] == 0).all() and got[4] == 200.0
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("per", [1, 3])
+def test_gates_of_far_values(act, per):
+    D, rows = 96, 3000
+    gate = far_values(D * -(-rows // per)).view(-1, D)
+    norm = dw.BlockNorm(D, "f32", after="none", before="none", gate_act=act)
+    one = torch.ones(rows, D, device=DEV)
+    z = gate.double()
+    p, q = torch.sigmoid(z), torch.sigmoid(-z)
+    want = p if act == "sigmoid" else z * p
+    h, _ = norm(one, gate=up(gate), rows_per_gate=per)
+    spread = lambda t: t.repeat_interleave(per, 0)[:rows]  # noqa: E731
+    within(h, spread(want), spread((SIG if act == "sigmoid" else SILU) * want.abs()), act)
+    dgate = norm.backward(one, one, gate=up(gate), rows_per_gate=per)[2]
+    # per equal terms are added: two roundings more
+    slope, size = (p * q, p * q) if act == "sigmoid" else (p * (1 + z * q), p * (1 + z.abs() * q))
+    within(dgate, per * slope, (SLOPE + per * ref.U) * per * size, act + " slope")
+    special = torch.tensor([[INF, NAN, -INF, -200.0, 200.0, -1e30, 0.0, -0.0]])
+    small = dw.BlockNorm(8, "f32", after="none", before="none", gate_act=act)
+    got = small(torch.ones(1, 8, device=DEV), gate=up(special))[0][0].cpu()
+    assert got[1].isnan()
+    if act == "sigmoid":
+        assert got[0] == 1 and got[2] == 0 and got[3] == 0 and got[4] == 1 and got[5] == 0 and (got[6:] == 0.5).all()
+    else:
+        assert got[0] == INF and got[2].isnan() and (got[[3, 5, 6, 7]] == 0).all() and got[4] == 200.0
