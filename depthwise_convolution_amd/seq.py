@@ -18,7 +18,10 @@ devices and strides, and allocate outputs and workspaces with torch:
 ``offsets`` (int32, one more than there are sequences) cuts the tokens into
 sequences; outputs of tokens behind the last one are left as they were.  What a
 call allocates belongs to ``stream`` where one is given, else to torch's
-current stream of the tensors' device.
+current stream of the tensors' device.  A given stream does not wait for the
+current one: order them with ``wait_stream``.  The caller's tensors may be dropped
+after a call on a torch stream; on a raw handle they have to live until the stream
+has passed the call.
 """
 import ctypes
 
@@ -252,19 +255,29 @@ def _current_raw(index):
 _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw)
 
 
-def _on(dev, stream, body):
+def _on(dev, stream, body, *tensors):
     """``body`` with the raw handle of ``stream`` (a torch stream, a raw handle,
     None: the current one), ``dev`` current and that stream the one torch
-    allocates for."""
+    allocates for.  ``tensors`` are the caller's: torch's allocator keeps their
+    memory until a torch stream has passed the call.  (Not for a raw handle, whose
+    stream may be gone by the time a tensor is freed.)"""
     if stream is None and torch.cuda.current_device() == dev.index:
         return body(_current_raw(dev.index))
+    keep = stream is not None and not isinstance(stream, (int, torch.cuda.ExternalStream))
+    if keep and stream.device != dev:
+        raise ValueError(f"stream: it belongs to {stream.device}, the tensors to {dev}")
     with torch.cuda.device(dev):
         if stream is None:
             return body(_current_raw(dev.index))
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
-            return body(stream.cuda_stream)
+            out = body(stream.cuda_stream)
+        if keep:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        return out
 
 
 class _Plan:
@@ -337,7 +350,7 @@ class CausalDepthwiseConv1d(_Plan):
                               _tokens("y", y, (n, self.C), dt, dev), raw)
             return y
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, x, w, bias, offsets, state_in, state_out, y)
 
     def step(self, x, w, bias, state, slots=None, y=None, stream=None):
         """One token for each row of x; ``state`` (cache entries x (K-1) x C) is
@@ -356,7 +369,7 @@ class CausalDepthwiseConv1d(_Plan):
                                _tokens("y", y, (n, self.C), dt, dev), raw)
             return y
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, x, w, bias, state, slots, y)
 
     def backward(self, x, w, dy, bias=None, offsets=None, state_in=None, dstate_out=None, dx=None, dw=None,
                  dbias=None, dstate_in=None, workspace=None, stream=None):
@@ -389,7 +402,7 @@ class CausalDepthwiseConv1d(_Plan):
                               _tokens("dx", dx, (n, self.C), dt, dev), dw, dbias, dstate_in, ws, raw)
             return dx, dw, dbias, dstate_in
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, x, w, bias, offsets, state_in, dy, dstate_out, dx, dw, dbias, dstate_in, workspace)
 
 
 class GatedDeltaRule(_Plan):
@@ -437,7 +450,7 @@ class GatedDeltaRule(_Plan):
                              _tokens("o", o, (n, self.Hv, self.Dv), dt, dev), ws, raw)
             return o
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, q, k, v, g, beta, offsets, state_in, state_out, o, workspace)
 
     def step(self, q, k, v, g, beta, state, slots=None, o=None, stream=None):
         """One token for each row; ``state`` (cache entries x Hv x Dk x Dv) is
@@ -455,7 +468,7 @@ class GatedDeltaRule(_Plan):
                               _tokens("o", o, (n, self.Hv, self.Dv), dt, dev), raw)
             return o
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, q, k, v, g, beta, state, slots, o)
 
     def backward(self, q, k, v, g, beta, do, offsets=None, state_in=None, dstate_out=None, dq=None, dk=None, dv=None,
                  dg=None, dbeta=None, dstate_in=None, workspace=None, stream=None):
@@ -495,7 +508,8 @@ class GatedDeltaRule(_Plan):
                              dv, _tokens("dv", dv, values, dt, dev), dg, dbeta, dstate_in, ws, raw)
             return dq, dk, dv, dg, dbeta, dstate_in
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, q, k, v, g, beta, do, offsets, state_in, dstate_out, dq, dk, dv, dg, dbeta,
+                   dstate_in, workspace)
 
 
 class BlockNorm(_Plan):
@@ -553,7 +567,7 @@ class BlockNorm(_Plan):
                             y, raw)
             return h, y
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, o, residual, gate, scale, w_after, b_after, w_before, b_before, h, y)
 
     def backward(self, o, dh=None, dy=None, residual=None, gate=None, scale=None, w_after=None, b_after=None,
                  w_before=None, b_before=None, rows_per_gate=1, workspace=None, stream=None):
@@ -575,4 +589,4 @@ class BlockNorm(_Plan):
                             dy, *grads, ws, raw)
             return tuple(grads)
 
-        return _on(dev, stream, body)
+        return _on(dev, stream, body, o, dh, dy, residual, gate, scale, w_after, b_after, w_before, b_before, workspace)

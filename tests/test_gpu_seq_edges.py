@@ -8,7 +8,7 @@ import depthwise_convolution_amd as dw
 import seq_reference as ref
 from gpu_helpers import DEV, say
 from seq_cases import readback, readback_bound, readback_terms
-from test_gpu_seq import delta_data, offsets_of, up
+from test_gpu_seq import delta_data, offsets_of, rand, up
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +160,58 @@ def test_gates_of_far_values(act, per):
         assert got[0] == 1 and got[2] == 0 and got[3] == 0 and got[4] == 1 and got[5] == 0 and (got[6:] == 0.5).all()
     else:
         assert got[0] == INF and got[2].isnan() and (got[[3, 5, 6, 7]] == 0).all() and got[4] == 200.0
+
+
+# ---------------------------------------------------------------------------
+# a given stream
+# ---------------------------------------------------------------------------
+CALLS = {
+    "causal forward": lambda: (dw.CausalDepthwiseConv1d(256, 4, "f32"), lambda p, t, **k: p(*t, **k),
+                                  lambda r: [r(300, 256), r(4, 256), r(256)]),
+    "causal step": lambda: (dw.CausalDepthwiseConv1d(256, 4, "f32"), lambda p, t, **k: p.step(*t, **k),
+                               lambda r: [r(300, 256), r(4, 256), r(256), r(300, 3, 256)]),
+    "causal backward": lambda: (dw.CausalDepthwiseConv1d(256, 4, "f32"), lambda p, t, **k: p.backward(*t, **k),
+                                   lambda r: [r(300, 256), r(4, 256), r(300, 256), r(256)]),
+    "delta forward": lambda: (dw.GatedDeltaRule(1, 2, 64, 64, "f32"), lambda p, t, **k: p(*t, **k),
+                                 lambda r: [r(300, 1, 64), r(300, 1, 64), r(300, 2, 64), -r(300, 2).abs(), r(300, 2)]),
+    "delta step": lambda: (dw.GatedDeltaRule(1, 2, 64, 64, "f32"), lambda p, t, **k: p.step(*t, **k),
+                              lambda r: [r(30, 1, 64), r(30, 1, 64), r(30, 2, 64), -r(30, 2).abs(), r(30, 2),
+                                         r(30, 2, 64, 64)]),
+    "delta backward": lambda: (dw.GatedDeltaRule(1, 2, 64, 64, "f32"), lambda p, t, **k: p.backward(*t, **k),
+                                  lambda r: [r(300, 1, 64), r(300, 1, 64), r(300, 2, 64), -r(300, 2).abs(), r(300, 2),
+                                             r(300, 2, 64)]),
+    "norm forward": lambda: (dw.BlockNorm(256, "f32"), lambda p, t, **k: p(t[0], t[1], t[2], None, t[3], None, t[4], **k),
+                                lambda r: [r(300, 256), r(300, 256), r(300, 256), r(256), r(256)]),
+    "norm backward": lambda: (dw.BlockNorm(256, "f32"),
+                                 lambda p, t, **k: p.backward(t[0], t[1], t[2], t[3], t[4], None, t[5], None, t[6], **k),
+                                 lambda r: [r(300, 256) for _ in range(5)] + [r(256), r(256)]),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_inputs_dropped_after_a_call_on_another_stream(name):
+    """Memory of inputs that are dropped while the call still waits on its stream is
+    not given to another tensor before the call has read it."""
+    say(f"[gpu] dropped inputs: {name}")
+    plan, call, make = CALLS[name]()
+    seeds = iter(range(100))
+    data = make(lambda *shape: rand(*shape, seed=next(seeds)) * 0.3)
+    want = call(plan, [up(t) for t in data])
+    want = [t.clone() for t in (want if isinstance(want, tuple) else (want,)) if t is not None]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    mine = [up(t) for t in data]
+    taken = {t.data_ptr() for t in mine}
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)
+    got = call(plan, mine, stream=side)
+    del mine
+    others = [torch.full_like(up(t), NAN) for t in data for _ in range(2)]
+    waiting = not side.query()
+    print(f"{name}: {'still waiting' if waiting else 'already run'}", flush=True)
+    assert not waiting or not taken & {t.data_ptr() for t in others}, "the memory of a dropped input is in use"
+    torch.cuda.synchronize()
+    got = [t for t in (got if isinstance(got, tuple) else (got,)) if t is not None]
+    assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))

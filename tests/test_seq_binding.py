@@ -111,3 +111,11 @@ def test_grids_are_refused_before_anything_is_launched():
     unsupported(dw.dwconv_delta_step, h, P[0], 8, P[1], 8, P[2], 64 * 4096, P[3], P[4], P[5], P[6], 5, 1 << 13, P[7],
                 64 * 4096, None)
     dw.dwconv_delta_destroy(h)
+
+
+def test_a_stream_of_another_device_is_refused():
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        seq._on(torch.device("cuda", 0), Stream(), lambda raw: pytest.fail("called"))
