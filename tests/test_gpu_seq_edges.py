@@ -208,7 +208,7 @@ def test_inputs_dropped_after_a_call_on_another_stream(name):
         torch.cuda._sleep(400_000_000)
     got = call(plan, mine, stream=side)
     del mine
-    others = [torch.full_like(up(t), NAN) for t in data for _ in range(2)]
+    others = [torch.full(t.shape, NAN, device=DEV) for t in data for _ in range(2)]  # (nothing here waits for a stream)
     waiting = not side.query()
     print(f"{name}: {'still waiting' if waiting else 'already run'}", flush=True)
     assert not waiting or not taken & {t.data_ptr() for t in others}, "the memory of a dropped input is in use"
