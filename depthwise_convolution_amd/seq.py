@@ -22,6 +22,10 @@ current stream of the tensors' device.  A given stream does not wait for the
 current one: order them with ``wait_stream``.  The caller's tensors may be dropped
 after a call on a torch stream; on a raw handle they have to live until the stream
 has passed the call.
+
+Nothing is recorded for autograd; ``backward`` gives the gradients.  A tensor that
+requires a gradient is refused while gradients are enabled: the outputs would carry
+none.  Under ``torch.no_grad()`` and in an ``autograd.Function`` it is taken.
 """
 import ctypes
 
@@ -261,6 +265,11 @@ def _on(dev, stream, body, *tensors):
     allocates for.  ``tensors`` are the caller's: torch's allocator keeps their
     memory until a torch stream has passed the call.  (Not for a raw handle, whose
     stream may be gone by the time a tensor is freed.)"""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("the sequence operators record nothing for autograd, but a tensor requires a gradient: "
+                                 "call them under torch.no_grad() (or in an autograd.Function) and use backward()")
     if stream is None and torch.cuda.current_device() == dev.index:
         return body(_current_raw(dev.index))
     keep = stream is not None and not isinstance(stream, (int, torch.cuda.ExternalStream))

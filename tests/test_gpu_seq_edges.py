@@ -215,3 +215,41 @@ def test_inputs_dropped_after_a_call_on_another_stream(name):
     torch.cuda.synchronize()
     got = [t for t in (got if isinstance(got, tuple) else (got,)) if t is not None]
     assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------------------
+# autograd
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("name", CALLS)
+def test_a_tensor_that_requires_a_gradient_is_refused(name):
+    """Whichever input it is; without gradients enabled it is taken."""
+    plan, call, make = CALLS[name]()
+    data = [up(t) for t in make(lambda *shape: rand(*shape) * 0.3)]
+    for i in range(len(data)):
+        d = [t.detach().clone().requires_grad_(j == i) for j, t in enumerate(data)]
+        with pytest.raises(ValueError, match="autograd"):
+            call(plan, d)
+        with torch.no_grad():
+            call(plan, d)
+
+
+def test_the_operators_in_an_autograd_function():
+    """How a training step has them: forward and backward as a Function's."""
+    conv = dw.CausalDepthwiseConv1d(64, 4, "f32")
+
+    class Mix(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, b):
+            ctx.save_for_backward(x, w, b)
+            return conv(x, w, b)
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, w, b = ctx.saved_tensors
+            return conv.backward(x, w, dy.contiguous(), b)[:3]
+
+    x, w, b = (up(rand(*s)).requires_grad_() for s in ((50, 64), (4, 64), (64,)))
+    (Mix.apply(x, w, b) * 3).sum().backward()
+    with torch.no_grad():
+        want = conv.backward(x, w, torch.full_like(x, 3.0), b)
+    assert all(torch.equal(t.grad, g) for t, g in zip((x, w, b), want))

@@ -119,3 +119,19 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(ValueError, match="cuda:1"):
         seq._on(torch.device("cuda", 0), Stream(), lambda raw: pytest.fail("called"))
+
+
+def test_a_tensor_that_requires_a_gradient_is_refused(any_device):
+    """Before anything is allocated or launched, on every entry point."""
+    def r(*shape):
+        return meta(*shape).requires_grad_()
+
+    x, w, q, v, g, one = meta(6, 8), meta(4, 8), meta(6, 1, 8), meta(6, 2, 8), meta(6, 2), meta(8)
+    conv, rule, norm = dw.CausalDepthwiseConv1d(8, 4, "f32"), dw.GatedDeltaRule(1, 2, 8, 8, "f32"), dw.BlockNorm(8, "f32")
+    for call in (lambda: conv(x, r(4, 8)), lambda: conv.step(x, w, r(8), state=meta(6, 3, 8)),
+                 lambda: conv.backward(x, w, r(6, 8)), lambda: rule(q, q, v, r(6, 2), g),
+                 lambda: rule.step(q, q, v, g, g, state=r(6, 2, 8, 8)), lambda: rule.backward(q, q, v, g, g, r(6, 2, 8)),
+                 lambda: norm(x, r(6, 8), w_after=one, w_before=one),
+                 lambda: norm.backward(x, x, x, gate=r(6, 8), w_after=one, w_before=one)):
+        with pytest.raises(ValueError, match="autograd"):
+            call()
