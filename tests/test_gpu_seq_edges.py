@@ -7,7 +7,8 @@ import torch
 import depthwise_convolution_amd as dw
 import seq_reference as ref
 from gpu_helpers import DEV, say
-from seq_cases import readback, readback_bound, readback_terms
+from seq_cases import CONV_GRADS, conv_grad_bounds, conv_grad_data, readback, readback_bound, readback_terms
+from seq_reference import leaves, rel
 from test_gpu_seq import delta_data, offsets_of, rand, up
 
 pytestmark = pytest.mark.gpu
@@ -253,3 +254,61 @@ def test_the_operators_in_an_autograd_function():
     with torch.no_grad():
         want = conv.backward(x, w, torch.full_like(x, 3.0), b)
     assert all(torch.equal(t.grad, g) for t, g in zip((x, w, b), want))
+
+
+# ---------------------------------------------------------------------------
+# keys and queries of length zero
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("fmt,Hk,Hv,Dk,Dv,lens,state", [
+    ("f32", 1, 2, 40, 24, [70, 20], True), ("bf16", 1, 2, 128, 48, [130], False), ("f16", 2, 4, 64, 33, [65, 1, 90], True),
+    ("bf16", 1, 1, 200, 40, [100], True), ("f16", 1, 3, 250, 16, [64, 30], True),
+], ids=str)
+def test_delta_gradients_at_zero_keys_and_queries(fmt, Hk, Hv, Dk, Dv, lens, state):
+    """|x| = sqrt(sum x^2 + eps) has a slope at zero: the gradient of the unit vector
+    over sqrt(eps), a thousand times it.  So is its error: the bounds of the other
+    rows (tests/test_gpu_seq.py), times that for these."""
+    say(f"[gpu] delta zero keys {fmt} {Hk} {Hv} {Dk} {Dv} {lens}")
+    q, k, v, g, beta, s = delta_data(fmt, Hk, Hv, Dk, Dv, lens, state, gates="plain", seed=90)
+    T, eps = sum(lens), 1e-6
+    k[1::9], q[2::7], k[5::31], q[5::31] = 0.0, 0.0, 0.0, 0.0
+    do = rand(T, Hv, Dv, seed=50, dtype=fmt)
+    dso = rand(len(lens), Hv, Dk, Dv, seed=51, std=0.3) if state else None
+    got = dw.GatedDeltaRule(Hk, Hv, Dk, Dv, fmt, eps=eps).backward(*(up(t) for t in (q, k, v, g, beta, do)),
+                                                                    offsets=offsets_of(lens), state_in=up(s), dstate_out=up(dso))
+    args = leaves(q, k, v, g, beta, s)
+    o, states, size = ref.delta(*args[:5], lens, args[5], Dk ** -0.5, True, eps)
+    outs, gives, wrt = ([o, states], [do.double(), dso.double()], args) if state else ([o], [do.double()], args[:5])
+    want = torch.autograd.grad(outs, wrt, gives)
+    half, n = ref.HALF[q.dtype], Dk + 64 + Dv
+    for name, i, x in (("dq", 0, q), ("dk", 1, k)):
+        a, w, zero = got[i].double().cpu(), want[i], x.double().abs().sum(-1) == 0
+        assert zero.any() and not zero.all()
+        for rows, lift in ((zero, eps ** -0.5), (~zero, 1.0)):
+            top = float(w[rows].abs().max()) / lift + float(w[~zero].abs().max()) + size
+            off = (a[rows] - w[rows]).abs()
+            assert (off <= half * w[rows].abs() + 8 * n * ref.U * top * lift).all(), (name, lift, float(off.max()))
+            many = 24 * n ** 0.5 * ref.U * top * lift * w[rows].numel() ** 0.5
+            assert float(off.norm()) <= half * float(w[rows].norm()) + many, (name, lift)
+    for name, i in (("dv", 2), ("dg", 3), ("dbeta", 4)):
+        assert rel(got[i].cpu(), want[i]) <= (half if i == 2 else 0) + 24 * n ** 0.5 * ref.U, name
+
+
+# ---------------------------------------------------------------------------
+# gradients of the convolution within bounds of their own size
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("case", CONV_GRADS, ids=lambda c: f"{c[0]}-C{c[1]}-K{c[2]}-{sum(c[3])}-{c[4]}")
+def test_conv_gradients_to_the_sums_own_accuracy(case):
+    """Element by element and in the 2-norm; the bounds see gradients that were summed
+    or kept in fewer bits (tests/test_seq_bounds.py)."""
+    say(f"[gpu] causal bwd, own accuracy {case}")
+    x, w, b, s, dy, dso = conv_grad_data(case)
+    fmt, C, K, lens, act, state = case
+    got = dw.CausalDepthwiseConv1d(C, K, fmt, act=act).backward(
+        up(x), up(w), up(dy), up(b), offsets=offsets_of(lens), state_in=up(s), dstate_out=up(dso))
+    for name, g, (want, bound) in zip(("dx", "dw", "dbias", "dstate"), got, conv_grad_bounds(case, x, w, b, s, dy, dso)):
+        if want is None:
+            assert g is None
+            continue
+        off = (g.double().cpu() - want).abs()
+        print(f"{name}: {float((off / bound).max()):.2f} of the bound, {float(off.norm() / bound.norm()):.2f} in the 2-norm", flush=True)
+        assert (off <= bound).all() and float(off.norm()) <= 0.5 * float(bound.norm()), name
