@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
                 const f32x4 kq = KQ[j * 64];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float d = __expf((float)(br[i] - by[j]));
+                    const float d = expf((float)(br[i] - by[j]));  // as k_prepare made it
                     const float x = half ? -dD[j][i] * d : c.scale * dD[j][i] * d;
                     const bool in = half ? row + i > y : row + i >= y;
                     const float z = in ? x : 0.0f, zk = in ? x * kq[i] : 0.0f;

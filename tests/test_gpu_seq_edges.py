@@ -312,3 +312,24 @@ def test_conv_gradients_to_the_sums_own_accuracy(case):
         off = (g.double().cpu() - want).abs()
         print(f"{name}: {float((off / bound).max()):.2f} of the bound, {float(off.norm() / bound.norm()):.2f} in the 2-norm", flush=True)
         assert (off <= bound).all() and float(off.norm()) <= 0.5 * float(bound.norm()), name
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "f32"])
+def test_delta_gradient_through_a_large_exponent(fmt):
+    """Sequences of two tokens whose second has g = 46 .. 85: its gradient is e^g times
+    two dot products, of Dk and Dv positive products, so each relative error is the
+    exponential's and the sums' rounding, sqrt(Dk + Dv) u, with 64 more for the
+    products in between; e^g of a rounded g / ln 2 would be off by 25 u on average."""
+    Dk, Dv, n = 64, 32, 128
+    q, k, v, _, beta, _ = delta_data(fmt, 1, 1, Dk, Dv, [2] * n, False, gates="plain", seed=120)
+    q, k, v, do = (t.abs() for t in (q, k, v, rand(2 * n, 1, Dv, seed=122, dtype=fmt)))
+    g = torch.zeros(2 * n, 1)
+    g[1::2, 0] = torch.linspace(46, 85, n)
+    beta = beta.clamp_min(0.2)
+    got = dw.GatedDeltaRule(1, 1, Dk, Dv, fmt).backward(*(up(t) for t in (q, k, v, g, beta, do)), offsets=offsets_of([2] * n))
+    args = leaves(q, k, v, g, beta)
+    o, _, _ = ref.delta(*args, [2] * n, None, Dk ** -0.5, True, 1e-6)
+    want = torch.autograd.grad(o, args, do.double())[3][1::2]
+    off = got[3].double().cpu()[1::2] / want - 1
+    print(f"{fmt}: {float(off.norm()) / n ** 0.5 / ref.U:.1f} u on average", flush=True)
+    assert float(off.norm()) / n ** 0.5 <= (Dk + 64 + Dv) ** 0.5 * ref.U
