@@ -19,9 +19,12 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     return a && b && na && nb && x < y + nb && y < x + na;
 }
 
+// Counts of tokens and sequences to which a chunk, a run or one may be added.
+constexpr int MOST = INT32_MAX - 128;
+
 // Sequences: one without offsets, any number with them.
 bool sequences(const int32_t *offsets, int seqs, int tokens) {
-    return tokens >= 0 && tokens <= INT32_MAX - 128 && seqs >= 0 && (offsets || seqs == 1) && at(offsets, 4);
+    return tokens >= 0 && tokens <= MOST && seqs >= 0 && seqs <= MOST && (offsets || seqs == 1) && at(offsets, 4);
 }
 
 // A tensor of `n` tokens with `width` dense channels of `e` bytes.
@@ -96,7 +99,7 @@ dwconv_status_t dwconv_causal_step(dwconv_causal_t h, const void *x, int64_t ldx
 }
 
 dwconv_status_t dwconv_causal_bwd_workspace(dwconv_causal_t h, int tokens, size_t *bytes) {
-    if (!h || !bytes || tokens < 0) return DWCONV_ERR_INVALID_ARG;
+    if (!h || !bytes || tokens < 0 || tokens > MOST) return DWCONV_ERR_INVALID_ARG;
     *bytes = dw::causal_bwd_bytes(*h, tokens);
     return DWCONV_OK;
 }
@@ -137,7 +140,7 @@ dwconv_status_t dwconv_delta_destroy(dwconv_delta_t h) {
 }
 
 dwconv_status_t dwconv_delta_workspace(dwconv_delta_t h, int seqs, int tokens, int backward, size_t *bytes) {
-    if (!h || !bytes || seqs < 0 || tokens < 0) return DWCONV_ERR_INVALID_ARG;
+    if (!h || !bytes || seqs < 0 || seqs > MOST || tokens < 0 || tokens > MOST) return DWCONV_ERR_INVALID_ARG;
     *bytes = dw::delta_bytes(*h, seqs, tokens, backward != 0);
     return DWCONV_OK;
 }

@@ -56,7 +56,7 @@ __device__ __forceinline__ int first_slot(const Packed &p, int s) { return p.beg
 __device__ __forceinline__ Chunk chunk_of(const Packed &p, int slot) {
     int lo = 0, hi = p.seqs;  // first_slot(lo) <= slot
     while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
+        const int m = lo + ((hi - lo) >> 1);
         if (first_slot(p, m) <= slot) lo = m; else hi = m;
     }
     const int c = slot - first_slot(p, lo), a = p.begin(lo), b = p.end(lo);

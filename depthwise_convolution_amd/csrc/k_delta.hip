@@ -679,7 +679,6 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
     Ctx c{};
     c.seq = {a.offsets, a.seqs, a.tokens};
     c.Hk = p.Hk, c.Hv = p.Hv, c.Dk = p.Dk, c.Dv = p.Dv, c.DvP = (p.Dv + 31) / 32 * 32;
-    c.slots = a.tokens / CH + a.seqs;
     c.scale = p.scale, c.eps = p.eps, c.normalize = p.normalize;
     c.vec4 = rows_of<X>(4, a.q, a.ldq, p.Dk) && rows_of<X>(4, a.k, a.ldk, p.Dk);
     c.vec8 = rows_of<X>(8, a.q, a.ldq, p.Dk) && rows_of<X>(8, a.k, a.ldk, p.Dk);
@@ -688,10 +687,11 @@ hipError_t run(const dwconv_delta_plan &p, const DeltaArgs &a, bool backward, hi
     c.T = ws + l.T, c.P = ws + l.P, c.vecs = ws + l.vecs;
     c.keys = (char *)(ws + l.keys), c.heads = (char *)(ws + l.heads), c.sums = (double *)(ws + l.sums);
     c.key_bytes = (int64_t)l.key_bytes, c.head_bytes = (int64_t)l.head_bytes;
-    const uint64_t chunks = (uint64_t)c.slots * p.Hk, walks = (uint64_t)a.seqs * p.Hv * ((p.Dv + 63) / 64);
+    const uint64_t chunks = ((uint64_t)(a.tokens / CH) + a.seqs) * p.Hk, walks = (uint64_t)a.seqs * p.Hv * ((p.Dv + 63) / 64);
     // a grid holds fewer than 2^32 lanes; the 16-bit walks' grid is rounded up (eight
     // times at most), so it is looked at as it will be, before anything is launched
     if (chunks >= (1u << 23) || walks >= (1u << 21)) return hipErrorInvalidConfiguration;
+    c.slots = a.tokens / CH + a.seqs;
     if (split_runs(p.dtype) && split_blocks(c, backward) >= (1u << 24)) return hipErrorInvalidConfiguration;
     const int vec = std::is_same<DT, F32>::value ? 4 : 8;
     const GradArgs ga{ws + l.S0s, ws + l.Us, ws + l.dSs, ws + l.dRs, a.d_o, a.lddo, a.dq, a.dk, a.lddq, a.lddk, a.dg,

@@ -112,7 +112,7 @@ struct Packed {
         if (!offsets) return 0;
         int lo = -1, hi = seqs;  // offsets[lo] <= t < offsets[hi], hi past the end
         while (hi - lo > 1) {
-            const int m = (lo + hi) >> 1;
+            const int m = lo + ((hi - lo) >> 1);  // (lo + hi may pass 2^31)
             if (offsets[m] <= t) lo = m; else hi = m;
         }
         return lo;

@@ -12,11 +12,11 @@
  * Tokens of several sequences lie one behind the other.  `offsets` holds
  * seqs + 1 int32 device values: sequence s is tokens offsets[s] ..
  * offsets[s+1]-1; they rise, start at 0 and end at or below `tokens`.  A
- * sequence may be empty.  What tokens behind the last sequence hold does not
- * matter, and their outputs are left as they were.  offsets == NULL: one sequence of all tokens
- * (seqs must be 1).  The offsets are device data that the host does not see:
- * the kernels clamp them to [0, tokens], so wrong ones give wrong results but
- * no access out of bounds.
+ * sequence may be empty.  tokens and seqs are at most 2^31 - 129.  What tokens
+ * behind the last sequence hold does not matter, and their outputs are left as
+ * they were.  offsets == NULL: one sequence of all tokens (seqs must be 1).  The
+ * offsets are device data that the host does not see: the kernels clamp them to
+ * [0, tokens], so wrong ones give wrong results but no access out of bounds.
  *
  * Token strides (ld...) count elements between two tokens; within a token the
  * channels (heads x channels) are dense.  A stride is at least the token's

@@ -333,3 +333,20 @@ def test_delta_gradient_through_a_large_exponent(fmt):
     off = got[3].double().cpu()[1::2] / want - 1
     print(f"{fmt}: {float(off.norm()) / n ** 0.5 / ref.U:.1f} u on average", flush=True)
     assert float(off.norm()) / n ** 0.5 <= (Dk + 64 + Dv) ** 0.5 * ref.U
+
+
+def test_more_sequences_than_2_to_the_30():
+    """Nearly all of them empty: the search for a token's sequence passes sums of
+    2^31, and the last sequence's tokens still find it."""
+    C, K, n = 8, 3, 2 ** 30 + 5
+    say("[gpu] 2^30 sequences")
+    x, w = up(rand(9, C, seed=1)), up(rand(K, C, seed=2))
+    off = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    off[n - 1], off[n] = 4, 9  # the last two have tokens
+    conv = dw.CausalDepthwiseConv1d(C, K, "f32")
+    few = offsets_of([4, 5])
+    assert torch.equal(conv(x, w, offsets=off), conv(x, w, offsets=few))
+    a, b = (conv.backward(x, w, x, offsets=o) for o in (off, few))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    del off
+    torch.cuda.empty_cache()

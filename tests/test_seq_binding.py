@@ -135,3 +135,30 @@ def test_a_tensor_that_requires_a_gradient_is_refused(any_device):
                  lambda: norm.backward(x, x, x, gate=r(6, 8), w_after=one, w_before=one)):
         with pytest.raises(ValueError, match="autograd"):
             call()
+
+
+def test_counts_near_2_to_the_31_are_refused():
+    """Kernels add a run, a chunk or one to a count of tokens or sequences."""
+    h = dw.dwconv_causal_create(8, 4, "bf16", "silu")
+    r = dw.dwconv_delta_create(1, 1, 8, 8, "bf16", 1.0, True, 1e-6)
+    P = [1 << 20 | i << 16 for i in range(16)]
+    most = 2 ** 31 - 129
+    for n in (most + 1, 2 ** 31 - 1):
+        for call in (lambda: dw.dwconv_causal_fwd(h, P[0], 8, P[1], None, P[2], n, 10, None, None, P[3], 8, None),
+                     lambda: dw.dwconv_causal_fwd(h, P[0], 8, P[1], None, P[2], 2, n, None, None, P[3], 8, None),
+                     lambda: dw.dwconv_causal_bwd(h, P[0], 8, P[1], None, P[2], n, 10, None, P[3], 8, None, P[4], 8, P[5],
+                                                  None, None, P[6], None),
+                     lambda: dw.dwconv_causal_bwd_workspace(h, n), lambda: dw.dwconv_delta_workspace(r, n, 10, False),
+                     lambda: dw.dwconv_delta_workspace(r, 1, n, True),
+                     lambda: dw.dwconv_delta_fwd(r, P[0], 8, P[1], 8, P[2], 8, P[3], P[4], P[5], n, 10, None, None, P[6],
+                                                 8, P[7], None)):
+            with pytest.raises(dw.DwconvError) as e:
+                call()
+            assert e.value.status == 1
+    assert dw.dwconv_causal_bwd_workspace(h, most) > dw.dwconv_causal_bwd_workspace(h, most - 2 ** 20)
+    # as many sequences as the delta rule's grid does not hold are told apart from bad ones
+    with pytest.raises(dw.DwconvError) as e:
+        dw.dwconv_delta_fwd(r, P[0], 8, P[1], 8, P[2], 8, P[3], P[4], P[5], most, most, None, None, P[6], 8, P[7], None)
+    assert e.value.status == 2
+    dw.dwconv_causal_destroy(h)
+    dw.dwconv_delta_destroy(r)
