@@ -105,11 +105,7 @@ __global__ void __launch_bounds__(256) k_fwd(Geo G, const typename DT::X *x, int
             const int tt = t + u;
             if (tt >= stop) break;
             if (tt >= b) {  // the next sequence that holds a token
-                while (s + 1 < P.seqs && tt >= b) {
-                    ++s;
-                    a = P.begin(s);
-                    b = P.end(s);
-                }
+                P.advance(tt, s, a, b);
                 if (tt < a || tt >= b) return;  // behind the last sequence
                 const X *sn = state_in ? state_in + (int64_t)s * (K - 1) * G.C + c : nullptr;
                 fill_window<DT, VEC, K>(win, x, ldx, sn, G.C, a, tt);
@@ -308,11 +304,7 @@ __global__ void __launch_bounds__(256) k_bwd(Geo G, const typename DT::X *x, int
                     flush(b);
                     live = tt < t1;
                     if (!live) break;
-                    while (s + 1 < P.seqs && tt >= b) {
-                        ++s;
-                        a = P.begin(s);
-                        b = P.end(s);
-                    }
+                    P.advance(tt, s, a, b);
                     live = tt >= a && tt < b;
                     if (!live) break;
                     fill_window<DT, VEC, K>(win, x, ldx, state_in ? state_in + (int64_t)s * (K - 1) * G.C + c : nullptr,

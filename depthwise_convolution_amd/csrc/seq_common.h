@@ -117,6 +117,18 @@ struct Packed {
         }
         return lo;
     }
+    // From sequence s, which ends at or before t, to the one that may hold t: the next
+    // one as a rule, else by the search (any number of empty ones may lie between).
+    __device__ __forceinline__ void advance(int t, int &s, int &a, int &b) const {
+        if (s + 1 < seqs && end(s + 1) > t) ++s;
+        else s = find(t);
+        if (s < 0) {
+            a = b = 0;
+            return;
+        }
+        a = begin(s);
+        b = end(s);
+    }
 };
 
 // Which rows of a step share this row's cache entry.  Rows with the same slot

@@ -350,3 +350,27 @@ def test_more_sequences_than_2_to_the_30():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     del off
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("fmt,C,K", [("bf16", 64, 4), ("f32", 9, 3)])
+def test_many_empty_sequences_between_tokens(fmt, C, K):
+    """A border in the middle of a run with 2^26 empty sequences on it is passed in a
+    search, not one by one."""
+    say(f"[gpu] empty sequences {fmt}")
+    lens, n = [5, 30, 1, 20], 2 ** 26
+    x, w, dy = up(rand(60, C, seed=1, dtype=fmt)), up(rand(K, C, seed=2, dtype=fmt)), up(rand(60, C, seed=3, dtype=fmt))
+    conv, few = dw.CausalDepthwiseConv1d(C, K, fmt), offsets_of(lens)
+    off = torch.full((3 * n + 5,), 5, dtype=torch.int32, device=DEV)
+    off[0], off[n + 2:2 * n + 3], off[2 * n + 3:3 * n + 4], off[3 * n + 4] = 0, 35, 36, 56
+    assert off.diff().min() >= 0 and (off.diff() > 0).sum() == 4
+    y, want = torch.full((60, C), 7.0, dtype=x.dtype, device=DEV), torch.full((60, C), 7.0, dtype=x.dtype, device=DEV)
+    start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    conv(x, w, offsets=few, y=want)
+    start.record()
+    conv(x, w, offsets=off, y=y)
+    stop.record()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and start.elapsed_time(stop) < 100, start.elapsed_time(stop)
+    dx, dxw = y.clone(), y.clone()
+    a, b = (conv.backward(x, w, dy, offsets=o, dx=d) for o, d in ((off, dx), (few, dxw)))
+    assert torch.equal(dx, dxw) and torch.equal(a[1], b[1])
