@@ -560,7 +560,8 @@ class BlockNorm(_Plan):
 
     def __call__(self, o, residual=None, gate=None, scale=None, w_after=None, b_after=None, w_before=None,
                  b_before=None, rows_per_gate=1, h=None, y=None, stream=None):
-        """Returns (h, y); y is None where ``before`` is "none"."""
+        """Returns (h, y); y is None where ``before`` is "none" (a given one is not
+        written)."""
         dev, rows, per = self._common(o, residual, gate, scale, w_after, b_after, w_before, b_before, rows_per_gate)
 
         def body(raw):
@@ -574,7 +575,7 @@ class BlockNorm(_Plan):
                 _dense("y", y, tuple(o.shape), self.dtype, dev)
             dwconv_norm_fwd(self.handle, rows, o, residual, gate, per, scale, w_after, b_after, w_before, b_before, h,
                             y, raw)
-            return h, y
+            return h, y if self.before else None
 
         return _on(dev, stream, body, o, residual, gate, scale, w_after, b_after, w_before, b_before, h, y)
 

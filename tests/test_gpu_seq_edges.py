@@ -374,3 +374,40 @@ def test_many_empty_sequences_between_tokens(fmt, C, K):
     dx, dxw = y.clone(), y.clone()
     a, b = (conv.backward(x, w, dy, offsets=o, dx=d) for o, d in ((off, dx), (few, dxw)))
     assert torch.equal(dx, dxw) and torch.equal(a[1], b[1])
+
+
+def test_norm_without_a_second_norm_returns_no_second_output():
+    o, w = up(rand(5, 64)), torch.ones(64, device=DEV)
+    given = torch.full_like(o, 7.0)
+    h, y = dw.BlockNorm(64, "f32", before="none")(o, w_after=w, y=given)
+    assert y is None and (given == 7.0).all() and torch.isfinite(h).all()
+
+
+def test_captured_with_a_given_stream():
+    """Passes captured on the stream that they are given, inputs dropped inside the
+    capture, replayed between eager ones."""
+    conv, rule = dw.CausalDepthwiseConv1d(192, 4, "bf16"), dw.GatedDeltaRule(1, 1, 64, 64, "bf16")
+    x, w, b = up(rand(130, 192, seed=1, dtype="bf16")), up(rand(4, 192, seed=2, dtype="bf16")), up(rand(192, seed=3))
+    g, beta = -up(rand(130, 1, seed=4)).abs(), torch.sigmoid(up(rand(130, 1, seed=5)))
+
+    def passes(stream):
+        mixed = conv(x * 2, w, b, stream=stream)
+        q, k, v = (t.unflatten(1, (1, 64)) for t in mixed.split([64, 64, 64], 1))
+        o = rule(q, k, v, g, beta, stream=stream)
+        del mixed, q, k, v
+        return o, conv.backward(x * 3, w, x * 5, b, stream=stream)[1]
+
+    want = [t.clone() for t in passes(None)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = passes(torch.cuda.current_stream())
+    for _ in range(3):
+        for t in got:
+            t.fill_(-7)
+        eager = passes(None)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(got, want, eager))
+    del graph
