@@ -7,8 +7,8 @@
 // x = S^T k and y = S^T q over the state as it was,
 //   u = beta (v - a x),   o = a y + (k . q) u,   S <- a S + k u^T
 // so both sums come from one pass and one exchange through LDS.
-// Measured, bf16, 32 heads of 128 x 128: 96 sequences 89 us (4.5 TB/s; a large
-// copy 5.15), one sequence 5.6 us.
+// Measured, bf16, 32 heads of 128 x 128, states from HBM: 96 sequences 86 us
+// (4.7 TB/s; a large copy 5.15), one sequence 5.5 us.
 #include "seq_common.h"
 #include "seq_plan.h"
 
@@ -154,11 +154,16 @@ hipError_t pick(const Ctx &c, hipStream_t st) {
                      (((uintptr_t)c.v | (uintptr_t)c.o) & (4 * sizeof(X) - 1)) == 0;
     const int pad = (c.Dk + 63) / 64;
     if (!vec) return pad <= 2 ? launch<DT, 1, 32, 16>(c, st) : launch<DT, 1, 32, 32>(c, st);
-    // 128 columns a workgroup read whole 512-byte rows; with few heads in
-    // flight 32 columns a workgroup put four times as many CUs to work (bf16,
-    // 32 heads of 128 x 128, 128 against 32 columns: 1 sequence 7.4 and 5.0 us,
-    // 8: 8.7 and 7.6, 16: 11.6 and 14.5, 96: 65 and 67)
-    if ((int64_t)c.rows * c.Hv < 512) return pad <= 2 ? launch<DT, 4, 8, 4>(c, st) : launch<DT, 4, 8, 8>(c, st);
+    // 32 columns a workgroup, whose lanes have few rows each; 128, which read whole
+    // 512-byte rows, where the heads make two to four workgroups a CU.  States from
+    // HBM, bf16, 32 heads of 128 x 128, 32 and 128 columns: 1 sequence 5.5 and 7.8 us,
+    // 4: 7.8 and 9.6, 8: 13.0 and 12.8, 16: 21.4 and 19.4, 32: 34.9 and 36.0, 64: 59.6
+    // and 64.7, 96: 86 and 90, 192: 167 and 165; 16 and 48 sequences with keys of 256:
+    // 34.1 and 33.5, 84.8 and 93.2; 24 and (16 heads of 64 x 64) 192 sequences with keys
+    // of 64: 20.4 and 15.7, 63.5 and 65.9.  (Where the finer grid passes its limit too.)
+    const int64_t heads = (int64_t)c.rows * c.Hv;
+    if (heads < 512 || (heads >= 1024 && heads * ((c.Dv + 31) / 32) < (1 << 24)))
+        return pad <= 2 ? launch<DT, 4, 8, 4>(c, st) : launch<DT, 4, 8, 8>(c, st);
     return pad <= 2 ? launch<DT, 4, 32, 16>(c, st) : launch<DT, 4, 32, 32>(c, st);
 }
 

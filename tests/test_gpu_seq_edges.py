@@ -9,6 +9,7 @@ import seq_reference as ref
 from gpu_helpers import DEV, say
 from seq_cases import CONV_GRADS, conv_grad_bounds, conv_grad_data, readback, readback_bound, readback_terms
 from seq_reference import leaves, rel
+import test_gpu_seq
 from test_gpu_seq import delta_data, offsets_of, rand, up
 
 pytestmark = pytest.mark.gpu
@@ -411,3 +412,10 @@ def test_captured_with_a_given_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(got, want, eager))
     del graph
+
+
+@pytest.mark.parametrize("case", [("bf16", 4, 8, 128, 128, 140), ("f16", 2, 16, 200, 48, 66), ("f32", 1, 4, 30, 68, 300)],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_delta_steps_of_many_heads(case):
+    """More than 1024 heads of all rows together."""
+    test_gpu_seq.test_delta_steps_follow_the_definition(case)
