@@ -9,9 +9,10 @@
 // while the present ones are computed.  Sequence borders are met on the way:
 // at a border the window is filled from the state instead.
 // Measured, K = 4, bf16, inputs from HBM: forward 16384 tokens x 8192 channels
-// 122 us (4.4 TB/s; a large copy 5.15), gradients of 8192 x 8192 95 us
-// (4.2 TB/s), one token of 8192 channels 3.1 us.  Rows that are not aligned run
-// single elements: fp32 gradients of 8191 x 2049, K = 3, 67 us (3.0 TB/s).
+// 124 us (4.3 TB/s; a large copy 5.15), gradients of 8192 x 8192 95 us
+// (4.2 TB/s), one token of 8192 channels 3.1 us.  Rows that are not 16-byte aligned
+// run single elements here, which is this kernel's choice (the loads themselves need
+// only the element's alignment): fp32 gradients of 8191 x 2049, K = 3, 68 us (3.0 TB/s).
 #include "seq_common.h"
 #include "seq_plan.h"
 
@@ -379,11 +380,11 @@ __global__ void __launch_bounds__(256) k_sum(const float *part, int64_t runs, in
 
 // Tokens a lane walks: long runs spend less on the rows around them (and on
 // the run's sums in the backward pass); short ones give the chip enough waves.
-// bf16, K = 4, runs of 8 and of 64 tokens: forward 128 and 122 us at 16384
-// tokens x 8192 channels, 12 and 33 us at 4096 x 2048; backward with its sums
-// 200 and 102 us at 8192 x 8192, 35 and 62 us at 4096 x 2048.  The backward
+// bf16, K = 4, inputs from HBM, runs of 8 and of 64 tokens: forward 136 and 125 us
+// at 16384 tokens x 8192 channels, 15 and 36 us at 4096 x 2048; backward with its
+// sums 195 and 100 us at 8192 x 8192, 35 and 63 us at 4096 x 2048.  The backward
 // pass, which writes sums for every run, stops at half the lanes (4096 x 2048,
-// runs of 8, 16 and 32 tokens: 35, 31 and 39 us; forward 12, 13 and 20 us).
+// runs of 8 and 16 tokens: 35 and 32 us; forward 15 and 17 us).
 int run_tokens(int tokens, int C, int vec, bool back) {
     int tt = 64;
     const int64_t ncv = (C + vec - 1) / vec, lanes = back ? 65536 : 131072;

@@ -44,8 +44,11 @@
 //
 // Bound by fp32 matrix products (the walks: one wavefront's chain of them).
 // Measured, fp32, heads of 128 x 128: 8192 tokens, 16 key and 32 value heads,
-// five sequences: k_prepare 169 us, k_scan 658; gradients of 4096 tokens, 8 and
-// 16 heads, four sequences: k_prepare 57, k_scan 225, k_rscan 300, k_grad 418.
+// five sequences: k_prepare 176 us, k_scan 646; gradients of 4096 tokens, 8 and
+// 16 heads, four sequences: k_prepare 61, k_scan 230, k_rscan 302, k_grad 422 (with
+// 62 spilled registers a lane; 319 and 393 at keys of 192 and 256).  The forward walk's
+// products would take 197 us at the rate of a large fp32 product; here one wavefront
+// has the whole chain for 16 columns.
 #include <type_traits>
 
 #include "delta_common.h"

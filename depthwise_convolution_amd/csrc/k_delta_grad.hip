@@ -17,10 +17,10 @@
 //
 // 2900 products of 16x16x32 a head and chunk at Dk = Dv = 128 (11.6 thousand
 // cycles of a CU) against 128 KB of states read.  Measured, bf16, 4096 tokens in
-// four sequences, 8 key and 16 value heads: 164 us, some 65 thousand cycles a head
+// four sequences, 8 key and 16 value heads: 165 us, some 65 thousand cycles a head
 // and chunk: bound by waits for loads and barriers with two wavefronts a SIMD,
 // and by whole rounds of workgroups, one a CU (here 528: one sequence's 512 take
-// 114 us, 520 take 153, 768 take 166).
+// 112 us, 520 take 151, 768 take 168).
 #include "delta_split.h"
 
 namespace dw {
@@ -138,7 +138,8 @@ __global__ void __launch_bounds__(512) k_grad(Ctx c, GradArgs ga) {
     }
     // Operands of a head's next 32 columns.  The next head's first ones are on their
     // way while the sums over tokens run (167 -> 164 us at the sizes above), where there
-    // are registers for it: keys of more than 128 channels would spill.
+    // are registers for it: keys of more than 128 channels would spill (those of 256 do as
+    // it is, 65 and 75 registers a lane for bf16 and fp16).
     constexpr bool AHEAD = T == 1;
     f32x4 s0[T][2], ds[T][2], ud[2];  // ud: U (first half) or dR
     u32x4 od, vv;

@@ -22,11 +22,12 @@
 //
 // Bound by each chunk's chain of dependent products, splits and barriers, not
 // by a rate: measured, bf16, heads of 128 x 128, 8192 tokens of 32 value heads
-// in five sequences, k_scan 196 us (91 matrix instructions of 16 cycles a
-// wavefront and chunk in some nine thousand cycles; one wavefront for a group
-// of columns took 265 us, fetches in bursts 208); gradients of 4096 tokens, 16 heads,
-// four sequences: k_scan 60, k_rscan 92.  One fp16 sequence of 5003 tokens, 6
-// heads of 96 x 104: 153 us, 1.9 us a chunk.
+// in five sequences, k_scan 188 to 197 us (108 matrix instructions of 16 cycles a
+// wavefront and chunk in some nine thousand cycles), 640 workgroups on 512 places;
+// gradients of 4096 tokens, 16 heads, four sequences: k_scan 60, k_rscan 94.  One
+// fp16 sequence of 5003 tokens, 6 heads of 96 x 104: 154 us, 1.9 us a chunk.  Few
+// registers spill: 6 a lane in k_rscan of bf16 with 32 columns at keys of 128 and
+// with 16 at keys of 256, 11 in k_scan of bf16 with 16 columns at keys of 256.
 #include "delta_split.h"
 
 namespace dw {
@@ -36,8 +37,11 @@ using namespace delta;
 
 // One chunk and key head: lengths, the triangles of its value heads, and all
 // left operands as fragments.  8192 tokens, 16 key and 32 value heads of 128,
-// bf16: 88 us, bound by the latency of the triangle's inverse (16 dependent
-// steps a tile, then the tiles below it), three workgroups a CU.
+// bf16: 90 us, bound by the latency of the triangle's inverse (16 dependent
+// steps a tile, then the tiles below it), three workgroups a CU, for which four
+// registers a lane spill at keys of up to 128 channels.  It writes 38 KB a value head
+// and chunk and 48 KB a key head, 260 MB here, which the walks read back once for
+// each group of columns.
 // (LDS: the rows of q and k, later the triangles.)
 template <int DK>
 constexpr size_t lds_prepare() {
@@ -371,8 +375,10 @@ __device__ __forceinline__ void keep_tokens(float *p, const Ctx &c, const f32x4 
 // Which walk a workgroup has.  The column groups of the value heads of one key
 // head and sequence (a unit) share operands: they go to one XCD, one behind the
 // other; units go round the XCDs, so that each gets its share of every
-// sequence.  `width`: columns walked (the backward pass also fills the padded
-// ones).  A grid that the XCDs do not divide has workgroups without a walk.
+// sequence.  Fewer than eight units leave XCDs without work: 8192 bf16 tokens in
+// one sequence, 16 value heads of 128 x 128, k_scan with 16 key heads 224 us, with
+// one 577.  `width`: columns walked (the backward pass also fills the padded ones).
+// A grid that the XCDs do not divide has workgroups without a walk.
 struct Walk {
     int first, h, s;
     __device__ __forceinline__ Walk(const Ctx &c, int cols, int width) {
@@ -729,9 +735,11 @@ __global__ void __launch_bounds__(256, (walks_a_cu<DT, DK, NT>())) k_rscan(Ctx c
 }
 
 // Columns of the state a workgroup walks: 32, or 16 where a CU would have no
-// second walk to fill its waits.  8192 bf16 tokens, 32 heads of 128 x 128, k_scan
-// with 16 columns against 32: one sequence (128 walks of 32 columns) 273 and
-// 369 us, two 216 and 238, three 229 and 200, five 234 and 197.
+// second walk to fill its waits, were the walks spread over all CUs (Walk says when
+// they are not).  8192 bf16 tokens, 16 key and 32 value heads of 128 x 128, k_scan
+// with 16 columns against 32: one sequence (128 walks of 32 columns) 294 and
+// 355 us, two 230 and 232, three 245 and 202, five 258 and 189; one fp16 sequence of
+// 5003 tokens, 6 heads of 96 x 104: 154 and 261.
 int walk_tiles(const Ctx &c) { return (int64_t)c.seq.seqs * c.Hv * ((c.Dv + 31) / 32) <= 256 ? 1 : 2; }
 
 template <int NT>

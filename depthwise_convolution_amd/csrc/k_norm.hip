@@ -2,7 +2,7 @@
 // and the norm before the next block (include/dwconv_seq.h), in one pass over
 // the rows, and their gradients.
 //
-// Bound by HBM: each tensor is read or written once.  A row lives in the
+// Bound by HBM up to 4096 channels: each tensor is read or written once.  A row lives in the
 // registers of TPR lanes (part of a wavefront, or a workgroup where rows are
 // long), E channels a lane, so that the second norm and the backward pass's
 // row sums need no second read; the backward pass forms the forward pass's
@@ -13,7 +13,10 @@
 // (5.3 TB/s; a large copy 5.15), residual block norm of 8192 rows of 4096 55 us
 // (4.9 TB/s); gradients of 200704 fp16 rows of 96 with a gate an image 96 us
 // (2.4 TB/s): there vector operations bound, some 60 a channel and eight sums a
-// row, with 12 of a row's 16 lanes at work.
+// row, with 12 of a row's 16 lanes at work; of 8192 bf16 rows of 4096, residual and
+// two norms, 143 us (2.8 TB/s).  Gradients of longer rows run 1024 lanes, which have
+// 128 registers each and spill 180 to 1208 of them to memory, again for every row:
+// 4096 bf16 rows of 5120 432 us and of 8192 466, where their bytes take 49 and 78.
 #include "seq_common.h"
 #include "seq_plan.h"
 
@@ -483,16 +486,17 @@ __global__ void __launch_bounds__(1024) k_sum(const float *part, int64_t blocks,
 }
 
 // Lanes a row of the backward pass, 8 channels each (their arrays and sums stay
-// in registers; 16 only for rows of more than 8192); the forward pass takes 16
-// channels a lane where that saves lanes (8192 bf16 rows, 16 channels against
-// 8: 14 and 19 us at D = 1024, 42 and 44 us at 4096).
+// in registers up to 512 lanes; 16 only for rows of more than 8192); the forward
+// pass takes 16 channels a lane where that saves lanes (8192 bf16 rows from HBM, 16
+// channels against 8: 16 and 23 us at D = 1024, 38 and 43 at 2560, 53 and 52 at 4096).
 int lanes_of(int D) { return D <= 128 ? 16 : D <= 512 ? 64 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024; }
 
 // Two workgroups a CU (one of more than 256 lanes), each with rows enough for
 // its sums to be worth writing: more write more sums and read parameters more
-// often, fewer leave loads without company.  200704 fp16 rows of 96, one, two,
-// three and four a CU, with the join: 122, 82, 99 and 93 us; 8192 bf16 rows of
-// 4096, one, two and four: 143, 147 and 161 us.
+// often, fewer leave loads without company.  Inputs from HBM, with the join, one, two,
+// three and four a CU: 200704 fp16 rows of 96 146, 97, 124 and 109 us, 262144 bf16
+// rows of 128 157, 101, 129 and 106; 8192 bf16 rows of 4096, one, three and four:
+// 143, 157 and 164 us, 4096 of 8192 466, 558 and 565.
 Deal deal_of(int D, int rows, int per) {
     const int tpr = lanes_of(D), rpb = tpr >= 256 ? 1 : 256 / tpr, target = tpr > 256 ? 256 : 512;
     Deal d{};

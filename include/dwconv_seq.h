@@ -142,14 +142,15 @@ dwconv_status_t dwconv_causal_bwd(dwconv_causal_t h, const void *x, int64_t ldx,
  *   state_*    seqs x Hv x Dk x Dv float, dense; NULL state_in: zeros; NULL
  *              state_out: not written; state_out may be state_in itself
  *
- * Forward, a NaN or infinity reaches no token before its own, no other sequence
- * or head and, from v or a state, no other column of the state; from its own
- * token on the outputs that depend on it are not finite.  In the gradients it
- * may reach any token of its sequence and the heads that share its key head.
+ * Forward, a NaN or infinity reaches no token before its own, no other sequence,
+ * no other head (from q and k: the value heads of their key head) and, from v or a
+ * state, no other column of the state; from its own token on the outputs that
+ * depend on it are not finite.  In the gradients it may reach any token of its
+ * sequence and the heads that share its key head.
  * ------------------------------------------------------------------------ */
 
-/* Hk, Hv >= 1, Hv a multiple of Hk, 1 <= Dk <= 256, 1 <= Dv <= 4096, dtype
- * F32 / F16 / BF16, finite scale, eps >= 0 and finite. */
+/* Hk, Hv >= 1, Hv a multiple of Hk and at most 65536, 1 <= Dk <= 256, 1 <= Dv <=
+ * 4096, dtype F32 / F16 / BF16, finite scale, eps >= 0 and finite. */
 dwconv_status_t dwconv_delta_create(dwconv_delta_t *out, int Hk, int Hv, int Dk, int Dv,
                                     dwconv_dtype_t dtype, float scale, int normalize, float eps);
 dwconv_status_t dwconv_delta_destroy(dwconv_delta_t h);
