@@ -16,12 +16,12 @@ devices and strides, and allocate outputs and workspaces with torch:
     z, _ = norm(o, gate=gate, w_after=w)
 
 ``offsets`` (int32, one more than there are sequences) cuts the tokens into
-sequences; outputs of tokens behind the last one are left as they were.  What a
-call allocates belongs to ``stream`` where one is given, else to torch's
-current stream of the tensors' device.  A given stream does not wait for the
-current one: order them with ``wait_stream``.  The caller's tensors may be dropped
-after a call on a torch stream; on a raw handle they have to live until the stream
-has passed the call.
+sequences; outputs of tokens behind the last one are left as they were (not
+initialised where the call allocates them).  What a call allocates belongs to
+``stream`` where one is given, else to torch's current stream of the tensors'
+device.  A given stream does not wait for the current one: order them with
+``wait_stream``.  The caller's tensors may be dropped after a call on a torch
+stream; on a raw handle they have to live until the stream has passed the call.
 
 Nothing is recorded for autograd; ``backward`` gives the gradients.  A tensor that
 requires a gradient is refused while gradients are enabled: the outputs would carry
@@ -173,8 +173,8 @@ def dwconv_delta_step(h, q, ldq, k, ldk, v, ldv, g, beta, state, slots, n_slots,
 def dwconv_delta_bwd(h, q, ldq, k, ldk, v, ldv, g, beta, offsets, seqs, tokens, state_in, d_o, lddo, dstate_out, dq,
                      lddq, dk, lddk, dv, lddv, dg, dbeta, dstate_in, workspace, stream):
     _call("dwconv_delta_bwd", h, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(g), _p(beta), _p(offsets), _n("seqs", seqs),
-          _n("tokens", tokens), _p(state_in), _p(d_o), lddo, _p(dstate_out), _p(dq), lddq, _p(dk), lddk, _p(dv), lddv, _p(dg), _p(dbeta),
-          _p(dstate_in), _p(workspace), stream)
+          _n("tokens", tokens), _p(state_in), _p(d_o), lddo, _p(dstate_out), _p(dq), lddq, _p(dk), lddk, _p(dv), lddv,
+          _p(dg), _p(dbeta), _p(dstate_in), _p(workspace), stream)
 
 
 def dwconv_norm_create(D, dtype, after, before, gate_act, eps):
@@ -200,8 +200,8 @@ def dwconv_norm_bwd_workspace(p, rows, rows_per_gate) -> int:
 def dwconv_norm_bwd(p, rows, o, residual, gate, rows_per_gate, scale, w_after, b_after, w_before, b_before, dh, dy,
                     d_o, dresidual, dgate, dscale, dw_after, db_after, dw_before, db_before, workspace, stream):
     _call("dwconv_norm_bwd", p, _n("rows", rows), _p(o), _p(residual), _p(gate), _n("rows_per_gate", rows_per_gate),
-          _p(scale), _p(w_after), _p(b_after), _p(w_before), _p(b_before), _p(dh), _p(dy), _p(d_o), _p(dresidual), _p(dgate), _p(dscale),
-          _p(dw_after), _p(db_after), _p(dw_before), _p(db_before), _p(workspace), stream)
+          _p(scale), _p(w_after), _p(b_after), _p(w_before), _p(b_before), _p(dh), _p(dy), _p(d_o), _p(dresidual),
+          _p(dgate), _p(dscale), _p(dw_after), _p(db_after), _p(dw_before), _p(db_before), _p(workspace), stream)
 
 
 # --- plans with checks and allocation --------------------------------------
