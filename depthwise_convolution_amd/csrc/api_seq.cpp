@@ -312,4 +312,165 @@ dwconv_status_t dwconv_norm_bwd(dwconv_norm_t p, int rows, const void *o, const 
     return status(dw::norm_bwd(*p, a, stream));
 }
 
+dwconv_status_t dwconv_scan_create(dwconv_scan_t *out, int C, int N, int G, dwconv_dtype_t dtype, int softplus,
+                                   dwconv_seq_act_t gate_act) {
+    if (!out) return DWCONV_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (C < 1 || C > 1 << 24 || N < 1 || N > 128 || G < 1 || C % G || !float_dtype(dtype) ||
+        (int)gate_act < 0 || gate_act > DWCONV_SEQ_ACT_SIGMOID)
+        return DWCONV_ERR_INVALID_ARG;
+    return make(out, dwconv_scan_plan{C, N, G, (int)dtype, softplus != 0, (int)gate_act});
+}
+
+dwconv_status_t dwconv_scan_destroy(dwconv_scan_t h) {
+    delete h;
+    return DWCONV_OK;
+}
+
+dwconv_status_t dwconv_scan_workspace(dwconv_scan_t h, int seqs, int tokens, int backward, size_t *bytes) {
+    if (!h || !bytes || seqs < 0 || seqs > MOST || tokens < 0 || tokens > MOST) return DWCONV_ERR_INVALID_ARG;
+    *bytes = dw::scan_bytes(*h, seqs, tokens, backward != 0);
+    return DWCONV_OK;
+}
+
+// fills `s` with what the three passes read; false where it is not usable
+static bool scan_inputs(dw::ScanArgs &s, dwconv_scan_t h, const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                        const float *a, const void *b, int64_t ldb, const void *c, int64_t ldc, const float *skip,
+                        const float *dt_bias, const void *gate, int64_t ldgate, int n) {
+    if (!h || !a) return false;
+    const int e = elem(h->dtype);
+    const int64_t states = (int64_t)h->G * h->N;
+    if (!tensor(x, ldx, h->C, n, e) || !tensor(dt, lddt, h->C, n, e) || !tensor(b, ldb, states, n, e) ||
+        !tensor(c, ldc, states, n, e) || (gate && !tensor(gate, ldgate, h->C, n, e)) || !at(a, 4) || !at(skip, 4) ||
+        !at(dt_bias, 4))
+        return false;
+    s.x = x, s.ldx = ldx, s.dt = dt, s.lddt = lddt, s.a = a, s.b = b, s.ldb = ldb, s.c = c, s.ldc = ldc, s.skip = skip;
+    s.bias = dt_bias, s.gate = gate, s.ldgate = ldgate, s.tokens = n;
+    return true;
+}
+
+dwconv_status_t dwconv_scan_fwd(dwconv_scan_t h, const void *x, int64_t ldx, const void *dt, int64_t lddt, const float *a,
+                                const void *b, int64_t ldb, const void *c, int64_t ldc, const float *skip,
+                                const float *dt_bias, const void *gate, int64_t ldgate, const int32_t *offsets, int seqs,
+                                int tokens, const float *state_in, float *state_out, void *y, int64_t ldy, void *workspace,
+                                hipStream_t stream) {
+    dw::ScanArgs s{};
+    if (!sequences(offsets, seqs, tokens) ||
+        !scan_inputs(s, h, x, ldx, dt, lddt, a, b, ldb, c, ldc, skip, dt_bias, gate, ldgate, tokens) ||
+        !tensor(y, ldy, h->C, tokens, elem(h->dtype)) || !at(state_in, 4) || !at(state_out, 4) || !at(workspace, 16) ||
+        (tokens && (y == x || y == dt || y == b || y == c || y == gate)) ||
+        (!workspace && dw::scan_bytes(*h, seqs, tokens, false)))
+        return DWCONV_ERR_INVALID_ARG;
+    const size_t st = (size_t)seqs * h->C * h->N * sizeof(float);
+    if (state_in != state_out && overlap(state_in, st, state_out, st)) return DWCONV_ERR_INVALID_ARG;
+    s.offsets = offsets, s.seqs = seqs, s.state_in = state_in, s.state_out = state_out, s.y = y, s.ldy = ldy;
+    s.workspace = (float *)workspace;
+    return status(dw::scan_fwd(*h, s, stream));
+}
+
+dwconv_status_t dwconv_scan_step(dwconv_scan_t h, const void *x, int64_t ldx, const void *dt, int64_t lddt, const float *a,
+                                 const void *b, int64_t ldb, const void *c, int64_t ldc, const float *skip,
+                                 const float *dt_bias, const void *gate, int64_t ldgate, float *state,
+                                 const int32_t *slots, int n_slots, int rows, void *y, int64_t ldy, hipStream_t stream) {
+    dw::ScanArgs s{};
+    if (!slots_ok(slots, n_slots, rows) ||
+        !scan_inputs(s, h, x, ldx, dt, lddt, a, b, ldb, c, ldc, skip, dt_bias, gate, ldgate, rows) ||
+        !tensor(y, ldy, h->C, rows, elem(h->dtype)) || !at(state, 4) ||
+        (rows && (!state || y == x || y == dt || y == b || y == c || y == gate)))
+        return DWCONV_ERR_INVALID_ARG;
+    s.state = state, s.slots = slots, s.n_slots = n_slots, s.y = y, s.ldy = ldy;
+    return status(dw::scan_step(*h, s, stream));
+}
+
+dwconv_status_t dwconv_scan_bwd(dwconv_scan_t h, const void *x, int64_t ldx, const void *dt, int64_t lddt, const float *a,
+                                const void *b, int64_t ldb, const void *c, int64_t ldc, const float *skip,
+                                const float *dt_bias, const void *gate, int64_t ldgate, const int32_t *offsets, int seqs,
+                                int tokens, const float *state_in, const void *dy, int64_t lddy, const float *dstate_out,
+                                void *dx, int64_t lddx, void *ddt, int64_t ldddt, float *da, void *db, int64_t lddb,
+                                void *dc, int64_t lddc, float *dskip, float *ddt_bias, void *dgate, int64_t lddgate,
+                                float *dstate_in, void *workspace, hipStream_t stream) {
+    dw::ScanArgs s{};
+    if (!sequences(offsets, seqs, tokens) ||
+        !scan_inputs(s, h, x, ldx, dt, lddt, a, b, ldb, c, ldc, skip, dt_bias, gate, ldgate, tokens) || !da)
+        return DWCONV_ERR_INVALID_ARG;
+    if (!gate) dgate = nullptr;
+    if (!skip) dskip = nullptr;
+    if (!dt_bias) ddt_bias = nullptr;
+    const int e = elem(h->dtype);
+    const int64_t states = (int64_t)h->G * h->N;
+    if (!tensor(dy, lddy, h->C, tokens, e) || !tensor(dx, lddx, h->C, tokens, e) || !tensor(ddt, ldddt, h->C, tokens, e) ||
+        !tensor(db, lddb, states, tokens, e) || !tensor(dc, lddc, states, tokens, e) ||
+        (dgate && !tensor(dgate, lddgate, h->C, tokens, e)) || !at(da, 4) || !at(dskip, 4) || !at(ddt_bias, 4) ||
+        !at(state_in, 4) || !at(dstate_out, 4) || !at(dstate_in, 4) || !at(workspace, 16) ||
+        (!workspace && dw::scan_bytes(*h, seqs, tokens, true)))
+        return DWCONV_ERR_INVALID_ARG;
+    const void *in[] = {x, dt, b, c, gate, dy, a}, *out[] = {dx, ddt, db, dc, dgate, da};
+    if (tokens)
+        for (const void *i : in)
+            for (const void *o : out)
+                if (i && i == o) return DWCONV_ERR_INVALID_ARG;
+    const size_t st = (size_t)seqs * h->C * h->N * sizeof(float);
+    if (overlap(state_in, st, dstate_in, st) || (dstate_in != dstate_out && overlap(dstate_out, st, dstate_in, st)))
+        return DWCONV_ERR_INVALID_ARG;
+    s.offsets = offsets, s.seqs = seqs, s.state_in = state_in, s.dy = dy, s.lddy = lddy, s.dstate_out = dstate_out;
+    s.dx = dx, s.lddx = lddx, s.ddt = ddt, s.ldddt = ldddt, s.da = da, s.db = db, s.lddb = lddb, s.dc = dc, s.lddc = lddc;
+    s.dskip = dskip, s.dbias = ddt_bias, s.dgate = dgate, s.lddgate = lddgate, s.dstate_in = dstate_in;
+    s.workspace = (float *)workspace;
+    return status(dw::scan_bwd(*h, s, stream));
+}
+
+dwconv_status_t dwconv_group_create(dwconv_group_t *out, int C, int G, dwconv_dtype_t dtype, dwconv_group_act_t act,
+                                    float eps) {
+    if (!out) return DWCONV_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (C < 1 || C > 65536 || G < 1 || C % G || !float_dtype(dtype) || (int)act < 0 || act > DWCONV_GROUP_ACT_RELU ||
+        !isfinite(eps) || eps < 0.0f)
+        return DWCONV_ERR_INVALID_ARG;
+    return make(out, dwconv_group_plan{C, G, (int)dtype, (int)act, eps});
+}
+
+dwconv_status_t dwconv_group_destroy(dwconv_group_t h) {
+    delete h;
+    return DWCONV_OK;
+}
+
+// images x pixels rows that an int counts, with the few thousand that a kernel's loops look ahead
+static bool group_rows(int images, int pixels) {
+    return images >= 0 && pixels >= 0 && (int64_t)images * pixels <= INT32_MAX - 65536;
+}
+
+dwconv_status_t dwconv_group_workspace(dwconv_group_t h, int images, int pixels, int backward, size_t *bytes) {
+    if (!h || !bytes || !group_rows(images, pixels)) return DWCONV_ERR_INVALID_ARG;
+    *bytes = dw::group_bytes(*h, images, pixels, backward != 0);
+    return DWCONV_OK;
+}
+
+dwconv_status_t dwconv_group_fwd(dwconv_group_t h, int images, int pixels, const void *x, int64_t ldx, const float *w,
+                                 const float *b, void *y, int64_t ldy, void *workspace, hipStream_t stream) {
+    if (!h || !group_rows(images, pixels)) return DWCONV_ERR_INVALID_ARG;
+    const int e = elem(h->dtype), n = images * pixels;
+    if (!tensor(x, ldx, h->C, n, e) || !tensor(y, ldy, h->C, n, e) || !at(w, 4) || !at(b, 4) || !at(workspace, 16) ||
+        (n && x == y && ldx != ldy) || (!workspace && dw::group_bytes(*h, images, pixels, false)))
+        return DWCONV_ERR_INVALID_ARG;
+    dw::GroupArgs a{};
+    a.images = images, a.pixels = pixels, a.x = x, a.ldx = ldx, a.w = w, a.b = b, a.y = y, a.ldy = ldy;
+    a.workspace = (float *)workspace;
+    return status(dw::group_fwd(*h, a, stream));
+}
+
+dwconv_status_t dwconv_group_bwd(dwconv_group_t h, int images, int pixels, const void *x, int64_t ldx, const float *w,
+                                 const float *b, const void *dy, int64_t lddy, void *dx, int64_t lddx, float *dw,
+                                 float *db, void *workspace, hipStream_t stream) {
+    if (!h || !group_rows(images, pixels)) return DWCONV_ERR_INVALID_ARG;
+    const int e = elem(h->dtype), n = images * pixels;
+    if (!tensor(x, ldx, h->C, n, e) || !tensor(dy, lddy, h->C, n, e) || !tensor(dx, lddx, h->C, n, e) || !at(w, 4) ||
+        !at(b, 4) || !at(dw, 4) || !at(db, 4) || !at(workspace, 16) || (n && (dx == x || (dx == dy && lddx != lddy))) ||
+        (!workspace && dw::group_bytes(*h, images, pixels, true)))
+        return DWCONV_ERR_INVALID_ARG;
+    dw::GroupArgs a{};
+    a.images = images, a.pixels = pixels, a.x = x, a.ldx = ldx, a.w = w, a.b = b, a.dy = dy, a.lddy = lddy;
+    a.dx = dx, a.lddx = lddx, a.dw = dw, a.db = db, a.workspace = (float *)workspace;
+    return status(dw::group_bwd(*h, a, stream));
+}
+
 }  // extern "C"

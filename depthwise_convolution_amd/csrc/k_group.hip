@@ -1,0 +1,643 @@
+// k_group.hip -- norm over groups of channels of an image, with an activation
+// (include/dwconv_seq.h): forward and gradients.
+//
+//   u = (x - mean) r,  r = 1 / sqrt(var + eps)      y = act(z), z = u w + b
+//   dz = dy act'(z)    dw = sum dz u    db = sum dz
+//   dx = r (dz w - mean(dz w) - u mean(dz w u))     means over the group
+//
+// A workgroup takes whole groups of channels (a slice) of a run of pixels; a lane one
+// vector of 16 bytes of channels, the same for all its pixels, so that sums over pixels
+// stay in registers until the lanes' sums meet in LDS.  Mean and squares around it are
+// two sums over values in registers: no difference of large sums.  Three ways to run it:
+//   resident   an image's slice fits the registers of a workgroup: one launch, every
+//              element read and written once
+//   in passes  runs of pixels give their mean and squares around it, which k_join puts
+//              together; further launches read the image again
+#include "seq_common.h"
+#include "seq_plan.h"
+
+namespace dw {
+namespace {
+
+// How an image's channels and pixels are dealt to workgroups.
+struct Geo {
+    int images, S, C, G, cg;      // S pixels, cg channels a group
+    int slices;                   // parts <= 1: slice i has the groups i G / slices up to (i + 1) G / slices
+    int parts, part;              // parts > 1: slice i is channels part (i % parts) up of group i / parts
+    int vpr, rpp;                 // vectors of a slice's row; rows a workgroup has in hand
+    int runs, rows;               // runs of so many pixels an image
+    int act;
+    float eps;
+};
+
+struct Slice {
+    int g0, ng, c0, w;  // its first group, groups (1 where it is part of one), channels
+};
+__device__ __forceinline__ Slice slice_of(const Geo &g, int i) {
+    if (g.parts > 1) {
+        const int grp = i / g.parts, at = i % g.parts * g.part;
+        return {grp, 1, grp * g.cg + at, min(g.part, g.cg - at)};
+    }
+    const int a = (int)((int64_t)i * g.G / g.slices), b = (int)((int64_t)(i + 1) * g.G / g.slices);
+    return {a, b - a, a * g.cg, (b - a) * g.cg};
+}
+
+template <class X, int V>
+struct __attribute__((packed, aligned(sizeof(X)))) Any {
+    X v[V];
+};
+
+// A lane's vector of channels.  The last vector of a row ends with the row; what it
+// has in common with the one before (`skip` elements) counts there.
+template <class DT, int V>
+struct Lane {
+    using X = typename DT::X;
+    int row, c, skip;  // row -1: nothing to do
+    __device__ __forceinline__ Lane(const Geo &g, const Slice &s) {
+        const int col = (int)threadIdx.x % g.vpr;
+        row = (int)threadIdx.x / g.vpr;
+        const int at = min(col * V, s.w - V);
+        c = s.c0 + at;
+        skip = col * V - at;
+        if (row >= g.rpp || skip >= V) row = -1, skip = V, c = s.c0;
+    }
+    __device__ __forceinline__ bool counts(int i) const { return i >= skip; }
+    static __device__ __forceinline__ Any<X, V> load(const X *p) { return *(const Any<X, V> *)p; }
+    // `whole`: elements of the vector before may be written too (with the same values)
+    __device__ __forceinline__ void store(X *p, const float (&v)[V], bool whole) const {
+        if (whole || skip == 0) {
+            Any<X, V> a;
+#pragma unroll
+            for (int i = 0; i < V; ++i) a.v[i] = rounded<DT>(v[i]);
+            *(Any<X, V> *)p = a;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (counts(i)) p[i] = rounded<DT>(v[i]);
+        }
+    }
+};
+
+// act(z), and its slope
+template <class DT>
+__device__ __forceinline__ float act_of(float z, int act) {
+    return act == DWCONV_GROUP_ACT_SILU ? z * sigmoid_f32<DT>(z) : act == DWCONV_GROUP_ACT_RELU ? (z < 0.0f ? 0.0f : z) : z;
+}
+template <class DT>
+__device__ __forceinline__ float slope_of(float z, int act) {
+    if (act == DWCONV_GROUP_ACT_SILU) {
+        float q;
+        const float p = sigmoid_f32<DT>(z, q);
+        return p * __builtin_fmaf(z, q, 1.0f);
+    }
+    return act == DWCONV_GROUP_ACT_RELU ? (z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z) : 1.0f;
+}
+
+// Sums over a workgroup's lanes.  `cols` becomes the sums over rows of each channel of
+// the slice (in up to `segs` parts, segs x wide), `of_groups` those over the groups'
+// channels.  Every lane calls them; a barrier stands at the end of each.
+template <int TH, int V>
+struct Sums {
+    static constexpr int SEGS = 32;
+    float *lanes, *cols, *stat;  // TH x V, max(TH, TH x V), as many as groups
+    int wide, segs;
+    __device__ __forceinline__ Sums(float *lanes, float *cols, float *stat, const Geo &g)
+        : lanes(lanes), cols(cols), stat(stat), wide(g.vpr * V), segs(min(max(TH / (g.vpr * V), 1), g.rpp)) {}
+    template <class L>
+    __device__ __forceinline__ void rows(const float (&v)[V], const L &ln, const Geo &g) {
+        const int width = g.vpr * V;
+#pragma unroll
+        for (int i = 0; i < V; ++i) lanes[(int)threadIdx.x * V + i] = ln.row >= 0 && ln.counts(i) ? v[i] : 0.0f;
+        __syncthreads();
+        for (int k = threadIdx.x; k < width * segs; k += TH) {
+            float s = 0.0f;
+            for (int r = k / width; r < g.rpp; r += segs) s += lanes[r * width + k % width];
+            cols[k] = s;
+        }
+        __syncthreads();
+    }
+    // Column of channel i of the slice: the last vector is moved back by what it shares.
+    __device__ __forceinline__ int column(const Slice &s, int i) const {
+        const int last = (s.w + V - 1) / V - 1;
+        return i >= last * V ? i + (last + 1) * V - s.w : i;
+    }
+    __device__ __forceinline__ float channel(const Slice &s, int i) const {
+        const int at = column(s, i);
+        float t = 0.0f;
+        for (int k = 0; k < segs; ++k) t += cols[k * wide + at];
+        return t;
+    }
+    // stat[j] = done(sum of f(channel) over group j's channels): a wavefront a group, or
+    // a lane where groups are small
+    template <class F, class D>
+    __device__ __forceinline__ void of_groups(const Slice &s, int cg, F f, D done) {
+        const int n = s.ng > 1 ? cg : s.w;
+        if (n * segs <= 32) {
+            for (int j = threadIdx.x; j < s.ng; j += TH) {
+                float t = 0.0f;
+                for (int i = 0; i < n; ++i) t += f(j * n + i, channel(s, j * n + i));
+                done(j, t);
+            }
+        } else {
+            for (int j = (int)threadIdx.x >> 6; j < s.ng; j += TH / 64) {
+                float t = 0.0f;
+                for (int i = (int)threadIdx.x & 63; i < n; i += 64) t += f(j * n + i, channel(s, j * n + i));
+                t = sum_wave(t);
+                if (((int)threadIdx.x & 63) == 0) done(j, t);
+            }
+        }
+        __syncthreads();
+    }
+};
+
+__device__ __forceinline__ float inverse_root(float var, float eps) { return 1.0f / sqrtf(var + eps); }
+
+// A group's mean and r, where a lane's channel i of the slice belongs to it
+template <int V>
+struct Group {
+    int of[V];  // group of the slice, for each of the lane's channels
+    template <class L>
+    __device__ __forceinline__ Group(const Geo &g, const Slice &s, const L &ln) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) of[i] = s.ng > 1 ? (ln.c + i) / g.cg - s.g0 : 0;
+    }
+};
+
+__device__ __forceinline__ void params(float &v, const float *p, int c, float other) { v = p ? p[c] : other; }
+
+// The run's or image's mean of each group (in stat) and squares around it (in sq).
+template <class DT, int V, int TH, int K, class L>
+__device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &ln, const Group<V> &gr,
+                                        const Any<typename DT::X, V> (&x)[K], int n, Sums<TH, V> &sum, float *stat, float *sq,
+                                        float (&mean)[V]) {
+    const float inv = 1.0f / ((float)n * (float)(s.ng > 1 ? g.cg : s.w));
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (ln.row + k * g.rpp < n) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] += DT::widen(x[k].v[i]);
+        }
+    sum.rows(v, ln, g);
+    sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { stat[j] = t * inv; });
+#pragma unroll
+    for (int i = 0; i < V; ++i) mean[i] = stat[gr.of[i]], v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (ln.row + k * g.rpp < n) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float d = DT::widen(x[k].v[i]) - mean[i];
+                v[i] = __builtin_fmaf(d, d, v[i]);
+            }
+        }
+    sum.rows(v, ln, g);
+    sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { sq[j] = t; });
+}
+
+// K vectors of a lane, of the pixels row, row + rpp ... of a run of n
+template <class DT, int V, int K, class L>
+__device__ __forceinline__ void take(Any<typename DT::X, V> (&x)[K], const typename DT::X *p, int64_t ld, const Geo &g,
+                                     const L &ln, int n) {
+    if (ln.row < 0) return;
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = L::load(p + (int64_t)min(ln.row + k * g.rpp, n - 1) * ld + ln.c);
+}
+
+// Forward: resident (RUNS false), or the moments of a run of pixels (RUNS true), left
+// as mean and squares in stats[image][group][run x parts].
+template <class DT, int V, int TH, int K, bool RUNS>
+__global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int64_t ldx, const float *w, const float *b,
+                                            typename DT::X *y, int64_t ldy, float2 *stats, int max_groups) {
+    using X = typename DT::X;
+    extern __shared__ __align__(16) float sh[];
+    float *stat = sh + 2 * TH * V, *sq = stat + max_groups;
+    Sums<TH, V> sum(sh, sh + TH * V, stat, g);
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
+    const Slice s = slice_of(g, sl);
+    const Lane<DT, V> ln(g, s);
+    const Group<V> gr(g, s, ln);
+    const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
+    x += ((int64_t)img * g.S + p0) * ldx;
+    Any<X, V> v[K];
+    take<DT, V>(v, x, ldx, g, ln, n);
+    float mean[V];
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, sum, stat, sq, mean);
+    if (RUNS) {
+        const int per = g.runs * max(g.parts, 1), at = run * max(g.parts, 1) + (g.parts > 1 ? sl % g.parts : 0);
+        for (int j = threadIdx.x; j < s.ng; j += TH)
+            stats[((int64_t)img * g.G + s.g0 + j) * per + at] = make_float2(stat[j], sq[j]);
+        return;
+    }
+    const float inv = 1.0f / ((float)n * (float)g.cg);
+    float scale[V], shift[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        params(scale[i], w, ln.c + i, 1.0f);
+        params(shift[i], b, ln.c + i, 0.0f);
+        scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
+    }
+    if (ln.row < 0) return;
+    y += ((int64_t)img * g.S + p0) * ldy + ln.c;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int r = ln.row + k * g.rpp;
+        if (r >= n) break;
+        float o[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            o[i] = act_of<DT>(__builtin_fmaf(DT::widen(v[k].v[i]) - mean[i], scale[i], shift[i]), g.act);
+        ln.store(y + (int64_t)r * ldy, o, true);  // all loads of the slice are behind a barrier
+    }
+}
+
+// Puts the moments of a group's runs together: a wavefront a group.  With counts n_i,
+// means m_i and squares q_i: m = sum n_i m_i / n and q = sum (q_i + n_i (m_i - m)^2).
+// out: mean and r.
+__global__ void __launch_bounds__(256) k_join(Geo g, const float2 *stats, float2 *out) {
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (id >= (int64_t)g.images * g.G) return;
+    const int lane = threadIdx.x & 63, parts = max(g.parts, 1), per = g.runs * parts;
+    const float2 *p = stats + id * per;
+    auto count = [&](int i) {
+        const int run = i / parts, part = i % parts;
+        return (float)min(g.rows, g.S - run * g.rows) * (float)(parts > 1 ? min(g.part, g.cg - part * g.part) : g.cg);
+    };
+    const float inv = 1.0f / ((float)g.S * (float)g.cg);
+    float m = 0.0f, q = 0.0f;
+    for (int i = lane; i < per; i += 64) m = __builtin_fmaf(count(i) * inv, p[i].x, m);
+    m = sum_wave(m);
+    for (int i = lane; i < per; i += 64) {
+        const float d = p[i].x - m;
+        q += __builtin_fmaf(count(i) * d, d, p[i].y);
+    }
+    q = sum_wave(q);
+    if (lane == 0) out[id] = make_float2(m, inverse_root(q * inv, g.eps));
+}
+
+// A lane's parameters: mean, r, r w and b of its channels.
+template <int V>
+struct Known {
+    float mean[V], r[V], w[V], b[V];
+    template <class L>
+    __device__ __forceinline__ Known(const Geo &g, const Slice &s, const L &ln, const float2 *joined, int img, const float *pw,
+                                     const float *pb) {
+        const Group<V> gr(g, s, ln);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float2 m = joined[(int64_t)img * g.G + s.g0 + gr.of[i]];
+            mean[i] = m.x;
+            r[i] = m.y;
+            params(w[i], pw, ln.c + i, 1.0f);
+            params(b[i], pb, ln.c + i, 0.0f);
+        }
+    }
+};
+
+template <class DT, int V, int TH, int U>
+__global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, int64_t ldx, const float2 *joined,
+                                              const float *w, const float *b, typename DT::X *y, int64_t ldy) {
+    using X = typename DT::X;
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
+    const Slice s = slice_of(g, sl);
+    const Lane<DT, V> ln(g, s);
+    if (ln.row < 0) return;
+    const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
+    x += ((int64_t)img * g.S + p0) * ldx + ln.c;
+    y += ((int64_t)img * g.S + p0) * ldy + ln.c;
+    const bool apart = (const void *)x != (const void *)y;
+    const Known<V> kn(g, s, ln, joined, img, w, b);
+    float scale[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) scale[i] = kn.r[i] * kn.w[i];
+    for (int r = ln.row; r < n; r += U * g.rpp) {
+        Any<X, V> v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) v[k] = Lane<DT, V>::load(x + (int64_t)min(r + k * g.rpp, n - 1) * ldx);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int t = r + k * g.rpp;
+            if (t >= n) break;
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                o[i] = act_of<DT>(__builtin_fmaf(DT::widen(v[k].v[i]) - kn.mean[i], scale[i], kn.b[i]), g.act);
+            ln.store(y + (int64_t)t * ldy, o, apart);
+        }
+    }
+}
+
+// A lane's share of the sums dz and dz u of one vector
+template <class DT, int V>
+__device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const Any<typename DT::X, V> &x,
+                                         const Any<typename DT::X, V> &dy, const Known<V> &kn, int act) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float u = (DT::widen(x.v[i]) - kn.mean[i]) * kn.r[i];
+        const float dz = DT::widen(dy.v[i]) * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
+        s1[i] += dz;
+        s2[i] = __builtin_fmaf(dz, u, s2[i]);
+    }
+}
+
+// Sums of dz and dz u over a run's pixels, for each channel: part[image][run][2][C].
+template <class DT, int V, int TH, int U>
+__global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
+                                             int64_t lddy, const float2 *joined, const float *w, const float *b, float *part) {
+    using X = typename DT::X;
+    extern __shared__ __align__(16) float sh[];
+    Sums<TH, V> sum(sh, sh + TH * V, nullptr, g);
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
+    const Slice s = slice_of(g, sl);
+    const Lane<DT, V> ln(g, s);
+    const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
+    x += ((int64_t)img * g.S + p0) * ldx + ln.c;
+    dy += ((int64_t)img * g.S + p0) * lddy + ln.c;
+    const Known<V> kn(g, s, ln, joined, img, w, b);
+    float s1[V], s2[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
+    if (ln.row >= 0)
+        for (int r = ln.row; r < n; r += U * g.rpp) {
+            Any<X, V> vx[U], vd[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int64_t t = min(r + k * g.rpp, n - 1);
+                vx[k] = Lane<DT, V>::load(x + t * ldx);
+                vd[k] = Lane<DT, V>::load(dy + t * lddy);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (r + k * g.rpp < n) add_sums<DT, V>(s1, s2, vx[k], vd[k], kn, g.act);
+        }
+    float *o = part + ((int64_t)img * g.runs + run) * 2 * g.C + s.c0;
+    sum.rows(s1, ln, g);
+    for (int i = threadIdx.x; i < s.w; i += TH) o[i] = sum.channel(s, i);
+    __syncthreads();
+    sum.rows(s2, ln, g);
+    for (int i = threadIdx.x; i < s.w; i += TH) o[g.C + i] = sum.channel(s, i);
+}
+
+// Sums of `n` rows of `cols` columns: 64 columns a workgroup, wave w takes every 16th
+// row from w on, the 16 sums are added in order.  Row r of set i is in + (i n + r) cols.
+__device__ __forceinline__ float column_sum(const float *in, int64_t n, int64_t cols, int64_t col, float (*sh)[64]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (col < cols) {
+        int64_t r = wave;
+        for (; r + 48 < n; r += 64) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] += in[(r + 16 * k) * cols + col];
+        }
+        for (; r < n; r += 16) s[0] += in[r * cols + col];
+    }
+    sh[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) t += sh[k][lane];
+    return t;
+}
+__global__ void __launch_bounds__(1024) k_fold(const float *part, int runs, int64_t cols, uint32_t blocks, float *out) {
+    __shared__ float sh[16][64];
+    const int64_t set = blockIdx.x / blocks, col = (int64_t)(blockIdx.x % blocks) * 64 + (threadIdx.x & 63);
+    const float t = column_sum(part + set * runs * cols, runs, cols, col, sh);
+    if (threadIdx.x < 64 && col < cols) out[set * cols + col] = t;
+}
+
+// From the channels' sums of each image ([image][2][C]: dz, dz u): the first `param`
+// workgroups db and dw over the images, the others the means of dz w and of dz w u of
+// each group, a wavefront a group.
+__global__ void __launch_bounds__(1024) k_means(Geo g, const float *sums, int images, const float *w, float *dw, float *db,
+                                                uint32_t param, float2 *means) {
+    __shared__ float sh[16][64];
+    if (blockIdx.x < param) {
+        const int64_t cols = 2 * (int64_t)g.C, col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
+        const float t = column_sum(sums, images, cols, col, sh);
+        if (threadIdx.x >= 64 || col >= cols) return;
+        if (col < g.C) {
+            if (db) db[col] = t;
+        } else if (dw) {
+            dw[col - g.C] = t;
+        }
+        return;
+    }
+    const int64_t id = (int64_t)(blockIdx.x - param) * 16 + (threadIdx.x >> 6);
+    if (id >= (int64_t)g.images * g.G) return;
+    const int64_t img = id / g.G;
+    const int c0 = (int)(id % g.G) * g.cg, lane = threadIdx.x & 63;
+    const float *p = sums + img * 2 * g.C + c0;
+    const float inv = 1.0f / ((float)g.S * (float)g.cg);
+    float a = 0.0f, b = 0.0f;
+    for (int i = lane; i < g.cg; i += 64) {
+        const float v = w ? w[c0 + i] : 1.0f;
+        a = __builtin_fmaf(v, p[i], a);
+        b = __builtin_fmaf(v, p[g.C + i], b);
+    }
+    a = sum_wave(a);
+    b = sum_wave(b);
+    if (lane == 0) means[id] = make_float2(a * inv, b * inv);
+}
+
+template <class DT, int V>
+__device__ __forceinline__ void grad_of(float (&o)[V], const Any<typename DT::X, V> &x, const Any<typename DT::X, V> &dy,
+                                        const Known<V> &kn, const float (&m1)[V], const float (&m2)[V], int act) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float u = (DT::widen(x.v[i]) - kn.mean[i]) * kn.r[i];
+        const float dz = DT::widen(dy.v[i]) * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
+        o[i] = kn.r[i] * (__builtin_fmaf(dz, kn.w[i], -m1[i]) - u * m2[i]);
+    }
+}
+
+template <class DT, int V, int TH, int U>
+__global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy, int64_t lddy,
+                                           const float2 *joined, const float2 *means, const float *w, const float *b,
+                                           typename DT::X *dx, int64_t lddx) {
+    using X = typename DT::X;
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
+    const Slice s = slice_of(g, sl);
+    const Lane<DT, V> ln(g, s);
+    if (ln.row < 0) return;
+    const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
+    x += ((int64_t)img * g.S + p0) * ldx + ln.c;
+    dy += ((int64_t)img * g.S + p0) * lddy + ln.c;
+    dx += ((int64_t)img * g.S + p0) * lddx + ln.c;
+    const bool apart = (const void *)dx != (const void *)dy;
+    const Known<V> kn(g, s, ln, joined, img, w, b);
+    const Group<V> gr(g, s, ln);
+    float m1[V], m2[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float2 m = means[(int64_t)img * g.G + s.g0 + gr.of[i]];
+        m1[i] = m.x;
+        m2[i] = m.y;
+    }
+    for (int r = ln.row; r < n; r += U * g.rpp) {
+        Any<X, V> vx[U], vd[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t t = min(r + k * g.rpp, n - 1);
+            vx[k] = Lane<DT, V>::load(x + t * ldx);
+            vd[k] = Lane<DT, V>::load(dy + t * lddy);
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int t = r + k * g.rpp;
+            if (t >= n) break;
+            float o[V];
+            grad_of<DT, V>(o, vx[k], vd[k], kn, m1, m2, g.act);
+            ln.store(dx + (int64_t)t * lddx, o, apart);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+constexpr int PASS_TH = 256, PASS_K = 8;
+
+Geo base(const dwconv_group_plan &p, int images, int pixels) {
+    return {images, pixels, p.C, p.G, p.C / p.G, 1, 1, 0, 1, 1, 1, pixels, p.act, p.eps};
+}
+
+// In passes: slices of at most 256 vectors, whole groups or parts of one.
+Geo passes(const dwconv_group_plan &p, int images, int pixels, int V) {
+    Geo g = base(p, images, pixels);
+    const int most = PASS_TH * V;
+    if (g.cg > most) {
+        g.parts = (g.cg + most - 1) / most;
+        g.part = ((g.cg + g.parts - 1) / g.parts + V - 1) / V * V;
+        g.parts = (g.cg + g.part - 1) / g.part;
+        g.slices = g.G * g.parts;
+        g.vpr = g.part / V;
+    } else {
+        g.slices = (p.C + most - 1) / most;
+        while ((g.G + g.slices - 1) / g.slices * g.cg > most) ++g.slices;
+        g.vpr = ((g.G + g.slices - 1) / g.slices * g.cg + V - 1) / V;
+    }
+    g.rpp = PASS_TH / g.vpr;
+    g.rows = g.rpp * PASS_K;
+    g.runs = (pixels + g.rows - 1) / g.rows;
+    return g;
+}
+// The same with longer runs for passes that know the statistics: some workgroups a CU.
+Geo streams(Geo g) {
+    const int64_t tiles = (int64_t)g.images * g.slices * g.runs, per = tiles / 2048;
+    if (per > 1) {
+        g.rows *= (int)(per < g.runs ? per : g.runs);
+        g.runs = (g.S + g.rows - 1) / g.rows;
+    }
+    return g;
+}
+
+bool too_many(int64_t blocks) { return blocks >= (1 << 24); }
+
+struct Sizes {
+    size_t stats, joined, part, sums, means, all;  // floats
+};
+Sizes sizes(const Geo &g, bool back) {
+    Sizes z{};
+    const Geo f = streams(g);
+    const size_t groups = (size_t)g.images * g.G;
+    z.stats = groups * g.runs * (g.parts > 1 ? g.parts : 1) * 2;
+    z.joined = groups * 2;
+    if (back) {
+        z.part = (size_t)g.images * f.runs * 2 * g.C;
+        z.sums = (size_t)g.images * 2 * g.C;
+        z.means = groups * 2;
+    }
+    z.all = z.stats + z.joined + z.part + z.sums + z.means;
+    return z;
+}
+
+template <class DT, int V>
+hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
+    using X = typename DT::X;
+    const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
+    const Sizes z = sizes(g, false);
+    const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
+    if (too_many(blocks) || too_many((groups + 3) / 4)) return hipErrorInvalidConfiguration;
+    if (!blocks) return hipSuccess;
+    float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
+    const int mg = (g.G + g.slices - 1) / g.slices;
+    const size_t lds = (2 * (size_t)PASS_TH * V + 2 * (size_t)mg) * sizeof(float);
+    k_fwd<DT, V, PASS_TH, PASS_K, true><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr, 0,
+                                                                               stats, mg);
+    k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
+    k_apply<DT, V, PASS_TH, 4><<<(uint32_t)((int64_t)f.images * f.slices * f.runs), PASS_TH, 0, st>>>(
+        f, (const X *)a.x, a.ldx, joined, a.w, a.b, (X *)a.y, a.ldy);
+    return hipGetLastError();
+}
+
+template <class DT, int V>
+hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
+    using X = typename DT::X;
+    const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
+    const Sizes z = sizes(g, true);
+    const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
+    const int64_t cols = 2 * (int64_t)g.C, folds = (cols + 63) / 64;
+    const uint32_t param = a.dw || a.db ? (uint32_t)folds : 0;
+    if (too_many(blocks) || too_many(groups + param) || (uint64_t)folds * g.images >= (1u << 22))
+        return hipErrorInvalidConfiguration;
+    float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
+    float *part = (float *)joined + z.joined, *sums = part + z.part;
+    float2 *means = (float2 *)(sums + z.sums);
+    const int mg = (g.G + g.slices - 1) / g.slices;
+    const size_t lds = (2 * (size_t)PASS_TH * V + 2 * (size_t)mg) * sizeof(float);
+    const uint32_t streaming = (uint32_t)((int64_t)f.images * f.slices * f.runs);
+    if (blocks) {
+        k_fwd<DT, V, PASS_TH, PASS_K, true><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr,
+                                                                                   0, stats, mg);
+        k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
+        k_sums<DT, V, PASS_TH, 4><<<streaming, PASS_TH, 2 * PASS_TH * V * sizeof(float), st>>>(
+            f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, a.w, a.b, part);
+        k_fold<<<(uint32_t)(folds * g.images), 1024, 0, st>>>(part, f.runs, cols, (uint32_t)folds, sums);
+    }
+    const uint32_t wg = blocks ? (uint32_t)((groups + 15) / 16) : 0;
+    if (param + wg)
+        k_means<<<param + wg, 1024, 0, st>>>(g, sums, blocks ? g.images : 0, a.w, a.dw, a.db, param, means);
+    if (blocks)
+        k_dx<DT, V, PASS_TH, 4><<<streaming, PASS_TH, 0, st>>>(f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, means,
+                                                              a.w, a.b, (X *)a.dx, a.lddx);
+    return hipGetLastError();
+}
+
+// Vectors of 16 bytes where a slice has as many channels, else single elements.
+int vec_of(const dwconv_group_plan &p) {
+    const int v = p.dtype == DWCONV_F32 ? 4 : 8;
+    return p.C >= v ? v : 1;
+}
+
+template <bool BACK, class DT>
+hipError_t pick_vec(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
+    constexpr int V = 16 / (int)sizeof(typename DT::X);
+    if constexpr (BACK) return vec_of(p) == V ? bwd<DT, V>(p, a, st) : bwd<DT, 1>(p, a, st);
+    else return vec_of(p) == V ? fwd<DT, V>(p, a, st) : fwd<DT, 1>(p, a, st);
+}
+
+template <bool BACK>
+hipError_t pick(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
+    switch (p.dtype) {
+        case DWCONV_F32: return pick_vec<BACK, F32>(p, a, st);
+        case DWCONV_F16: return pick_vec<BACK, F16>(p, a, st);
+        default: return pick_vec<BACK, BF16>(p, a, st);
+    }
+}
+
+}  // namespace
+
+hipError_t group_fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) { return pick<false>(p, a, st); }
+hipError_t group_bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) { return pick<true>(p, a, st); }
+
+size_t group_bytes(const dwconv_group_plan &p, int images, int pixels, bool back) {
+    return sizes(passes(p, images, pixels, vec_of(p)), back).all * sizeof(float);
+}
+
+}  // namespace dw

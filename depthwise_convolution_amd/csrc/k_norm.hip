@@ -70,20 +70,6 @@ struct RowSum {
     }
 };
 
-// act(g), and act'(g) in `slope`
-template <class DT>
-__device__ __forceinline__ float gate_value(float g, int act, float &slope) {
-    float rest;
-    const float p = sigmoid_f32<DT>(g, rest), q = p * rest;
-    slope = act == DWCONV_SEQ_ACT_NONE ? 1.0f : act == DWCONV_SEQ_ACT_SILU ? __builtin_fmaf(g, q, p) : q;
-    return act == DWCONV_SEQ_ACT_NONE ? g : act == DWCONV_SEQ_ACT_SILU ? g * p : p;
-}
-template <class DT>
-__device__ __forceinline__ float gate_value(float g, int act) {
-    float slope;
-    return gate_value<DT>(g, act, slope);
-}
-
 // A lane's E channels: NV vectors of VEC, TPR vectors apart.  Vectors past D
 // are read as the row's first one (no branch around a load) and count as zeros.
 template <class DT, int VEC, int TPR, int E>

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/dwconv_seq.h"
 #include "dw_common.h"
 
 namespace dw {
@@ -73,6 +74,20 @@ template <class DT>
 __device__ __forceinline__ float sigmoid_f32(float z) {
     float rest;
     return sigmoid_f32<DT>(z, rest);
+}
+
+// act(g), and act'(g) in `slope`
+template <class DT>
+__device__ __forceinline__ float gate_value(float g, int act, float &slope) {
+    float rest;
+    const float p = sigmoid_f32<DT>(g, rest), q = p * rest;
+    slope = act == DWCONV_SEQ_ACT_NONE ? 1.0f : act == DWCONV_SEQ_ACT_SILU ? __builtin_fmaf(g, q, p) : q;
+    return act == DWCONV_SEQ_ACT_NONE ? g : act == DWCONV_SEQ_ACT_SILU ? g * p : p;
+}
+template <class DT>
+__device__ __forceinline__ float gate_value(float g, int act) {
+    float slope;
+    return gate_value<DT>(g, act, slope);
 }
 
 // v plus the value n lanes round in each row of 16 (one instruction).

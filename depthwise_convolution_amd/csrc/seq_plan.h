@@ -23,6 +23,15 @@ struct dwconv_norm_plan {
     float eps;
 };
 
+struct dwconv_scan_plan {
+    int C, N, G, dtype, softplus, act;
+};
+
+struct dwconv_group_plan {
+    int C, G, dtype, act;
+    float eps;
+};
+
 namespace dw {
 
 struct CausalArgs {
@@ -97,5 +106,51 @@ struct NormArgs {
 hipError_t norm_fwd(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st);
 hipError_t norm_bwd(const dwconv_norm_plan &p, const NormArgs &a, hipStream_t st);
 size_t norm_bwd_bytes(const dwconv_norm_plan &p, int rows, int per);
+
+struct ScanArgs {
+    const void *x, *dt, *b, *c, *gate;
+    int64_t ldx, lddt, ldb, ldc, ldgate;
+    const float *a, *skip, *bias;
+    const int32_t *offsets;
+    int seqs, tokens;
+    const float *state_in;
+    float *state_out;
+    void *y;
+    int64_t ldy;
+    // step
+    float *state;
+    const int32_t *slots;
+    int n_slots;
+    // backward
+    const void *dy;
+    int64_t lddy;
+    const float *dstate_out;
+    void *dx, *ddt, *db, *dc, *dgate;
+    int64_t lddx, ldddt, lddb, lddc, lddgate;
+    float *da, *dskip, *dbias, *dstate_in;
+    float *workspace;
+};
+hipError_t scan_fwd(const dwconv_scan_plan &p, const ScanArgs &a, hipStream_t st);
+hipError_t scan_step(const dwconv_scan_plan &p, const ScanArgs &a, hipStream_t st);
+hipError_t scan_bwd(const dwconv_scan_plan &p, const ScanArgs &a, hipStream_t st);
+size_t scan_bytes(const dwconv_scan_plan &p, int seqs, int tokens, bool backward);
+
+struct GroupArgs {
+    int images, pixels;
+    const void *x;
+    int64_t ldx;
+    const float *w, *b;
+    void *y;
+    int64_t ldy;
+    const void *dy;
+    int64_t lddy;
+    void *dx;
+    int64_t lddx;
+    float *dw, *db;
+    float *workspace;
+};
+hipError_t group_fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st);
+hipError_t group_bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st);
+size_t group_bytes(const dwconv_group_plan &p, int images, int pixels, bool backward);
 
 }  // namespace dw

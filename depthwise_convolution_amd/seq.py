@@ -1,6 +1,6 @@
 """Python binding of the sequence operators (``include/dwconv_seq.h``): the
-causal depthwise convolution, the gated delta rule and the norms around a
-block.
+causal depthwise convolution, the gated delta rule, the norms around a block,
+the selective scan and the group norm.
 
 The functions carry the C ABI's names and only marshal arguments (GPU tensors
 or raw device pointers as ints); the classes own a plan, check shapes, types,
@@ -14,6 +14,10 @@ devices and strides, and allocate outputs and workspaces with torch:
              g, beta, offsets=offsets, state_out=state)
     norm = BlockNorm(Dv, "bf16", after="rms", before="none", gate_act="silu")
     z, _ = norm(o, gate=gate, w_after=w)
+    scan = SelectiveScan(C=8192, N=16, dtype="bf16")
+    y = scan(mixed, dt, a, b, c, skip=skip, dt_bias=dt_bias, gate=gate, offsets=offsets, state_out=state)
+    group = GroupNorm(C=128, G=32, dtype="bf16", act="silu")
+    y = group(x, w, b)                                     # images x H x W x C
 
 ``offsets`` (int32, one more than there are sequences) cuts the tokens into
 sequences; outputs of tokens behind the last one are left as they were (not
@@ -33,16 +37,19 @@ import torch
 
 from . import DwconvError, _dtype_code, _lib
 
-__all__ = ["CausalDepthwiseConv1d", "GatedDeltaRule", "BlockNorm", "SEQ_ACTIVATIONS", "NORM_KINDS"]
+__all__ = ["CausalDepthwiseConv1d", "GatedDeltaRule", "BlockNorm", "SelectiveScan", "GroupNorm", "SEQ_ACTIVATIONS",
+           "NORM_KINDS", "GROUP_ACTIVATIONS"]
 
 SEQ_ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
+GROUP_ACTIVATIONS = {"none": 0, "silu": 1, "relu": 2}
 _TORCH = {0: torch.float32, 1: torch.float16, 2: torch.bfloat16}
 
 _H, _I, _L, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _OUT, _SIZE = ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_size_t)
 _QKV = [_H, _L, _H, _L, _H, _L, _H, _H]
 _NORM = [_H, _I, _H, _H, _H, _I, _H, _H, _H, _H, _H]
+_SCAN = [_H, _H, _L, _H, _L, _H, _H, _L, _H, _L, _H, _H, _H, _L]
 _SIGNATURES = {
     "dwconv_causal_create": [_OUT, _I, _I, _I, _I],
     "dwconv_causal_destroy": [_H],
@@ -61,6 +68,17 @@ _SIGNATURES = {
     "dwconv_norm_fwd": _NORM + [_H, _H, _H],
     "dwconv_norm_bwd_workspace": [_H, _I, _I, _SIZE],
     "dwconv_norm_bwd": _NORM + [_H] * 12,
+    "dwconv_scan_create": [_OUT, _I, _I, _I, _I, _I, _I],
+    "dwconv_scan_destroy": [_H],
+    "dwconv_scan_workspace": [_H, _I, _I, _I, _SIZE],
+    "dwconv_scan_fwd": _SCAN + [_H, _I, _I, _H, _H, _H, _L, _H, _H],
+    "dwconv_scan_step": _SCAN + [_H, _H, _I, _I, _H, _L, _H],
+    "dwconv_scan_bwd": _SCAN + [_H, _I, _I, _H, _H, _L, _H, _H, _L, _H, _L, _H, _H, _L, _H, _L, _H, _H, _H, _L, _H, _H, _H],
+    "dwconv_group_create": [_OUT, _I, _I, _I, _I, _F],
+    "dwconv_group_destroy": [_H],
+    "dwconv_group_workspace": [_H, _I, _I, _I, _SIZE],
+    "dwconv_group_fwd": [_H, _I, _I, _H, _L, _H, _H, _H, _L, _H, _H],
+    "dwconv_group_bwd": [_H, _I, _I, _H, _L, _H, _H, _H, _L, _H, _L, _H, _H, _H, _H],
 }
 for _name, _args in _SIGNATURES.items():
     getattr(_lib, _name).argtypes = _args
@@ -202,6 +220,64 @@ def dwconv_norm_bwd(p, rows, o, residual, gate, rows_per_gate, scale, w_after, b
     _call("dwconv_norm_bwd", p, _n("rows", rows), _p(o), _p(residual), _p(gate), _n("rows_per_gate", rows_per_gate),
           _p(scale), _p(w_after), _p(b_after), _p(w_before), _p(b_before), _p(dh), _p(dy), _p(d_o), _p(dresidual),
           _p(dgate), _p(dscale), _p(dw_after), _p(db_after), _p(dw_before), _p(db_before), _p(workspace), stream)
+
+
+def dwconv_scan_create(C, N, G, dtype, softplus, gate_act):
+    """Plan of a selective scan (an int); DwconvError on bad sizes."""
+    return _create("dwconv_scan_create", C, N, G, _dtype_code(dtype), int(softplus), _code(SEQ_ACTIVATIONS, gate_act))
+
+
+def dwconv_scan_destroy(h):
+    _lib.dwconv_scan_destroy(h)
+
+
+def dwconv_scan_workspace(h, seqs, tokens, backward) -> int:
+    return _bytes("dwconv_scan_workspace", h, _n("seqs", seqs), _n("tokens", tokens), int(backward))
+
+
+def dwconv_scan_fwd(h, x, ldx, dt, lddt, a, b, ldb, c, ldc, skip, dt_bias, gate, ldgate, offsets, seqs, tokens, state_in,
+                    state_out, y, ldy, workspace, stream):
+    _call("dwconv_scan_fwd", h, _p(x), ldx, _p(dt), lddt, _p(a), _p(b), ldb, _p(c), ldc, _p(skip), _p(dt_bias), _p(gate),
+          ldgate, _p(offsets), _n("seqs", seqs), _n("tokens", tokens), _p(state_in), _p(state_out), _p(y), ldy,
+          _p(workspace), stream)
+
+
+def dwconv_scan_step(h, x, ldx, dt, lddt, a, b, ldb, c, ldc, skip, dt_bias, gate, ldgate, state, slots, n_slots, rows, y,
+                     ldy, stream):
+    _call("dwconv_scan_step", h, _p(x), ldx, _p(dt), lddt, _p(a), _p(b), ldb, _p(c), ldc, _p(skip), _p(dt_bias), _p(gate),
+          ldgate, _p(state), _p(slots), _n("n_slots", n_slots), _n("rows", rows), _p(y), ldy, stream)
+
+
+def dwconv_scan_bwd(h, x, ldx, dt, lddt, a, b, ldb, c, ldc, skip, dt_bias, gate, ldgate, offsets, seqs, tokens, state_in,
+                    dy, lddy, dstate_out, dx, lddx, ddt, ldddt, da, db, lddb, dc, lddc, dskip, ddt_bias, dgate, lddgate,
+                    dstate_in, workspace, stream):
+    _call("dwconv_scan_bwd", h, _p(x), ldx, _p(dt), lddt, _p(a), _p(b), ldb, _p(c), ldc, _p(skip), _p(dt_bias), _p(gate),
+          ldgate, _p(offsets), _n("seqs", seqs), _n("tokens", tokens), _p(state_in), _p(dy), lddy, _p(dstate_out), _p(dx),
+          lddx, _p(ddt), ldddt, _p(da), _p(db), lddb, _p(dc), lddc, _p(dskip), _p(ddt_bias), _p(dgate), lddgate,
+          _p(dstate_in), _p(workspace), stream)
+
+
+def dwconv_group_create(C, G, dtype, act, eps):
+    """Plan of a group norm (an int); DwconvError on bad sizes."""
+    return _create("dwconv_group_create", C, G, _dtype_code(dtype), _code(GROUP_ACTIVATIONS, act), eps)
+
+
+def dwconv_group_destroy(h):
+    _lib.dwconv_group_destroy(h)
+
+
+def dwconv_group_workspace(h, images, pixels, backward) -> int:
+    return _bytes("dwconv_group_workspace", h, _n("images", images), _n("pixels", pixels), int(backward))
+
+
+def dwconv_group_fwd(h, images, pixels, x, ldx, w, b, y, ldy, workspace, stream):
+    _call("dwconv_group_fwd", h, _n("images", images), _n("pixels", pixels), _p(x), ldx, _p(w), _p(b), _p(y), ldy,
+          _p(workspace), stream)
+
+
+def dwconv_group_bwd(h, images, pixels, x, ldx, w, b, dy, lddy, dx, lddx, dw, db, workspace, stream):
+    _call("dwconv_group_bwd", h, _n("images", images), _n("pixels", pixels), _p(x), ldx, _p(w), _p(b), _p(dy), lddy, _p(dx),
+          lddx, _p(dw), _p(db), _p(workspace), stream)
 
 
 # --- plans with checks and allocation --------------------------------------
@@ -600,3 +676,196 @@ class BlockNorm(_Plan):
             return tuple(grads)
 
         return _on(dev, stream, body, o, dh, dy, residual, gate, scale, w_after, b_after, w_before, b_before, workspace)
+
+
+class SelectiveScan(_Plan):
+    """h_t = e^{d a} h + d x b, y = (sum_n h c + skip x) act(gate) with d = softplus(dt
+    + dt_bias) (``softplus`` False: dt + dt_bias), N states for each of C channels.
+    x, dt, gate, y: tokens x C; a: C x N float32; b, c: tokens x G x N, one for each
+    of G groups of channels; skip, dt_bias: C float32 or None; states: sequences x C x N
+    float32.  ``gate_act``: "silu", "sigmoid" or "none"."""
+
+    _destroy = "dwconv_scan_destroy"
+
+    def __init__(self, C, N, G=1, dtype="bf16", softplus=True, gate_act="silu"):
+        code = _dtype_code(dtype)
+        self.handle = dwconv_scan_create(C, N, G, code, softplus, gate_act)
+        self.C, self.N, self.G, self.dtype = C, N, G, _TORCH[code]
+
+    def _common(self, x, dt, a, b, c, skip, dt_bias, gate):
+        dev, t = self._device("x", x), self.dtype
+        if x.dim() != 2:
+            raise ValueError("x: tokens x channels")
+        n = _n("x", x.shape[0])
+        rows, states = (n, self.C), (n, self.G, self.N)
+        ldx, lddt = _tokens("x", x, rows, t, dev), _tokens("dt", dt, rows, t, dev)
+        _dense("a", a, (self.C, self.N), torch.float32, dev)
+        ldb, ldc = _tokens("b", b, states, t, dev), _tokens("c", c, states, t, dev)
+        for name, v in (("skip", skip), ("dt_bias", dt_bias)):
+            if v is not None:
+                _dense(name, v, (self.C,), torch.float32, dev)
+        ldgate = 0 if gate is None else _tokens("gate", gate, rows, t, dev)
+        return dev, n, (x, ldx, dt, lddt, a, b, ldb, c, ldc, skip, dt_bias, gate, ldgate)
+
+    def _states(self, seqs, dev, **states):
+        for name, t in states.items():
+            if t is not None:
+                _dense(name, t, (seqs, self.C, self.N), torch.float32, dev)
+
+    def __call__(self, x, dt, a, b, c, skip=None, dt_bias=None, gate=None, offsets=None, state_in=None, state_out=None,
+                 y=None, workspace=None, stream=None):
+        """Returns y; ``state_out``, where given, gets every sequence's last state
+        (it may be state_in itself)."""
+        dev, n, args = self._common(x, dt, a, b, c, skip, dt_bias, gate)
+        seqs = _sequences(offsets, dev)
+        self._states(seqs, dev, state_in=state_in, state_out=state_out)
+
+        def body(raw):
+            nonlocal y
+            need = dwconv_scan_workspace(self.handle, seqs, n, False)
+            ws = _workspace(workspace, need, dev) if need else None
+            if y is None:
+                y = torch.empty((n, self.C), dtype=self.dtype, device=dev)
+            dwconv_scan_fwd(self.handle, *args, offsets, seqs, n, state_in, state_out, y,
+                            _tokens("y", y, (n, self.C), self.dtype, dev), ws, raw)
+            return y
+
+        return _on(dev, stream, body, x, dt, a, b, c, skip, dt_bias, gate, offsets, state_in, state_out, y, workspace)
+
+    def step(self, x, dt, a, b, c, state, skip=None, dt_bias=None, gate=None, slots=None, y=None, stream=None):
+        """One token for each row; ``state`` (cache entries x C x N) is updated in
+        place.  Slots as for CausalDepthwiseConv1d.step."""
+        dev, n, args = self._common(x, dt, a, b, c, skip, dt_bias, gate)
+        entries = state.shape[0]
+        self._states(entries, dev, state=state)
+        _slots(slots, n, entries, dev)
+
+        def body(raw):
+            nonlocal y
+            if y is None:
+                y = torch.empty((n, self.C), dtype=self.dtype, device=dev)
+            dwconv_scan_step(self.handle, *args, state, slots, entries, n, y,
+                             _tokens("y", y, (n, self.C), self.dtype, dev), raw)
+            return y
+
+        return _on(dev, stream, body, x, dt, a, b, c, state, skip, dt_bias, gate, slots, y)
+
+    def backward(self, x, dt, a, b, c, dy, skip=None, dt_bias=None, gate=None, offsets=None, state_in=None,
+                 dstate_out=None, dx=None, ddt=None, da=None, db=None, dc=None, dskip=None, ddt_bias=None, dgate=None,
+                 dstate_in=None, workspace=None, stream=None):
+        """(dx, ddt, da, db, dc, dskip, ddt_bias, dgate, dstate_in) for the output
+        gradient dy and, where given, the gradient dstate_out of the final states; None
+        for what was not given.  da, dskip, ddt_bias and dstate_in are float32."""
+        dev, n, args = self._common(x, dt, a, b, c, skip, dt_bias, gate)
+        t, seqs = self.dtype, _sequences(offsets, dev)
+        rows, states, f32 = (n, self.C), (n, self.G, self.N), torch.float32
+        lddy = _tokens("dy", dy, rows, t, dev)
+        self._states(seqs, dev, state_in=state_in, dstate_out=dstate_out)
+
+        def body(raw):
+            nonlocal dx, ddt, da, db, dc, dskip, ddt_bias, dgate, dstate_in
+            ws = _workspace(workspace, dwconv_scan_workspace(self.handle, seqs, n, True), dev)
+
+            def new(given, shape, dtype, wanted=True):
+                return torch.empty(shape, dtype=dtype, device=dev) if given is None and wanted else given
+
+            dx, ddt, da = new(dx, rows, t), new(ddt, rows, t), new(da, (self.C, self.N), f32)
+            db, dc = new(db, states, t), new(dc, states, t)
+            dskip, ddt_bias = new(dskip, (self.C,), f32, skip is not None), new(ddt_bias, (self.C,), f32, dt_bias is not None)
+            dgate = new(dgate, rows, t, gate is not None)
+            dstate_in = new(dstate_in, (seqs, self.C, self.N), f32, state_in is not None)
+            _dense("da", da, (self.C, self.N), f32, dev)
+            for name, v in (("dskip", dskip), ("ddt_bias", ddt_bias)):
+                if v is not None:
+                    _dense(name, v, (self.C,), f32, dev)
+            self._states(seqs, dev, dstate_in=dstate_in)
+            dwconv_scan_bwd(self.handle, *args, offsets, seqs, n, state_in, dy, lddy, dstate_out,
+                            dx, _tokens("dx", dx, rows, t, dev), ddt, _tokens("ddt", ddt, rows, t, dev), da,
+                            db, _tokens("db", db, states, t, dev), dc, _tokens("dc", dc, states, t, dev), dskip, ddt_bias,
+                            dgate, 0 if dgate is None else _tokens("dgate", dgate, rows, t, dev), dstate_in, ws, raw)
+            return (dx, ddt, da, db, dc, None if skip is None else dskip, None if dt_bias is None else ddt_bias,
+                    None if gate is None else dgate, dstate_in)
+
+        return _on(dev, stream, body, x, dt, a, b, c, dy, skip, dt_bias, gate, offsets, state_in, dstate_out, dx, ddt, da,
+                   db, dc, dskip, ddt_bias, dgate, dstate_in, workspace)
+
+
+class GroupNorm(_Plan):
+    """y = act(u w + b), u = (x - mean) / sqrt(var + eps) over each image's pixels and
+    each of G groups of C / G channels.  x, y: images x ... x C, the pixels of all
+    images equally far apart (slices of wider pixels are taken as they are); w, b: C
+    float32 or None.  ``act``: "silu", "relu" or "none"."""
+
+    _destroy = "dwconv_group_destroy"
+
+    def __init__(self, C, G, dtype="bf16", act="silu", eps=1e-5):
+        code = _dtype_code(dtype)
+        self.handle = dwconv_group_create(C, G, code, act, eps)
+        self.C, self.G, self.dtype = C, G, _TORCH[code]
+
+    def _pixels(self, name, t, shape, dev):
+        """Pixel stride of ``t``, whose channels are dense."""
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+        flat = t
+        if t.dim() != 2 and t.numel():
+            try:
+                flat = t.view(-1, self.C)
+            except RuntimeError:
+                raise ValueError(f"{name}: pixels have to be equally far apart, got {tuple(t.shape)} strides {t.stride()}") \
+                    from None
+        elif t.dim() != 2:
+            flat = t.reshape(0, self.C)
+        return _tokens(name, flat, (t.numel() // self.C, self.C), self.dtype, dev)
+
+    def _common(self, x, w, b):
+        dev = self._device("x", x)
+        if x.dim() < 2 or x.shape[-1] != self.C:
+            raise ValueError(f"x: images x pixels x {self.C} channels")
+        images = _n("x", x.shape[0])
+        pixels = _n("x", x.shape[1:-1].numel())
+        _n("x", images * pixels)
+        ldx = self._pixels("x", x, x.shape, dev)
+        for name, v in (("w", w), ("b", b)):
+            if v is not None:
+                _dense(name, v, (self.C,), torch.float32, dev)
+        return dev, images, pixels, ldx
+
+    def __call__(self, x, w=None, b=None, y=None, workspace=None, stream=None):
+        """Returns y (it may be x itself)."""
+        dev, images, pixels, ldx = self._common(x, w, b)
+
+        def body(raw):
+            nonlocal y
+            need = dwconv_group_workspace(self.handle, images, pixels, False)
+            ws = _workspace(workspace, need, dev) if need else None
+            if y is None:
+                y = torch.empty(x.shape, dtype=self.dtype, device=dev)
+            dwconv_group_fwd(self.handle, images, pixels, x, ldx, w, b, y, self._pixels("y", y, x.shape, dev), ws, raw)
+            return y
+
+        return _on(dev, stream, body, x, w, b, y, workspace)
+
+    def backward(self, x, dy, w=None, b=None, dx=None, dw=None, db=None, workspace=None, stream=None):
+        """(dx, dw, db) for the output gradient dy (dx may be dy itself); dw and db are
+        float32, None where w and b are."""
+        dev, images, pixels, ldx = self._common(x, w, b)
+        lddy = self._pixels("dy", dy, x.shape, dev)
+
+        def body(raw):
+            nonlocal dx, dw, db
+            ws = _workspace(workspace, dwconv_group_workspace(self.handle, images, pixels, True), dev)
+            if dx is None:
+                dx = torch.empty(x.shape, dtype=self.dtype, device=dev)
+            if dw is None and w is not None:
+                dw = torch.empty(self.C, dtype=torch.float32, device=dev)
+            if db is None and b is not None:
+                db = torch.empty(self.C, dtype=torch.float32, device=dev)
+            for name, v in (("dw", dw), ("db", db)):
+                if v is not None:
+                    _dense(name, v, (self.C,), torch.float32, dev)
+            dwconv_group_bwd(self.handle, images, pixels, x, ldx, w, b, dy, lddy, dx, self._pixels("dx", dx, x.shape, dev),
+                             None if w is None else dw, None if b is None else db, ws, raw)
+            return dx, None if w is None else dw, None if b is None else db
+
+        return _on(dev, stream, body, x, dy, w, b, dx, dw, db, workspace)

@@ -6,6 +6,10 @@
  *   dwconv_delta_*   the gated delta rule (one matrix of state per head)
  *   dwconv_norm_*    norm after a block, gate, residual scale, residual and
  *                    the norm before the next block, in one pass
+ *   dwconv_scan_*    the selective scan of a state space mixer (a few states
+ *                    per channel)
+ *   dwconv_group_*   norm over groups of channels of an image or a sequence,
+ *                    with an activation
  *
  * Shared conventions (status codes, dtypes and errors as in dwconv.h):
  *
@@ -46,9 +50,15 @@
  *   its step     2^24 rows x value heads x ceil(Dv / 128), with Dv / 32 where rows
  *                are not aligned to four elements
  *   norms        2^32 lanes, 16 to 1024 a row
+ *   scan         2^24 workgroups of 256 lanes, a workgroup 64 channels of a group (32,
+ *                16, 8 for N > 16, 32, 64) of a sequence or of 64 or more tokens of
+ *                it, in a step of one row; gradients also 2^24 for every 8 (4, 2, 1)
+ *                tokens of a group of channels; the workspace's size is then given as
+ *                SIZE_MAX
+ *   group norm   2^24 workgroups of an image's 8 channels or more, or of 8 KB or more
  *
- * float (fp32) everywhere: biases, scales, norm weights, decays, write
- * strengths, matrix states and the gradients of all of these.  Sums and
+ * float (fp32) everywhere: biases, scales, norm weights, decays, rates, write
+ * strengths, states of the rule and the scan and the gradients of all of these.  Sums and
  * statistics are fp32 or wider; a value of type `dtype` is rounded once, to
  * nearest even, when it is stored.
  */
@@ -67,6 +77,8 @@ extern "C" {
 typedef struct dwconv_causal_plan *dwconv_causal_t;
 typedef struct dwconv_delta_plan *dwconv_delta_t;
 typedef struct dwconv_norm_plan *dwconv_norm_t;
+typedef struct dwconv_scan_plan *dwconv_scan_t;
+typedef struct dwconv_group_plan *dwconv_group_t;
 
 /* Activation of the causal convolution's output and of a gate. */
 typedef enum {
@@ -233,6 +245,111 @@ dwconv_status_t dwconv_norm_bwd(dwconv_norm_t p, int rows, const void *o, const 
                                 void *dresidual, void *dgate, float *dscale, float *dw_after,
                                 float *db_after, float *dw_before, float *db_before,
                                 void *workspace, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Selective scan.  Per channel c of group g = c / (C / G), with N states:
+ *
+ *   d_t = softplus(dt_t + dt_bias)          or dt_t + dt_bias without softplus
+ *   h_t[n] = e^{d_t a[n]} h_{t-1}[n] + d_t x_t b_t[g, n]
+ *   y_t = (sum_n h_t[n] c_t[g, n] + skip x_t) * act(gate_t)
+ *
+ *   x, dt, y, gate  tokens x C (dtype), token strides ldx, lddt, ldy, ldgate; gate
+ *                   may be NULL
+ *   a               C x N float: the states' rates, below zero as a rule
+ *   b, c            tokens x G x N (dtype), token strides ldb, ldc
+ *   skip, dt_bias   C float or NULL (zeros)
+ *   state_*         seqs x C x N float, dense; NULL state_in: zeros; NULL
+ *                   state_out: not written; state_out may be state_in itself
+ *
+ * Forward, a NaN or infinity reaches no token before its own, no other sequence and,
+ * but for those of b and c, no other channel.  In the gradients it may reach any
+ * token of its sequence and, through db and dc, the sums over the group's channels.
+ * ------------------------------------------------------------------------ */
+
+/* 1 <= C <= 2^24, G >= 1, C a multiple of G, 1 <= N <= 128, dtype F32 / F16 / BF16,
+ * gate_act as for a gate above. */
+dwconv_status_t dwconv_scan_create(dwconv_scan_t *out, int C, int N, int G, dwconv_dtype_t dtype,
+                                   int softplus, dwconv_seq_act_t gate_act);
+dwconv_status_t dwconv_scan_destroy(dwconv_scan_t h);
+
+/* Bytes of workspace of dwconv_scan_fwd (backward == 0, 0 for many plans) or
+ * dwconv_scan_bwd (backward != 0); the workspace is 16-byte aligned.  The backward
+ * pass keeps the states of every 16 tokens. */
+dwconv_status_t dwconv_scan_workspace(dwconv_scan_t h, int seqs, int tokens, int backward,
+                                      size_t *bytes);
+
+dwconv_status_t dwconv_scan_fwd(dwconv_scan_t h, const void *x, int64_t ldx, const void *dt,
+                                int64_t lddt, const float *a, const void *b, int64_t ldb,
+                                const void *c, int64_t ldc, const float *skip,
+                                const float *dt_bias, const void *gate, int64_t ldgate,
+                                const int32_t *offsets, int seqs, int tokens,
+                                const float *state_in, float *state_out, void *y, int64_t ldy,
+                                void *workspace, hipStream_t stream);
+
+/* One token for each of `rows` sequences, states in a cache of n_slots x C x N
+ * floats updated in place; slots as for dwconv_causal_step. */
+dwconv_status_t dwconv_scan_step(dwconv_scan_t h, const void *x, int64_t ldx, const void *dt,
+                                 int64_t lddt, const float *a, const void *b, int64_t ldb,
+                                 const void *c, int64_t ldc, const float *skip,
+                                 const float *dt_bias, const void *gate, int64_t ldgate,
+                                 float *state, const int32_t *slots, int n_slots, int rows,
+                                 void *y, int64_t ldy, hipStream_t stream);
+
+/* Gradients for dy (as y) and dstate_out (as state_out; NULL: zeros) of the forward
+ * pass from the same inputs (its intermediates are computed again): dx, ddt, dgate (as
+ * x, dt, gate; dgate may be NULL), da (as a), db, dc (as b, c; sums over the
+ * channels of the group), dskip, ddt_bias (C float or NULL) and dstate_in (as
+ * state_in; it may be dstate_out itself) or NULL. */
+dwconv_status_t dwconv_scan_bwd(dwconv_scan_t h, const void *x, int64_t ldx, const void *dt,
+                                int64_t lddt, const float *a, const void *b, int64_t ldb,
+                                const void *c, int64_t ldc, const float *skip,
+                                const float *dt_bias, const void *gate, int64_t ldgate,
+                                const int32_t *offsets, int seqs, int tokens,
+                                const float *state_in, const void *dy, int64_t lddy,
+                                const float *dstate_out, void *dx, int64_t lddx, void *ddt,
+                                int64_t ldddt, float *da, void *db, int64_t lddb, void *dc,
+                                int64_t lddc, float *dskip, float *ddt_bias, void *dgate,
+                                int64_t lddgate, float *dstate_in, void *workspace,
+                                hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Group norm with an activation.  For each image (or sequence) of `pixels` rows of C
+ * channels, and each of its G groups of C / G channels one beside the other:
+ *
+ *   u = (x - mean) / sqrt(var + eps)        over the group's pixels x C / G values
+ *   y = act(u * w + b)
+ *
+ *   x, y        images x pixels x C (dtype), ldx, ldy elements between two pixels,
+ *               images one behind the other; y may be x itself (with ldy == ldx)
+ *   w, b        C float or NULL (ones, zeros)
+ * ------------------------------------------------------------------------ */
+typedef enum {
+    DWCONV_GROUP_ACT_NONE = 0,   /* identity                                   */
+    DWCONV_GROUP_ACT_SILU = 1,   /* z / (1 + exp(-z))                          */
+    DWCONV_GROUP_ACT_RELU = 2    /* max(z, 0); slope 0 at 0                    */
+} dwconv_group_act_t;
+
+/* C, G >= 1, C a multiple of G and at most 65536, dtype F32 / F16 / BF16, eps >= 0
+ * and finite. */
+dwconv_status_t dwconv_group_create(dwconv_group_t *out, int C, int G, dwconv_dtype_t dtype,
+                                    dwconv_group_act_t act, float eps);
+dwconv_status_t dwconv_group_destroy(dwconv_group_t h);
+
+/* Bytes of workspace of dwconv_group_fwd (backward == 0, 0 for small images) or
+ * dwconv_group_bwd (backward != 0); the workspace is 16-byte aligned. */
+dwconv_status_t dwconv_group_workspace(dwconv_group_t h, int images, int pixels, int backward,
+                                       size_t *bytes);
+
+dwconv_status_t dwconv_group_fwd(dwconv_group_t h, int images, int pixels, const void *x,
+                                 int64_t ldx, const float *w, const float *b, void *y,
+                                 int64_t ldy, void *workspace, hipStream_t stream);
+
+/* Gradients for dy (as y) from the forward pass's inputs: dx (as x; it may be dy itself
+ * with lddx == lddy), dw and db (C float, or NULL: not wanted). */
+dwconv_status_t dwconv_group_bwd(dwconv_group_t h, int images, int pixels, const void *x,
+                                 int64_t ldx, const float *w, const float *b, const void *dy,
+                                 int64_t lddy, void *dx, int64_t lddx, float *dw, float *db,
+                                 void *workspace, hipStream_t stream);
 
 #ifdef __cplusplus
 }
