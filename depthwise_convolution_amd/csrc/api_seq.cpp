@@ -1,5 +1,6 @@
 // api_seq.cpp -- the extern "C" entry points declared in include/dwconv_seq.h:
 // argument checks in front of the launchers.
+#include <initializer_list>
 #include <math.h>
 #include <new>
 #include <stdint.h>
@@ -349,6 +350,13 @@ static bool scan_inputs(dw::ScanArgs &s, dwconv_scan_t h, const void *x, int64_t
     return true;
 }
 
+// Kernels keep a lane's place in 16 tokens in 32 bits.
+static bool scan_strides(std::initializer_list<int64_t> lds) {
+    for (int64_t ld : lds)
+        if (ld > 1 << 26) return false;
+    return true;
+}
+
 dwconv_status_t dwconv_scan_fwd(dwconv_scan_t h, const void *x, int64_t ldx, const void *dt, int64_t lddt, const float *a,
                                 const void *b, int64_t ldb, const void *c, int64_t ldc, const float *skip,
                                 const float *dt_bias, const void *gate, int64_t ldgate, const int32_t *offsets, int seqs,
@@ -363,6 +371,7 @@ dwconv_status_t dwconv_scan_fwd(dwconv_scan_t h, const void *x, int64_t ldx, con
         return DWCONV_ERR_INVALID_ARG;
     const size_t st = (size_t)seqs * h->C * h->N * sizeof(float);
     if (state_in != state_out && overlap(state_in, st, state_out, st)) return DWCONV_ERR_INVALID_ARG;
+    if (!scan_strides({ldx, lddt, ldb, ldc, gate ? ldgate : 0, ldy})) return DWCONV_ERR_UNSUPPORTED;
     s.offsets = offsets, s.seqs = seqs, s.state_in = state_in, s.state_out = state_out, s.y = y, s.ldy = ldy;
     s.workspace = (float *)workspace;
     return status(dw::scan_fwd(*h, s, stream));
@@ -412,6 +421,8 @@ dwconv_status_t dwconv_scan_bwd(dwconv_scan_t h, const void *x, int64_t ldx, con
     const size_t st = (size_t)seqs * h->C * h->N * sizeof(float);
     if (overlap(state_in, st, dstate_in, st) || (dstate_in != dstate_out && overlap(dstate_out, st, dstate_in, st)))
         return DWCONV_ERR_INVALID_ARG;
+    if (!scan_strides({ldx, lddt, ldb, ldc, gate ? ldgate : 0, lddy, lddx, ldddt, lddb, lddc, dgate ? lddgate : 0}))
+        return DWCONV_ERR_UNSUPPORTED;
     s.offsets = offsets, s.seqs = seqs, s.state_in = state_in, s.dy = dy, s.lddy = lddy, s.dstate_out = dstate_out;
     s.dx = dx, s.lddx = lddx, s.ddt = ddt, s.ldddt = ldddt, s.da = da, s.db = db, s.lddb = lddb, s.dc = dc, s.lddc = lddc;
     s.dskip = dskip, s.dbias = ddt_bias, s.dgate = dgate, s.lddgate = lddgate, s.dstate_in = dstate_in;

@@ -95,74 +95,128 @@ struct Across {
 // slots begin / CH + s and up: no table, and no two alike.
 struct Piece {
     int s, t0, t1;
-    bool last;
 };
 __device__ __forceinline__ int64_t slot_base(const ScanGeo &G, int s) { return G.CH ? (int64_t)(G.seq.begin(s) / G.CH) + s : s; }
 __device__ __forceinline__ Piece piece(const ScanGeo &G, int64_t slot) {
-    if (!G.CH) {
-        const int s = (int)slot;
-        return {s, G.seq.begin(s), G.seq.end(s), true};
+    int s = (int)slot, t0, t1;
+    if (G.CH) {
+        int lo = 0, hi = G.seq.seqs;
+        while (hi - lo > 1) {
+            const int m = lo + ((hi - lo) >> 1);
+            if (slot_base(G, m) <= slot) lo = m; else hi = m;
+        }
+        const int b = G.seq.begin(lo), e = G.seq.end(lo);
+        const int64_t t = b + (slot - slot_base(G, lo)) * G.CH;
+        const bool in = t >= b && t < e;
+        s = lo;
+        t0 = in ? (int)t : 0;
+        t1 = !in ? 0 : e - t > G.CH ? (int)t + G.CH : e;
+    } else {
+        t0 = G.seq.begin(s);
+        t1 = G.seq.end(s);
     }
-    int lo = 0, hi = G.seq.seqs;
-    while (hi - lo > 1) {
-        const int m = lo + ((hi - lo) >> 1);
-        if (slot_base(G, m) <= slot) lo = m; else hi = m;
+    return {uniform(s), uniform(t0), uniform(t1)};  // the same for all lanes, which loads from memory do not tell
+}
+
+// Whole sequences, longest first.  Workgroups of a launch that fits the chip go to its CUs
+// in rounds of 256, every second one backwards here, so that the CU with the longest
+// sequence of one round has the shortest of the next; later ones go where a place is free.
+// For up to 64 sequences, whose lengths a wavefront sorts; of more, every CU has some of each.
+// (7 sequences of 1553 to 3465 tokens, 8192 channels: 858 us in order, ORDERED.)
+__device__ __forceinline__ void longest_first(const ScanGeo &G, uint32_t &id, uint32_t all) {
+    if (G.CH || !G.seq.offsets || G.seq.seqs > 64 || G.slots != (uint32_t)G.seq.seqs || G.seq.seqs < 2) return;
+    const uint32_t round = id / 256;
+    if (round & 1) id = round * 256 + min(255u, all - 1 - round * 256) - id % 256;
+    const int j = (int)threadIdx.x & 63, len = j < G.seq.seqs ? G.seq.end(j) - G.seq.begin(j) : -1;
+    int rank = 0;
+    for (int k = 0; k < G.seq.seqs; ++k) {
+        const int other = __builtin_amdgcn_readlane(len, k);
+        rank += other > len || (other == len && k < j);
     }
-    const int b = G.seq.begin(lo), e = G.seq.end(lo);
-    const int64_t t = b + (slot - slot_base(G, lo)) * G.CH;
-    if (t < b || t >= e) return {lo, e, e, false};
-    return {lo, (int)t, e - t > G.CH ? (int)t + G.CH : e, e - t <= G.CH};
+    const uint64_t mine = __ballot(j < G.seq.seqs && rank == (int)(id / G.nblk));
+    id = (uint32_t)__builtin_ctzll(mine) * G.nblk + id % G.nblk;
+}
+
+// Workgroups are handed to the 8 XCDs round-robin, and so to their CUs: the pieces of a
+// long sequence, which lie one beside the other, on all of them.  Only the workgroups
+// that share 128-byte lines of a row (LPC / 4 of 16-bit data) keep to one XCD, whose L2
+// they share.
+template <int LPC>
+__device__ __forceinline__ uint32_t spread(uint32_t b, uint32_t all) {
+    constexpr uint32_t U = LPC / 4;
+    if (U == 1 || b >= all / (8 * U) * (8 * U)) return b;
+    const uint32_t k = b / 8;
+    return (k / U * 8 + b % 8) * U + k % U;
 }
 
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
+// A tensor as a workgroup walks it: the address of its first token (a scalar) and the
+// lane's offset in a tile, 32 bits (strides are at most 2^26 elements): whole tiles of
+// whole vectors cost a load each and no other vector instruction.
+template <class X>
+struct Walk {
+    const X *p;
+    int64_t ld;
+    uint32_t off;  // bytes
+    __device__ __forceinline__ Walk(const void *base, int64_t ld, int row, int col) : p((const X *)base), ld(ld) {
+        off = ((uint32_t)row * (uint32_t)ld + (uint32_t)col) * (uint32_t)sizeof(X);
+    }
+    __device__ __forceinline__ X *at(int t) const { return (X *)((char *)(p + (int64_t)t * ld) + off); }
+};
+
 // 16 tokens of the workgroup's channels, a vector of four a lane.  The vectors need
 // no more than the element's alignment: the loads take any.
 template <class DT, int LPC>
 struct Rows {
     using X = typename DT::X;
+    // four elements as words: what is on its way stays as it comes (elements taken apart
+    // would wait for the load)
+    static constexpr int W = (int)sizeof(X);
+    using Words = Vec<uint32_t, W>;
     struct __attribute__((packed, aligned(sizeof(X)))) Any {
-        X v[4];
+        uint32_t w[W];
     };
     static constexpr int CPW = THREADS / LPC, VPR = CPW / 4, LD = CPW + 16;
     static constexpr int SIZE = TT * LD;
-    Vec<X, 4> v;
+    Any v;
     static __device__ __forceinline__ int row() { return (int)threadIdx.x / VPR; }
     static __device__ __forceinline__ int col() { return (int)threadIdx.x % VPR * 4; }
-    __device__ __forceinline__ void fetch(const X *p, int64_t ld, int t, int cnt, int c0, int cend) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v.v[i] = (X)0;
-        const int c = c0 + col();
-        if (row() >= cnt || c >= cend) return;
-        const X *at = p + (int64_t)(t + row()) * ld + c;
-        if (c + 4 <= cend) {
-            const Any a = *(const Any *)at;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v.v[i] = a.v[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (c + i < cend) v.v[i] = at[i];
+    // the tensor from channel c0 on; lanes past a tile follow its first row
+    static __device__ __forceinline__ Walk<X> walk(const void *p, int64_t ld, int c0) {
+        return {p ? (const X *)p + c0 : nullptr, ld, row() < TT ? row() : 0, col()};
+    }
+    // `width`: channels of the workgroup
+    __device__ __forceinline__ void fetch(const Walk<X> &w, int t, int cnt, int width) {
+        const X *at = w.at(t);
+        if (cnt == TT && width >= CPW) {
+            v = *(const Any *)at;
+            return;
         }
+        X e[4] = {(X)0, (X)0, (X)0, (X)0};
+        if (row() < cnt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col() + i < width) e[i] = at[i];
+        }
+        __builtin_memcpy(&v, e, sizeof(v));
     }
     __device__ __forceinline__ void put(X *lds) const {
-        if (row() < TT) *(Vec<X, 4> *)(lds + row() * LD + col()) = v;
+        if (row() < TT) *(Words *)(lds + row() * LD + col()) = __builtin_bit_cast(Words, v);
     }
-    static __device__ __forceinline__ void flush(const X *lds, X *p, int64_t ld, int t, int cnt, int c0, int cend) {
-        const int c = c0 + col();
-        if (row() >= cnt || c >= cend) return;
-        const Vec<X, 4> w = *(const Vec<X, 4> *)(lds + row() * LD + col());
-        X *at = p + (int64_t)(t + row()) * ld + c;
-        if (c + 4 <= cend) {
-            Any a;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a.v[i] = w.v[i];
-            *(Any *)at = a;
+    static __device__ __forceinline__ void flush(const X *lds, const Walk<X> &w, int t, int cnt, int width) {
+        if (row() >= cnt) return;
+        const Words u = *(const Words *)(lds + row() * LD + col());
+        X *at = w.at(t);
+        if (width >= CPW) {
+            *(Any *)at = __builtin_bit_cast(Any, u);
         } else {
+            X e[4];
+            __builtin_memcpy(e, &u, sizeof(e));
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (c + i < cend) at[i] = w.v[i];
+            for (int i = 0; i < 4; ++i)
+                if (col() + i < width) at[i] = e[i];
         }
     }
     static __device__ __forceinline__ float get(const X *lds, int tok, int ch) { return DT::widen(lds[tok * LD + ch]); }
@@ -173,36 +227,90 @@ struct Rows {
 template <class DT, int LPC>
 struct Shared {
     using X = typename DT::X;
-    static constexpr int NP = 4 * LPC, PT = TT * NP / THREADS, SIZE = TT * NP;
+    static constexpr int NP = 4 * LPC, PT = TT * NP / THREADS, SIZE = TT * NP, ROWS = THREADS / NP > 0 ? THREADS / NP : 1;
     X v[PT];
-    __device__ __forceinline__ void fetch(const X *p, int64_t ld, int t, int cnt, int n0, int N) {
+    static __device__ __forceinline__ int state() { return (int)threadIdx.x % NP; }
+    // the tensor from state n0 on; a lane has one state of every ROWS-th token
+    static __device__ __forceinline__ Walk<X> walk(const void *p, int64_t ld, int n0, int N) {
+        return {(const X *)p + n0, ld, (int)threadIdx.x / NP, state() < N ? state() : 0};
+    }
+    __device__ __forceinline__ void fetch(const Walk<X> &w, int t, int cnt) {
 #pragma unroll
         for (int k = 0; k < PT; ++k) {
-            const int i = (int)threadIdx.x + k * THREADS, n = i % NP, r = i / NP;
-            v[k] = r < cnt && n < N ? p[(int64_t)(t + r) * ld + n0 + n] : (X)0;
+            const int r = (int)threadIdx.x / NP + k * ROWS;
+            v[k] = (X)0;
+            if (cnt == TT || r < cnt) v[k] = *w.at(t + k * ROWS);
         }
     }
-    __device__ __forceinline__ void put(float *lds) const {
+    __device__ __forceinline__ void put(float *lds, int N) const {
 #pragma unroll
-        for (int k = 0; k < PT; ++k) lds[threadIdx.x + k * THREADS] = DT::widen(v[k]);
+        for (int k = 0; k < PT; ++k) lds[threadIdx.x + k * THREADS] = state() < N ? DT::widen(v[k]) : 0.0f;
     }
     static __device__ __forceinline__ void get(float (&o)[4], const float *lds, int tok, int j) {
         load_f32<F32, 4>(o, lds + tok * NP + 4 * j);
     }
 };
 
+// What a tile's tokens need once a channel; lane q of a quad has tokens q, 4 + q ...
+// Tokens past the end have width zero: they change no state.
+template <class DT, int LPC>
+struct Own {
+    float x[4], d[4], u[4], slope[4];  // u = d x
+    __device__ __forceinline__ Own(const typename DT::X *sx, const typename DT::X *sd, const ScanLane<LPC> &w, float bias,
+                                   int soft, int cnt) {
+        using R = Rows<DT, LPC>;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int own = 4 * k + w.q;
+            x[k] = R::get(sx, own, w.ch);
+            d[k] = R::get(sd, own, w.ch) + bias;
+            slope[k] = 1.0f;
+        }
+        if (soft) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[k] = softplus<DT>(d[k], slope[k]);
+        }
+        if (cnt < TT) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[k] = 4 * k + w.q < cnt ? d[k] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = d[k] * x[k];
+    }
+};
+// The value of lane S of each quad, for a token's number in the tile
+__device__ __forceinline__ float of_token(const float (&v)[4], int t) {
+    const float w = v[t / 4];
+    return t % 4 == 0 ? quad<0>(w) : t % 4 == 1 ? quad<1>(w) : t % 4 == 2 ? quad<2>(w) : quad<3>(w);
+}
+// f(k) for the four quads of tokens that a tile of cnt has; all of them at once where it
+// is full, so that one quad's sums run beside the next one's products
+template <class F>
+__device__ __forceinline__ void quads(int cnt, F f) {
+    if (cnt == TT) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f(k);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (4 * k < cnt) f(k);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <class DT, int LPC>
-__global__ void __launch_bounds__(THREADS)
+template <class DT, int LPC, bool GATE>
+__global__ void __launch_bounds__(THREADS, sizeof(typename DT::X) == 2 && LPC <= 8 ? 5 : 3)
     k_out(ScanGeo G, ScanIn in, const float *state_in, const float *starts, float *state_out, typename DT::X *y, int64_t ldy) {
     using X = typename DT::X;
     using R = Rows<DT, LPC>;
     using S = Shared<DT, LPC>;
-    __shared__ __align__(16) X sx[2][R::SIZE], sd[2][R::SIZE], sz[2][R::SIZE], sy[2][R::SIZE];
+    __shared__ __align__(16) X sx[2][R::SIZE], sd[2][R::SIZE], sz[2][GATE ? R::SIZE : 8], sy[2][R::SIZE];
     __shared__ __align__(16) float sb[2][S::SIZE], sc[2][S::SIZE];
-    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    uint32_t id = spread<LPC>(blockIdx.x, gridDim.x);
+    longest_first(G, id, gridDim.x);
+    id = (uint32_t)uniform((int)id);
     const ScanLane<LPC> w(G, id % G.nblk);
     const uint32_t slot = id / G.nblk;
     const Piece p = piece(G, slot);
@@ -213,61 +321,56 @@ __global__ void __launch_bounds__(THREADS)
     if (starts) load_f32<F32, 4>(h, starts + ((int64_t)id * THREADS + threadIdx.x) * 4);
     else load_states(h, state_in ? state_in + srow : nullptr, 4 * w.j, G.N, w.live && state_in);
     const float bias = in.bias && w.live ? in.bias[w.c] : 0.0f, skip = in.skip && w.live ? in.skip[w.c] : 0.0f;
+    const Walk<X> wx = R::walk(in.x, in.ldx, w.c0), wd = R::walk(in.dt, in.lddt, w.c0), wz = R::walk(in.gate, in.ldgate, w.c0),
+                  wy = R::walk(y, ldy, w.c0), wb = S::walk(in.b, in.ldb, w.g * G.N, G.N), wc = S::walk(in.c, in.ldc, w.g * G.N, G.N);
+    const int width = w.cend - w.c0;
     R rx, rd, rz;
     S rb, rc;
     auto fetch = [&](int t) {
         const int cnt = min(TT, p.t1 - t);
-        rx.fetch((const X *)in.x, in.ldx, t, cnt, w.c0, w.cend);
-        rd.fetch((const X *)in.dt, in.lddt, t, cnt, w.c0, w.cend);
-        if (in.gate) rz.fetch((const X *)in.gate, in.ldgate, t, cnt, w.c0, w.cend);
-        rb.fetch((const X *)in.b, in.ldb, t, cnt, w.g * G.N, G.N);
-        rc.fetch((const X *)in.c, in.ldc, t, cnt, w.g * G.N, G.N);
+        rx.fetch(wx, t, cnt, width);
+        rd.fetch(wd, t, cnt, width);
+        if (GATE) rz.fetch(wz, t, cnt, width);
+        rb.fetch(wb, t, cnt);
+        rc.fetch(wc, t, cnt);
     };
     int k = 0;
     if (p.t0 < p.t1) fetch(p.t0);
     for (int t = p.t0; t < p.t1; t += TT, k ^= 1) {
         rx.put(sx[k]);
         rd.put(sd[k]);
-        if (in.gate) rz.put(sz[k]);
-        rb.put(sb[k]);
-        rc.put(sc[k]);
+        if (GATE) rz.put(sz[k]);
+        rb.put(sb[k], G.N);
+        rc.put(sc[k], G.N);
         __syncthreads();  // the one barrier a tile: what a tile writes is read in its own turn or the next
-        if (t > p.t0) R::flush(sy[k ^ 1], y, ldy, t - TT, TT, w.c0, w.cend);
+        if (t > p.t0) R::flush(sy[k ^ 1], wy, t - TT, TT, width);
         if (p.t1 - t > TT) fetch(t + TT);
         const int cnt = min(TT, p.t1 - t);
-        for (int u = 0; u < cnt; u += 4) {
-            const int own = u + w.q;
-            const float xv = R::get(sx[k], own, w.ch);
-            float slope;
-            float d = step_width<DT>(R::get(sd[k], own, w.ch) + bias, G.soft, slope);
-            d = own < cnt ? d : 0.0f;
-            const float dx = d * xv;
-            float yy = 0.0f;
-            auto token = [&](int s, float ds, float us) {
-                float bv[4], cv[4], v = 0.0f;
-                S::get(bv, sb[k], u + s, w.j);
-                S::get(cv, sc[k], u + s, w.j);
+        const Own<DT, LPC> own(sx[k], sd[k], w, bias, G.soft, cnt);
+        quads(cnt, [&](int n) {
+            float v[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float ds = of_token(own.d, 4 * n + s), us = of_token(own.u, 4 * n + s);
+                float bv[4], cv[4];
+                S::get(bv, sb[k], 4 * n + s, w.j);
+                S::get(cv, sc[k], 4 * n + s, w.j);
+                v[s] = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * a2[i]), h[i], us * bv[i]);
-                    v = __builtin_fmaf(h[i], cv[i], v);
+                    v[s] = __builtin_fmaf(h[i], cv[i], v[s]);
                 }
-                v = sum_states<LPC>(v);
-                yy = w.q == s ? v : yy;
-            };
-            token(0, quad<0>(d), quad<0>(dx));
-            token(1, quad<1>(d), quad<1>(dx));
-            token(2, quad<2>(d), quad<2>(dx));
-            token(3, quad<3>(d), quad<3>(dx));
-            yy = __builtin_fmaf(skip, xv, yy);
-            if (in.gate) yy *= gate_value<DT>(R::get(sz[k], own, w.ch), G.act);
-            if (w.j < 4) R::set(sy[k], own, w.ch, yy);
-        }
+            }
+            float yy = __builtin_fmaf(skip, own.x[n], sum_states4<LPC>(v, w.q));
+            if (GATE) yy *= gate_value<DT>(R::get(sz[k], 4 * n + w.q, w.ch), G.act);
+            if (w.j < 4) R::set(sy[k], 4 * n + w.q, w.ch, yy);
+        });
     }
     if (p.t0 < p.t1) {
         __syncthreads();
         const int t = p.t0 + (p.t1 - p.t0 - 1) / TT * TT;
-        R::flush(sy[k ^ 1], y, ldy, t, p.t1 - t, w.c0, w.cend);
+        R::flush(sy[k ^ 1], wy, t, p.t1 - t, width);
     }
     if (state_out && !starts) store_states(state_out + srow, h, 4 * w.j, G.N, w.live);
 }
@@ -283,7 +386,7 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
     constexpr int B = BACK ? 1 : 0;
     __shared__ __align__(16) X sx[2][R::SIZE], sd[2][R::SIZE], sy[B + 1][B ? R::SIZE : 8], sz[B + 1][B ? R::SIZE : 8];
     __shared__ __align__(16) float sb[2][S::SIZE], sc[B + 1][B ? S::SIZE : 4];
-    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const uint32_t id = spread<LPC>(blockIdx.x, gridDim.x);
     const ScanLane<LPC> w(G, id % G.nblk);
     const Piece p = piece(G, id / G.nblk);
     if (p.t0 >= p.t1) return;
@@ -292,17 +395,21 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
 #pragma unroll
     for (int i = 0; i < 4; ++i) h[i] = g[i] = 0.0f, fade[i] = 1.0f;
     const float bias = in.bias && w.live ? in.bias[w.c] : 0.0f;
+    const Walk<X> wx = R::walk(in.x, in.ldx, w.c0), wd = R::walk(in.dt, in.lddt, w.c0), wz = R::walk(in.gate, in.ldgate, w.c0),
+                  wy = R::walk(in.dy, in.lddy, w.c0), wb = S::walk(in.b, in.ldb, w.g * G.N, G.N),
+                  wc = S::walk(in.c, in.ldc, w.g * G.N, G.N);
+    const int chans = w.cend - w.c0;
     R rx, rd, ry, rz;
     S rb, rc;
     auto fetch = [&](int t) {
         const int cnt = min(TT, p.t1 - t);
-        rx.fetch((const X *)in.x, in.ldx, t, cnt, w.c0, w.cend);
-        rd.fetch((const X *)in.dt, in.lddt, t, cnt, w.c0, w.cend);
-        rb.fetch((const X *)in.b, in.ldb, t, cnt, w.g * G.N, G.N);
+        rx.fetch(wx, t, cnt, chans);
+        rd.fetch(wd, t, cnt, chans);
+        rb.fetch(wb, t, cnt);
         if (BACK) {
-            ry.fetch((const X *)in.dy, in.lddy, t, cnt, w.c0, w.cend);
-            if (in.gate) rz.fetch((const X *)in.gate, in.ldgate, t, cnt, w.c0, w.cend);
-            rc.fetch((const X *)in.c, in.ldc, t, cnt, w.g * G.N, G.N);
+            ry.fetch(wy, t, cnt, chans);
+            if (in.gate) rz.fetch(wz, t, cnt, chans);
+            rc.fetch(wc, t, cnt);
         }
     };
     int k = 0;
@@ -310,45 +417,40 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
     for (int t = p.t0; t < p.t1; t += TT, k ^= 1) {
         rx.put(sx[k]);
         rd.put(sd[k]);
-        rb.put(sb[k]);
+        rb.put(sb[k], G.N);
         if (BACK) {
             ry.put(sy[k & B]);
             if (in.gate) rz.put(sz[k & B]);
-            rc.put(sc[k & B]);
+            rc.put(sc[k & B], G.N);
         }
         __syncthreads();
         if (p.t1 - t > TT) fetch(t + TT);
         const int cnt = min(TT, p.t1 - t);
-        for (int u = 0; u < cnt; u += 4) {
-            const int own = u + w.q;
-            float slope, dy = 0.0f;
-            float d = step_width<DT>(R::get(sd[k], own, w.ch) + bias, G.soft, slope);
-            d = own < cnt ? d : 0.0f;
-            sum += d;
-            const float dx = d * R::get(sx[k], own, w.ch);
+        const Own<DT, LPC> own(sx[k], sd[k], w, bias, G.soft, cnt);
+        quads(cnt, [&](int n) {
+            sum += own.d[n];
+            float dy[4];
             if (BACK) {
-                dy = R::get(sy[k & B], own, w.ch);
-                if (in.gate) dy *= gate_value<DT>(R::get(sz[k & B], own, w.ch), G.act);
+                dy[n] = R::get(sy[k & B], 4 * n + w.q, w.ch);
+                if (in.gate) dy[n] *= gate_value<DT>(R::get(sz[k & B], 4 * n + w.q, w.ch), G.act);
             }
-            auto token = [&](int s, float ds, float us, float ys) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const float ds = of_token(own.d, 4 * n + s), us = of_token(own.u, 4 * n + s);
                 float bv[4], cv[4];
-                S::get(bv, sb[k], u + s, w.j);
-                if (BACK) S::get(cv, sc[k & B], u + s, w.j);
+                S::get(bv, sb[k], 4 * n + s, w.j);
+                if (BACK) S::get(cv, sc[k & B], 4 * n + s, w.j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float e = __builtin_amdgcn_exp2f(ds * a2[i]);
                     h[i] = __builtin_fmaf(e, h[i], us * bv[i]);
                     if (BACK) {
                         fade[i] *= e;
-                        g[i] = __builtin_fmaf(fade[i], cv[i] * ys, g[i]);
+                        g[i] = __builtin_fmaf(fade[i], cv[i] * of_token(dy, 4 * n + s), g[i]);
                     }
                 }
-            };
-            token(0, quad<0>(d), quad<0>(dx), quad<0>(dy));
-            token(1, quad<1>(d), quad<1>(dx), quad<1>(dy));
-            token(2, quad<2>(d), quad<2>(dx), quad<2>(dy));
-            token(3, quad<3>(d), quad<3>(dx), quad<3>(dy));
-        }
+            }
+        });
     }
     const int64_t at = ((int64_t)id * THREADS + threadIdx.x) * 4;
     store_f32<F32, 4>(ends + at, h);
@@ -359,12 +461,12 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
 }
 
 // Walks the runs of a sequence: `ends` becomes the state before each run, `back` the
-// gradient of the state after it.  Four runs are on their way at a time.
+// gradient of the state after it.  Sixteen runs are on their way at a time.
 template <int LPC, bool BACK>
 __global__ void __launch_bounds__(THREADS)
     k_join(ScanGeo G, const float *a, const float *state_in, float *state_out, const float *dstate_out, float *dstate_in,
            float *ends, const float *width, float *back) {
-    constexpr int U = 4, CPW = ScanLane<LPC>::CPW;
+    constexpr int U = 16, CPW = ScanLane<LPC>::CPW;
     const uint32_t cb = blockIdx.x % G.nblk;
     const int s = (int)(blockIdx.x / G.nblk);
     const ScanLane<LPC> w(G, cb);
@@ -413,7 +515,7 @@ struct Out {
     float *pa, *ps;         // walkers x channel blocks x (256 x 4: da; 2 x CPW: dskip, dbias)
 };
 
-template <class DT, int LPC>
+template <class DT, int LPC, bool GATE>
 __global__ void __launch_bounds__(THREADS, 2)
     k_grad(ScanGeo G, ScanIn in, Out o, const float *state_in, const float *dstate_out, float *dstate_in, const float *starts,
            const float *afters) {
@@ -423,10 +525,12 @@ __global__ void __launch_bounds__(THREADS, 2)
     using A = Across<LPC>;
     constexpr int NP = 4 * LPC, CPW = THREADS / LPC;
     constexpr int ROUND = LPC <= 8 ? 16 : LPC == 16 ? 8 : 4;  // tokens whose sums over channels LDS holds (16 KB)
-    __shared__ __align__(16) X sx[R::SIZE], sd[R::SIZE], sy[R::SIZE], sz[R::SIZE];
+    __shared__ __align__(16) X sx[R::SIZE], sd[R::SIZE], sy[R::SIZE], sz[GATE ? R::SIZE : 8];
     __shared__ __align__(16) float sb[S::SIZE], sc[S::SIZE];
     __shared__ float red[4][ROUND * 2 * NP];
-    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x), cb = id % G.nblk, walker = id / G.nblk;
+    uint32_t id = spread<LPC>(blockIdx.x, gridDim.x);
+    if (G.walkers == G.slots) longest_first(G, id, gridDim.x);
+    const uint32_t cb = id % G.nblk, walker = id / G.nblk;
     const ScanLane<LPC> w(G, cb);
     const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
     float a2[4], da[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dskip = 0.0f, dbias = 0.0f;
@@ -437,7 +541,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (G.CH && p.t0 >= p.t1) continue;
         const int64_t srow = ((int64_t)p.s * G.C + (w.live ? w.c : 0)) * G.N;
         const int64_t mine = ((int64_t)slot * G.nblk + cb) * THREADS + threadIdx.x;
-        const int begin = G.seq.begin(p.s);
+        const int begin = uniform(G.seq.begin(p.s));
         // the kept state of the block that begins at token t
         auto kept = [&](int t) {
             const int64_t block = (int64_t)(begin / TT) + p.s + (t - begin) / TT;
@@ -449,50 +553,46 @@ __global__ void __launch_bounds__(THREADS, 2)
         if (afters) load_f32<F32, 4>(g, afters + mine * 4);
         else load_states(g, dstate_out ? dstate_out + srow : nullptr, 4 * w.j, G.N, w.live && dstate_out);
         const int tl = p.t1 > p.t0 ? p.t0 + (p.t1 - p.t0 - 1) / TT * TT : p.t0;  // the last block
+        const Walk<X> wx = R::walk(in.x, in.ldx, w.c0), wd = R::walk(in.dt, in.lddt, w.c0),
+                      wz = R::walk(in.gate, in.ldgate, w.c0), wy = R::walk(in.dy, in.lddy, w.c0),
+                      wb = S::walk(in.b, in.ldb, w.g * G.N, G.N), wc = S::walk(in.c, in.ldc, w.g * G.N, G.N);
+        const int width = w.cend - w.c0;
         R rx, rd, ry, rz;
         S rb, rc;
         // forward to the last block, keeping the states before each
         auto fetch_in = [&](int t) {
-            rx.fetch((const X *)in.x, in.ldx, t, TT, w.c0, w.cend);
-            rd.fetch((const X *)in.dt, in.lddt, t, TT, w.c0, w.cend);
-            rb.fetch((const X *)in.b, in.ldb, t, TT, w.g * G.N, G.N);
+            rx.fetch(wx, t, TT, width);
+            rd.fetch(wd, t, TT, width);
+            rb.fetch(wb, t, TT);
         };
         if (p.t0 < tl) fetch_in(p.t0);
         for (int t = p.t0; t < tl; t += TT) {
             __syncthreads();
             rx.put(sx);
             rd.put(sd);
-            rb.put(sb);
+            rb.put(sb, G.N);
             __syncthreads();
             if (t + TT < tl) fetch_in(t + TT);
             store_f32<F32, 4>(kept(t), h);
-            for (int u = 0; u < TT; u += 4) {
-                const int own = u + w.q;
-                float slope;
-                const float d = step_width<DT>(R::get(sd, own, w.ch) + bias, G.soft, slope);
-                const float dx = d * R::get(sx, own, w.ch);
-                auto token = [&](int s, float ds, float us) {
-                    float bv[4];
-                    S::get(bv, sb, u + s, w.j);
+            const Own<DT, LPC> own(sx, sd, w, bias, G.soft, TT);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * a2[i]), h[i], us * bv[i]);
-                };
-                token(0, quad<0>(d), quad<0>(dx));
-                token(1, quad<1>(d), quad<1>(dx));
-                token(2, quad<2>(d), quad<2>(dx));
-                token(3, quad<3>(d), quad<3>(dx));
+            for (int s = 0; s < TT; ++s) {
+                const float ds = of_token(own.d, s), us = of_token(own.u, s);
+                float bv[4];
+                S::get(bv, sb, s, w.j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * a2[i]), h[i], us * bv[i]);
             }
         }
         // back over the blocks
         auto fetch = [&](int t) {
             const int cnt = min(TT, p.t1 - t);
-            rx.fetch((const X *)in.x, in.ldx, t, cnt, w.c0, w.cend);
-            rd.fetch((const X *)in.dt, in.lddt, t, cnt, w.c0, w.cend);
-            ry.fetch((const X *)in.dy, in.lddy, t, cnt, w.c0, w.cend);
-            if (in.gate) rz.fetch((const X *)in.gate, in.ldgate, t, cnt, w.c0, w.cend);
-            rb.fetch((const X *)in.b, in.ldb, t, cnt, w.g * G.N, G.N);
-            rc.fetch((const X *)in.c, in.ldc, t, cnt, w.g * G.N, G.N);
+            rx.fetch(wx, t, cnt, width);
+            rd.fetch(wd, t, cnt, width);
+            ry.fetch(wy, t, cnt, width);
+            if (GATE) rz.fetch(wz, t, cnt, width);
+            rb.fetch(wb, t, cnt);
+            rc.fetch(wc, t, cnt);
         };
         if (p.t0 < p.t1) fetch(tl);
         for (int t = tl; t >= p.t0 && p.t0 < p.t1; t -= TT) {
@@ -501,9 +601,9 @@ __global__ void __launch_bounds__(THREADS, 2)
             rx.put(sx);
             rd.put(sd);
             ry.put(sy);
-            if (in.gate) rz.put(sz);
-            rb.put(sb);
-            rc.put(sc);
+            if (GATE) rz.put(sz);
+            rb.put(sb, G.N);
+            rc.put(sc, G.N);
             __syncthreads();
             float h0[4];
 #pragma unroll
@@ -512,42 +612,32 @@ __global__ void __launch_bounds__(THREADS, 2)
                 fetch(t - TT);
                 load_f32<F32, 4>(h, kept(t - TT));  // for the next block
             }
-            // the block's states and decays, and what its tokens need once a channel
-            float hs[TT][4], es[TT][4], d[4], slope[4], dy[4];
+            // the block's states and decays
+            float hs[TT][4], es[TT][4], dy[4];
+            const Own<DT, LPC> own(sx, sd, w, bias, G.soft, cnt);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int own = 4 * k + w.q;
-                d[k] = step_width<DT>(R::get(sd, own, w.ch) + bias, G.soft, slope[k]);
-                d[k] = own < cnt ? d[k] : 0.0f;
-                const float xv = R::get(sx, own, w.ch), dx = d[k] * xv;
-                dy[k] = R::get(sy, own, w.ch);
-                float yy = 0.0f;
-                auto token = [&](int s, float ds, float us) {
-                    float bv[4], cv[4], v = 0.0f;
-                    S::get(bv, sb, 4 * k + s, w.j);
-                    if (in.gate) S::get(cv, sc, 4 * k + s, w.j);
+                dy[k] = R::get(sy, 4 * k + w.q, w.ch);
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int n = 4 * k + s;
+                    const float ds = of_token(own.d, n), us = of_token(own.u, n);
+                    float bv[4], cv[4];
+                    S::get(bv, sb, n, w.j);
+                    if (GATE) S::get(cv, sc, n, w.j);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float e = __builtin_amdgcn_exp2f(ds * a2[i]);
-                        const float before = k + s ? hs[k + s ? 4 * k + s - 1 : 0][i] : h0[i];
-                        es[4 * k + s][i] = e;
-                        hs[4 * k + s][i] = __builtin_fmaf(e, before, us * bv[i]);
-                        if (in.gate) v = __builtin_fmaf(hs[4 * k + s][i], cv[i], v);
+                        es[n][i] = __builtin_amdgcn_exp2f(ds * a2[i]);
+                        hs[n][i] = __builtin_fmaf(es[n][i], n ? hs[n ? n - 1 : 0][i] : h0[i], us * bv[i]);
+                        if (GATE) v[s] = __builtin_fmaf(hs[n][i], cv[i], v[s]);
                     }
-                    if (in.gate) {
-                        v = sum_states<LPC>(v);
-                        yy = w.q == s ? v : yy;
-                    }
-                };
-                token(0, quad<0>(d[k]), quad<0>(dx));
-                token(1, quad<1>(d[k]), quad<1>(dx));
-                token(2, quad<2>(d[k]), quad<2>(dx));
-                token(3, quad<3>(d[k]), quad<3>(dx));
-                if (in.gate) {
+                }
+                if (GATE) {
                     float gs;
-                    const float gv = gate_value<DT>(R::get(sz, own, w.ch), G.act, gs);
-                    yy = __builtin_fmaf(skip, xv, yy);
-                    if (w.j < 4) R::set(sz, own, w.ch, dy[k] * yy * gs);
+                    const float gv = gate_value<DT>(R::get(sz, 4 * k + w.q, w.ch), G.act, gs);
+                    const float yy = __builtin_fmaf(skip, own.x[k], sum_states4<LPC>(v, w.q));
+                    if (w.j < 4) R::set(sz, 4 * k + w.q, w.ch, dy[k] * yy * gs);
                     dy[k] *= gv;
                 }
             }
@@ -556,50 +646,42 @@ __global__ void __launch_bounds__(THREADS, 2)
             const int first = A::first(lane);
 #pragma unroll
             for (int k = 3; k >= 0; --k) {
-                const int own = 4 * k + w.q;
-                const float xv = R::get(sx, own, w.ch), dx = d[k] * xv;
-                float du = 0.0f, dd = 0.0f;
-                auto token = [&](int s, float ds, float us, float ys) {
-                    float bv[4], cv[4], vu = 0.0f, vd = 0.0f;
-                    S::get(bv, sb, 4 * k + s, w.j);
-                    S::get(cv, sc, 4 * k + s, w.j);
-                    const int to = (4 * k + s) % A::TOK * 8;
+                float vu[4] = {0.0f, 0.0f, 0.0f, 0.0f}, vd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 3; s >= 0; --s) {
+                    const int n = 4 * k + s, to = n % A::TOK * 8;
+                    const float ds = of_token(own.d, n), us = of_token(own.u, n), ys = of_token(dy, n);
+                    float bv[4], cv[4];
+                    S::get(bv, sb, n, w.j);
+                    S::get(cv, sc, n, w.j);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         g[i] = __builtin_fmaf(cv[i], ys, g[i]);
                         v[to + i] = g[i] * us;
-                        v[to + 4 + i] = hs[4 * k + s][i] * ys;
-                        vu = __builtin_fmaf(g[i], bv[i], vu);
-                        g[i] *= es[4 * k + s][i];
-                        const float gh = g[i] * (k + s ? hs[k + s ? 4 * k + s - 1 : 0][i] : h0[i]);
-                        vd = __builtin_fmaf(gh, a2[i], vd);
+                        v[to + 4 + i] = hs[n][i] * ys;
+                        vu[s] = __builtin_fmaf(g[i], bv[i], vu[s]);
+                        g[i] *= es[n][i];
+                        const float gh = g[i] * (n ? hs[n ? n - 1 : 0][i] : h0[i]);
+                        vd[s] = __builtin_fmaf(gh, a2[i], vd[s]);
                         da[i] = __builtin_fmaf(gh, ds, da[i]);
                     }
-                    vu = sum_states<LPC>(vu);
-                    vd = sum_states<LPC>(vd);
-                    du = w.q == s ? vu : du;
-                    dd = w.q == s ? vd : dd;
-                    if ((4 * k + s) % A::TOK == 0) {
+                    if (n % A::TOK == 0) {
                         A::sum(v, lane);
 #pragma unroll
                         for (int r = 0; r < A::R; ++r) {
-                            const int i = first + r, tok = (4 * k + s) % ROUND + i / 8;
+                            const int i = first + r, tok = n % ROUND + i / 8;
                             red[wave][(tok * 2 + i / 4 % 2) * NP + 4 * w.j + i % 4] = v[r];
                         }
                     }
-                };
-                token(3, quad<3>(d[k]), quad<3>(dx), quad<3>(dy[k]));
-                token(2, quad<2>(d[k]), quad<2>(dx), quad<2>(dy[k]));
-                token(1, quad<1>(d[k]), quad<1>(dx), quad<1>(dy[k]));
-                token(0, quad<0>(d[k]), quad<0>(dx), quad<0>(dy[k]));
-                // own tokens past the end have d = dy = 0: they add nothing
-                const float dw = __builtin_fmaf(du, xv, dd * LN2) * slope[k];
-                const float add = own < cnt ? dw : 0.0f;
-                dbias += add;
-                dskip = __builtin_fmaf(dy[k], xv, dskip);
+                }
+                const float du = sum_states4<LPC>(vu, w.q), dd = sum_states4<LPC>(vd, w.q);
+                // tokens past the end have d = dy = 0: they add nothing
+                const float dw = __builtin_fmaf(du, own.x[k], dd * LN2) * own.slope[k];
+                dbias += 4 * k + w.q < cnt ? dw : 0.0f;
+                dskip = __builtin_fmaf(dy[k], own.x[k], dskip);
                 if (w.j < 4) {
-                    R::set(sx, own, w.ch, __builtin_fmaf(du, d[k], skip * dy[k]));
-                    R::set(sd, own, w.ch, dw);
+                    R::set(sx, 4 * k + w.q, w.ch, __builtin_fmaf(du, own.d[k], skip * dy[k]));
+                    R::set(sd, 4 * k + w.q, w.ch, dw);
                 }
                 if (4 * k % ROUND == 0) {
                     __syncthreads();
@@ -611,9 +693,9 @@ __global__ void __launch_bounds__(THREADS, 2)
                     if (k) __syncthreads();
                 }
             }
-            R::flush(sx, (X *)o.dx, o.lddx, t, cnt, w.c0, w.cend);
-            R::flush(sd, (X *)o.ddt, o.ldddt, t, cnt, w.c0, w.cend);
-            if (in.gate && o.dgate) R::flush(sz, (X *)o.dgate, o.lddgate, t, cnt, w.c0, w.cend);
+            R::flush(sx, R::walk(o.dx, o.lddx, w.c0), t, cnt, width);
+            R::flush(sd, R::walk(o.ddt, o.ldddt, w.c0), t, cnt, width);
+            if (GATE && o.dgate) R::flush(sz, R::walk(o.dgate, o.lddgate, w.c0), t, cnt, width);
         }
         if (dstate_in && !afters) store_states(dstate_in + srow, g, 4 * w.j, G.N, w.live);
     }
@@ -740,7 +822,8 @@ hipError_t fwd(const dwconv_scan_plan &p, const ScanArgs &a, hipStream_t st) {
         k_join<LPC, false><<<(uint32_t)joins, THREADS, 0, st>>>(G, a.a, a.state_in, a.state_out, nullptr, nullptr, starts,
                                                                 width, nullptr);
     }
-    k_out<DT, LPC><<<(uint32_t)blocks, THREADS, 0, st>>>(G, in, a.state_in, starts, a.state_out, (typename DT::X *)a.y, a.ldy);
+    (a.gate ? k_out<DT, LPC, true> : k_out<DT, LPC, false>)<<<(uint32_t)blocks, THREADS, 0, st>>>(
+        G, in, a.state_in, starts, a.state_out, (typename DT::X *)a.y, a.ldy);
     return hipGetLastError();
 }
 
@@ -769,8 +852,8 @@ hipError_t bwd(const dwconv_scan_plan &p, const ScanArgs &a, hipStream_t st) {
                                                                width, back);
     }
     if (walks)
-        k_grad<DT, LPC><<<(uint32_t)walks, THREADS, 0, st>>>(G, in, o, a.state_in, a.dstate_out, a.dstate_in,
-                                                             G.CH ? ends : nullptr, G.CH ? back : nullptr);
+        (a.gate ? k_grad<DT, LPC, true> : k_grad<DT, LPC, false>)<<<(uint32_t)walks, THREADS, 0, st>>>(
+            G, in, o, a.state_in, a.dstate_out, a.dstate_in, G.CH ? ends : nullptr, G.CH ? back : nullptr);
     const Total tot{a.db, a.dc, a.lddb, a.lddc, a.da, a.dskip, a.dbias, (uint32_t)bc, (uint32_t)ab};
     k_total<DT, LPC><<<(uint32_t)(bc + ab + sb), THREADS, 0, st>>>(G, o, tot);
     return hipGetLastError();

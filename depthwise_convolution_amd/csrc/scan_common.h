@@ -49,6 +49,27 @@ __device__ __forceinline__ float sum_states(float v) {
     return v;
 }
 
+// Of four tokens' values at once: lane q of each quad gets the sum over the channel's
+// lanes of token q's value.
+template <int LPC>
+__device__ __forceinline__ float sum_states4(const float (&v)[4], int q) {
+    const bool odd = q & 1, hi = q & 2;
+    const float a = (odd ? v[1] : v[0]) + dpp<0xB1>(odd ? v[0] : v[1]);
+    const float b = (odd ? v[3] : v[2]) + dpp<0xB1>(odd ? v[2] : v[3]);
+    float s = (hi ? b : a) + dpp<0x4E>(hi ? a : b);
+    if (LPC == 8) s += dpp_banks<0x104, 0x5>(s) + dpp_banks<0x114, 0xa>(s);  // lane ^ 4
+    if (LPC >= 16) {
+        s += dpp<0x128>(s);  // eight lanes round
+        s += dpp<0x124>(s);  // four
+    }
+    if (LPC >= 32) {
+        float w = s;
+        swap16(s, w);
+        s += w;
+    }
+    return s;
+}
+
 // softplus(v) = max(v, 0) + ln(1 + t), t = e^-|v| <= 1, and its slope 1 / (1 + e^-v).
 // ln(1 + t) is ln w of the rounded w = 1 + t plus what the rounding left, t - (w - 1)
 // (over w, but that factor only counts where t is next to 1 and so the rest next to
@@ -56,10 +77,11 @@ __device__ __forceinline__ float sum_states(float v) {
 // h = |v| / ln 2, so off by |v| units more, which fp32 data puts right.
 template <class DT>
 __device__ __forceinline__ float softplus(float v, float &slope) {
-    const float m = __builtin_fabsf(v), lim = m > 200.0f ? 200.0f : m, h = lim * LOG2E;
-    float t = __builtin_amdgcn_exp2f(-h);
+    float t = __builtin_amdgcn_exp2f(__builtin_fabsf(v) * -LOG2E);
     if (sizeof(typename DT::X) == 4) {
+        const float m = __builtin_fabsf(v), lim = m > 200.0f ? 200.0f : m, h = lim * LOG2E;
         const float r = __builtin_fmaf(h, 1.90465421e-9f, __builtin_fmaf(h, -LN2, lim));
+        t = __builtin_amdgcn_exp2f(-h);
         t = __builtin_fmaf(t, -r, t);
     }
     const float w = 1.0f + t, s = __builtin_amdgcn_rcpf(w);

@@ -54,7 +54,7 @@
  *                16, 8 for N > 16, 32, 64) of a sequence or of 64 or more tokens of
  *                it, in a step of one row; gradients also 2^24 for every 8 (4, 2, 1)
  *                tokens of a group of channels; the workspace's size is then given as
- *                SIZE_MAX
+ *                SIZE_MAX.  Token strides are at most 2^26 elements there (but in a step)
  *   group norm   2^24 workgroups of an image's 8 channels or more, or of 8 KB or more
  *
  * float (fp32) everywhere: biases, scales, norm weights, decays, rates, write

@@ -168,6 +168,12 @@ def test_grids_that_pass_their_limit_are_unsupported():
                                        lddgate=2 ** 24, state_in=None, dstate_out=None, dstate_in=None, **wide)) == 2
     assert dw.dwconv_scan_workspace(h, 64, 64, True) == 2 ** 64 - 1
     dw.dwconv_scan_destroy(h)
+    h = dw.dwconv_scan_create(8, 4, 1, "f32", True, "silu")
+    for name in ("ldx", "lddt", "ldb", "ldc", "ldgate", "ldy"):
+        assert status_of(lambda: call_scan("fwd", h, **{name: 2 ** 26 + 1})) == 2
+    for name in ("ldx", "lddt", "ldb", "ldc", "ldgate", "lddy", "lddx", "ldddt", "lddb", "lddc", "lddgate"):
+        assert status_of(lambda: call_scan("bwd", h, **{name: 2 ** 26 + 1})) == 2
+    dw.dwconv_scan_destroy(h)
     h = dw.dwconv_group_create(65536, 65536, "f32", "none", 1e-5)
     assert status_of(lambda: call_group(False, h, images=2 ** 20, pixels=1, ldx=65536, ldy=65536)) == 2
     assert status_of(lambda: call_group(True, h, images=2 ** 20, pixels=1, ldx=65536, ldy=65536, lddy=65536)) == 2
