@@ -17,16 +17,17 @@
 // Gradients, with G the gradient of the state after a token:
 //   G += c dy     dc = sum_channels dy h     db = sum_channels d x G
 //   du = sum_n G b     G *= e^(d a)     dd = sum_n G h_before a + x du     da += d G h_before
-// walk back over blocks of 16 tokens whose first states a walk forward has left in the
+// walk back over blocks of 8 tokens whose first states a walk forward has left in the
 // workspace; a block's states and decays are formed again and stay in registers.
-#include "seq_common.h"
-#include "seq_plan.h"
+#include <type_traits>
+
 #include "scan_common.h"
 
 namespace dw {
 namespace {
 
-constexpr int TT = 16;         // tokens a tile, and between two kept states
+constexpr int TT = 16;         // tokens a tile
+constexpr int HT = 8;          // tokens between two kept states
 constexpr int THREADS = 256;
 // ---------------------------------------------------------------------------
 // lanes
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(THREADS)
 struct Out {
     void *dx, *ddt, *dgate;
     int64_t lddx, ldddt, lddgate;
-    float *kept;            // states before each block of 16 tokens
+    float *kept;            // states before each block of HT tokens
     float *part;            // channel blocks x tokens x 2 x NP: db, dc
     float *pa, *ps;         // walkers x channel blocks x (256 x 4: da; 2 x CPW: dskip, dbias)
 };
@@ -525,8 +526,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     using A = Across<LPC>;
     constexpr int NP = 4 * LPC, CPW = THREADS / LPC;
     constexpr int ROUND = LPC <= 8 ? 16 : LPC == 16 ? 8 : 4;  // tokens whose sums over channels LDS holds (16 KB)
-    __shared__ __align__(16) X sx[R::SIZE], sd[R::SIZE], sy[R::SIZE], sz[GATE ? R::SIZE : 8];
-    __shared__ __align__(16) float sb[S::SIZE], sc[S::SIZE];
+    __shared__ __align__(16) X sx[2][R::SIZE], sd[2][R::SIZE], sy[2][R::SIZE], sz[2][GATE ? R::SIZE : 8];
+    __shared__ __align__(16) float sb[2][S::SIZE], sc[2][S::SIZE];
     __shared__ float red[4][ROUND * 2 * NP];
     uint32_t id = spread<LPC>(blockIdx.x, gridDim.x);
     if (G.walkers == G.slots) longest_first(G, id, gridDim.x);
@@ -536,15 +537,16 @@ __global__ void __launch_bounds__(THREADS, 2)
     float a2[4], da[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dskip = 0.0f, dbias = 0.0f;
     load_rates(a2, in.a, G, w.c, 4 * w.j, w.live);
     const float bias = in.bias && w.live ? in.bias[w.c] : 0.0f, skip = in.skip && w.live ? in.skip[w.c] : 0.0f;
+    int m = 0;  // the half of LDS that the tile has
     for (uint32_t slot = walker; slot < G.slots; slot += G.walkers) {
         const Piece p = piece(G, slot);
         if (G.CH && p.t0 >= p.t1) continue;
         const int64_t srow = ((int64_t)p.s * G.C + (w.live ? w.c : 0)) * G.N;
         const int64_t mine = ((int64_t)slot * G.nblk + cb) * THREADS + threadIdx.x;
         const int begin = uniform(G.seq.begin(p.s));
-        // the kept state of the block that begins at token t
+        // the kept state of the block of HT tokens that begins at token t
         auto kept = [&](int t) {
-            const int64_t block = (int64_t)(begin / TT) + p.s + (t - begin) / TT;
+            const int64_t block = (int64_t)(begin / HT) + p.s + (t - begin) / HT;
             return o.kept + ((block * G.nblk + cb) * THREADS + threadIdx.x) * 4;
         };
         float h[4], g[4];
@@ -552,7 +554,6 @@ __global__ void __launch_bounds__(THREADS, 2)
         else load_states(h, state_in ? state_in + srow : nullptr, 4 * w.j, G.N, w.live && state_in);
         if (afters) load_f32<F32, 4>(g, afters + mine * 4);
         else load_states(g, dstate_out ? dstate_out + srow : nullptr, 4 * w.j, G.N, w.live && dstate_out);
-        const int tl = p.t1 > p.t0 ? p.t0 + (p.t1 - p.t0 - 1) / TT * TT : p.t0;  // the last block
         const Walk<X> wx = R::walk(in.x, in.ldx, w.c0), wd = R::walk(in.dt, in.lddt, w.c0),
                       wz = R::walk(in.gate, in.ldgate, w.c0), wy = R::walk(in.dy, in.lddy, w.c0),
                       wb = S::walk(in.b, in.ldb, w.g * G.N, G.N), wc = S::walk(in.c, in.ldc, w.g * G.N, G.N);
@@ -561,25 +562,28 @@ __global__ void __launch_bounds__(THREADS, 2)
         S rb, rc;
         // forward to the last block, keeping the states before each
         auto fetch_in = [&](int t) {
-            rx.fetch(wx, t, TT, width);
-            rd.fetch(wd, t, TT, width);
-            rb.fetch(wb, t, TT);
+            const int cnt = min(TT, p.t1 - t);
+            rx.fetch(wx, t, cnt, width);
+            rd.fetch(wd, t, cnt, width);
+            rb.fetch(wb, t, cnt);
         };
-        if (p.t0 < tl) fetch_in(p.t0);
-        for (int t = p.t0; t < tl; t += TT) {
+        if (p.t0 + HT < p.t1) fetch_in(p.t0);
+        for (int t = p.t0; t + HT < p.t1; t += TT, m ^= 1) {
+            rx.put(sx[m]);
+            rd.put(sd[m]);
+            rb.put(sb[m], G.N);
             __syncthreads();
-            rx.put(sx);
-            rd.put(sd);
-            rb.put(sb, G.N);
-            __syncthreads();
-            if (t + TT < tl) fetch_in(t + TT);
-            store_f32<F32, 4>(kept(t), h);
-            const Own<DT, LPC> own(sx, sd, w, bias, G.soft, TT);
+            if (t + TT + HT < p.t1) fetch_in(t + TT);
+            const Own<DT, LPC> own(sx[m], sd[m], w, bias, G.soft, min(TT, p.t1 - t));
 #pragma unroll
             for (int s = 0; s < TT; ++s) {
+                if (s % HT == 0) {
+                    if (t + s + HT >= p.t1) break;
+                    store_f32<F32, 4>(kept(t + s), h);
+                }
                 const float ds = of_token(own.d, s), us = of_token(own.u, s);
                 float bv[4];
-                S::get(bv, sb, s, w.j);
+                S::get(bv, sb[m], s, w.j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(ds * a2[i]), h[i], us * bv[i]);
             }
@@ -594,108 +598,111 @@ __global__ void __launch_bounds__(THREADS, 2)
             rb.fetch(wb, t, cnt);
             rc.fetch(wc, t, cnt);
         };
+        const int tl = p.t1 > p.t0 ? p.t0 + (p.t1 - p.t0 - 1) / TT * TT : p.t0;  // the last tile
         if (p.t0 < p.t1) fetch(tl);
-        for (int t = tl; t >= p.t0 && p.t0 < p.t1; t -= TT) {
+        for (int t = tl; t >= p.t0 && p.t0 < p.t1; t -= TT, m ^= 1) {
             const int cnt = min(TT, p.t1 - t);
-            __syncthreads();  // the tile before has been written out
-            rx.put(sx);
-            rd.put(sd);
-            ry.put(sy);
-            if (GATE) rz.put(sz);
-            rb.put(sb, G.N);
-            rc.put(sc, G.N);
+            rx.put(sx[m]);
+            rd.put(sd[m]);
+            ry.put(sy[m]);
+            if (GATE) rz.put(sz[m]);
+            rb.put(sb[m], G.N);
+            rc.put(sc[m], G.N);
             __syncthreads();
-            float h0[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h0[i] = h[i];
-            if (t > p.t0) {
-                fetch(t - TT);
-                load_f32<F32, 4>(h, kept(t - TT));  // for the next block
-            }
-            // the block's states and decays
-            float hs[TT][4], es[TT][4], dy[4];
-            const Own<DT, LPC> own(sx, sd, w, bias, G.soft, cnt);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                dy[k] = R::get(sy, 4 * k + w.q, w.ch);
-                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int n = 4 * k + s;
-                    const float ds = of_token(own.d, n), us = of_token(own.u, n);
-                    float bv[4], cv[4];
-                    S::get(bv, sb, n, w.j);
-                    if (GATE) S::get(cv, sc, n, w.j);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        es[n][i] = __builtin_amdgcn_exp2f(ds * a2[i]);
-                        hs[n][i] = __builtin_fmaf(es[n][i], n ? hs[n ? n - 1 : 0][i] : h0[i], us * bv[i]);
-                        if (GATE) v[s] = __builtin_fmaf(hs[n][i], cv[i], v[s]);
-                    }
-                }
-                if (GATE) {
-                    float gs;
-                    const float gv = gate_value<DT>(R::get(sz, 4 * k + w.q, w.ch), G.act, gs);
-                    const float yy = __builtin_fmaf(skip, own.x[k], sum_states4<LPC>(v, w.q));
-                    if (w.j < 4) R::set(sz, 4 * k + w.q, w.ch, dy[k] * yy * gs);
-                    dy[k] *= gv;
-                }
-            }
-            // back over its tokens
+            if (t > p.t0) fetch(t - TT);
+            const Own<DT, LPC> own(sx[m], sd[m], w, bias, G.soft, cnt);
             float v[A::V];
             const int first = A::first(lane);
+            // the tokens of quads K and K + 1, the last first
+            auto block = [&](auto quad_of) {
+                constexpr int K = decltype(quad_of)::value;
+                // the block's states and decays
+                float h0[4], hs[HT][4], es[HT][4], dy[4];
 #pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                float vu[4] = {0.0f, 0.0f, 0.0f, 0.0f}, vd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < 4; ++i) h0[i] = h[i];
+                if (t + 4 * K > p.t0) load_f32<F32, 4>(h, kept(t + 4 * K - HT));  // for the next block
 #pragma unroll
-                for (int s = 3; s >= 0; --s) {
-                    const int n = 4 * k + s, to = n % A::TOK * 8;
-                    const float ds = of_token(own.d, n), us = of_token(own.u, n), ys = of_token(dy, n);
-                    float bv[4], cv[4];
-                    S::get(bv, sb, n, w.j);
-                    S::get(cv, sc, n, w.j);
+                for (int k = K; k < K + 2; ++k) {
+                    dy[k] = R::get(sy[m], 4 * k + w.q, w.ch);
+                    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        g[i] = __builtin_fmaf(cv[i], ys, g[i]);
-                        v[to + i] = g[i] * us;
-                        v[to + 4 + i] = hs[n][i] * ys;
-                        vu[s] = __builtin_fmaf(g[i], bv[i], vu[s]);
-                        g[i] *= es[n][i];
-                        const float gh = g[i] * (n ? hs[n ? n - 1 : 0][i] : h0[i]);
-                        vd[s] = __builtin_fmaf(gh, a2[i], vd[s]);
-                        da[i] = __builtin_fmaf(gh, ds, da[i]);
-                    }
-                    if (n % A::TOK == 0) {
-                        A::sum(v, lane);
+                    for (int s = 0; s < 4; ++s) {
+                        const int n = 4 * k + s, l = n - 4 * K;
+                        const float ds = of_token(own.d, n), us = of_token(own.u, n);
+                        float bv[4], cv[4];
+                        S::get(bv, sb[m], n, w.j);
+                        if (GATE) S::get(cv, sc[m], n, w.j);
 #pragma unroll
-                        for (int r = 0; r < A::R; ++r) {
-                            const int i = first + r, tok = n % ROUND + i / 8;
-                            red[wave][(tok * 2 + i / 4 % 2) * NP + 4 * w.j + i % 4] = v[r];
+                        for (int i = 0; i < 4; ++i) {
+                            es[l][i] = __builtin_amdgcn_exp2f(ds * a2[i]);
+                            hs[l][i] = __builtin_fmaf(es[l][i], l ? hs[l ? l - 1 : 0][i] : h0[i], us * bv[i]);
+                            if (GATE) y[s] = __builtin_fmaf(hs[l][i], cv[i], y[s]);
                         }
                     }
-                }
-                const float du = sum_states4<LPC>(vu, w.q), dd = sum_states4<LPC>(vd, w.q);
-                // tokens past the end have d = dy = 0: they add nothing
-                const float dw = __builtin_fmaf(du, own.x[k], dd * LN2) * own.slope[k];
-                dbias += 4 * k + w.q < cnt ? dw : 0.0f;
-                dskip = __builtin_fmaf(dy[k], own.x[k], dskip);
-                if (w.j < 4) {
-                    R::set(sx, 4 * k + w.q, w.ch, __builtin_fmaf(du, own.d[k], skip * dy[k]));
-                    R::set(sd, 4 * k + w.q, w.ch, dw);
-                }
-                if (4 * k % ROUND == 0) {
-                    __syncthreads();
-                    for (int i = threadIdx.x; i < ROUND * 2 * NP; i += THREADS) {
-                        const int tok = t + 4 * k + i / (2 * NP);
-                        const float sum = (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
-                        if (tok < p.t1) o.part[((int64_t)cb * G.seq.tokens + tok) * (2 * NP) + i % (2 * NP)] = sum;
+                    if (GATE) {
+                        float gs;
+                        const float gv = gate_value<DT>(R::get(sz[m], 4 * k + w.q, w.ch), G.act, gs);
+                        const float yy = __builtin_fmaf(skip, own.x[k], sum_states4<LPC>(y, w.q));
+                        if (w.j < 4) R::set(sz[m], 4 * k + w.q, w.ch, dy[k] * yy * gs);
+                        dy[k] *= gv;
                     }
-                    if (k) __syncthreads();
                 }
-            }
-            R::flush(sx, R::walk(o.dx, o.lddx, w.c0), t, cnt, width);
-            R::flush(sd, R::walk(o.ddt, o.ldddt, w.c0), t, cnt, width);
-            if (GATE && o.dgate) R::flush(sz, R::walk(o.dgate, o.lddgate, w.c0), t, cnt, width);
+                // back over its tokens
+#pragma unroll
+                for (int k = K + 1; k >= K; --k) {
+                    float vu[4] = {0.0f, 0.0f, 0.0f, 0.0f}, vd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 3; s >= 0; --s) {
+                        const int n = 4 * k + s, l = n - 4 * K, to = n % A::TOK * 8;
+                        const float ds = of_token(own.d, n), us = of_token(own.u, n), ys = of_token(dy, n);
+                        float bv[4], cv[4];
+                        S::get(bv, sb[m], n, w.j);
+                        S::get(cv, sc[m], n, w.j);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            g[i] = __builtin_fmaf(cv[i], ys, g[i]);
+                            v[to + i] = g[i] * us;
+                            v[to + 4 + i] = hs[l][i] * ys;
+                            vu[s] = __builtin_fmaf(g[i], bv[i], vu[s]);
+                            g[i] *= es[l][i];
+                            const float gh = g[i] * (l ? hs[l ? l - 1 : 0][i] : h0[i]);
+                            vd[s] = __builtin_fmaf(gh, a2[i], vd[s]);
+                            da[i] = __builtin_fmaf(gh, ds, da[i]);
+                        }
+                        if (n % A::TOK == 0) {
+                            A::sum(v, lane);
+#pragma unroll
+                            for (int r = 0; r < A::R; ++r) {
+                                const int i = first + r, tok = n % ROUND + i / 8;
+                                red[wave][(tok * 2 + i / 4 % 2) * NP + 4 * w.j + i % 4] = v[r];
+                            }
+                        }
+                    }
+                    const float du = sum_states4<LPC>(vu, w.q), dd = sum_states4<LPC>(vd, w.q);
+                    // tokens past the end have d = dy = 0: they add nothing
+                    const float dw = __builtin_fmaf(du, own.x[k], dd * LN2) * own.slope[k];
+                    dbias += 4 * k + w.q < cnt ? dw : 0.0f;
+                    dskip = __builtin_fmaf(dy[k], own.x[k], dskip);
+                    if (w.j < 4) {
+                        R::set(sx[m], 4 * k + w.q, w.ch, __builtin_fmaf(du, own.d[k], skip * dy[k]));
+                        R::set(sd[m], 4 * k + w.q, w.ch, dw);
+                    }
+                    if (4 * k % ROUND == 0) {
+                        __syncthreads();
+                        for (int i = threadIdx.x; i < ROUND * 2 * NP; i += THREADS) {
+                            const int tok = t + 4 * k + i / (2 * NP);
+                            const float sum = (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
+                            if (tok < p.t1) o.part[((int64_t)cb * G.seq.tokens + tok) * (2 * NP) + i % (2 * NP)] = sum;
+                        }
+                        if (k) __syncthreads();  // the next tile's first barrier stands behind the last round
+                    }
+                }
+            };
+            if (cnt > HT) block(std::integral_constant<int, 2>());
+            block(std::integral_constant<int, 0>());
+            R::flush(sx[m], R::walk(o.dx, o.lddx, w.c0), t, cnt, width);
+            R::flush(sd[m], R::walk(o.ddt, o.ldddt, w.c0), t, cnt, width);
+            if (GATE && o.dgate) R::flush(sz[m], R::walk(o.dgate, o.lddgate, w.c0), t, cnt, width);
         }
         if (dstate_in && !afters) store_states(dstate_in + srow, g, 4 * w.j, G.N, w.live);
     }
@@ -798,7 +805,7 @@ Sizes sizes(const ScanGeo &G, int lpc, bool back) {
         z.back = back ? z.ends : 0;
     }
     if (back) {
-        z.kept = ((size_t)G.seq.tokens / TT + G.seq.seqs) * block;
+        z.kept = ((size_t)G.seq.tokens / HT + G.seq.seqs) * block;
         z.part = (size_t)G.nblk * G.seq.tokens * 8 * lpc;
         z.pa = G.walkers * block;
         z.ps = (size_t)G.walkers * G.nblk * 2 * cpw;

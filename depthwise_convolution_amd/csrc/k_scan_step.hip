@@ -4,8 +4,6 @@
 // Bound by HBM for many rows: a state is read and written once, eight bytes against
 // seven operations; by latency for few.  A lane owns four states of a channel, LPC
 // lanes a channel, so that a wavefront's states are one run of memory.
-#include "seq_common.h"
-#include "seq_plan.h"
 #include "scan_common.h"
 
 namespace dw {

@@ -274,7 +274,7 @@ dwconv_status_t dwconv_scan_destroy(dwconv_scan_t h);
 
 /* Bytes of workspace of dwconv_scan_fwd (backward == 0, 0 for many plans) or
  * dwconv_scan_bwd (backward != 0); the workspace is 16-byte aligned.  The backward
- * pass keeps the states of every 16 tokens. */
+ * pass keeps the states of every 8 tokens. */
 dwconv_status_t dwconv_scan_workspace(dwconv_scan_t h, int seqs, int tokens, int backward,
                                       size_t *bytes);
 
