@@ -475,21 +475,24 @@ __global__ void __launch_bounds__(THREADS)
     load_rates(a2, a, G, w.c, 4 * w.j, w.live);
     const int64_t srow = ((int64_t)s * G.C + (w.live ? w.c : 0)) * G.N;
     const int64_t base = slot_base(G, s), runs = ((int64_t)G.seq.end(s) - G.seq.begin(s) + G.CH - 1) / G.CH;
-    auto at = [&](int64_t r) { return ((base + r) * G.nblk + cb) * THREADS + threadIdx.x; };
-    auto wide = [&](int64_t r) { return width[((base + r) * G.nblk + cb) * CPW + w.ch]; };
+    const int64_t row = (int64_t)G.nblk * THREADS * 4;  // floats between two runs
     auto walk = [&](float *p, bool down) {
+        const int64_t first = base + (down && runs ? runs - 1 : 0), by = down ? -1 : 1;
+        float *out = p + (first * G.nblk + cb) * THREADS * 4 + threadIdx.x * 4;
+        const float *in = out, *wd = width + (first * G.nblk + cb) * CPW + w.ch;
         for (int64_t r = 0; r < runs; r += U) {
             float e[U][4], d[U];
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int64_t n = r + i < runs ? r + i : runs - 1, m = down ? runs - 1 - n : n;
-                load_f32<F32, 4>(e[i], p + at(m) * 4);
-                d[i] = wide(m);
+                load_f32<F32, 4>(e[i], in);
+                d[i] = *wd;
+                if (r + i + 1 < runs) in += by * row, wd += by * G.nblk * CPW;
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 if (r + i >= runs) break;
-                store_f32<F32, 4>(p + at(down ? runs - 1 - (r + i) : r + i) * 4, v);
+                store_f32<F32, 4>(out, v);
+                out += by * row;
 #pragma unroll
                 for (int n = 0; n < 4; ++n) v[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[i] * a2[n]), v[n], e[i][n]);
             }
@@ -780,8 +783,15 @@ __global__ void __launch_bounds__(THREADS) k_total(ScanGeo G, Out o, Total z) {
 ScanGeo geometry(const dwconv_scan_plan &p, const int32_t *offsets, int seqs, int tokens, bool back) {
     ScanGeo G = scan_blocks(p, scan_lanes(p.N));
     G.seq = {offsets, seqs, tokens};
-    const int64_t enough = back ? 512 : 768, want = back ? 1024 : 1536;
-    if ((int64_t)seqs * G.nblk < enough && seqs > 0) {
+    // Whole sequences where they give each CU a workgroup, and in the forward pass two
+    // where there are several long ones, whose lengths may differ.  Else runs of as many
+    // tokens as give a CU six (four in the gradients).  N = 16, whole sequences and runs:
+    // 16384 and 32768 channels x 2048 tokens 220 and 312 us, 246 and 479; two sequences of
+    // 150 tokens, 8192 channels 29 and 38; four of 593 to 1266, 1024 channels, N = 64, 160
+    // and 145; gradients of four of 297 to 633 tokens, 4096 channels, 229 and 253.
+    const int64_t blocks = (int64_t)seqs * G.nblk, want = back ? 1024 : 1536;
+    const bool ragged = !back && seqs > 1 && tokens / seqs >= 512;
+    if (seqs > 0 && blocks < (ragged ? 512 : 256)) {
         int ch = 1024;
         while (ch > 64 && ((int64_t)tokens / ch + seqs) * G.nblk < want) ch /= 2;
         if (tokens / seqs > ch) G.CH = ch;
