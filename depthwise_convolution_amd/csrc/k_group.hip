@@ -13,6 +13,9 @@
 //              element read and written once
 //   in passes  runs of pixels give their mean and squares around it, which k_join puts
 //              together; further launches read the image again
+#include <algorithm>
+#include <type_traits>
+
 #include "seq_common.h"
 #include "seq_plan.h"
 
@@ -42,9 +45,23 @@ __device__ __forceinline__ Slice slice_of(const Geo &g, int i) {
     return {a, b - a, a * g.cg, (b - a) * g.cg};
 }
 
-template <class X, int V>
-struct __attribute__((packed, aligned(sizeof(X)))) Any {
-    X v[V];
+// V elements at any element's alignment, as they come: words that are taken apart where
+// they are used (elements would take a register each, and wait for their load).
+template <class DT, int V>
+struct __attribute__((packed, aligned(sizeof(typename DT::X)))) Any {
+    using X = typename DT::X;
+    using W = std::conditional_t<V * sizeof(X) % 4 == 0, uint32_t, X>;
+    static constexpr int N = V * (int)sizeof(X) / (int)sizeof(W);
+    W w[N];
+    __device__ __forceinline__ float operator[](int i) const {
+        if constexpr (sizeof(W) == sizeof(X)) {
+            return DT::widen(__builtin_bit_cast(X, w[i]));
+        } else if constexpr (std::is_same_v<DT, BF16>) {
+            return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        } else {
+            return DT::widen(__builtin_bit_cast(X, (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2])));
+        }
+    }
 };
 
 // A lane's vector of channels.  The last vector of a row ends with the row; what it
@@ -62,14 +79,16 @@ struct Lane {
         if (row >= g.rpp || skip >= V) row = -1, skip = V, c = s.c0;
     }
     __device__ __forceinline__ bool counts(int i) const { return i >= skip; }
-    static __device__ __forceinline__ Any<X, V> load(const X *p) { return *(const Any<X, V> *)p; }
+    static __device__ __forceinline__ Any<DT, V> load(const X *p) { return *(const Any<DT, V> *)p; }
     // `whole`: elements of the vector before may be written too (with the same values)
     __device__ __forceinline__ void store(X *p, const float (&v)[V], bool whole) const {
         if (whole || skip == 0) {
-            Any<X, V> a;
+            struct __attribute__((packed, aligned(sizeof(X)))) {
+                X v[V];
+            } a;
 #pragma unroll
             for (int i = 0; i < V; ++i) a.v[i] = rounded<DT>(v[i]);
-            *(Any<X, V> *)p = a;
+            *(decltype(a) *)p = a;
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -99,7 +118,7 @@ __device__ __forceinline__ float slope_of(float z, int act) {
 template <int TH, int V>
 struct Sums {
     static constexpr int SEGS = 32;
-    float *lanes, *cols, *stat;  // TH x V, max(TH, TH x V), as many as groups
+    float *lanes, *cols, *stat;  // TH x V, at least TH and a row, as many as groups
     int wide, segs;
     __device__ __forceinline__ Sums(float *lanes, float *cols, float *stat, const Geo &g)
         : lanes(lanes), cols(cols), stat(stat), wide(g.vpr * V), segs(min(max(TH / (g.vpr * V), 1), g.rpp)) {}
@@ -168,7 +187,7 @@ __device__ __forceinline__ void params(float &v, const float *p, int c, float ot
 // The run's or image's mean of each group (in stat) and squares around it (in sq).
 template <class DT, int V, int TH, int K, class L>
 __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &ln, const Group<V> &gr,
-                                        const Any<typename DT::X, V> (&x)[K], int n, Sums<TH, V> &sum, float *stat, float *sq,
+                                        const Any<DT, V> (&x)[K], int n, Sums<TH, V> &sum, float *stat, float *sq,
                                         float (&mean)[V]) {
     const float inv = 1.0f / ((float)n * (float)(s.ng > 1 ? g.cg : s.w));
     float v[V];
@@ -178,7 +197,7 @@ __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &l
     for (int k = 0; k < K; ++k)
         if (ln.row + k * g.rpp < n) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) v[i] += DT::widen(x[k].v[i]);
+            for (int i = 0; i < V; ++i) v[i] += x[k][i];
         }
     sum.rows(v, ln, g);
     sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { stat[j] = t * inv; });
@@ -189,7 +208,7 @@ __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &l
         if (ln.row + k * g.rpp < n) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float d = DT::widen(x[k].v[i]) - mean[i];
+                const float d = x[k][i] - mean[i];
                 v[i] = __builtin_fmaf(d, d, v[i]);
             }
         }
@@ -199,7 +218,7 @@ __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &l
 
 // K vectors of a lane, of the pixels row, row + rpp ... of a run of n
 template <class DT, int V, int K, class L>
-__device__ __forceinline__ void take(Any<typename DT::X, V> (&x)[K], const typename DT::X *p, int64_t ld, const Geo &g,
+__device__ __forceinline__ void take(Any<DT, V> (&x)[K], const typename DT::X *p, int64_t ld, const Geo &g,
                                      const L &ln, int n) {
     if (ln.row < 0) return;
 #pragma unroll
@@ -211,9 +230,8 @@ __device__ __forceinline__ void take(Any<typename DT::X, V> (&x)[K], const typen
 template <class DT, int V, int TH, int K, bool RUNS>
 __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int64_t ldx, const float *w, const float *b,
                                             typename DT::X *y, int64_t ldy, float2 *stats, int max_groups) {
-    using X = typename DT::X;
     extern __shared__ __align__(16) float sh[];
-    float *stat = sh + 2 * TH * V, *sq = stat + max_groups;
+    float *stat = sh + TH * V + max(TH, g.vpr * V), *sq = stat + max_groups;
     Sums<TH, V> sum(sh, sh + TH * V, stat, g);
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
@@ -222,7 +240,7 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
     const Group<V> gr(g, s, ln);
     const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
     x += ((int64_t)img * g.S + p0) * ldx;
-    Any<X, V> v[K];
+    Any<DT, V> v[K];
     take<DT, V>(v, x, ldx, g, ln, n);
     float mean[V];
     moments<DT, V, TH, K>(g, s, ln, gr, v, n, sum, stat, sq, mean);
@@ -249,7 +267,7 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
         float o[V];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            o[i] = act_of<DT>(__builtin_fmaf(DT::widen(v[k].v[i]) - mean[i], scale[i], shift[i]), g.act);
+            o[i] = act_of<DT>(__builtin_fmaf(v[k][i] - mean[i], scale[i], shift[i]), g.act);
         ln.store(y + (int64_t)r * ldy, o, true);  // all loads of the slice are behind a barrier
     }
 }
@@ -282,6 +300,7 @@ __global__ void __launch_bounds__(256) k_join(Geo g, const float2 *stats, float2
 template <int V>
 struct Known {
     float mean[V], r[V], w[V], b[V];
+    Known() = default;
     template <class L>
     __device__ __forceinline__ Known(const Geo &g, const Slice &s, const L &ln, const float2 *joined, int img, const float *pw,
                                      const float *pb) {
@@ -300,7 +319,6 @@ struct Known {
 template <class DT, int V, int TH, int U>
 __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, int64_t ldx, const float2 *joined,
                                               const float *w, const float *b, typename DT::X *y, int64_t ldy) {
-    using X = typename DT::X;
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
     const Slice s = slice_of(g, sl);
@@ -315,7 +333,7 @@ __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, in
 #pragma unroll
     for (int i = 0; i < V; ++i) scale[i] = kn.r[i] * kn.w[i];
     for (int r = ln.row; r < n; r += U * g.rpp) {
-        Any<X, V> v[U];
+        Any<DT, V> v[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) v[k] = Lane<DT, V>::load(x + (int64_t)min(r + k * g.rpp, n - 1) * ldx);
 #pragma unroll
@@ -325,7 +343,7 @@ __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, in
             float o[V];
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                o[i] = act_of<DT>(__builtin_fmaf(DT::widen(v[k].v[i]) - kn.mean[i], scale[i], kn.b[i]), g.act);
+                o[i] = act_of<DT>(__builtin_fmaf(v[k][i] - kn.mean[i], scale[i], kn.b[i]), g.act);
             ln.store(y + (int64_t)t * ldy, o, apart);
         }
     }
@@ -333,22 +351,106 @@ __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, in
 
 // A lane's share of the sums dz and dz u of one vector
 template <class DT, int V>
-__device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const Any<typename DT::X, V> &x,
-                                         const Any<typename DT::X, V> &dy, const Known<V> &kn, int act) {
+__device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const Any<DT, V> &x,
+                                         const Any<DT, V> &dy, const Known<V> &kn, int act) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float u = (DT::widen(x.v[i]) - kn.mean[i]) * kn.r[i];
-        const float dz = DT::widen(dy.v[i]) * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
+        const float u = (x[i] - kn.mean[i]) * kn.r[i];
+        const float dz = dy[i] * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
         s1[i] += dz;
         s2[i] = __builtin_fmaf(dz, u, s2[i]);
     }
+}
+
+template <class DT, int V>
+__device__ __forceinline__ void grad_of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
+                                        const Known<V> &kn, const float (&m1)[V], const float (&m2)[V], int act) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float u = (x[i] - kn.mean[i]) * kn.r[i];
+        const float dz = dy[i] * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
+        o[i] = kn.r[i] * (__builtin_fmaf(dz, kn.w[i], -m1[i]) - u * m2[i]);
+    }
+}
+
+// Gradients with x of an image's slice in registers: dy is read twice, the second time
+// from a cache as a rule.  sums: [image][2][C], dz and dz u over the pixels.
+template <class DT, int V, int TH, int K>
+__global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
+                                                 int64_t lddy, const float *w, const float *b, typename DT::X *dx,
+                                                 int64_t lddx, float *sums, int max_groups) {
+    constexpr int U = 4;
+    extern __shared__ __align__(16) float sh[];
+    float *stat = sh + TH * V + max(TH, g.vpr * V), *sq = stat + max_groups;
+    Sums<TH, V> sum(sh, sh + TH * V, stat, g);
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const int sl = (int)(id % g.slices), img = (int)(id / g.slices);
+    const Slice s = slice_of(g, sl);
+    const Lane<DT, V> ln(g, s);
+    const Group<V> gr(g, s, ln);
+    const int n = g.S;
+    x += (int64_t)img * n * ldx;
+    dy += (int64_t)img * n * lddy + ln.c;
+    Any<DT, V> v[K];
+    take<DT, V>(v, x, ldx, g, ln, n);
+    Known<V> kn;
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, sum, stat, sq, kn.mean);
+    const float inv = 1.0f / ((float)n * (float)g.cg);
+    float s1[V], s2[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        kn.r[i] = inverse_root(sq[gr.of[i]] * inv, g.eps);
+        params(kn.w[i], w, ln.c + i, 1.0f);
+        params(kn.b[i], b, ln.c + i, 0.0f);
+        s1[i] = s2[i] = 0.0f;
+    }
+    // the lane's pixels of dy, U on their way while the ones before are used
+    auto over = [&](auto f) {
+        if (ln.row < 0) return;
+        Any<DT, V> d[2][U];
+        auto fetch = [&](Any<DT, V>(&to)[U], int k) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) to[u] = Lane<DT, V>::load(dy + (int64_t)min(ln.row + (k + u) * g.rpp, n - 1) * lddy);
+        };
+        fetch(d[0], 0);
+#pragma unroll
+        for (int k = 0; k < K; k += U) {
+            if (k + U < K) fetch(d[(k / U + 1) & 1], k + U);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (k + u < K && ln.row + (k + u) * g.rpp < n) f(k + u, d[(k / U) & 1][u]);
+        }
+    };
+    over([&](int k, const Any<DT, V> &d) { add_sums<DT, V>(s1, s2, v[k], d, kn, g.act); });
+    float *o = sums + (int64_t)img * 2 * g.C + s.c0;
+    float m1[V], m2[V];
+    __syncthreads();  // stat and sq have been read
+    auto both = [&](float *out, const float (&part)[V], float *mean) {
+        sum.rows(part, ln, g);
+        sum.of_groups(s, g.cg, [&](int i, float c) {
+            out[i] = c;  // each channel once
+            return w ? c * w[s.c0 + i] : c;
+        }, [&](int j, float a) { mean[j] = a * inv; });
+    };
+    both(o, s1, stat);
+    both(o + g.C, s2, sq);
+#pragma unroll
+    for (int i = 0; i < V; ++i) m1[i] = stat[gr.of[i]], m2[i] = sq[gr.of[i]];
+    // every lane's second reading of dy stands behind all first ones, but not behind
+    // other lanes' writes of dx: where that is dy, shared elements are written by one
+    const bool apart = (const void *)dx != (const void *)(dy - ln.c - (int64_t)img * n * lddy);
+    dx += (int64_t)img * n * lddx + ln.c;
+    over([&](int k, const Any<DT, V> &d) {
+        float r[V];
+        grad_of<DT, V>(r, v[k], d, kn, m1, m2, g.act);
+        ln.store(dx + (int64_t)(ln.row + k * g.rpp) * lddx, r, apart);
+    });
 }
 
 // Sums of dz and dz u over a run's pixels, for each channel: part[image][run][2][C].
 template <class DT, int V, int TH, int U>
 __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
                                              int64_t lddy, const float2 *joined, const float *w, const float *b, float *part) {
-    using X = typename DT::X;
     extern __shared__ __align__(16) float sh[];
     Sums<TH, V> sum(sh, sh + TH * V, nullptr, g);
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
@@ -364,7 +466,7 @@ __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int
     for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
     if (ln.row >= 0)
         for (int r = ln.row; r < n; r += U * g.rpp) {
-            Any<X, V> vx[U], vd[U];
+            Any<DT, V> vx[U], vd[U];
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 const int64_t t = min(r + k * g.rpp, n - 1);
@@ -384,7 +486,7 @@ __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int
 }
 
 // Sums of `n` rows of `cols` columns: 64 columns a workgroup, wave w takes every 16th
-// row from w on, the 16 sums are added in order.  Row r of set i is in + (i n + r) cols.
+// row from w on, the 16 sums are added in order.
 __device__ __forceinline__ float column_sum(const float *in, int64_t n, int64_t cols, int64_t col, float (*sh)[64]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -403,22 +505,16 @@ __device__ __forceinline__ float column_sum(const float *in, int64_t n, int64_t 
     for (int k = 0; k < 16; ++k) t += sh[k][lane];
     return t;
 }
-__global__ void __launch_bounds__(1024) k_fold(const float *part, int runs, int64_t cols, uint32_t blocks, float *out) {
-    __shared__ float sh[16][64];
-    const int64_t set = blockIdx.x / blocks, col = (int64_t)(blockIdx.x % blocks) * 64 + (threadIdx.x & 63);
-    const float t = column_sum(part + set * runs * cols, runs, cols, col, sh);
-    if (threadIdx.x < 64 && col < cols) out[set * cols + col] = t;
-}
 
-// From the channels' sums of each image ([image][2][C]: dz, dz u): the first `param`
-// workgroups db and dw over the images, the others the means of dz w and of dz w u of
-// each group, a wavefront a group.
-__global__ void __launch_bounds__(1024) k_means(Geo g, const float *sums, int images, const float *w, float *dw, float *db,
+// From the runs' sums of each channel ([image][run][2][C]: dz, dz u): the first `param`
+// workgroups db and dw over images and runs, the others the means of dz w and of dz w u
+// of each group, a wavefront a group.
+__global__ void __launch_bounds__(1024) k_means(Geo g, const float *sums, int64_t rows, const float *w, float *dw, float *db,
                                                 uint32_t param, float2 *means) {
     __shared__ float sh[16][64];
     if (blockIdx.x < param) {
         const int64_t cols = 2 * (int64_t)g.C, col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-        const float t = column_sum(sums, images, cols, col, sh);
+        const float t = column_sum(sums, rows, cols, col, sh);
         if (threadIdx.x >= 64 || col >= cols) return;
         if (col < g.C) {
             if (db) db[col] = t;
@@ -431,35 +527,25 @@ __global__ void __launch_bounds__(1024) k_means(Geo g, const float *sums, int im
     if (id >= (int64_t)g.images * g.G) return;
     const int64_t img = id / g.G;
     const int c0 = (int)(id % g.G) * g.cg, lane = threadIdx.x & 63;
-    const float *p = sums + img * 2 * g.C + c0;
+    const float *p = sums + img * g.runs * 2 * g.C + c0;
     const float inv = 1.0f / ((float)g.S * (float)g.cg);
     float a = 0.0f, b = 0.0f;
-    for (int i = lane; i < g.cg; i += 64) {
-        const float v = w ? w[c0 + i] : 1.0f;
-        a = __builtin_fmaf(v, p[i], a);
-        b = __builtin_fmaf(v, p[g.C + i], b);
+    const int64_t all = (int64_t)g.runs * g.cg;
+    for (int64_t i = lane; i < all; i += 64) {
+        const int64_t run = i / g.cg, c = i % g.cg;
+        const float v = w ? w[c0 + c] : 1.0f, *q = p + run * 2 * g.C + c;
+        a = __builtin_fmaf(v, q[0], a);
+        b = __builtin_fmaf(v, q[g.C], b);
     }
     a = sum_wave(a);
     b = sum_wave(b);
     if (lane == 0) means[id] = make_float2(a * inv, b * inv);
 }
 
-template <class DT, int V>
-__device__ __forceinline__ void grad_of(float (&o)[V], const Any<typename DT::X, V> &x, const Any<typename DT::X, V> &dy,
-                                        const Known<V> &kn, const float (&m1)[V], const float (&m2)[V], int act) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float u = (DT::widen(x.v[i]) - kn.mean[i]) * kn.r[i];
-        const float dz = DT::widen(dy.v[i]) * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
-        o[i] = kn.r[i] * (__builtin_fmaf(dz, kn.w[i], -m1[i]) - u * m2[i]);
-    }
-}
-
 template <class DT, int V, int TH, int U>
 __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy, int64_t lddy,
                                            const float2 *joined, const float2 *means, const float *w, const float *b,
                                            typename DT::X *dx, int64_t lddx) {
-    using X = typename DT::X;
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
     const Slice s = slice_of(g, sl);
@@ -480,7 +566,7 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
         m2[i] = m.y;
     }
     for (int r = ln.row; r < n; r += U * g.rpp) {
-        Any<X, V> vx[U], vd[U];
+        Any<DT, V> vx[U], vd[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int64_t t = min(r + k * g.rpp, n - 1);
@@ -537,10 +623,35 @@ Geo streams(Geo g) {
     return g;
 }
 
+// Resident: slices of whole groups whose x fits the registers of TH lanes, K vectors each.
+// The width is a multiple of the vector where groups allow it.  false: there are none.
+bool resident(const dwconv_group_plan &p, int images, int pixels, int V, int TH, int K, Geo &g) {
+    g = base(p, images, pixels);
+    if (V == 1 || pixels < 1 || images < 1) return false;
+    int unit = 1;  // groups that make whole vectors
+    while (unit < V && unit * g.cg % V) ++unit;
+    if (unit > p.G || p.G % unit) unit = 1;
+    const int bytes = 16 / V;
+    // at least 64 bytes of a row where they fit, else at least 32
+    for (int least : {64, 32}) {
+        int k = unit;
+        while (k * g.cg * bytes < least && k + unit <= p.G) k += unit;
+        while (k < p.G && p.G % k) k += unit;
+        if (k > p.G) k = p.G;
+        if (k * g.cg < V) return false;
+        g.slices = p.G / k;
+        g.vpr = (k * g.cg + V - 1) / V;
+        if (g.vpr > TH) continue;
+        g.rpp = TH / g.vpr;
+        if (((int64_t)pixels + g.rpp - 1) / g.rpp <= K) return true;
+    }
+    return false;
+}
+
 bool too_many(int64_t blocks) { return blocks >= (1 << 24); }
 
 struct Sizes {
-    size_t stats, joined, part, sums, means, all;  // floats
+    size_t stats, joined, part, means, all;  // floats
 };
 Sizes sizes(const Geo &g, bool back) {
     Sizes z{};
@@ -550,24 +661,48 @@ Sizes sizes(const Geo &g, bool back) {
     z.joined = groups * 2;
     if (back) {
         z.part = (size_t)g.images * f.runs * 2 * g.C;
-        z.sums = (size_t)g.images * 2 * g.C;
         z.means = groups * 2;
     }
-    z.all = z.stats + z.joined + z.part + z.sums + z.means;
+    z.all = z.stats + z.joined + z.part + z.means;
     return z;
+}
+
+// LDS of a workgroup: lanes' values, columns, two values a group
+size_t lds_bytes(const Geo &g, int th, int V, int groups) {
+    return ((size_t)th * V + std::max(th, g.vpr * V) + 2 * (size_t)groups) * sizeof(float);
+}
+
+// groups a slice has at most
+int most_groups(const Geo &g) { return (g.G + g.slices - 1) / g.slices; }
+
+template <class DT, int V, int TH, int K>
+hipError_t fwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
+    using X = typename DT::X;
+    const int64_t blocks = (int64_t)g.images * g.slices;
+    if (too_many(blocks)) return hipErrorInvalidConfiguration;
+    const int mg = most_groups(g);
+    k_fwd<DT, V, TH, K, false><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
+        g, (const X *)a.x, a.ldx, a.w, a.b, (X *)a.y, a.ldy, nullptr, mg);
+    return hipGetLastError();
 }
 
 template <class DT, int V>
 hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
+    if constexpr (V > 1) {
+        Geo g;
+        if (resident(p, a.images, a.pixels, V, 256, 4, g)) return fwd_resident<DT, V, 256, 4>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 256, 16, g)) return fwd_resident<DT, V, 256, 16>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 1024, 16, g)) return fwd_resident<DT, V, 1024, 16>(g, a, st);
+    }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, false);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
     if (too_many(blocks) || too_many((groups + 3) / 4)) return hipErrorInvalidConfiguration;
     if (!blocks) return hipSuccess;
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
-    const int mg = (g.G + g.slices - 1) / g.slices;
-    const size_t lds = (2 * (size_t)PASS_TH * V + 2 * (size_t)mg) * sizeof(float);
+    const int mg = most_groups(g);
+    const size_t lds = lds_bytes(g, PASS_TH, V, mg);
     k_fwd<DT, V, PASS_TH, PASS_K, true><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr, 0,
                                                                                stats, mg);
     k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
@@ -576,33 +711,48 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <class DT, int V, int TH, int K>
+hipError_t bwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
+    using X = typename DT::X;
+    const int64_t blocks = (int64_t)g.images * g.slices;
+    if (too_many(blocks)) return hipErrorInvalidConfiguration;
+    const int mg = most_groups(g);
+    k_resident<DT, V, TH, K><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
+        g, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, a.w, a.b, (X *)a.dx, a.lddx, a.workspace, mg);
+    const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 63) / 64) : 0;
+    if (param) k_means<<<param, 1024, 0, st>>>(g, a.workspace, g.images, a.w, a.dw, a.db, param, nullptr);
+    return hipGetLastError();
+}
+
 template <class DT, int V>
 hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
+    if constexpr (V > 1) {
+        Geo g;
+        if (resident(p, a.images, a.pixels, V, 256, 8, g)) return bwd_resident<DT, V, 256, 8>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 512, 20, g)) return bwd_resident<DT, V, 512, 20>(g, a, st);
+    }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, true);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
-    const int64_t cols = 2 * (int64_t)g.C, folds = (cols + 63) / 64;
-    const uint32_t param = a.dw || a.db ? (uint32_t)folds : 0;
-    if (too_many(blocks) || too_many(groups + param) || (uint64_t)folds * g.images >= (1u << 22))
-        return hipErrorInvalidConfiguration;
+    const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 63) / 64) : 0;
+    if (too_many(blocks) || too_many(groups + 16 * param)) return hipErrorInvalidConfiguration;
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
-    float *part = (float *)joined + z.joined, *sums = part + z.part;
-    float2 *means = (float2 *)(sums + z.sums);
-    const int mg = (g.G + g.slices - 1) / g.slices;
-    const size_t lds = (2 * (size_t)PASS_TH * V + 2 * (size_t)mg) * sizeof(float);
+    float *part = (float *)joined + z.joined;
+    float2 *means = (float2 *)(part + z.part);
+    const int mg = most_groups(g);
+    const size_t lds = lds_bytes(g, PASS_TH, V, mg);
     const uint32_t streaming = (uint32_t)((int64_t)f.images * f.slices * f.runs);
     if (blocks) {
         k_fwd<DT, V, PASS_TH, PASS_K, true><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr,
                                                                                    0, stats, mg);
         k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
-        k_sums<DT, V, PASS_TH, 4><<<streaming, PASS_TH, 2 * PASS_TH * V * sizeof(float), st>>>(
+        k_sums<DT, V, PASS_TH, 4><<<streaming, PASS_TH, lds_bytes(f, PASS_TH, V, 0), st>>>(
             f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, a.w, a.b, part);
-        k_fold<<<(uint32_t)(folds * g.images), 1024, 0, st>>>(part, f.runs, cols, (uint32_t)folds, sums);
     }
     const uint32_t wg = blocks ? (uint32_t)((groups + 15) / 16) : 0;
     if (param + wg)
-        k_means<<<param + wg, 1024, 0, st>>>(g, sums, blocks ? g.images : 0, a.w, a.dw, a.db, param, means);
+        k_means<<<param + wg, 1024, 0, st>>>(f, part, blocks ? (int64_t)f.images * f.runs : 0, a.w, a.dw, a.db, param, means);
     if (blocks)
         k_dx<DT, V, PASS_TH, 4><<<streaming, PASS_TH, 0, st>>>(f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, means,
                                                               a.w, a.b, (X *)a.dx, a.lddx);
@@ -636,8 +786,13 @@ hipError_t pick(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) 
 hipError_t group_fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) { return pick<false>(p, a, st); }
 hipError_t group_bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) { return pick<true>(p, a, st); }
 
+// The gradients always have one: small images too keep their channels' sums.
 size_t group_bytes(const dwconv_group_plan &p, int images, int pixels, bool back) {
-    return sizes(passes(p, images, pixels, vec_of(p)), back).all * sizeof(float);
+    const int V = vec_of(p);
+    Geo g;
+    if (!back && resident(p, images, pixels, V, 1024, 16, g)) return 0;
+    if (back && resident(p, images, pixels, V, 512, 20, g)) return (size_t)images * 2 * p.C * sizeof(float);
+    return sizes(passes(p, images, pixels, V), back).all * sizeof(float);
 }
 
 }  // namespace dw
