@@ -19,6 +19,13 @@
 #include "seq_common.h"
 #include "seq_plan.h"
 
+#ifndef RTH
+#define RTH 512
+#define RK 20
+#endif
+#ifndef RU
+#define RU 4
+#endif
 namespace dw {
 namespace {
 
@@ -69,14 +76,16 @@ struct __attribute__((packed, aligned(sizeof(typename DT::X)))) Any {
 template <class DT, int V>
 struct Lane {
     using X = typename DT::X;
-    int row, c, skip;  // row -1: nothing to do
+    int row, c, skip;
+    bool live;  // lanes without a vector follow the first one of the first row, and count and write nothing
     __device__ __forceinline__ Lane(const Geo &g, const Slice &s) {
         const int col = (int)threadIdx.x % g.vpr;
         row = (int)threadIdx.x / g.vpr;
         const int at = min(col * V, s.w - V);
         c = s.c0 + at;
         skip = col * V - at;
-        if (row >= g.rpp || skip >= V) row = -1, skip = V, c = s.c0;
+        live = row < g.rpp && skip < V;
+        if (!live) row = 0, skip = V, c = s.c0;
     }
     __device__ __forceinline__ bool counts(int i) const { return i >= skip; }
     static __device__ __forceinline__ Any<DT, V> load(const X *p) { return *(const Any<DT, V> *)p; }
@@ -97,19 +106,31 @@ struct Lane {
     }
 };
 
-// act(z), and its slope
-template <class DT>
-__device__ __forceinline__ float act_of(float z, int act) {
-    return act == DWCONV_GROUP_ACT_SILU ? z * sigmoid_f32<DT>(z) : act == DWCONV_GROUP_ACT_RELU ? (z < 0.0f ? 0.0f : z) : z;
-}
-template <class DT>
-__device__ __forceinline__ float slope_of(float z, int act) {
-    if (act == DWCONV_GROUP_ACT_SILU) {
-        float q;
-        const float p = sigmoid_f32<DT>(z, q);
-        return p * __builtin_fmaf(z, q, 1.0f);
+// z becomes act(z)
+template <class DT, int ACT, int V>
+__device__ __forceinline__ void activate(float (&z)[V]) {
+    if (ACT == DWCONV_GROUP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] *= sigmoid_f32<DT>(z[i]);
+    } else if (ACT == DWCONV_GROUP_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];  // NaN stays
     }
-    return act == DWCONV_GROUP_ACT_RELU ? (z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z) : 1.0f;
+}
+// d times the slope of act at z
+template <class DT, int ACT, int V>
+__device__ __forceinline__ void back_through(float (&d)[V], const float (&z)[V]) {
+    if (ACT == DWCONV_GROUP_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float q;
+            const float p = sigmoid_f32<DT>(z[i], q);
+            d[i] *= p * __builtin_fmaf(z[i], q, 1.0f);
+        }
+    } else if (ACT == DWCONV_GROUP_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] *= z[i] > 0.0f ? 1.0f : z[i] <= 0.0f ? 0.0f : z[i];  // NaN stays
+    }
 }
 
 // Sums over a workgroup's lanes.  `cols` becomes the sums over rows of each channel of
@@ -126,7 +147,7 @@ struct Sums {
     __device__ __forceinline__ void rows(const float (&v)[V], const L &ln, const Geo &g) {
         const int width = g.vpr * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i) lanes[(int)threadIdx.x * V + i] = ln.row >= 0 && ln.counts(i) ? v[i] : 0.0f;
+        for (int i = 0; i < V; ++i) lanes[(int)threadIdx.x * V + i] = ln.live && ln.counts(i) ? v[i] : 0.0f;
         __syncthreads();
         for (int k = threadIdx.x; k < width * segs; k += TH) {
             float s = 0.0f;
@@ -184,50 +205,76 @@ struct Group {
 
 __device__ __forceinline__ void params(float &v, const float *p, int c, float other) { v = p ? p[c] : other; }
 
+// A lane's pixels row, row + rpp ... of a run of n: `whole` of them every lane has, the
+// next one the first `rest` rows.  f(k) for each; the test costs no vector instruction
+// but for that one.
+struct Have {
+    int whole;
+    bool more;
+    template <class L>
+    __device__ __forceinline__ Have(const Geo &g, const L &ln, int n) : whole(n / g.rpp), more(ln.row < n % g.rpp) {}
+    __device__ __forceinline__ bool has(int k) const { return k < whole || (k == whole && more); }
+    template <int K, class F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (has(k)) f(k);
+    }
+    // the same for any number of them, U at a time: fetch(u, k), then use(u, k)
+    template <int U, class F, class G>
+    __device__ __forceinline__ void stream(F fetch, G use) const {
+        int k = 0;
+        for (; k + U <= whole; k += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) fetch(u, k + u);
+#pragma unroll
+            for (int u = 0; u < U; ++u) use(u, k + u);
+        }
+        for (; k <= whole; ++k)
+            if (has(k)) {
+                fetch(0, k);
+                use(0, k);
+            }
+    }
+};
+
 // The run's or image's mean of each group (in stat) and squares around it (in sq).
 template <class DT, int V, int TH, int K, class L>
 __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &ln, const Group<V> &gr,
-                                        const Any<DT, V> (&x)[K], int n, Sums<TH, V> &sum, float *stat, float *sq,
+                                        const Any<DT, V> (&x)[K], int n, const Have &have, Sums<TH, V> &sum, float *stat, float *sq,
                                         float (&mean)[V]) {
     const float inv = 1.0f / ((float)n * (float)(s.ng > 1 ? g.cg : s.w));
     float v[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
+    have.each<K>([&](int k) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (ln.row + k * g.rpp < n) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] += x[k][i];
-        }
+        for (int i = 0; i < V; ++i) v[i] += x[k][i];
+    });
     sum.rows(v, ln, g);
     sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { stat[j] = t * inv; });
 #pragma unroll
     for (int i = 0; i < V; ++i) mean[i] = stat[gr.of[i]], v[i] = 0.0f;
+    have.each<K>([&](int k) {
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-        if (ln.row + k * g.rpp < n) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float d = x[k][i] - mean[i];
-                v[i] = __builtin_fmaf(d, d, v[i]);
-            }
+        for (int i = 0; i < V; ++i) {
+            const float d = x[k][i] - mean[i];
+            v[i] = __builtin_fmaf(d, d, v[i]);
         }
+    });
     sum.rows(v, ln, g);
     sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { sq[j] = t; });
 }
 
-// K vectors of a lane, of the pixels row, row + rpp ... of a run of n
-template <class DT, int V, int K, class L>
-__device__ __forceinline__ void take(Any<DT, V> (&x)[K], const typename DT::X *p, int64_t ld, const Geo &g,
-                                     const L &ln, int n) {
-    if (ln.row < 0) return;
-#pragma unroll
-    for (int k = 0; k < K; ++k) x[k] = L::load(p + (int64_t)min(ln.row + k * g.rpp, n - 1) * ld + ln.c);
+// K vectors of a lane
+template <class DT, int V, int K>
+__device__ __forceinline__ void take(Any<DT, V> (&x)[K], const typename DT::X *p, int64_t step, const Have &have) {
+    have.each<K>([&](int k) { x[k] = Lane<DT, V>::load(p + k * step); });
 }
 
 // Forward: resident (RUNS false), or the moments of a run of pixels (RUNS true), left
 // as mean and squares in stats[image][group][run x parts].
-template <class DT, int V, int TH, int K, bool RUNS>
+template <class DT, int V, int TH, int K, bool RUNS, int ACT>
 __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int64_t ldx, const float *w, const float *b,
                                             typename DT::X *y, int64_t ldy, float2 *stats, int max_groups) {
     extern __shared__ __align__(16) float sh[];
@@ -239,11 +286,11 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
     const Lane<DT, V> ln(g, s);
     const Group<V> gr(g, s, ln);
     const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
-    x += ((int64_t)img * g.S + p0) * ldx;
+    const Have have(g, ln, n);
     Any<DT, V> v[K];
-    take<DT, V>(v, x, ldx, g, ln, n);
+    take(v, x + ((int64_t)img * g.S + p0 + ln.row) * ldx + ln.c, g.rpp * ldx, have);
     float mean[V];
-    moments<DT, V, TH, K>(g, s, ln, gr, v, n, sum, stat, sq, mean);
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
     if (RUNS) {
         const int per = g.runs * max(g.parts, 1), at = run * max(g.parts, 1) + (g.parts > 1 ? sl % g.parts : 0);
         for (int j = threadIdx.x; j < s.ng; j += TH)
@@ -258,18 +305,16 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
         params(shift[i], b, ln.c + i, 0.0f);
         scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
     }
-    if (ln.row < 0) return;
-    y += ((int64_t)img * g.S + p0) * ldy + ln.c;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int r = ln.row + k * g.rpp;
-        if (r >= n) break;
+    if (!ln.live) return;
+    y += ((int64_t)img * g.S + p0 + ln.row) * ldy + ln.c;
+    const int64_t step = g.rpp * ldy;
+    have.each<K>([&](int k) {
         float o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            o[i] = act_of<DT>(__builtin_fmaf(v[k][i] - mean[i], scale[i], shift[i]), g.act);
-        ln.store(y + (int64_t)r * ldy, o, true);  // all loads of the slice are behind a barrier
-    }
+        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[k][i] - mean[i], scale[i], shift[i]);
+        activate<DT, ACT>(o);
+        ln.store(y + k * step, o, true);  // all loads of the slice are behind a barrier
+    });
 }
 
 // Puts the moments of a group's runs together: a wavefront a group.  With counts n_i,
@@ -316,70 +361,77 @@ struct Known {
     }
 };
 
-template <class DT, int V, int TH, int U>
+template <class DT, int V, int TH, int U, int ACT>
 __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, int64_t ldx, const float2 *joined,
                                               const float *w, const float *b, typename DT::X *y, int64_t ldy) {
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
     const Slice s = slice_of(g, sl);
     const Lane<DT, V> ln(g, s);
-    if (ln.row < 0) return;
+    if (!ln.live) return;
     const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
-    x += ((int64_t)img * g.S + p0) * ldx + ln.c;
-    y += ((int64_t)img * g.S + p0) * ldy + ln.c;
     const bool apart = (const void *)x != (const void *)y;
+    x += ((int64_t)img * g.S + p0 + ln.row) * ldx + ln.c;
+    y += ((int64_t)img * g.S + p0 + ln.row) * ldy + ln.c;
+    const int64_t sx = g.rpp * ldx, sy = g.rpp * ldy;
     const Known<V> kn(g, s, ln, joined, img, w, b);
     float scale[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) scale[i] = kn.r[i] * kn.w[i];
-    for (int r = ln.row; r < n; r += U * g.rpp) {
-        Any<DT, V> v[U];
+    Any<DT, V> v[U];
+    Have(g, ln, n).stream<U>([&](int u, int k) { v[u] = Lane<DT, V>::load(x + k * sx); },
+                             [&](int u, int k) {
+                                 float o[V];
 #pragma unroll
-        for (int k = 0; k < U; ++k) v[k] = Lane<DT, V>::load(x + (int64_t)min(r + k * g.rpp, n - 1) * ldx);
+                                 for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[u][i] - kn.mean[i], scale[i], kn.b[i]);
+                                 activate<DT, ACT>(o);
+                                 ln.store(y + k * sy, o, apart);
+                             });
+}
+
+// u and dz of one vector
+template <int ACT, class DT, int V>
+__device__ __forceinline__ void unit_and_dz(float (&u)[V], float (&dz)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
+                                            const Known<V> &kn) {
+    float z[V];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int t = r + k * g.rpp;
-            if (t >= n) break;
-            float o[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                o[i] = act_of<DT>(__builtin_fmaf(v[k][i] - kn.mean[i], scale[i], kn.b[i]), g.act);
-            ln.store(y + (int64_t)t * ldy, o, apart);
-        }
+    for (int i = 0; i < V; ++i) {
+        u[i] = (x[i] - kn.mean[i]) * kn.r[i];
+        z[i] = __builtin_fmaf(u[i], kn.w[i], kn.b[i]);
+        dz[i] = dy[i];
     }
+    back_through<DT, ACT>(dz, z);
 }
 
 // A lane's share of the sums dz and dz u of one vector
-template <class DT, int V>
-__device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const Any<DT, V> &x,
-                                         const Any<DT, V> &dy, const Known<V> &kn, int act) {
+template <int ACT, class DT, int V>
+__device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
+                                         const Known<V> &kn) {
+    float u[V], dz[V];
+    unit_and_dz<ACT>(u, dz, x, dy, kn);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const float u = (x[i] - kn.mean[i]) * kn.r[i];
-        const float dz = dy[i] * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
-        s1[i] += dz;
-        s2[i] = __builtin_fmaf(dz, u, s2[i]);
+        s1[i] += dz[i];
+        s2[i] = __builtin_fmaf(dz[i], u[i], s2[i]);
     }
 }
 
-template <class DT, int V>
-__device__ __forceinline__ void grad_of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
-                                        const Known<V> &kn, const float (&m1)[V], const float (&m2)[V], int act) {
+template <int ACT, class DT, int V>
+__device__ __forceinline__ void grad_of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy, const Known<V> &kn,
+                                        const float (&m1)[V], const float (&m2)[V]) {
+    float u[V], dz[V];
+    unit_and_dz<ACT>(u, dz, x, dy, kn);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float u = (x[i] - kn.mean[i]) * kn.r[i];
-        const float dz = dy[i] * slope_of<DT>(__builtin_fmaf(u, kn.w[i], kn.b[i]), act);
-        o[i] = kn.r[i] * (__builtin_fmaf(dz, kn.w[i], -m1[i]) - u * m2[i]);
-    }
+    for (int i = 0; i < V; ++i) o[i] = kn.r[i] * (__builtin_fmaf(dz[i], kn.w[i], -m1[i]) - u[i] * m2[i]);
 }
 
 // Gradients with x of an image's slice in registers: dy is read twice, the second time
 // from a cache as a rule.  sums: [image][2][C], dz and dz u over the pixels.
-template <class DT, int V, int TH, int K>
+template <class DT, int V, int TH, int K, int ACT>
 __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
                                                  int64_t lddy, const float *w, const float *b, typename DT::X *dx,
                                                  int64_t lddx, float *sums, int max_groups) {
-    constexpr int U = 4;
+    constexpr int U = RU;
     extern __shared__ __align__(16) float sh[];
     float *stat = sh + TH * V + max(TH, g.vpr * V), *sq = stat + max_groups;
     Sums<TH, V> sum(sh, sh + TH * V, stat, g);
@@ -389,12 +441,15 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     const Lane<DT, V> ln(g, s);
     const Group<V> gr(g, s, ln);
     const int n = g.S;
-    x += (int64_t)img * n * ldx;
-    dy += (int64_t)img * n * lddy + ln.c;
+    const bool apart = (const void *)dx != (const void *)dy;
+    dy += ((int64_t)img * n + ln.row) * lddy + ln.c;
+    dx += ((int64_t)img * n + ln.row) * lddx + ln.c;
+    const int64_t sy = g.rpp * lddy, sx = g.rpp * lddx;
+    const Have have(g, ln, n);
     Any<DT, V> v[K];
-    take<DT, V>(v, x, ldx, g, ln, n);
+    take(v, x + ((int64_t)img * n + ln.row) * ldx + ln.c, g.rpp * ldx, have);
     Known<V> kn;
-    moments<DT, V, TH, K>(g, s, ln, gr, v, n, sum, stat, sq, kn.mean);
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, kn.mean);
     const float inv = 1.0f / ((float)n * (float)g.cg);
     float s1[V], s2[V];
 #pragma unroll
@@ -406,11 +461,11 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     }
     // the lane's pixels of dy, U on their way while the ones before are used
     auto over = [&](auto f) {
-        if (ln.row < 0) return;
         Any<DT, V> d[2][U];
         auto fetch = [&](Any<DT, V>(&to)[U], int k) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) to[u] = Lane<DT, V>::load(dy + (int64_t)min(ln.row + (k + u) * g.rpp, n - 1) * lddy);
+            for (int u = 0; u < U; ++u)
+                if (have.has(k + u)) to[u] = Lane<DT, V>::load(dy + (k + u) * sy);
         };
         fetch(d[0], 0);
 #pragma unroll
@@ -418,10 +473,10 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
             if (k + U < K) fetch(d[(k / U + 1) & 1], k + U);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (k + u < K && ln.row + (k + u) * g.rpp < n) f(k + u, d[(k / U) & 1][u]);
+                if (k + u < K && have.has(k + u)) f(k + u, d[(k / U) & 1][u]);
         }
     };
-    over([&](int k, const Any<DT, V> &d) { add_sums<DT, V>(s1, s2, v[k], d, kn, g.act); });
+    over([&](int k, const Any<DT, V> &d) { add_sums<ACT>(s1, s2, v[k], d, kn); });
     float *o = sums + (int64_t)img * 2 * g.C + s.c0;
     float m1[V], m2[V];
     __syncthreads();  // stat and sq have been read
@@ -436,19 +491,18 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     both(o + g.C, s2, sq);
 #pragma unroll
     for (int i = 0; i < V; ++i) m1[i] = stat[gr.of[i]], m2[i] = sq[gr.of[i]];
-    // every lane's second reading of dy stands behind all first ones, but not behind
-    // other lanes' writes of dx: where that is dy, shared elements are written by one
-    const bool apart = (const void *)dx != (const void *)(dy - ln.c - (int64_t)img * n * lddy);
-    dx += (int64_t)img * n * lddx + ln.c;
+    // Every lane's second reading of dy stands behind all first ones, but not behind
+    // other lanes' writes of dx: where that is dy, shared elements are written by one.
+    if (!ln.live) return;
     over([&](int k, const Any<DT, V> &d) {
         float r[V];
-        grad_of<DT, V>(r, v[k], d, kn, m1, m2, g.act);
-        ln.store(dx + (int64_t)(ln.row + k * g.rpp) * lddx, r, apart);
+        grad_of<ACT>(r, v[k], d, kn, m1, m2);
+        ln.store(dx + k * sx, r, apart);
     });
 }
 
 // Sums of dz and dz u over a run's pixels, for each channel: part[image][run][2][C].
-template <class DT, int V, int TH, int U>
+template <class DT, int V, int TH, int U, int ACT>
 __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
                                              int64_t lddy, const float2 *joined, const float *w, const float *b, float *part) {
     extern __shared__ __align__(16) float sh[];
@@ -458,25 +512,16 @@ __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int
     const Slice s = slice_of(g, sl);
     const Lane<DT, V> ln(g, s);
     const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
-    x += ((int64_t)img * g.S + p0) * ldx + ln.c;
-    dy += ((int64_t)img * g.S + p0) * lddy + ln.c;
+    x += ((int64_t)img * g.S + p0 + ln.row) * ldx + ln.c;
+    dy += ((int64_t)img * g.S + p0 + ln.row) * lddy + ln.c;
+    const int64_t sx = g.rpp * ldx, sy = g.rpp * lddy;
     const Known<V> kn(g, s, ln, joined, img, w, b);
     float s1[V], s2[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
-    if (ln.row >= 0)
-        for (int r = ln.row; r < n; r += U * g.rpp) {
-            Any<DT, V> vx[U], vd[U];
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int64_t t = min(r + k * g.rpp, n - 1);
-                vx[k] = Lane<DT, V>::load(x + t * ldx);
-                vd[k] = Lane<DT, V>::load(dy + t * lddy);
-            }
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-                if (r + k * g.rpp < n) add_sums<DT, V>(s1, s2, vx[k], vd[k], kn, g.act);
-        }
+    Any<DT, V> vx[U], vd[U];
+    Have(g, ln, n).stream<U>([&](int u, int k) { vx[u] = Lane<DT, V>::load(x + k * sx), vd[u] = Lane<DT, V>::load(dy + k * sy); },
+                             [&](int u, int) { add_sums<ACT>(s1, s2, vx[u], vd[u], kn); });
     float *o = part + ((int64_t)img * g.runs + run) * 2 * g.C + s.c0;
     sum.rows(s1, ln, g);
     for (int i = threadIdx.x; i < s.w; i += TH) o[i] = sum.channel(s, i);
@@ -542,7 +587,7 @@ __global__ void __launch_bounds__(1024) k_means(Geo g, const float *sums, int64_
     if (lane == 0) means[id] = make_float2(a * inv, b * inv);
 }
 
-template <class DT, int V, int TH, int U>
+template <class DT, int V, int TH, int U, int ACT>
 __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy, int64_t lddy,
                                            const float2 *joined, const float2 *means, const float *w, const float *b,
                                            typename DT::X *dx, int64_t lddx) {
@@ -550,12 +595,13 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
     const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
     const Slice s = slice_of(g, sl);
     const Lane<DT, V> ln(g, s);
-    if (ln.row < 0) return;
+    if (!ln.live) return;
     const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
-    x += ((int64_t)img * g.S + p0) * ldx + ln.c;
-    dy += ((int64_t)img * g.S + p0) * lddy + ln.c;
-    dx += ((int64_t)img * g.S + p0) * lddx + ln.c;
     const bool apart = (const void *)dx != (const void *)dy;
+    x += ((int64_t)img * g.S + p0 + ln.row) * ldx + ln.c;
+    dy += ((int64_t)img * g.S + p0 + ln.row) * lddy + ln.c;
+    dx += ((int64_t)img * g.S + p0 + ln.row) * lddx + ln.c;
+    const int64_t sx = g.rpp * ldx, sy = g.rpp * lddy, so = g.rpp * lddx;
     const Known<V> kn(g, s, ln, joined, img, w, b);
     const Group<V> gr(g, s, ln);
     float m1[V], m2[V];
@@ -565,23 +611,13 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
         m1[i] = m.x;
         m2[i] = m.y;
     }
-    for (int r = ln.row; r < n; r += U * g.rpp) {
-        Any<DT, V> vx[U], vd[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int64_t t = min(r + k * g.rpp, n - 1);
-            vx[k] = Lane<DT, V>::load(x + t * ldx);
-            vd[k] = Lane<DT, V>::load(dy + t * lddy);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int t = r + k * g.rpp;
-            if (t >= n) break;
-            float o[V];
-            grad_of<DT, V>(o, vx[k], vd[k], kn, m1, m2, g.act);
-            ln.store(dx + (int64_t)t * lddx, o, apart);
-        }
-    }
+    Any<DT, V> vx[U], vd[U];
+    Have(g, ln, n).stream<U>([&](int u, int k) { vx[u] = Lane<DT, V>::load(x + k * sx), vd[u] = Lane<DT, V>::load(dy + k * sy); },
+                             [&](int u, int k) {
+                                 float o[V];
+                                 grad_of<ACT>(o, vx[u], vd[u], kn, m1, m2);
+                                 ln.store(dx + k * so, o, apart);
+                             });
 }
 
 // ---------------------------------------------------------------------------
@@ -675,25 +711,25 @@ size_t lds_bytes(const Geo &g, int th, int V, int groups) {
 // groups a slice has at most
 int most_groups(const Geo &g) { return (g.G + g.slices - 1) / g.slices; }
 
-template <class DT, int V, int TH, int K>
+template <class DT, int V, int TH, int K, int ACT>
 hipError_t fwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     const int64_t blocks = (int64_t)g.images * g.slices;
     if (too_many(blocks)) return hipErrorInvalidConfiguration;
     const int mg = most_groups(g);
-    k_fwd<DT, V, TH, K, false><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
+    k_fwd<DT, V, TH, K, false, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, a.w, a.b, (X *)a.y, a.ldy, nullptr, mg);
     return hipGetLastError();
 }
 
-template <class DT, int V>
+template <class DT, int V, int ACT>
 hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     if constexpr (V > 1) {
         Geo g;
-        if (resident(p, a.images, a.pixels, V, 256, 4, g)) return fwd_resident<DT, V, 256, 4>(g, a, st);
-        if (resident(p, a.images, a.pixels, V, 256, 16, g)) return fwd_resident<DT, V, 256, 16>(g, a, st);
-        if (resident(p, a.images, a.pixels, V, 1024, 16, g)) return fwd_resident<DT, V, 1024, 16>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 256, 4, g)) return fwd_resident<DT, V, 256, 4, ACT>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 256, 16, g)) return fwd_resident<DT, V, 256, 16, ACT>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 1024, 16, g)) return fwd_resident<DT, V, 1024, 16, ACT>(g, a, st);
     }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, false);
@@ -703,34 +739,34 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
     const int mg = most_groups(g);
     const size_t lds = lds_bytes(g, PASS_TH, V, mg);
-    k_fwd<DT, V, PASS_TH, PASS_K, true><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr, 0,
+    k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr, 0,
                                                                                stats, mg);
     k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
-    k_apply<DT, V, PASS_TH, 4><<<(uint32_t)((int64_t)f.images * f.slices * f.runs), PASS_TH, 0, st>>>(
+    k_apply<DT, V, PASS_TH, 4, ACT><<<(uint32_t)((int64_t)f.images * f.slices * f.runs), PASS_TH, 0, st>>>(
         f, (const X *)a.x, a.ldx, joined, a.w, a.b, (X *)a.y, a.ldy);
     return hipGetLastError();
 }
 
-template <class DT, int V, int TH, int K>
+template <class DT, int V, int TH, int K, int ACT>
 hipError_t bwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     const int64_t blocks = (int64_t)g.images * g.slices;
     if (too_many(blocks)) return hipErrorInvalidConfiguration;
     const int mg = most_groups(g);
-    k_resident<DT, V, TH, K><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
+    k_resident<DT, V, TH, K, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, a.w, a.b, (X *)a.dx, a.lddx, a.workspace, mg);
     const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 63) / 64) : 0;
     if (param) k_means<<<param, 1024, 0, st>>>(g, a.workspace, g.images, a.w, a.dw, a.db, param, nullptr);
     return hipGetLastError();
 }
 
-template <class DT, int V>
+template <class DT, int V, int ACT>
 hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     if constexpr (V > 1) {
         Geo g;
-        if (resident(p, a.images, a.pixels, V, 256, 8, g)) return bwd_resident<DT, V, 256, 8>(g, a, st);
-        if (resident(p, a.images, a.pixels, V, 512, 20, g)) return bwd_resident<DT, V, 512, 20>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 256, 8, g)) return bwd_resident<DT, V, 256, 8, ACT>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, RTH, RK, g)) return bwd_resident<DT, V, RTH, RK, ACT>(g, a, st);
     }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, true);
@@ -744,17 +780,17 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     const size_t lds = lds_bytes(g, PASS_TH, V, mg);
     const uint32_t streaming = (uint32_t)((int64_t)f.images * f.slices * f.runs);
     if (blocks) {
-        k_fwd<DT, V, PASS_TH, PASS_K, true><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr,
+        k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr,
                                                                                    0, stats, mg);
         k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
-        k_sums<DT, V, PASS_TH, 4><<<streaming, PASS_TH, lds_bytes(f, PASS_TH, V, 0), st>>>(
+        k_sums<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, lds_bytes(f, PASS_TH, V, 0), st>>>(
             f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, a.w, a.b, part);
     }
     const uint32_t wg = blocks ? (uint32_t)((groups + 15) / 16) : 0;
     if (param + wg)
         k_means<<<param + wg, 1024, 0, st>>>(f, part, blocks ? (int64_t)f.images * f.runs : 0, a.w, a.dw, a.db, param, means);
     if (blocks)
-        k_dx<DT, V, PASS_TH, 4><<<streaming, PASS_TH, 0, st>>>(f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, means,
+        k_dx<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, 0, st>>>(f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, means,
                                                               a.w, a.b, (X *)a.dx, a.lddx);
     return hipGetLastError();
 }
@@ -765,11 +801,23 @@ int vec_of(const dwconv_group_plan &p) {
     return p.C >= v ? v : 1;
 }
 
+template <bool BACK, class DT, int V>
+hipError_t pick_act(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
+    auto go = [&](auto act) {
+        if constexpr (BACK) return bwd<DT, V, decltype(act)::value>(p, a, st);
+        else return fwd<DT, V, decltype(act)::value>(p, a, st);
+    };
+    switch (p.act) {
+        case DWCONV_GROUP_ACT_SILU: return go(std::integral_constant<int, DWCONV_GROUP_ACT_SILU>());
+        case DWCONV_GROUP_ACT_RELU: return go(std::integral_constant<int, DWCONV_GROUP_ACT_RELU>());
+        default: return go(std::integral_constant<int, DWCONV_GROUP_ACT_NONE>());
+    }
+}
+
 template <bool BACK, class DT>
 hipError_t pick_vec(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     constexpr int V = 16 / (int)sizeof(typename DT::X);
-    if constexpr (BACK) return vec_of(p) == V ? bwd<DT, V>(p, a, st) : bwd<DT, 1>(p, a, st);
-    else return vec_of(p) == V ? fwd<DT, V>(p, a, st) : fwd<DT, 1>(p, a, st);
+    return vec_of(p) == V ? pick_act<BACK, DT, V>(p, a, st) : pick_act<BACK, DT, 1>(p, a, st);
 }
 
 template <bool BACK>
@@ -791,7 +839,7 @@ size_t group_bytes(const dwconv_group_plan &p, int images, int pixels, bool back
     const int V = vec_of(p);
     Geo g;
     if (!back && resident(p, images, pixels, V, 1024, 16, g)) return 0;
-    if (back && resident(p, images, pixels, V, 512, 20, g)) return (size_t)images * 2 * p.C * sizeof(float);
+    if (back && resident(p, images, pixels, V, RTH, RK, g)) return (size_t)images * 2 * p.C * sizeof(float);
     return sizes(passes(p, images, pixels, V), back).all * sizeof(float);
 }
 
