@@ -22,9 +22,7 @@
 #ifndef RTH
 #define RTH 512
 #define RK 20
-#endif
-#ifndef RU
-#define RU 4
+#define RK1 8
 #endif
 namespace dw {
 namespace {
@@ -317,27 +315,45 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
     });
 }
 
-// Puts the moments of a group's runs together: a wavefront a group.  With counts n_i,
+// Two sums over the W wavefronts that share a group, in all of their lanes.
+template <int W>
+__device__ __forceinline__ void sum_group(float &a, float &b, float *sh) {
+    a = sum_wave(a);
+    b = sum_wave(b);
+    if (W == 1) return;
+    const int wave = (int)threadIdx.x >> 6;
+    __syncthreads();
+    if (((int)threadIdx.x & 63) == 0) sh[wave] = a, sh[16 + wave] = b;
+    __syncthreads();
+    a = b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) a += sh[i], b += sh[16 + i];
+}
+
+// Puts the moments of a group's runs together: W wavefronts a group.  With counts n_i,
 // means m_i and squares q_i: m = sum n_i m_i / n and q = sum (q_i + n_i (m_i - m)^2).
 // out: mean and r.
-__global__ void __launch_bounds__(256) k_join(Geo g, const float2 *stats, float2 *out) {
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+template <int W>
+__global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const float2 *stats, float2 *out) {
+    constexpr int TH = W > 4 ? W * 64 : 256;
+    __shared__ float sh[32];
+    const int64_t id = (int64_t)blockIdx.x * (TH / 64 / W) + (W == 1 ? threadIdx.x >> 6 : 0);
     if (id >= (int64_t)g.images * g.G) return;
-    const int lane = threadIdx.x & 63, parts = max(g.parts, 1), per = g.runs * parts;
+    const int lane = (int)threadIdx.x % (64 * W), parts = max(g.parts, 1), per = g.runs * parts;
     const float2 *p = stats + id * per;
     auto count = [&](int i) {
         const int run = i / parts, part = i % parts;
         return (float)min(g.rows, g.S - run * g.rows) * (float)(parts > 1 ? min(g.part, g.cg - part * g.part) : g.cg);
     };
     const float inv = 1.0f / ((float)g.S * (float)g.cg);
-    float m = 0.0f, q = 0.0f;
-    for (int i = lane; i < per; i += 64) m = __builtin_fmaf(count(i) * inv, p[i].x, m);
-    m = sum_wave(m);
-    for (int i = lane; i < per; i += 64) {
+    float m = 0.0f, q = 0.0f, none = 0.0f;
+    for (int i = lane; i < per; i += 64 * W) m = __builtin_fmaf(count(i) * inv, p[i].x, m);
+    sum_group<W>(m, none, sh);
+    for (int i = lane; i < per; i += 64 * W) {
         const float d = p[i].x - m;
         q += __builtin_fmaf(count(i) * d, d, p[i].y);
     }
-    q = sum_wave(q);
+    sum_group<W>(q, none, sh);
     if (lane == 0) out[id] = make_float2(m, inverse_root(q * inv, g.eps));
 }
 
@@ -425,13 +441,12 @@ __device__ __forceinline__ void grad_of(float (&o)[V], const Any<DT, V> &x, cons
     for (int i = 0; i < V; ++i) o[i] = kn.r[i] * (__builtin_fmaf(dz[i], kn.w[i], -m1[i]) - u[i] * m2[i]);
 }
 
-// Gradients with x of an image's slice in registers: dy is read twice, the second time
-// from a cache as a rule.  sums: [image][2][C], dz and dz u over the pixels.
+// Gradients with x and dy of an image's slice in registers.  sums: [image][2][C], dz and
+// dz u over the pixels.
 template <class DT, int V, int TH, int K, int ACT>
 __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
                                                  int64_t lddy, const float *w, const float *b, typename DT::X *dx,
                                                  int64_t lddx, float *sums, int max_groups) {
-    constexpr int U = RU;
     extern __shared__ __align__(16) float sh[];
     float *stat = sh + TH * V + max(TH, g.vpr * V), *sq = stat + max_groups;
     Sums<TH, V> sum(sh, sh + TH * V, stat, g);
@@ -441,13 +456,12 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     const Lane<DT, V> ln(g, s);
     const Group<V> gr(g, s, ln);
     const int n = g.S;
-    const bool apart = (const void *)dx != (const void *)dy;
-    dy += ((int64_t)img * n + ln.row) * lddy + ln.c;
     dx += ((int64_t)img * n + ln.row) * lddx + ln.c;
-    const int64_t sy = g.rpp * lddy, sx = g.rpp * lddx;
+    const int64_t sx = g.rpp * lddx;
     const Have have(g, ln, n);
-    Any<DT, V> v[K];
+    Any<DT, V> v[K], d[K];  // dy is on its way while the moments of x are formed
     take(v, x + ((int64_t)img * n + ln.row) * ldx + ln.c, g.rpp * ldx, have);
+    take(d, dy + ((int64_t)img * n + ln.row) * lddy + ln.c, g.rpp * lddy, have);
     Known<V> kn;
     moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, kn.mean);
     const float inv = 1.0f / ((float)n * (float)g.cg);
@@ -459,24 +473,7 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
         params(kn.b[i], b, ln.c + i, 0.0f);
         s1[i] = s2[i] = 0.0f;
     }
-    // the lane's pixels of dy, U on their way while the ones before are used
-    auto over = [&](auto f) {
-        Any<DT, V> d[2][U];
-        auto fetch = [&](Any<DT, V>(&to)[U], int k) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (have.has(k + u)) to[u] = Lane<DT, V>::load(dy + (k + u) * sy);
-        };
-        fetch(d[0], 0);
-#pragma unroll
-        for (int k = 0; k < K; k += U) {
-            if (k + U < K) fetch(d[(k / U + 1) & 1], k + U);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (k + u < K && have.has(k + u)) f(k + u, d[(k / U) & 1][u]);
-        }
-    };
-    over([&](int k, const Any<DT, V> &d) { add_sums<ACT>(s1, s2, v[k], d, kn); });
+    have.each<K>([&](int k) { add_sums<ACT>(s1, s2, v[k], d[k], kn); });
     float *o = sums + (int64_t)img * 2 * g.C + s.c0;
     float m1[V], m2[V];
     __syncthreads();  // stat and sq have been read
@@ -491,13 +488,11 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     both(o + g.C, s2, sq);
 #pragma unroll
     for (int i = 0; i < V; ++i) m1[i] = stat[gr.of[i]], m2[i] = sq[gr.of[i]];
-    // Every lane's second reading of dy stands behind all first ones, but not behind
-    // other lanes' writes of dx: where that is dy, shared elements are written by one.
-    if (!ln.live) return;
-    over([&](int k, const Any<DT, V> &d) {
+    if (!ln.live) return;  // all loads of the slice are behind a barrier
+    have.each<K>([&](int k) {
         float r[V];
-        grad_of<ACT>(r, v[k], d, kn, m1, m2);
-        ln.store(dx + k * sx, r, apart);
+        grad_of<ACT>(r, v[k], d[k], kn, m1, m2);
+        ln.store(dx + k * sx, r, true);
     });
 }
 
@@ -530,37 +525,31 @@ __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int
     for (int i = threadIdx.x; i < s.w; i += TH) o[g.C + i] = sum.channel(s, i);
 }
 
-// Sums of `n` rows of `cols` columns: 64 columns a workgroup, wave w takes every 16th
-// row from w on, the 16 sums are added in order.
-__device__ __forceinline__ float column_sum(const float *in, int64_t n, int64_t cols, int64_t col, float (*sh)[64]) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (col < cols) {
-        int64_t r = wave;
-        for (; r + 48 < n; r += 64) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) s[k] += in[(r + 16 * k) * cols + col];
-        }
-        for (; r < n; r += 16) s[0] += in[r * cols + col];
-    }
-    sh[wave][lane] = (s[0] + s[1]) + (s[2] + s[3]);
-    __syncthreads();
-    float t = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) t += sh[k][lane];
-    return t;
-}
-
 // From the runs' sums of each channel ([image][run][2][C]: dz, dz u): the first `param`
-// workgroups db and dw over images and runs, the others the means of dz w and of dz w u
-// of each group, a wavefront a group.
+// workgroups db and dw over images and runs, 16 columns each, of which every 64th row is
+// one lane's and the 64 sums are added in order; the others the means of dz w and of
+// dz w u of each group, W wavefronts a group.
+template <int W>
 __global__ void __launch_bounds__(1024) k_means(Geo g, const float *sums, int64_t rows, const float *w, float *dw, float *db,
                                                 uint32_t param, float2 *means) {
-    __shared__ float sh[16][64];
+    __shared__ float sh[64][17];
     if (blockIdx.x < param) {
-        const int64_t cols = 2 * (int64_t)g.C, col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
-        const float t = column_sum(sums, rows, cols, col, sh);
-        if (threadIdx.x >= 64 || col >= cols) return;
+        const int c = (int)threadIdx.x & 15, first = (int)threadIdx.x >> 4;
+        const int64_t cols = 2 * (int64_t)g.C, col = (int64_t)blockIdx.x * 16 + c;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (col < cols) {
+            int64_t r = first;
+            for (; r + 192 < rows; r += 256) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[k] += sums[(r + 64 * k) * cols + col];
+            }
+            for (; r < rows; r += 64) s[0] += sums[r * cols + col];
+        }
+        sh[first][c] = (s[0] + s[1]) + (s[2] + s[3]);
+        __syncthreads();
+        if (threadIdx.x >= 16 || col >= cols) return;
+        float t = 0.0f;
+        for (int k = 0; k < 64; ++k) t += sh[k][c];
         if (col < g.C) {
             if (db) db[col] = t;
         } else if (dw) {
@@ -568,22 +557,21 @@ __global__ void __launch_bounds__(1024) k_means(Geo g, const float *sums, int64_
         }
         return;
     }
-    const int64_t id = (int64_t)(blockIdx.x - param) * 16 + (threadIdx.x >> 6);
+    const int64_t id = (int64_t)(blockIdx.x - param) * (16 / W) + (W == 1 ? threadIdx.x >> 6 : 0);
     if (id >= (int64_t)g.images * g.G) return;
     const int64_t img = id / g.G;
-    const int c0 = (int)(id % g.G) * g.cg, lane = threadIdx.x & 63;
+    const int c0 = (int)(id % g.G) * g.cg, lane = (int)threadIdx.x % (64 * W);
     const float *p = sums + img * g.runs * 2 * g.C + c0;
     const float inv = 1.0f / ((float)g.S * (float)g.cg);
     float a = 0.0f, b = 0.0f;
     const int64_t all = (int64_t)g.runs * g.cg;
-    for (int64_t i = lane; i < all; i += 64) {
+    for (int64_t i = lane; i < all; i += 64 * W) {
         const int64_t run = i / g.cg, c = i % g.cg;
         const float v = w ? w[c0 + c] : 1.0f, *q = p + run * 2 * g.C + c;
         a = __builtin_fmaf(v, q[0], a);
         b = __builtin_fmaf(v, q[g.C], b);
     }
-    a = sum_wave(a);
-    b = sum_wave(b);
+    sum_group<W>(a, b, &sh[0][0]);
     if (lane == 0) means[id] = make_float2(a * inv, b * inv);
 }
 
@@ -623,7 +611,10 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-constexpr int PASS_TH = 256, PASS_K = 8;
+#ifndef PK
+#define PK 8
+#endif
+constexpr int PASS_TH = 256, PASS_K = PK;
 
 Geo base(const dwconv_group_plan &p, int images, int pixels) {
     return {images, pixels, p.C, p.G, p.C / p.G, 1, 1, 0, 1, 1, 1, pixels, p.act, p.eps};
@@ -711,6 +702,15 @@ size_t lds_bytes(const Geo &g, int th, int V, int groups) {
 // groups a slice has at most
 int most_groups(const Geo &g) { return (g.G + g.slices - 1) / g.slices; }
 
+// as many values a group as are worth a workgroup
+bool many(int64_t values) { return values > 512; }
+
+void join(const Geo &g, const float2 *stats, float2 *joined, hipStream_t st) {
+    const int64_t groups = (int64_t)g.images * g.G;
+    if (many((int64_t)g.runs * g.parts)) k_join<16><<<(uint32_t)groups, 1024, 0, st>>>(g, stats, joined);
+    else k_join<1><<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
+}
+
 template <class DT, int V, int TH, int K, int ACT>
 hipError_t fwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
@@ -734,14 +734,14 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, false);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
-    if (too_many(blocks) || too_many((groups + 3) / 4)) return hipErrorInvalidConfiguration;
+    if (too_many(blocks) || groups >= 1 << 22) return hipErrorInvalidConfiguration;
     if (!blocks) return hipSuccess;
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
     const int mg = most_groups(g);
     const size_t lds = lds_bytes(g, PASS_TH, V, mg);
     k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr, 0,
                                                                                stats, mg);
-    k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
+    join(g, stats, joined, st);
     k_apply<DT, V, PASS_TH, 4, ACT><<<(uint32_t)((int64_t)f.images * f.slices * f.runs), PASS_TH, 0, st>>>(
         f, (const X *)a.x, a.ldx, joined, a.w, a.b, (X *)a.y, a.ldy);
     return hipGetLastError();
@@ -755,8 +755,8 @@ hipError_t bwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     const int mg = most_groups(g);
     k_resident<DT, V, TH, K, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, a.w, a.b, (X *)a.dx, a.lddx, a.workspace, mg);
-    const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 63) / 64) : 0;
-    if (param) k_means<<<param, 1024, 0, st>>>(g, a.workspace, g.images, a.w, a.dw, a.db, param, nullptr);
+    const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 15) / 16) : 0;
+    if (param) k_means<1><<<param, 1024, 0, st>>>(g, a.workspace, g.images, a.w, a.dw, a.db, param, nullptr);
     return hipGetLastError();
 }
 
@@ -765,14 +765,14 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     if constexpr (V > 1) {
         Geo g;
-        if (resident(p, a.images, a.pixels, V, 256, 8, g)) return bwd_resident<DT, V, 256, 8, ACT>(g, a, st);
+        if (resident(p, a.images, a.pixels, V, 256, RK1, g)) return bwd_resident<DT, V, 256, RK1, ACT>(g, a, st);
         if (resident(p, a.images, a.pixels, V, RTH, RK, g)) return bwd_resident<DT, V, RTH, RK, ACT>(g, a, st);
     }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, true);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
-    const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 63) / 64) : 0;
-    if (too_many(blocks) || too_many(groups + 16 * param)) return hipErrorInvalidConfiguration;
+    const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 15) / 16) : 0;
+    if (too_many(blocks) || groups + param >= 1 << 22) return hipErrorInvalidConfiguration;
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
     float *part = (float *)joined + z.joined;
     float2 *means = (float2 *)(part + z.part);
@@ -782,13 +782,15 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     if (blocks) {
         k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr,
                                                                                    0, stats, mg);
-        k_join<<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
+        join(g, stats, joined, st);
         k_sums<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, lds_bytes(f, PASS_TH, V, 0), st>>>(
             f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, a.w, a.b, part);
     }
-    const uint32_t wg = blocks ? (uint32_t)((groups + 15) / 16) : 0;
+    const bool wide = many((int64_t)f.runs * f.cg);
+    const uint32_t wg = !blocks ? 0 : (uint32_t)(wide ? groups : (groups + 15) / 16);
     if (param + wg)
-        k_means<<<param + wg, 1024, 0, st>>>(f, part, blocks ? (int64_t)f.images * f.runs : 0, a.w, a.dw, a.db, param, means);
+        (wide ? k_means<16> : k_means<1>)<<<param + wg, 1024, 0, st>>>(f, part, blocks ? (int64_t)f.images * f.runs : 0, a.w,
+                                                                      a.dw, a.db, param, means);
     if (blocks)
         k_dx<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, 0, st>>>(f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, means,
                                                               a.w, a.b, (X *)a.dx, a.lddx);
