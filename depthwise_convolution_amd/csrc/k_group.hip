@@ -19,11 +19,6 @@
 #include "seq_common.h"
 #include "seq_plan.h"
 
-#ifndef RTH
-#define RTH 512
-#define RK 20
-#define RK1 8
-#endif
 namespace dw {
 namespace {
 
@@ -287,7 +282,14 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
     const Have have(g, ln, n);
     Any<DT, V> v[K];
     take(v, x + ((int64_t)img * g.S + p0 + ln.row) * ldx + ln.c, g.rpp * ldx, have);
-    float mean[V];
+    float mean[V], scale[V], shift[V];
+    if (!RUNS) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            params(scale[i], w, ln.c + i, 1.0f);
+            params(shift[i], b, ln.c + i, 0.0f);
+        }
+    }
     moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
     if (RUNS) {
         const int per = g.runs * max(g.parts, 1), at = run * max(g.parts, 1) + (g.parts > 1 ? sl % g.parts : 0);
@@ -296,13 +298,8 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
         return;
     }
     const float inv = 1.0f / ((float)n * (float)g.cg);
-    float scale[V], shift[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        params(scale[i], w, ln.c + i, 1.0f);
-        params(shift[i], b, ln.c + i, 0.0f);
-        scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
-    }
+    for (int i = 0; i < V; ++i) scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
     if (!ln.live) return;
     y += ((int64_t)img * g.S + p0 + ln.row) * ldy + ln.c;
     const int64_t step = g.rpp * ldy;
@@ -611,10 +608,7 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-#ifndef PK
-#define PK 8
-#endif
-constexpr int PASS_TH = 256, PASS_K = PK;
+constexpr int PASS_TH = 256, PASS_K = 16;
 
 Geo base(const dwconv_group_plan &p, int images, int pixels) {
     return {images, pixels, p.C, p.G, p.C / p.G, 1, 1, 0, 1, 1, 1, pixels, p.act, p.eps};
@@ -650,29 +644,25 @@ Geo streams(Geo g) {
     return g;
 }
 
-// Resident: slices of whole groups whose x fits the registers of TH lanes, K vectors each.
-// The width is a multiple of the vector where groups allow it.  false: there are none.
-bool resident(const dwconv_group_plan &p, int images, int pixels, int V, int TH, int K, Geo &g) {
+// Resident: slices of whole groups, `least` bytes of a row or more, that TH lanes hold in K
+// vectors each.  The width is a multiple of the vector where groups allow it.  false: none.
+bool resident(const dwconv_group_plan &p, int images, int pixels, int V, int TH, int K, int least, Geo &g) {
     g = base(p, images, pixels);
     if (V == 1 || pixels < 1 || images < 1) return false;
     int unit = 1;  // groups that make whole vectors
     while (unit < V && unit * g.cg % V) ++unit;
     if (unit > p.G || p.G % unit) unit = 1;
-    const int bytes = 16 / V;
-    // at least 64 bytes of a row where they fit, else at least 32
-    for (int least : {64, 32}) {
-        int k = unit;
-        while (k * g.cg * bytes < least && k + unit <= p.G) k += unit;
-        while (k < p.G && p.G % k) k += unit;
-        if (k > p.G) k = p.G;
-        if (k * g.cg < V) return false;
-        g.slices = p.G / k;
-        g.vpr = (k * g.cg + V - 1) / V;
-        if (g.vpr > TH) continue;
-        g.rpp = TH / g.vpr;
-        if (((int64_t)pixels + g.rpp - 1) / g.rpp <= K) return true;
-    }
-    return false;
+    int k = unit;
+    while (k < p.G && (k * g.cg * (16 / V) < least || p.G % k)) k += unit;
+    if (k > p.G) k = p.G;
+    if (k * g.cg < V) return false;
+    g.slices = p.G / k;
+    g.vpr = (k * g.cg + V - 1) / V;
+    if (g.vpr > TH) return false;
+    g.rpp = TH / g.vpr;
+    // rows of 64 bytes only where they leave half the CUs a slice: 8 images of 56x56x128 take
+    // 23 us in 32 slices of 64 bytes, 18 in 64 of 32; 64 images 32 and 34
+    return ((int64_t)pixels + g.rpp - 1) / g.rpp <= K && (least < 64 || k == p.G || (int64_t)images * g.slices >= 128);
 }
 
 bool too_many(int64_t blocks) { return blocks >= (1 << 24); }
@@ -727,9 +717,12 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     if constexpr (V > 1) {
         Geo g;
-        if (resident(p, a.images, a.pixels, V, 256, 4, g)) return fwd_resident<DT, V, 256, 4, ACT>(g, a, st);
-        if (resident(p, a.images, a.pixels, V, 256, 16, g)) return fwd_resident<DT, V, 256, 16, ACT>(g, a, st);
-        if (resident(p, a.images, a.pixels, V, 1024, 16, g)) return fwd_resident<DT, V, 1024, 16, ACT>(g, a, st);
+        for (int least : {64, 32}) {
+            if (resident(p, a.images, a.pixels, V, 256, 4, least, g)) return fwd_resident<DT, V, 256, 4, ACT>(g, a, st);
+            if (resident(p, a.images, a.pixels, V, 256, 16, least, g)) return fwd_resident<DT, V, 256, 16, ACT>(g, a, st);
+            if (resident(p, a.images, a.pixels, V, 512, 16, least, g)) return fwd_resident<DT, V, 512, 16, ACT>(g, a, st);
+            if (resident(p, a.images, a.pixels, V, 1024, 16, least, g)) return fwd_resident<DT, V, 1024, 16, ACT>(g, a, st);
+        }
     }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, false);
@@ -765,8 +758,10 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     if constexpr (V > 1) {
         Geo g;
-        if (resident(p, a.images, a.pixels, V, 256, RK1, g)) return bwd_resident<DT, V, 256, RK1, ACT>(g, a, st);
-        if (resident(p, a.images, a.pixels, V, RTH, RK, g)) return bwd_resident<DT, V, RTH, RK, ACT>(g, a, st);
+        for (int least : {64, 32}) {
+            if (resident(p, a.images, a.pixels, V, 256, 8, least, g)) return bwd_resident<DT, V, 256, 8, ACT>(g, a, st);
+            if (resident(p, a.images, a.pixels, V, 512, 20, least, g)) return bwd_resident<DT, V, 512, 20, ACT>(g, a, st);
+        }
     }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(g, true);
@@ -840,8 +835,10 @@ hipError_t group_bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t
 size_t group_bytes(const dwconv_group_plan &p, int images, int pixels, bool back) {
     const int V = vec_of(p);
     Geo g;
-    if (!back && resident(p, images, pixels, V, 1024, 16, g)) return 0;
-    if (back && resident(p, images, pixels, V, RTH, RK, g)) return (size_t)images * 2 * p.C * sizeof(float);
+    for (int least : {64, 32}) {
+        if (!back && resident(p, images, pixels, V, 1024, 16, least, g)) return 0;
+        if (back && resident(p, images, pixels, V, 512, 20, least, g)) return (size_t)images * 2 * p.C * sizeof(float);
+    }
     return sizes(passes(p, images, pixels, V), back).all * sizeof(float);
 }
 
