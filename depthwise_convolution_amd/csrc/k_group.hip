@@ -13,7 +13,6 @@
 //              element read and written once
 //   in passes  runs of pixels give their mean and squares around it, which k_join puts
 //              together; further launches read the image again
-#include <algorithm>
 #include <type_traits>
 
 #include "seq_common.h"
@@ -126,50 +125,74 @@ __device__ __forceinline__ void back_through(float (&d)[V], const float (&z)[V])
     }
 }
 
-// Sums over a workgroup's lanes.  `cols` becomes the sums over rows of each channel of
-// the slice (in up to `segs` parts, segs x wide), `of_groups` those over the groups'
-// channels.  Every lane calls them; a barrier stands at the end of each.
+// The same words, of which the compiler does not know that it has taken them apart before:
+// else it keeps the fp32 values from one use to the next, in twice the registers.
+template <class DT, int V, int K>
+__device__ __forceinline__ void fresh(Any<DT, V> (&x)[K]) {
+    if constexpr (sizeof(typename DT::X) == 2 && V > 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < Any<DT, V>::N; ++i) {
+                uint32_t w = x[k].w[i];
+                asm("" : "+v"(w));
+                x[k].w[i] = w;
+            }
+    }
+}
+
+// Sums over a workgroup's lanes.  `cols` becomes the sums over rows of each column of the
+// slice's vectors, `of_groups` those over the groups' channels.  Every lane calls them; a
+// barrier stands at the end of each.
 template <int TH, int V>
 struct Sums {
-    static constexpr int SEGS = 32;
-    float *lanes, *cols, *stat;  // TH x V, at least TH and a row, as many as groups
-    int wide, segs;
-    __device__ __forceinline__ Sums(float *lanes, float *cols, float *stat, const Geo &g)
-        : lanes(lanes), cols(cols), stat(stat), wide(g.vpr * V), segs(min(max(TH / (g.vpr * V), 1), g.rpp)) {}
+    float *lanes, *cols;  // rpp rows of `ld`, a row
+    int wide, ld;
+    __device__ __forceinline__ Sums(float *sh, const Geo &g) : lanes(sh), wide(g.vpr * V), ld(g.vpr * V + 4) {
+        cols = sh + g.rpp * ld;
+    }
     template <class L>
     __device__ __forceinline__ void rows(const float (&v)[V], const L &ln, const Geo &g) {
-        const int width = g.vpr * V;
+        if ((int)threadIdx.x < g.rpp * g.vpr) {
+            float *at = lanes + (int)threadIdx.x / g.vpr * ld + (int)threadIdx.x % g.vpr * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i) lanes[(int)threadIdx.x * V + i] = ln.live && ln.counts(i) ? v[i] : 0.0f;
+            for (int i = 0; i < V; ++i) at[i] = ln.live && ln.counts(i) ? v[i] : 0.0f;
+        }
         __syncthreads();
-        for (int k = threadIdx.x; k < width * segs; k += TH) {
-            float s = 0.0f;
-            for (int r = k / width; r < g.rpp; r += segs) s += lanes[r * width + k % width];
-            cols[k] = s;
+        if (g.rpp >= 16) {  // 16 lanes a column, every 16th row each (rows are 4 banks apart)
+            const int part = (int)threadIdx.x & 15;
+            for (int k = (int)threadIdx.x >> 4; k < (wide + TH / 16 - 1) / (TH / 16) * (TH / 16); k += TH / 16) {
+                float s = 0.0f;
+                if (k < wide)
+                    for (int r = part; r < g.rpp; r += 16) s += lanes[r * ld + k];
+                s = sum_row16(s);
+                if (part == 0 && k < wide) cols[k] = s;
+            }
+        } else {
+            for (int k = threadIdx.x; k < wide; k += TH) {
+                float s = 0.0f;
+                for (int r = 0; r < g.rpp; ++r) s += lanes[r * ld + k];
+                cols[k] = s;
+            }
         }
         __syncthreads();
     }
-    // Column of channel i of the slice: the last vector is moved back by what it shares.
-    __device__ __forceinline__ int column(const Slice &s, int i) const {
-        const int last = (s.w + V - 1) / V - 1;
-        return i >= last * V ? i + (last + 1) * V - s.w : i;
-    }
+    // Sum of channel i of the slice: the last vector is moved back by what it shares.
     __device__ __forceinline__ float channel(const Slice &s, int i) const {
-        const int at = column(s, i);
-        float t = 0.0f;
-        for (int k = 0; k < segs; ++k) t += cols[k * wide + at];
-        return t;
+        const int last = (s.w + V - 1) / V - 1;
+        return cols[i >= last * V ? i + (last + 1) * V - s.w : i];
     }
-    // stat[j] = done(sum of f(channel) over group j's channels): a wavefront a group, or
-    // a lane where groups are small
+    // done(j, sum of f(channel) over group j's channels): 16 lanes a group, or a wavefront
     template <class F, class D>
     __device__ __forceinline__ void of_groups(const Slice &s, int cg, F f, D done) {
         const int n = s.ng > 1 ? cg : s.w;
-        if (n * segs <= 32) {
-            for (int j = threadIdx.x; j < s.ng; j += TH) {
-                float t = 0.0f;
-                for (int i = 0; i < n; ++i) t += f(j * n + i, channel(s, j * n + i));
-                done(j, t);
+        if (n == 1) {
+            for (int j = threadIdx.x; j < s.ng; j += TH) done(j, f(j, channel(s, j)));
+        } else if (n <= 16) {
+            const int i = (int)threadIdx.x & 15;
+            for (int j = (int)threadIdx.x >> 4; j < (s.ng + TH / 16 - 1) / (TH / 16) * (TH / 16); j += TH / 16) {
+                const float t = sum_row16(i < n && j < s.ng ? f(j * n + i, channel(s, j * n + i)) : 0.0f);
+                if (i == 0 && j < s.ng) done(j, t);
             }
         } else {
             for (int j = (int)threadIdx.x >> 6; j < s.ng; j += TH / 64) {
@@ -234,7 +257,7 @@ struct Have {
 // The run's or image's mean of each group (in stat) and squares around it (in sq).
 template <class DT, int V, int TH, int K, class L>
 __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &ln, const Group<V> &gr,
-                                        const Any<DT, V> (&x)[K], int n, const Have &have, Sums<TH, V> &sum, float *stat, float *sq,
+                                        Any<DT, V> (&x)[K], int n, const Have &have, Sums<TH, V> &sum, float *stat, float *sq,
                                         float (&mean)[V]) {
     const float inv = 1.0f / ((float)n * (float)(s.ng > 1 ? g.cg : s.w));
     float v[V];
@@ -248,6 +271,7 @@ __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &l
     sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { stat[j] = t * inv; });
 #pragma unroll
     for (int i = 0; i < V; ++i) mean[i] = stat[gr.of[i]], v[i] = 0.0f;
+    fresh(x);
     have.each<K>([&](int k) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -257,6 +281,7 @@ __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &l
     });
     sum.rows(v, ln, g);
     sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { sq[j] = t; });
+    fresh(x);
 }
 
 // K vectors of a lane
@@ -271,8 +296,8 @@ template <class DT, int V, int TH, int K, bool RUNS, int ACT>
 __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int64_t ldx, const float *w, const float *b,
                                             typename DT::X *y, int64_t ldy, float2 *stats, int max_groups) {
     extern __shared__ __align__(16) float sh[];
-    float *stat = sh + TH * V + max(TH, g.vpr * V), *sq = stat + max_groups;
-    Sums<TH, V> sum(sh, sh + TH * V, stat, g);
+    Sums<TH, V> sum(sh, g);
+    float *stat = sum.cols + sum.wide, *sq = stat + max_groups;
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
     const Slice s = slice_of(g, sl);
@@ -299,14 +324,17 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
     }
     const float inv = 1.0f / ((float)n * (float)g.cg);
 #pragma unroll
-    for (int i = 0; i < V; ++i) scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
+    for (int i = 0; i < V; ++i) {
+        scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
+        shift[i] = __builtin_fmaf(-mean[i], scale[i], shift[i]);
+    }
     if (!ln.live) return;
     y += ((int64_t)img * g.S + p0 + ln.row) * ldy + ln.c;
     const int64_t step = g.rpp * ldy;
     have.each<K>([&](int k) {
         float o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[k][i] - mean[i], scale[i], shift[i]);
+        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[k][i], scale[i], shift[i]);
         activate<DT, ACT>(o);
         ln.store(y + k * step, o, true);  // all loads of the slice are behind a barrier
     });
@@ -354,11 +382,17 @@ __global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const floa
     if (lane == 0) out[id] = make_float2(m, inverse_root(q * inv, g.eps));
 }
 
-// A lane's parameters: mean, r, r w and b of its channels.
+// A lane's parameters: mean, r, w and b of its channels, and u = r x + off.  (That the mean
+// is taken from x only after the product with r costs a rounding of r mean, no more than
+// the mean's own.)
 template <int V>
 struct Known {
-    float mean[V], r[V], w[V], b[V];
+    float mean[V], r[V], w[V], b[V], off[V];
     Known() = default;
+    __device__ __forceinline__ void ready() {
+#pragma unroll
+        for (int i = 0; i < V; ++i) off[i] = -mean[i] * r[i];
+    }
     template <class L>
     __device__ __forceinline__ Known(const Geo &g, const Slice &s, const L &ln, const float2 *joined, int img, const float *pw,
                                      const float *pb) {
@@ -371,6 +405,7 @@ struct Known {
             params(w[i], pw, ln.c + i, 1.0f);
             params(b[i], pb, ln.c + i, 0.0f);
         }
+        ready();
     }
 };
 
@@ -388,15 +423,18 @@ __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, in
     y += ((int64_t)img * g.S + p0 + ln.row) * ldy + ln.c;
     const int64_t sx = g.rpp * ldx, sy = g.rpp * ldy;
     const Known<V> kn(g, s, ln, joined, img, w, b);
-    float scale[V];
+    float scale[V], shift[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) scale[i] = kn.r[i] * kn.w[i];
+    for (int i = 0; i < V; ++i) {
+        scale[i] = kn.r[i] * kn.w[i];
+        shift[i] = __builtin_fmaf(-kn.mean[i], scale[i], kn.b[i]);
+    }
     Any<DT, V> v[U];
     Have(g, ln, n).stream<U>([&](int u, int k) { v[u] = Lane<DT, V>::load(x + k * sx); },
                              [&](int u, int k) {
                                  float o[V];
 #pragma unroll
-                                 for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[u][i] - kn.mean[i], scale[i], kn.b[i]);
+                                 for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[u][i], scale[i], shift[i]);
                                  activate<DT, ACT>(o);
                                  ln.store(y + k * sy, o, apart);
                              });
@@ -409,7 +447,7 @@ __device__ __forceinline__ void unit_and_dz(float (&u)[V], float (&dz)[V], const
     float z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        u[i] = (x[i] - kn.mean[i]) * kn.r[i];
+        u[i] = __builtin_fmaf(x[i], kn.r[i], kn.off[i]);
         z[i] = __builtin_fmaf(u[i], kn.w[i], kn.b[i]);
         dz[i] = dy[i];
     }
@@ -445,8 +483,8 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
                                                  int64_t lddy, const float *w, const float *b, typename DT::X *dx,
                                                  int64_t lddx, float *sums, int max_groups) {
     extern __shared__ __align__(16) float sh[];
-    float *stat = sh + TH * V + max(TH, g.vpr * V), *sq = stat + max_groups;
-    Sums<TH, V> sum(sh, sh + TH * V, stat, g);
+    Sums<TH, V> sum(sh, g);
+    float *stat = sum.cols + sum.wide, *sq = stat + max_groups;
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int sl = (int)(id % g.slices), img = (int)(id / g.slices);
     const Slice s = slice_of(g, sl);
@@ -470,6 +508,7 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
         params(kn.b[i], b, ln.c + i, 0.0f);
         s1[i] = s2[i] = 0.0f;
     }
+    kn.ready();
     have.each<K>([&](int k) { add_sums<ACT>(s1, s2, v[k], d[k], kn); });
     float *o = sums + (int64_t)img * 2 * g.C + s.c0;
     float m1[V], m2[V];
@@ -486,6 +525,8 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
 #pragma unroll
     for (int i = 0; i < V; ++i) m1[i] = stat[gr.of[i]], m2[i] = sq[gr.of[i]];
     if (!ln.live) return;  // all loads of the slice are behind a barrier
+    fresh(v);
+    fresh(d);
     have.each<K>([&](int k) {
         float r[V];
         grad_of<ACT>(r, v[k], d[k], kn, m1, m2);
@@ -498,7 +539,7 @@ template <class DT, int V, int TH, int U, int ACT>
 __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
                                              int64_t lddy, const float2 *joined, const float *w, const float *b, float *part) {
     extern __shared__ __align__(16) float sh[];
-    Sums<TH, V> sum(sh, sh + TH * V, nullptr, g);
+    Sums<TH, V> sum(sh, g);
     const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
     const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
     const Slice s = slice_of(g, sl);
@@ -685,8 +726,9 @@ Sizes sizes(const Geo &g, bool back) {
 }
 
 // LDS of a workgroup: lanes' values, columns, two values a group
-size_t lds_bytes(const Geo &g, int th, int V, int groups) {
-    return ((size_t)th * V + std::max(th, g.vpr * V) + 2 * (size_t)groups) * sizeof(float);
+size_t lds_bytes(const Geo &g, int V, int groups) {
+    const size_t wide = (size_t)g.vpr * V;
+    return (g.rpp * (wide + 4) + wide + 2 * (size_t)groups) * sizeof(float);
 }
 
 // groups a slice has at most
@@ -707,7 +749,7 @@ hipError_t fwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     const int64_t blocks = (int64_t)g.images * g.slices;
     if (too_many(blocks)) return hipErrorInvalidConfiguration;
     const int mg = most_groups(g);
-    k_fwd<DT, V, TH, K, false, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
+    k_fwd<DT, V, TH, K, false, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, a.w, a.b, (X *)a.y, a.ldy, nullptr, mg);
     return hipGetLastError();
 }
@@ -731,7 +773,7 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     if (!blocks) return hipSuccess;
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
     const int mg = most_groups(g);
-    const size_t lds = lds_bytes(g, PASS_TH, V, mg);
+    const size_t lds = lds_bytes(g, V, mg);
     k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr, 0,
                                                                                stats, mg);
     join(g, stats, joined, st);
@@ -746,7 +788,7 @@ hipError_t bwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     const int64_t blocks = (int64_t)g.images * g.slices;
     if (too_many(blocks)) return hipErrorInvalidConfiguration;
     const int mg = most_groups(g);
-    k_resident<DT, V, TH, K, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, TH, V, mg), st>>>(
+    k_resident<DT, V, TH, K, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, a.w, a.b, (X *)a.dx, a.lddx, a.workspace, mg);
     const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 15) / 16) : 0;
     if (param) k_means<1><<<param, 1024, 0, st>>>(g, a.workspace, g.images, a.w, a.dw, a.db, param, nullptr);
@@ -772,13 +814,13 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     float *part = (float *)joined + z.joined;
     float2 *means = (float2 *)(part + z.part);
     const int mg = most_groups(g);
-    const size_t lds = lds_bytes(g, PASS_TH, V, mg);
+    const size_t lds = lds_bytes(g, V, mg);
     const uint32_t streaming = (uint32_t)((int64_t)f.images * f.slices * f.runs);
     if (blocks) {
         k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr,
                                                                                    0, stats, mg);
         join(g, stats, joined, st);
-        k_sums<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, lds_bytes(f, PASS_TH, V, 0), st>>>(
+        k_sums<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, lds_bytes(f, V, 0), st>>>(
             f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, a.w, a.b, part);
     }
     const bool wide = many((int64_t)f.runs * f.cg);

@@ -807,6 +807,8 @@ class GroupNorm(_Plan):
         """Pixel stride of ``t``, whose channels are dense."""
         if t.shape != shape:
             raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+        if t.dtype is self.dtype and t.device == dev and t.is_contiguous():
+            return self.C
         flat = t
         if t.dim() != 2 and t.numel():
             try:
