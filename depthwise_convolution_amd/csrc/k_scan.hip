@@ -748,10 +748,9 @@ template <class DT, int LPC>
 __global__ void __launch_bounds__(THREADS) k_total(ScanGeo G, Out o, Total z) {
     using X = typename DT::X;
     constexpr int NP = 4 * LPC, CPW = THREADS / LPC;
-    const int cg = G.C / G.G;
     auto channel = [&](uint32_t cb, int ch) {  // -1: none
         const int c = (int)(cb % G.per_group) * CPW + ch;
-        return c < cg ? (int)(cb / G.per_group) * cg + c : -1;
+        return c < G.cg ? (int)(cb / G.per_group) * G.cg + c : -1;
     };
     if (blockIdx.x < z.blocks_bc) {
         const int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x, row = (int64_t)G.seq.tokens * 2 * NP;

@@ -96,9 +96,9 @@ __device__ __forceinline__ float step_width(float v, int soft, float &slope) {
 
 struct ScanGeo {
     Packed seq;
-    int C, N, G, CH;               // CH 0: a piece is a whole sequence
+    int C, N, G, cg, CH;           // cg channels a group; CH 0: a piece is a whole sequence
     uint32_t per_group, nblk;      // workgroups' channels: so many a group, so many in all
-    uint32_t slots, walkers;       // pieces; workgroups that share them (gradients)
+    uint32_t slots, walkers;       // pieces; workgroups that share them
     int soft, act;
 };
 
@@ -115,10 +115,9 @@ struct ScanLane {
     int g, c0, cend, ch, j, q, c;
     bool live;
     __device__ __forceinline__ ScanLane(const ScanGeo &G, uint32_t cb) {
-        const int cg = G.C / G.G;
-        g = (int)(cb / G.per_group);
-        c0 = g * cg + (int)(cb % G.per_group) * CPW;
-        cend = (g + 1) * cg;
+        g = G.G > 1 ? (int)(cb / G.per_group) : 0;
+        c0 = g * G.cg + (int)(cb - g * G.per_group) * CPW;
+        cend = (g + 1) * G.cg;
         ch = (int)threadIdx.x / LPC;
         j = (int)threadIdx.x % LPC;
         q = (int)threadIdx.x & 3;
@@ -174,9 +173,9 @@ inline ScanIn scan_inputs(const ScanArgs &a) {
 
 // Blocks of channels: 256 / lpc of one group each.
 inline ScanGeo scan_blocks(const dwconv_scan_plan &p, int lpc) {
-    ScanGeo G{{nullptr, 0, 0}, p.C, p.N, p.G, 0, 0, 0, 0, 0, p.softplus, p.act};
+    ScanGeo G{{nullptr, 0, 0}, p.C, p.N, p.G, p.C / p.G, 0, 0, 0, 0, 0, p.softplus, p.act};
     const int cpw = 256 / lpc;
-    G.per_group = (uint32_t)((p.C / p.G + cpw - 1) / cpw);
+    G.per_group = (uint32_t)((G.cg + cpw - 1) / cpw);
     G.nblk = G.per_group * (uint32_t)p.G;
     return G;
 }

@@ -67,6 +67,10 @@ GROUP = [
     ("f16", 1, 13000, 24, 8, "silu", True, 0),
     ("f32", 1, 40000, 4, 1, "silu", True, 0),
     ("bf16", 3, 784, 33, 11, "silu", True, 1),
+    ("bf16", 1, 5000, 32, 2, "silu", True, 0),
+    ("f16", 2, 2900, 64, 4, "silu", True, 0),
+    ("bf16", 1, 600000, 8, 1, "none", True, 0),
+    ("f32", 1, 9000, 256, 2, "silu", True, 0),
 ]
 
 

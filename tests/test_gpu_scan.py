@@ -141,6 +141,34 @@ def test_scan_step(case, slots):
         assert 0 <= s < cache.shape[0] or (y[i] == 7.0).all(), "a skipped row was written"
 
 
+@pytest.mark.parametrize("fmt, C, N, G, rows, shared", [
+    ("bf16", 2048, 16, 1, 203, False), ("bf16", 2048, 16, 1, 203, True), ("f16", 61, 11, 1, 4500, True),
+    ("f32", 520, 100, 2, 97, True), ("f32", 300, 32, 3, 331, False)])
+def test_scan_step_of_many_rows(fmt, C, N, G, rows, shared):
+    """More rows than workgroups that walk them, slots that come again after many rows."""
+    say(f"[gpu] scan step {fmt} {C} {N} {G} {rows} {shared}")
+    case = (fmt, C, N, G, [], False, "silu", True, True, 0)
+    entries = rows // 2 if shared else rows + 5
+    g = torch.Generator().manual_seed(rows)
+    at = torch.randint(-1, entries + 2, (rows,), generator=g) if shared else torch.randperm(entries, generator=g)[:rows]
+    d, cache = step_rows(case, rows, [entries - 3])
+    st, y = up(cache.clone()), torch.full((rows, C), 7.0, dtype=DTYPES[fmt], device=DEV)
+    plan_of(case).step(up(d["x"]), up(d["dt"]), up(d["a"]), up(d["b"]), up(d["c"]), st, skip=up(d["skip"]),
+                       dt_bias=up(d["bias"]), gate=up(d["gate"]), slots=up(at.to(torch.int32)), y=y)
+    valid = (at >= 0) & (at < entries)
+    order = torch.argsort(at, stable=True)
+    order = order[valid[order]]  # a slot's rows together and in their order
+    used, lens = torch.unique_consecutive(at[order], return_counts=True)
+    row = lambda k: d[k][order]  # noqa: E731
+    want = ref.scan_bounds(DTYPES[fmt], row("x"), row("dt"), d["a"], row("b"), row("c"), d["skip"], d["bias"], row("gate"),
+                           lens.tolist(), cache[used], True, "silu")
+    holds(y[up(order)], want["y"], "y")
+    holds(st[up(used)], want["state"], "state")
+    rest = torch.ones(entries, dtype=torch.bool)
+    rest[used] = False
+    assert torch.equal(st.cpu()[rest], cache[rest]) and (y[up(~valid)] == 7.0).all()
+
+
 def test_scan_of_nothing():
     """No tokens, no sequences, only empty sequences."""
     C, N = 40, 16
