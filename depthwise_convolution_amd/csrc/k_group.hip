@@ -479,14 +479,32 @@ __device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const A
     }
 }
 
-template <int ACT, class DT, int V>
-__device__ __forceinline__ void grad_of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy, const Known<V> &kn,
-                                        const float (&m1)[V], const float (&m2)[V]) {
-    float u[V], dz[V];
-    unit_and_dz<ACT>(u, dz, x, dy, kn);
+// r (dz w - m1 - u m2) as dz (r w) + x (-r r m2) + rest, z as x (r w) + shift
+template <int V>
+struct Grad {
+    float scale[V], shift[V], slope[V], rest[V];
+    __device__ __forceinline__ Grad(const Known<V> &kn, const float (&m1)[V], const float (&m2)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = kn.r[i] * (__builtin_fmaf(dz[i], kn.w[i], -m1[i]) - u[i] * m2[i]);
-}
+        for (int i = 0; i < V; ++i) {
+            scale[i] = kn.r[i] * kn.w[i];
+            shift[i] = __builtin_fmaf(kn.off[i], kn.w[i], kn.b[i]);
+            slope[i] = -kn.r[i] * kn.r[i] * m2[i];
+            rest[i] = -kn.r[i] * __builtin_fmaf(kn.off[i], m2[i], m1[i]);
+        }
+    }
+    template <int ACT, class DT>
+    __device__ __forceinline__ void of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy) const {
+        float z[V], dz[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            z[i] = __builtin_fmaf(x[i], scale[i], shift[i]);
+            dz[i] = dy[i];
+        }
+        back_through<DT, ACT>(dz, z);
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(dz[i], scale[i], __builtin_fmaf(x[i], slope[i], rest[i]));
+    }
+};
 
 // Gradients with x and dy of an image's slice in registers.  sums: [image][2][C], dz and
 // dz u over the pixels.
@@ -539,9 +557,10 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     if (!ln.live) return;  // all loads of the slice are behind a barrier
     fresh(v);
     fresh(d);
+    const Grad<V> grad(kn, m1, m2);
     have.each<K>([&](int k) {
         float r[V];
-        grad_of<ACT>(r, v[k], d[k], kn, m1, m2);
+        grad.template of<ACT>(r, v[k], d[k]);
         ln.store(dx + k * sx, r, true);
     });
 }
@@ -649,11 +668,12 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
         m1[i] = m.x;
         m2[i] = m.y;
     }
+    const Grad<V> grad(kn, m1, m2);
     Any<DT, V> vx[U], vd[U];
     Have(g, ln, n).stream<U>([&](int u, int k) { vx[u] = Lane<DT, V>::load(x + k * sx), vd[u] = Lane<DT, V>::load(dy + k * sy); },
                              [&](int u, int k) {
                                  float o[V];
-                                 grad_of<ACT>(o, vx[u], vd[u], kn, m1, m2);
+                                 grad.template of<ACT>(o, vx[u], vd[u]);
                                  ln.store(dx + k * so, o, apart);
                              });
 }
