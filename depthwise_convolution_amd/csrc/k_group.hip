@@ -394,30 +394,35 @@ __global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const floa
     if (lane == 0) out[id] = make_float2(m, inverse_root(q * inv, g.eps));
 }
 
-// A lane's parameters: mean, r, w and b of its channels, and u = r x + off.  (That the mean
-// is taken from x only after the product with r costs a rounding of r mean, no more than
-// the mean's own.)
+// A lane's channels: u = x r + off and z = x scale + shift with scale = r w.  (That the mean
+// is taken from x only after a product costs a rounding of r mean, no more than the mean's own.)
 template <int V>
 struct Known {
-    float mean[V], r[V], w[V], b[V], off[V];
+    float r[V], off[V], scale[V], shift[V];
     Known() = default;
-    __device__ __forceinline__ void ready() {
+    // from mean and r
+    __device__ __forceinline__ void ready(const float (&mean)[V], const float *w, const float *b, int c) {
+        params(scale, w, c, 1.0f);
+        params(shift, b, c, 0.0f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) off[i] = -mean[i] * r[i];
+        for (int i = 0; i < V; ++i) {
+            off[i] = -mean[i] * r[i];
+            scale[i] *= r[i];
+            shift[i] = __builtin_fmaf(-mean[i], scale[i], shift[i]);
+        }
     }
     template <class L>
-    __device__ __forceinline__ Known(const Geo &g, const Slice &s, const L &ln, const float2 *joined, int img, const float *pw,
-                                     const float *pb) {
+    __device__ __forceinline__ Known(const Geo &g, const Slice &s, const L &ln, const float2 *joined, int img, const float *w,
+                                     const float *b) {
         const Group<V> gr(g, s, ln);
+        float mean[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float2 m = joined[(int64_t)img * g.G + s.g0 + gr.of[i]];
             mean[i] = m.x;
             r[i] = m.y;
         }
-        params(w, pw, ln.c, 1.0f);
-        params(b, pb, ln.c, 0.0f);
-        ready();
+        ready(mean, w, b, ln.c);
     }
 };
 
@@ -435,32 +440,24 @@ __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, in
     y += ((int64_t)img * g.S + p0 + ln.row) * ldy + ln.c;
     const int64_t sx = g.rpp * ldx, sy = g.rpp * ldy;
     const Known<V> kn(g, s, ln, joined, img, w, b);
-    float scale[V], shift[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        scale[i] = kn.r[i] * kn.w[i];
-        shift[i] = __builtin_fmaf(-kn.mean[i], scale[i], kn.b[i]);
-    }
     Any<DT, V> v[U];
     Have(g, ln, n).stream<U>([&](int u, int k) { v[u] = Lane<DT, V>::load(x + k * sx); },
                              [&](int u, int k) {
                                  float o[V];
 #pragma unroll
-                                 for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[u][i], scale[i], shift[i]);
+                                 for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[u][i], kn.scale[i], kn.shift[i]);
                                  activate<DT, ACT>(o);
                                  ln.store(y + k * sy, o, apart);
                              });
 }
 
-// u and dz of one vector
+// dz of one vector
 template <int ACT, class DT, int V>
-__device__ __forceinline__ void unit_and_dz(float (&u)[V], float (&dz)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
-                                            const Known<V> &kn) {
+__device__ __forceinline__ void make_dz(float (&dz)[V], const Any<DT, V> &x, const Any<DT, V> &dy, const Known<V> &kn) {
     float z[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        u[i] = __builtin_fmaf(x[i], kn.r[i], kn.off[i]);
-        z[i] = __builtin_fmaf(u[i], kn.w[i], kn.b[i]);
+        z[i] = __builtin_fmaf(x[i], kn.scale[i], kn.shift[i]);
         dz[i] = dy[i];
     }
     back_through<DT, ACT>(dz, z);
@@ -470,39 +467,33 @@ __device__ __forceinline__ void unit_and_dz(float (&u)[V], float (&dz)[V], const
 template <int ACT, class DT, int V>
 __device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
                                          const Known<V> &kn) {
-    float u[V], dz[V];
-    unit_and_dz<ACT>(u, dz, x, dy, kn);
+    float dz[V];
+    make_dz<ACT>(dz, x, dy, kn);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         s1[i] += dz[i];
-        s2[i] = __builtin_fmaf(dz[i], u[i], s2[i]);
+        s2[i] = __builtin_fmaf(dz[i], __builtin_fmaf(x[i], kn.r[i], kn.off[i]), s2[i]);
     }
 }
 
-// r (dz w - m1 - u m2) as dz (r w) + x (-r r m2) + rest, z as x (r w) + shift
+// r (dz w - m1 - u m2) as r (dz w + x slope + rest)
 template <int V>
 struct Grad {
-    float scale[V], shift[V], slope[V], rest[V];
-    __device__ __forceinline__ Grad(const Known<V> &kn, const float (&m1)[V], const float (&m2)[V]) {
+    float w[V], slope[V], rest[V];
+    __device__ __forceinline__ Grad(const Known<V> &kn, const float *pw, int c, const float (&m1)[V], const float (&m2)[V]) {
+        params(w, pw, c, 1.0f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            scale[i] = kn.r[i] * kn.w[i];
-            shift[i] = __builtin_fmaf(kn.off[i], kn.w[i], kn.b[i]);
-            slope[i] = -kn.r[i] * kn.r[i] * m2[i];
-            rest[i] = -kn.r[i] * __builtin_fmaf(kn.off[i], m2[i], m1[i]);
+            slope[i] = -kn.r[i] * m2[i];
+            rest[i] = -__builtin_fmaf(kn.off[i], m2[i], m1[i]);
         }
     }
     template <int ACT, class DT>
-    __device__ __forceinline__ void of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy) const {
-        float z[V], dz[V];
+    __device__ __forceinline__ void of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy, const Known<V> &kn) const {
+        float dz[V];
+        make_dz<ACT>(dz, x, dy, kn);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            z[i] = __builtin_fmaf(x[i], scale[i], shift[i]);
-            dz[i] = dy[i];
-        }
-        back_through<DT, ACT>(dz, z);
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(dz[i], scale[i], __builtin_fmaf(x[i], slope[i], rest[i]));
+        for (int i = 0; i < V; ++i) o[i] = kn.r[i] * __builtin_fmaf(dz[i], w[i], __builtin_fmaf(x[i], slope[i], rest[i]));
     }
 };
 
@@ -528,7 +519,8 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     take(v, x + ((int64_t)img * n + ln.row) * ldx + ln.c, g.rpp * ldx, have);
     take(d, dy + ((int64_t)img * n + ln.row) * lddy + ln.c, g.rpp * lddy, have);
     Known<V> kn;
-    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, kn.mean);
+    float mean[V];
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
     const float inv = 1.0f / ((float)n * (float)g.cg);
     float s1[V], s2[V];
 #pragma unroll
@@ -536,9 +528,7 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
         kn.r[i] = inverse_root(sq[gr.of[i]] * inv, g.eps);
         s1[i] = s2[i] = 0.0f;
     }
-    params(kn.w, w, ln.c, 1.0f);
-    params(kn.b, b, ln.c, 0.0f);
-    kn.ready();
+    kn.ready(mean, w, b, ln.c);
     have.each<K>([&](int k) { add_sums<ACT>(s1, s2, v[k], d[k], kn); });
     float *o = sums + (int64_t)img * 2 * g.C + s.c0;
     float m1[V], m2[V];
@@ -557,10 +547,10 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     if (!ln.live) return;  // all loads of the slice are behind a barrier
     fresh(v);
     fresh(d);
-    const Grad<V> grad(kn, m1, m2);
+    const Grad<V> grad(kn, w, ln.c, m1, m2);
     have.each<K>([&](int k) {
         float r[V];
-        grad.template of<ACT>(r, v[k], d[k]);
+        grad.template of<ACT>(r, v[k], d[k], kn);
         ln.store(dx + k * sx, r, true);
     });
 }
@@ -668,12 +658,12 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
         m1[i] = m.x;
         m2[i] = m.y;
     }
-    const Grad<V> grad(kn, m1, m2);
+    const Grad<V> grad(kn, w, ln.c, m1, m2);
     Any<DT, V> vx[U], vd[U];
     Have(g, ln, n).stream<U>([&](int u, int k) { vx[u] = Lane<DT, V>::load(x + k * sx), vd[u] = Lane<DT, V>::load(dy + k * sy); },
                              [&](int u, int k) {
                                  float o[V];
-                                 grad.template of<ACT>(o, vx[u], vd[u]);
+                                 grad.template of<ACT>(o, vx[u], vd[u], kn);
                                  ln.store(dx + k * so, o, apart);
                              });
 }
