@@ -305,6 +305,25 @@ __device__ __forceinline__ void take(Any<DT, V> (&x)[K], const typename DT::X *p
     have.each<K>([&](int k) { x[k] = Lane<DT, V>::load(p + k * step); });
 }
 
+// A run's moments of a slice's groups in stats[image][group][run x parts]
+__device__ __forceinline__ void leave(const Geo &g, const Slice &s, float2 *stats, int img, int run, int sl, const float *stat,
+                                      const float *sq) {
+    const int parts = max(g.parts, 1), at = run * parts + (g.parts > 1 ? sl % g.parts : 0);
+    for (int j = threadIdx.x; j < s.ng; j += blockDim.x)
+        stats[((int64_t)img * g.G + s.g0 + j) * (g.runs * parts) + at] = make_float2(stat[j], sq[j]);
+}
+
+// The lanes' two sums of each channel, C apart
+template <int TH, int V, class L>
+__device__ __forceinline__ void channel_sums(const Geo &g, const Slice &s, const L &ln, Sums<TH, V> &sum, const float (&s1)[V],
+                                             const float (&s2)[V], float *out) {
+    sum.rows(s1, ln, g);
+    for (int i = threadIdx.x; i < s.w; i += TH) out[i] = sum.channel(s, i);
+    __syncthreads();
+    sum.rows(s2, ln, g);
+    for (int i = threadIdx.x; i < s.w; i += TH) out[g.C + i] = sum.channel(s, i);
+}
+
 // Forward: resident (RUNS false), or the moments of a run of pixels (RUNS true), left
 // as mean and squares in stats[image][group][run x parts].
 template <class DT, int V, int TH, int K, bool RUNS, int ACT>
@@ -329,9 +348,7 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
     }
     moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
     if (RUNS) {
-        const int per = g.runs * max(g.parts, 1), at = run * max(g.parts, 1) + (g.parts > 1 ? sl % g.parts : 0);
-        for (int j = threadIdx.x; j < s.ng; j += TH)
-            stats[((int64_t)img * g.G + s.g0 + j) * per + at] = make_float2(stat[j], sq[j]);
+        leave(g, s, stats, img, run, sl, stat, sq);
         return;
     }
     const float inv = 1.0f / ((float)n * (float)g.cg);
@@ -369,9 +386,9 @@ __device__ __forceinline__ void sum_group(float &a, float &b, float *sh) {
 
 // Puts the moments of a group's runs together: W wavefronts a group.  With counts n_i,
 // means m_i and squares q_i: m = sum n_i m_i / n and q = sum (q_i + n_i (m_i - m)^2).
-// out: mean and r.
+// out: mean and r.  part: the sums that k_both has left, or nullptr.
 template <int W>
-__global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const float2 *stats, float2 *out) {
+__global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const float2 *stats, float2 *out, float *part) {
     constexpr int TH = W > 4 ? W * 64 : 256;
     __shared__ float sh[32];
     const int64_t id = (int64_t)blockIdx.x * (TH / 64 / W) + (W == 1 ? threadIdx.x >> 6 : 0);
@@ -391,7 +408,17 @@ __global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const floa
         q += __builtin_fmaf(count(i) * d, d, p[i].y);
     }
     sum_group<W>(q, none, sh);
-    if (lane == 0) out[id] = make_float2(m, inverse_root(q * inv, g.eps));
+    const float r = inverse_root(q * inv, g.eps);
+    if (lane == 0) out[id] = make_float2(m, r);
+    if (!part) return;
+    part += id / g.G * g.runs * 2 * g.C + id % g.G * g.cg;
+    for (int run = lane / g.cg, c = lane % g.cg; run < g.runs;) {
+        float *at = part + (int64_t)run * 2 * g.C + c;
+        at[g.C] = r * __builtin_fmaf(p[run * parts + (parts > 1 ? c / g.part : 0)].x - m, at[0], at[g.C]);
+        run += 64 * W / g.cg;
+        c += 64 * W % g.cg;
+        if (c >= g.cg) c -= g.cg, ++run;
+    }
 }
 
 // A lane's channels: u = x r + off and z = x scale + shift with scale = r w.  (That the mean
@@ -576,12 +603,42 @@ __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int
     Any<DT, V> vx[U], vd[U];
     Have(g, ln, n).stream<U>([&](int u, int k) { vx[u] = Lane<DT, V>::load(x + k * sx), vd[u] = Lane<DT, V>::load(dy + k * sy); },
                              [&](int u, int) { add_sums<ACT>(s1, s2, vx[u], vd[u], kn); });
-    float *o = part + ((int64_t)img * g.runs + run) * 2 * g.C + s.c0;
-    sum.rows(s1, ln, g);
-    for (int i = threadIdx.x; i < s.w; i += TH) o[i] = sum.channel(s, i);
-    __syncthreads();
-    sum.rows(s2, ln, g);
-    for (int i = threadIdx.x; i < s.w; i += TH) o[g.C + i] = sum.channel(s, i);
+    channel_sums<TH>(g, s, ln, sum, s1, s2, part + ((int64_t)img * g.runs + run) * 2 * g.C + s.c0);
+}
+
+// Gradients without an activation, where dz = dy does not wait for the statistics: a run's
+// moments as k_fwd leaves them and, in one reading, the sums of dy and dy (x - m) with the
+// run's own mean m: part[image][run][2][C].  k_join makes of them the run's sum of dy u,
+// r (sum dy (x - m) + (m - mean) sum dy): no difference of large sums.
+template <class DT, int V, int TH, int K>
+__global__ void __launch_bounds__(TH) k_both(Geo g, const typename DT::X *x, int64_t ldx, const typename DT::X *dy,
+                                             int64_t lddy, float2 *stats, float *part, int max_groups) {
+    extern __shared__ __align__(16) float sh[];
+    Sums<TH, V> sum(sh, g);
+    float *stat = sum.cols + sum.wide, *sq = stat + max_groups;
+    const uint32_t id = xcd_remap(blockIdx.x, gridDim.x);
+    const int sl = (int)(id % g.slices), run = (int)(id / g.slices % g.runs), img = (int)(id / g.slices / g.runs);
+    const Slice s = slice_of(g, sl);
+    const Lane<DT, V> ln(g, s);
+    const Group<V> gr(g, s, ln);
+    const int p0 = run * g.rows, n = min(g.rows, g.S - p0);
+    const Have have(g, ln, n);
+    Any<DT, V> v[K], d[K];
+    take(v, x + ((int64_t)img * g.S + p0 + ln.row) * ldx + ln.c, g.rpp * ldx, have);
+    take(d, dy + ((int64_t)img * g.S + p0 + ln.row) * lddy + ln.c, g.rpp * lddy, have);
+    float mean[V], s1[V], s2[V];
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
+    leave(g, s, stats, img, run, sl, stat, sq);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
+    have.each<K>([&](int k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s1[i] += d[k][i];
+            s2[i] = __builtin_fmaf(d[k][i], v[k][i] - mean[i], s2[i]);
+        }
+    });
+    channel_sums<TH>(g, s, ln, sum, s1, s2, part + ((int64_t)img * g.runs + run) * 2 * g.C + s.c0);
 }
 
 // From the runs' sums of each channel ([image][run][2][C]: dz, dz u): the first `param`
@@ -686,6 +743,9 @@ Geo in_runs(Geo g, int want, int most) {
     return g;
 }
 
+// Gradients whose channels' sums k_both forms beside the moments
+bool with_sums(const dwconv_group_plan &p, bool back) { return back && p.act == DWCONV_GROUP_ACT_NONE; }
+
 // In passes: slices of at most 256 vectors, whole groups or parts of one.
 Geo passes(const dwconv_group_plan &p, int images, int pixels, int V) {
     Geo g = base(p, images, pixels);
@@ -734,14 +794,14 @@ bool too_many(int64_t blocks) { return blocks >= (1 << 24); }
 struct Sizes {
     size_t stats, joined, part, means, all;  // floats
 };
-Sizes sizes(const Geo &g, bool back) {
+Sizes sizes(const dwconv_group_plan &p, const Geo &g, bool back) {
     Sizes z{};
-    const Geo f = streams(g);
+    const int runs = with_sums(p, back) ? g.runs : streams(g).runs;
     const size_t groups = (size_t)g.images * g.G;
     z.stats = groups * g.runs * (g.parts > 1 ? g.parts : 1) * 2;
     z.joined = groups * 2;
     if (back) {
-        z.part = (size_t)g.images * f.runs * 2 * g.C;
+        z.part = (size_t)g.images * runs * 2 * g.C;
         z.means = groups * 2;
     }
     z.all = z.stats + z.joined + z.part + z.means;
@@ -760,10 +820,10 @@ int most_groups(const Geo &g) { return (g.G + g.slices - 1) / g.slices; }
 // as many values a group as are worth a workgroup
 bool many(int64_t values) { return values > 512; }
 
-void join(const Geo &g, const float2 *stats, float2 *joined, hipStream_t st) {
+void join(const Geo &g, const float2 *stats, float2 *joined, float *part, hipStream_t st) {
     const int64_t groups = (int64_t)g.images * g.G;
-    if (many((int64_t)g.runs * g.parts)) k_join<16><<<(uint32_t)groups, 1024, 0, st>>>(g, stats, joined);
-    else k_join<1><<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined);
+    if (many((int64_t)g.runs * (part ? g.cg : g.parts))) k_join<16><<<(uint32_t)groups, 1024, 0, st>>>(g, stats, joined, part);
+    else k_join<1><<<(uint32_t)((groups + 3) / 4), 256, 0, st>>>(g, stats, joined, part);
 }
 
 template <class DT, int V, int TH, int K, int ACT>
@@ -790,7 +850,7 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
         }
     }
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
-    const Sizes z = sizes(g, false);
+    const Sizes z = sizes(p, g, false);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
     if (too_many(blocks) || groups >= 1 << 22) return hipErrorInvalidConfiguration;
     if (!blocks) return hipSuccess;
@@ -799,7 +859,7 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     const size_t lds = lds_bytes(g, V, mg);
     k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr, 0,
                                                                                stats, mg);
-    join(g, stats, joined, st);
+    join(g, stats, joined, nullptr, st);
     k_apply<DT, V, PASS_TH, 4, ACT><<<(uint32_t)((int64_t)f.images * f.slices * f.runs), PASS_TH, 0, st>>>(
         f, (const X *)a.x, a.ldx, joined, a.w, a.b, (X *)a.y, a.ldy);
     return hipGetLastError();
@@ -814,7 +874,8 @@ hipError_t bwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     k_resident<DT, V, TH, K, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, a.w, a.b, (X *)a.dx, a.lddx, a.workspace, mg);
     const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 15) / 16) : 0;
-    if (param) k_means<1><<<param, 1024, 0, st>>>(g, a.workspace, g.images, a.w, a.dw, a.db, param, nullptr);
+    if (param)
+        k_means<1><<<param, 1024, 0, st>>>(g, a.workspace, g.images, a.w, a.dw, a.db, param, nullptr);
     return hipGetLastError();
 }
 
@@ -828,8 +889,9 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
             if (resident(p, a.images, a.pixels, V, 512, 20, least, g)) return bwd_resident<DT, V, 512, 20, ACT>(g, a, st);
         }
     }
-    const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
-    const Sizes z = sizes(g, true);
+    constexpr bool BOTH = ACT == DWCONV_GROUP_ACT_NONE;
+    const Geo g = passes(p, a.images, a.pixels, V), f = streams(g), &sums = BOTH ? g : f;
+    const Sizes z = sizes(p, g, true);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
     const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 15) / 16) : 0;
     if (too_many(blocks) || groups + param >= 1 << 22) return hipErrorInvalidConfiguration;
@@ -840,17 +902,26 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     const size_t lds = lds_bytes(g, V, mg);
     const uint32_t streaming = (uint32_t)((int64_t)f.images * f.slices * f.runs);
     if (blocks) {
-        k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, (const X *)a.x, a.ldx, a.w, a.b, nullptr,
-                                                                                   0, stats, mg);
-        join(g, stats, joined, st);
-        k_sums<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, lds_bytes(f, V, 0), st>>>(
-            f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, a.w, a.b, part);
+        const X *x = (const X *)a.x, *dy = (const X *)a.dy;
+        if constexpr (BOTH)
+            // 16 images of 112x112x61 have 7 rows a lane: 18.4 us, with room for 16 21.7; 2 fp32
+            // images of 256x256x256 16: 67 us, 69 in runs of 8 and then 11 more in the joins
+            (g.rows <= 8 * g.rpp ? k_both<DT, V, PASS_TH, 8> : k_both<DT, V, PASS_TH, PASS_K>)<<<(uint32_t)blocks, PASS_TH, lds,
+                                                                                               st>>>(
+                g, x, a.ldx, dy, a.lddy, stats, part, mg);
+        else
+            k_fwd<DT, V, PASS_TH, PASS_K, true, 0><<<(uint32_t)blocks, PASS_TH, lds, st>>>(g, x, a.ldx, a.w, a.b, nullptr, 0,
+                                                                                       stats, mg);
+        join(g, stats, joined, BOTH ? part : nullptr, st);
+        if constexpr (!BOTH)
+            k_sums<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, lds_bytes(f, V, 0), st>>>(f, x, a.ldx, dy, a.lddy, joined, a.w,
+                                                                                       a.b, part);
     }
-    const bool wide = many((int64_t)f.runs * f.cg);
+    const bool wide = many((int64_t)sums.runs * sums.cg);
     const uint32_t wg = !blocks ? 0 : (uint32_t)(wide ? groups : (groups + 15) / 16);
     if (param + wg)
-        (wide ? k_means<16> : k_means<1>)<<<param + wg, 1024, 0, st>>>(f, part, blocks ? (int64_t)f.images * f.runs : 0, a.w,
-                                                                      a.dw, a.db, param, means);
+        (wide ? k_means<16> : k_means<1>)<<<param + wg, 1024, 0, st>>>(
+            sums, part, blocks ? (int64_t)sums.images * sums.runs : 0, a.w, a.dw, a.db, param, means);
     if (blocks)
         k_dx<DT, V, PASS_TH, 4, ACT><<<streaming, PASS_TH, 0, st>>>(f, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, joined, means,
                                                               a.w, a.b, (X *)a.dx, a.lddx);
@@ -904,7 +975,7 @@ size_t group_bytes(const dwconv_group_plan &p, int images, int pixels, bool back
         if (!back && resident(p, images, pixels, V, 1024, 16, least, g)) return 0;
         if (back && resident(p, images, pixels, V, 512, 20, least, g)) return (size_t)images * 2 * p.C * sizeof(float);
     }
-    return sizes(passes(p, images, pixels, V), back).all * sizeof(float);
+    return sizes(p, passes(p, images, pixels, V), back).all * sizeof(float);
 }
 
 }  // namespace dw

@@ -71,6 +71,10 @@ GROUP = [
     ("f16", 2, 2900, 64, 4, "silu", True, 0),
     ("bf16", 1, 600000, 8, 1, "none", True, 0),
     ("f32", 1, 9000, 256, 2, "silu", True, 0),
+    ("f32", 1, 9000, 256, 2, "none", True, 0),
+    ("f16", 16, 2500, 61, 61, "none", True, 0),
+    ("f32", 1, 36000, 256, 8, "none", True, 0),
+    ("f32", 1, 720000, 3, 1, "none", True, 0),
 ]
 
 
