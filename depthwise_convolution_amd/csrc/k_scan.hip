@@ -19,6 +19,15 @@
 //   du = sum_n G b     G *= e^(d a)     dd = sum_n G h_before a + x du     da += d G h_before
 // walk back over blocks of 8 tokens whose first states a walk forward has left in the
 // workspace; a block's states and decays are formed again and stay in registers.
+//
+// Vector instructions bound all of it, an exponential (8 cycles) and four operations (4 each)
+// a state and token forward, in the gradients about 76 cycles: 16384 tokens x 8192 channels x
+// 16 states, bf16, 570 to 630 us by the card's clock (367 for those instructions at 2.14 GHz;
+// 204 for the bytes at a copy's rate; vector units 84 % busy, 92 % where sequences are
+// equally long); gradients of 4096 x 8192 640 (291 and 90; 77 % busy).  One sequence of 5003
+// x 2048 in runs of 64: k_ends 36, k_join 11, k_out 49 us.  Sums over channels on the matrix
+// units, with a left operand of zeros and ones, take longer (gradients 870): an fp32 product's
+// 32 cycles add to the vector unit's time.
 #include <type_traits>
 
 #include "scan_common.h"
@@ -123,7 +132,8 @@ __device__ __forceinline__ Piece piece(const ScanGeo &G, int64_t slot) {
 // in rounds of 256, every second one backwards here, so that the CU with the longest
 // sequence of one round has the shortest of the next; later ones go where a place is free.
 // For up to 64 sequences, whose lengths a wavefront sorts; of more, every CU has some of each.
-// (7 sequences of 1553 to 3465 tokens, 8192 channels: 858 us in order, ORDERED.)
+// 7 sequences of 1553 to 3465 tokens, 8192 channels: 630 us, in their order 692; gradients of
+// 4 of 593 to 1266 tokens 640 and 708.
 __device__ __forceinline__ void longest_first(const ScanGeo &G, uint32_t &id, uint32_t all) {
     if (G.CH || !G.seq.offsets || G.seq.seqs > 64 || G.slots != (uint32_t)G.seq.seqs || G.seq.seqs < 2) return;
     const uint32_t round = id / 256;
@@ -790,7 +800,7 @@ ScanGeo geometry(const dwconv_scan_plan &p, const int32_t *offsets, int seqs, in
     // tokens as give a CU six (four in the gradients).  N = 16, whole sequences and runs:
     // 16384 and 32768 channels x 2048 tokens 220 and 312 us, 246 and 479; two sequences of
     // 150 tokens, 8192 channels 29 and 38; four of 593 to 1266, 1024 channels, N = 64, 160
-    // and 145; gradients of four of 297 to 633 tokens, 4096 channels, 229 and 253.
+    // and 142; gradients of four of 297 to 633 tokens, 4096 channels, 229 and 253.
     const int64_t blocks = (int64_t)seqs * G.nblk, want = back ? 1024 : 1536;
     const bool ragged = !back && seqs > 1 && tokens / seqs >= 512;
     if (seqs > 0 && blocks < (ragged ? 512 : 256)) {

@@ -344,6 +344,20 @@ def test_group_backward(case):
     holds(same, want["dx"], "in place")
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("size, eps", [(1e15, 1e-5), (1e-15, 0.0)])
+@pytest.mark.parametrize("pixels", [60, 9000])
+def test_group_of_far_sizes(act, size, eps, pixels):
+    """Deviations whose squares are near fp32's ends."""
+    d = group_data(("f32", 1, pixels, 48, 6, act, True, 0))
+    x = d["x"] * size
+    want = ref.group_bounds(torch.float32, x, d["w"], d["b"], 6, act, eps, d["dy"])
+    plan = dw.GroupNorm(48, 6, "f32", act=act, eps=eps)
+    holds(plan(up(x), up(d["w"]), up(d["b"])), want["y"], "y")
+    for name, v in zip(("dx", "dw", "db"), plan.backward(up(x), up(d["dy"]), up(d["w"]), up(d["b"]))):
+        holds(v, want[name], name)
+
+
 def test_group_of_nothing():
     plan = dw.GroupNorm(8, 2, "f32")
     w = torch.ones(8, device=DEV)
@@ -448,7 +462,7 @@ def calls():
     x = torch.randn(3, 400, 96, device=DEV)
     big = torch.randn(2, 9000, 48, device=DEV)
     w, b = torch.rand(96, device=DEV), torch.rand(96, device=DEV)
-    norm, wide = dw.GroupNorm(96, 32, "f32"), dw.GroupNorm(48, 6, "f32")
+    norm, wide, plain = dw.GroupNorm(96, 32, "f32"), dw.GroupNorm(48, 6, "f32"), dw.GroupNorm(48, 6, "f32", act="none")
     T = sum(case[4])
     out = torch.zeros(T + TAIL, 320, dtype=torch.bfloat16, device=DEV)
     so = torch.zeros_like(st)
@@ -464,7 +478,8 @@ def calls():
         "scan backward": lambda s: [v[:T] if v.shape[0] == T + TAIL else v for v in plan.backward(
             *pos, dy, offsets=off, state_in=st, dstate_out=dst, stream=s, **named)],
         "group forward": lambda s: [norm(x, w, b, stream=s), wide(big, stream=s)],
-        "group backward": lambda s: list(norm.backward(x, x, w, b, stream=s)) + [wide.backward(big, big, stream=s)[0]],
+        "group backward": lambda s: list(norm.backward(x, x, w, b, stream=s)) + [wide.backward(big, big, stream=s)[0]]
+        + list(plain.backward(big, big, w[:48], b[:48], stream=s)),
     }
 
 
@@ -493,6 +508,32 @@ def test_replayed_graphs(name):
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(out, want)), (name, turn)
         assert all(torch.equal(a, b) for a, b in zip(fn(None), want))
+
+
+def test_replayed_steps():
+    """A captured step moves its cache with every replay as eager calls do theirs."""
+    C, N, rows = 512, 16, 150
+    d, cache = step_rows(("bf16", C, N, 1, [], False, "silu", True, True, 0), rows, [rows])
+    args = [up(d[k]) for k in ("x", "dt", "a", "b", "c")]
+    named = dict(skip=up(d["skip"]), dt_bias=up(d["bias"]), gate=up(d["gate"]),
+                 slots=up((torch.arange(rows) * 7 % 100).to(torch.int32)))
+    plan = dw.SelectiveScan(C, N, 1, "bf16")
+    eager, st = up(cache.clone()), up(cache.clone())
+    y = torch.empty(rows, C, dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(g, stream=side):
+        plan.step(*args, st, y=y, **named)
+    torch.cuda.synchronize()
+    assert torch.equal(st, eager), "capturing ran it"
+    for turn in range(3):
+        want = plan.step(*args, eager, **named)
+        torch.cuda.synchronize()
+        y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(st, eager), turn
 
 
 @pytest.mark.parametrize("name", ["scan forward", "scan step", "scan backward", "group forward", "group backward"])
