@@ -24,7 +24,7 @@
 // a state and token forward, in the gradients about 76 cycles: 16384 tokens x 8192 channels x
 // 16 states, bf16, 570 to 630 us by the card's clock (367 for those instructions at 2.14 GHz;
 // 204 for the bytes at a copy's rate; vector units 84 % busy, 92 % where sequences are
-// equally long); gradients of 4096 x 8192 640 (291 and 90; 77 % busy).  One sequence of 5003
+// equally long); gradients of 4096 x 8192 600 to 640 (291 and 90).  One sequence of 5003
 // x 2048 in runs of 64: k_ends 36, k_join 11, k_out 49 us.  Sums over channels on the matrix
 // units, with a left operand of zeros and ones, take longer (gradients 870): an fp32 product's
 // 32 cycles add to the vector unit's time.
@@ -51,7 +51,45 @@ struct Across {
     static constexpr int R = V * LPC / 64;             // values a lane keeps
     static __device__ __forceinline__ void sum(float (&v)[V], int lane) {
         int n = V;
-        if (LPC <= 8) {  // lane bit 3
+        if constexpr (LPC == 4) {
+            // Lane bits 3 and 2: lanes whose bit is 0 keep the value v[i] and add their partner's,
+            // the others v[i + n / 2].  Two instructions a value, since a bank mask leaves the other
+            // lanes of the destination as they are; the compiler takes a select and two (gradients of
+            // 4096 x 8192 690 -> 643 us).  It knows neither that these are lane moves, which read a
+            // register two wait states after its writing at the earliest, nor that the next may be.
+            asm("s_nop 1\n\t"
+                "v_add_f32_dpp %0, %0, %0 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %0, %8, %8 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %1, %1, %1 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %1, %9, %9 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %2, %2, %2 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %2, %10, %10 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %3, %3, %3 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %3, %11, %11 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %4, %4, %4 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %4, %12, %12 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %5, %5, %5 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %5, %13, %13 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %6, %6, %6 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %6, %14, %14 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %7, %7, %7 row_shl:8 row_mask:0xf bank_mask:0x3\n\t"
+                "v_add_f32_dpp %7, %15, %15 row_shr:8 row_mask:0xf bank_mask:0xc\n\t"
+                "v_add_f32_dpp %0, %0, %0 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+                "v_add_f32_dpp %0, %4, %4 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+                "v_add_f32_dpp %1, %1, %1 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+                "v_add_f32_dpp %1, %5, %5 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+                "v_add_f32_dpp %2, %2, %2 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+                "v_add_f32_dpp %2, %6, %6 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+                "v_add_f32_dpp %3, %3, %3 row_shl:4 row_mask:0xf bank_mask:0x5\n\t"
+                "v_add_f32_dpp %3, %7, %7 row_shr:4 row_mask:0xf bank_mask:0xa\n\t"
+                "s_nop 1"
+                : "+&v"(v[0]), "+&v"(v[1]), "+&v"(v[2]), "+&v"(v[3]),
+                  "+&v"(v[4]), "+&v"(v[5]), "+&v"(v[6]), "+&v"(v[7])
+                : "v"(v[8]), "v"(v[9]), "v"(v[10]), "v"(v[11]),
+                  "v"(v[12]), "v"(v[13]), "v"(v[14]), "v"(v[15]));
+            n = 4;
+        }
+        if (LPC == 8) {  // lane bit 3
             const bool hi = lane & 8;
             n /= 2;
 #pragma unroll
@@ -59,16 +97,6 @@ struct Across {
                 const float m = hi ? v[i + V / 2] : v[i], o = hi ? v[i] : v[i + V / 2];
                 v[i] = m + dpp<0x128>(o);  // lane ^ 8
             }
-        }
-        if (LPC <= 4) {  // lane bit 2
-            const bool hi = lane & 4;
-#pragma unroll
-            for (int i = 0; i < V / 4; ++i) {
-                float m = hi ? v[i + V / 4] : v[i];
-                m += dpp_banks<0x104, 0x5>(v[i]);           // from four lanes on, in quads 0 and 2
-                v[i] = m + dpp_banks<0x114, 0xa>(v[i + V / 4]);  // from four lanes back, in quads 1 and 3
-            }
-            n /= 2;
         }
         if (LPC <= 16) {  // lane bit 4
             n /= 2;
