@@ -9,6 +9,7 @@ import scan_reference as ref
 import seq_reference
 from gpu_helpers import DEV, say
 from scan_cases import GROUP, SCAN, group_data, group_id, scan_data, scan_id
+from depthwise_convolution_amd import seq
 from seq_reference import DTYPES, U, starts
 
 pytestmark = pytest.mark.gpu
@@ -189,6 +190,40 @@ def test_scan_of_nothing():
     assert plan.step(e(0, C), e(0, C), a, e(0, 1, N), e(0, 1, N), state).shape == (0, C)
 
 
+@pytest.mark.parametrize("T", [40, 900])
+def test_wrong_offsets_stay_in_bounds(T):
+    """Offsets that fall or run past the tokens are clamped, with whole sequences and with runs
+    of them: what lies around the outputs and the workspace stays as it was."""
+    C, N = 32, 16
+    plan = dw.SelectiveScan(C, N, 1, "f32")
+    g = torch.Generator().manual_seed(T)
+    x, dt = up(torch.randn(T, C, generator=g)), up(torch.randn(T, C, generator=g))
+    b, a = up(torch.randn(T, 1, N, generator=g)), -torch.ones(C, N, device=DEV)
+    for bad in ([0, T + 500, 20], [-7, 10, 2 ** 30], [T - 5, 20, 10], [0, T, -1], [-2 ** 31, 2 ** 31 - 1, 3], [T + 9, T + 8, 0]):
+        say(f"[gpu] scan offsets {bad}")
+        off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        rows = [torch.full((T + 64, C), 5.0, device=DEV) for _ in range(3)]
+        cols = [torch.full((T + 64, 1, N), 5.0, device=DEV) for _ in range(2)]
+        states = [torch.full((4, C, N), 5.0, device=DEV) for _ in range(2)]
+        y, dx, ddt = (v[32:32 + T] for v in rows)
+        db, dc = (v[32:32 + T] for v in cols)
+        so, ds = (v[1:3] for v in states)
+        for back in (False, True):
+            need = seq.dwconv_scan_workspace(plan.handle, 2, T, back)
+            ws = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+            if back:
+                plan.backward(x, dt, a, b, b, x, offsets=off, state_in=torch.zeros(2, C, N, device=DEV), dx=dx, ddt=ddt, db=db,
+                              dc=dc, dstate_in=ds, workspace=ws[256:256 + need])
+            else:
+                plan(x, dt, a, b, b, offsets=off, state_out=so, y=y, workspace=ws[256:256 + need])
+            torch.cuda.synchronize()
+            assert (ws[:256] == 77).all() and (ws[256 + need:] == 77).all()
+        for v in rows + cols:
+            assert (v[:32] == 5.0).all() and (v[32 + T:] == 5.0).all()
+        for v in states:
+            assert (v[0] == 5.0).all() and (v[3] == 5.0).all()
+
+
 def test_scan_repeats_its_bits_and_writes_states_in_place():
     case = ("bf16", 200, 16, 2, [300, 1, 90], True, "silu", True, True, 0)
     d = scan_data(case)
@@ -356,6 +391,23 @@ def test_group_of_far_sizes(act, size, eps, pixels):
     holds(plan(up(x), up(d["w"]), up(d["b"])), want["y"], "y")
     for name, v in zip(("dx", "dw", "db"), plan.backward(up(x), up(d["dy"]), up(d["w"]), up(d["b"]))):
         holds(v, want[name], name)
+
+
+@pytest.mark.parametrize("case", [c for c in GROUP if c[1] * c[2] * c[3] < 3e6], ids=group_id)
+def test_group_workspaces_hold_what_a_call_keeps(case):
+    fmt, n, S, C, G, act, _, _ = case
+    d = group_data(case)
+    x, dy, w, b = (up(d[k]) for k in ("x", "dy", "w", "b"))
+    plan = dw.GroupNorm(C, G, fmt, act=act)
+    for back in (False, True):
+        need = seq.dwconv_group_workspace(plan.handle, n, S, back)
+        ws = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+        if back:
+            plan.backward(x, dy, w, b, workspace=ws[256:256 + need])
+        else:
+            plan(x, w, b, workspace=ws[256:256 + need])
+        torch.cuda.synchronize()
+        assert (ws[:256] == 77).all() and (ws[256 + need:] == 77).all()
 
 
 def test_group_of_nothing():
