@@ -336,6 +336,10 @@ __device__ __forceinline__ void quads(int cnt, F f) {
     }
 }
 
+// 2^p, for p past 127 2^127 (NaN stays): one of two factors.  The product of both at 2^127
+// takes any normal number out of fp32's range, as whatever is larger would.
+__device__ __forceinline__ float grown(float p) { return __builtin_amdgcn_exp2f(p > 127.0f ? 127.0f : p); }
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
@@ -417,7 +421,10 @@ __global__ void __launch_bounds__(THREADS, sizeof(typename DT::X) == 2 && LPC <=
 // What a run leaves of a zero state (ends; in the forward pass of all but a sequence's last
 // run, which no other begins with: 4096 x 1024 x 64 147 -> 143 us), the sum of its step
 // widths (width), and with BACK the gradient that its outputs leave at the state before it (back): there
-// token t counts c dy times the decays of all tokens from the run's first to it.
+// token t counts c dy times the decays of all tokens from the run's first to it.  Four tokens'
+// c dy are led back to the first of them as k_grad does it, and from there to the run's first
+// by e^(D a), D the widths before them, as the square of its root: where states grow it may
+// pass fp32's range while what it meets is zero or small.
 template <class DT, int LPC, bool BACK>
 __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *ends, float *width, float *back) {
     using X = typename DT::X;
@@ -430,10 +437,10 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
     const ScanLane<LPC> w(G, id % G.nblk);
     const Piece p = piece(G, id / G.nblk);
     if (p.t0 >= p.t1 || (!BACK && p.t1 == G.seq.end(p.s))) return;
-    float a2[4], h[4], fade[4], g[4], sum = 0.0f;
+    float a2[4], h[4], g[4], sum = 0.0f, half = 0.0f;  // half of D
     load_rates(a2, in.a, G, w.c, 4 * w.j, w.live);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = g[i] = 0.0f, fade[i] = 1.0f;
+    for (int i = 0; i < 4; ++i) h[i] = g[i] = 0.0f;
     const float bias = in.bias && w.live ? in.bias[w.c] : 0.0f;
     const Walk<X> wx = R::walk(in.x, in.ldx, w.c0), wd = R::walk(in.dt, in.lddt, w.c0), wz = R::walk(in.gate, in.ldgate, w.c0),
                   wy = R::walk(in.dy, in.lddy, w.c0), wb = S::walk(in.b, in.ldb, w.g * G.N, G.N),
@@ -469,7 +476,7 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
         const Own<DT, LPC> own(sx[k], sd[k], w, bias, G.soft, cnt);
         quads(cnt, [&](int n) {
             sum += own.d[n];
-            float dy[4];
+            float dy[4], es[4][4];
             if (BACK) {
                 dy[n] = R::get(sy[k & B], 4 * n + w.q, w.ch);
                 if (in.gate) dy[n] *= gate_value<DT>(R::get(sz[k & B], 4 * n + w.q, w.ch), G.act);
@@ -477,18 +484,32 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const float ds = of_token(own.d, 4 * n + s), us = of_token(own.u, 4 * n + s);
-                float bv[4], cv[4];
+                float bv[4];
                 S::get(bv, sb[k], 4 * n + s, w.j);
-                if (BACK) S::get(cv, sc[k & B], 4 * n + s, w.j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(ds * a2[i]);
-                    h[i] = __builtin_fmaf(e, h[i], us * bv[i]);
-                    if (BACK) {
-                        fade[i] *= e;
-                        g[i] = __builtin_fmaf(fade[i], cv[i] * of_token(dy, 4 * n + s), g[i]);
-                    }
+                    es[s][i] = __builtin_amdgcn_exp2f(ds * a2[i]);
+                    h[i] = __builtin_fmaf(es[s][i], h[i], us * bv[i]);
                 }
+            }
+            if (BACK) {
+                float back4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 3; s >= 0; --s) {
+                    const float ys = of_token(dy, 4 * n + s);
+                    float cv[4];
+                    S::get(cv, sc[k & B], 4 * n + s, w.j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) back4[i] = es[s][i] * __builtin_fmaf(cv[i], ys, back4[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // at most 2^127 as in grown(); a width or rate that is NaN has made g NaN by now
+                    const float root = __builtin_amdgcn_exp2f(fminf(half * a2[i], 127.0f));
+                    g[i] = __builtin_fmaf(back4[i] * root, root, g[i]);
+                }
+                const float two = own.d[n] + dpp<0xB1>(own.d[n]);
+                half = __builtin_fmaf(two + dpp<0x4E>(two), 0.5f, half);
             }
         });
     }
@@ -504,6 +525,9 @@ __global__ void __launch_bounds__(THREADS) k_ends(ScanGeo G, ScanIn in, float *e
 // gradient of the state after it.  Sixteen runs are on their way at a time (79 runs of 2048
 // channels 11.4 us; with sixteen more on their way 12.6, a wavefront a workgroup 10.9).
 // Forward, what stands for the last run is read and not used: its end is k_out's.
+// A run in which states grow may have a factor beyond fp32's range.  Sixteen runs with such a
+// one are walked again with factors in two parts: a state of zero stays zero, and a small one
+// is where it should be.  (Always in two parts 16.2 us.)
 template <int LPC, bool BACK>
 __global__ void __launch_bounds__(THREADS)
     k_join(ScanGeo G, const float *a, const float *state_in, float *state_out, const float *dstate_out, float *dstate_in,
@@ -529,14 +553,32 @@ __global__ void __launch_bounds__(THREADS)
                 d[i] = *wd;
                 if (r + i + 1 < runs) in += by * row, wd += by * G.nblk * CPW;
             }
+            // f: v over a run of width d, for state n
+            auto over = [&](auto f) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (r + i >= runs) break;
-                store_f32<F32, 4>(out, v);
-                out += by * row;
+                for (int i = 0; i < U; ++i) {
+                    if (r + i >= runs) break;
+                    store_f32<F32, 4>(out + i * by * row, v);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) v[n] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[i] * a2[n]), v[n], e[i][n]);
+                    for (int n = 0; n < 4; ++n) v[n] = f(d[i] * a2[n], v[n], e[i][n]);
+                }
+            };
+            float first[4], top = 0.0f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) first[n] = v[n];
+            over([&](float p, float s, float end) {
+                const float decay = __builtin_amdgcn_exp2f(p);
+                top = fmaxf(top, decay);
+                return __builtin_fmaf(decay, s, end);
+            });
+            if (__any(top == __builtin_inff())) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) v[n] = first[n];
+                over([&](float p, float s, float end) {
+                    return __builtin_fmaf(grown(p), s * grown(p > 127.0f ? p - 127.0f : 0.0f), end);
+                });
             }
+            out += U * by * row;
         }
     };
     load_states(v, state_in ? state_in + srow : nullptr, 4 * w.j, G.N, w.live && state_in);

@@ -263,6 +263,10 @@ dwconv_status_t dwconv_norm_bwd(dwconv_norm_t p, int rows, const void *o, const 
  *   state_*         seqs x C x N float, dense; NULL state_in: zeros; NULL
  *                   state_out: not written; state_out may be state_in itself
  *
+ * Rates and widths may have any sign: states then grow.  A token's own e^{d a} is an fp32
+ * number, though, infinite from d a = 88.8 on, where it makes NaN of a state of zero; that
+ * of many tokens together has no such end.
+ *
  * Forward, a NaN or infinity reaches no token before its own, no other sequence and,
  * but for those of b and c, no other channel.  In the gradients it may reach any
  * token of its sequence and, through db and dc, the sums over the group's channels.
