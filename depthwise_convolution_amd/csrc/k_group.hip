@@ -797,7 +797,8 @@ bool resident(const dwconv_group_plan &p, int images, int pixels, int V, int TH,
     return ((int64_t)pixels + g.rpp - 1) / g.rpp <= K && (least < 64 || k == p.G || (int64_t)images * g.slices >= 128);
 }
 
-bool too_many(int64_t blocks) { return blocks >= (1 << 24); }
+// more lanes than a grid counts
+bool too_many(int64_t blocks, int lanes) { return blocks >= (int64_t)1 << 32 || blocks * lanes >= (int64_t)1 << 32; }
 
 struct Sizes {
     size_t stats, joined, part, means, all;  // floats
@@ -838,7 +839,7 @@ template <class DT, int V, int TH, int K, int ACT>
 hipError_t fwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     const int64_t blocks = (int64_t)g.images * g.slices;
-    if (too_many(blocks)) return hipErrorInvalidConfiguration;
+    if (too_many(blocks, TH)) return hipErrorInvalidConfiguration;
     const int mg = most_groups(g);
     k_fwd<DT, V, TH, K, false, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, a.w, a.b, (X *)a.y, a.ldy, nullptr, mg);
@@ -860,7 +861,7 @@ hipError_t fwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     const Geo g = passes(p, a.images, a.pixels, V), f = streams(g);
     const Sizes z = sizes(p, g, false);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
-    if (too_many(blocks) || groups >= 1 << 22) return hipErrorInvalidConfiguration;
+    if (too_many(blocks, PASS_TH) || groups >= 1 << 22) return hipErrorInvalidConfiguration;
     if (!blocks) return hipSuccess;
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
     const int mg = most_groups(g);
@@ -877,7 +878,7 @@ template <class DT, int V, int TH, int K, int ACT>
 hipError_t bwd_resident(const Geo &g, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     const int64_t blocks = (int64_t)g.images * g.slices;
-    if (too_many(blocks)) return hipErrorInvalidConfiguration;
+    if (too_many(blocks, TH)) return hipErrorInvalidConfiguration;
     const int mg = most_groups(g);
     k_resident<DT, V, TH, K, ACT><<<(uint32_t)blocks, TH, lds_bytes(g, V, mg), st>>>(
         g, (const X *)a.x, a.ldx, (const X *)a.dy, a.lddy, a.w, a.b, (X *)a.dx, a.lddx, a.workspace, mg);
@@ -902,7 +903,7 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     const Sizes z = sizes(p, g, true);
     const int64_t blocks = (int64_t)g.images * g.slices * g.runs, groups = (int64_t)g.images * g.G;
     const uint32_t param = a.dw || a.db ? (uint32_t)((2 * (int64_t)g.C + 15) / 16) : 0;
-    if (too_many(blocks) || groups + param >= 1 << 22) return hipErrorInvalidConfiguration;
+    if (too_many(blocks, PASS_TH) || groups + param >= 1 << 22) return hipErrorInvalidConfiguration;
     float2 *stats = (float2 *)a.workspace, *joined = (float2 *)(a.workspace + z.stats);
     float *part = (float *)joined + z.joined;
     float2 *means = (float2 *)(part + z.part);

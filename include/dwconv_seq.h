@@ -55,7 +55,8 @@
  *                it, in a step of one row; gradients also 2^24 for every 8 (4, 2, 1)
  *                tokens of a group of channels; the workspace's size is then given as
  *                SIZE_MAX.  Token strides are at most 2^26 elements there (but in a step)
- *   group norm   2^24 workgroups of an image's 8 channels or more, or of 8 KB or more;
+ *   group norm   2^24 workgroups of 256 lanes, 2^23 of 512, 2^22 of 1024, each 8 channels
+ *                or more of an image, or 8 KB or more;
  *                2^22 groups of all images where one image is more than a workgroup's
  *                registers hold (in gradients groups + C / 8)
  *
