@@ -101,6 +101,7 @@ def _call(name, *args):
 
 
 _INT = 2 ** 31 - 1
+_MOST_BYTES = 2 ** 63 - 1
 
 
 def _n(name, v):
@@ -389,6 +390,8 @@ class _Plan:
 
 
 def _workspace(ws, need, dev):
+    if need > _MOST_BYTES:  # what the library says of a call whose grid passes its limit
+        raise DwconvError(2, "workspace")
     if ws is None:
         return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
