@@ -5,8 +5,12 @@ import torch
 
 import depthwise_convolution_amd as dw
 import scan_reference as ref
+import test_gpu_scan as base
 from gpu_helpers import DEV, say
-from seq_reference import U, leaves
+from scan_cases import SCAN, scan_data, scan_id
+from scan_long import LONG, long_bounds, long_data, long_id
+from depthwise_convolution_amd import seq
+from seq_reference import DTYPES, U, leaves, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +86,92 @@ def test_scan_of_states_that_grow(T, C, N, x_at, dy_at, small, falling):
     near(so, ws, tol, "state")
     for name, got, want in zip(("dx", "ddt", "da", "db", "dc", "dstate"), g[:5] + g[8:], grads):
         near(got, want, tol, name)
+
+
+# ---------------------------------------------------------------------------
+# every number of lanes a channel, type and gate, whole sequences and runs; long runs
+# ---------------------------------------------------------------------------
+# as SCAN in tests/scan_cases.py
+LANES = [
+    ("f32", 70, 24, 1, [33, 40, 2], True, "silu", True, True, 0),          # 8 lanes a channel, whole
+    ("f16", 64, 32, 2, [40, 1, 0, 33], True, "silu", True, True, 0),
+    ("bf16", 61, 19, 1, [50, 17], False, "sigmoid", True, True, 3),
+    ("f32", 33, 17, 1, [50, 30], True, None, True, True, 0),
+    ("f16", 40, 30, 1, [64, 3], True, None, False, True, 1),
+    ("f32", 33, 20, 1, [300], True, "silu", True, True, 0),                # and in runs
+    ("f16", 50, 17, 1, [400, 5], True, "sigmoid", True, True, 0),
+    ("bf16", 96, 32, 3, [300, 10], True, "silu", True, True, 5),
+    ("bf16", 40, 25, 1, [200], True, None, True, False, 0),
+    ("bf16", 512, 24, 1, [3, 5, 0, 1] * 500, True, "silu", True, True, 0),  # more sequences than walkers of the gradients
+    ("f32", 24, 64, 2, [40, 33], True, "silu", True, True, 0),             # 16 lanes
+    ("bf16", 17, 33, 1, [30, 50], True, "silu", True, True, 0),
+    ("f16", 40, 48, 1, [50, 40], True, "sigmoid", True, True, 0),
+    ("f32", 20, 40, 1, [200, 9], True, "silu", True, True, 0),
+    ("bf16", 36, 50, 2, [250], True, "silu", True, True, 2),
+    ("f16", 12, 70, 1, [40, 9], True, "silu", True, True, 0),              # 32 lanes
+    ("f32", 9, 128, 1, [30, 41], True, "silu", True, True, 0),
+    ("bf16", 20, 66, 2, [33, 1], False, None, True, True, 0),
+    ("f16", 10, 65, 1, [200, 70], True, "silu", True, True, 1),
+    ("bf16", 11, 127, 1, [300], True, "sigmoid", True, True, 0),
+]
+
+
+@pytest.mark.parametrize("case", LANES, ids=scan_id)
+def test_scan_forward_of_any_lanes(case):
+    base.test_scan_forward(case)
+
+
+@pytest.mark.parametrize("case", LANES, ids=scan_id)
+def test_scan_backward_of_any_lanes(case):
+    base.test_scan_backward(case)
+
+
+@pytest.mark.parametrize("case", LONG, ids=long_id)
+def test_scan_in_long_runs(case):
+    """Runs of 128 to 1024 tokens, half of the states slow enough to pass from one to the next.
+    Inputs of one sign, whose sums are not smaller than their terms."""
+    fmt, C, N, G, lens, act, run = case
+    say(f"[gpu] scan long {long_id(case)}")
+    d = long_data(case)
+    T, dt = sum(lens), DTYPES[fmt]
+    plan, off = dw.SelectiveScan(C, N, G, fmt, gate_act=act), base.offsets_of(lens)
+    pos = [up(d[k]) for k in ("x", "dt", "a", "b", "c")]
+    named = dict(skip=up(d["skip"]), dt_bias=up(d["bias"]), gate=up(d["gate"]), offsets=off, state_in=up(d["state"]))
+    so = torch.empty(len(lens), C, N, device=DEV)
+    y = plan(*pos, state_out=so, **named)
+    got = dict(zip(("dx", "ddt", "da", "db", "dc", "dskip", "dbias", "dgate", "dstate"),
+                   plan.backward(*pos, up(d["dy"]), dstate_out=up(d["dstate"]), **named)), y=y, state=so)
+    torch.cuda.synchronize()
+    # a sum over tokens: a run's, then four chains of up to 2048 walkers' in all
+    wants = []
+    for i, (s, n) in enumerate(zip(starts(lens), lens)):
+        cut = lambda t: t[s:s + n]  # noqa: E731
+        wants.append(long_bounds(dt, cut(d["x"]), cut(d["dt"]), d["a"], cut(d["b"]), cut(d["c"]), d["skip"], d["bias"],
+                                 cut(d["gate"]), d["state"][i], True, act, cut(d["dy"]), d["dstate"][i], run + 512 + 8))
+    for k, v in got.items():
+        whole = k in ("da", "dskip", "dbias")
+        want = tuple(sum(w[k][j] for w in wants) if whole else torch.cat([w[k][j] for w in wants]) for j in (0, 1))
+        base.holds(v, want, k)
+
+
+# ---------------------------------------------------------------------------
+# workspaces
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("case", SCAN + LANES, ids=scan_id)
+def test_scan_workspaces_hold_what_a_call_keeps(case):
+    """What lies around a workspace of just its size stays as it was."""
+    fmt, C, N, G, lens, state, act, soft, _, _ = case
+    say(f"[gpu] scan workspace {scan_id(case)}")
+    d = scan_data(case)
+    plan, off = base.plan_of(case), base.offsets_of(lens)
+    pos = [up(d[k]) for k in ("x", "dt", "a", "b", "c")]
+    named = dict(skip=up(d["skip"]), dt_bias=up(d["bias"]), gate=up(d["gate"]), offsets=off, state_in=up(d["state"]))
+    for back in (False, True):
+        need = seq.dwconv_scan_workspace(plan.handle, len(lens), sum(lens), back)
+        ws = torch.full((need + 512,), 77, dtype=torch.uint8, device=DEV)
+        if back:
+            plan.backward(*pos, up(d["dy"]), dstate_out=up(d["dstate"]), workspace=ws[256:256 + need], **named)
+        else:
+            plan(*pos, state_out=torch.empty(len(lens), C, N, device=DEV), workspace=ws[256:256 + need], **named)
+        torch.cuda.synchronize()
+        assert (ws[:256] == 77).all() and (ws[256 + need:] == 77).all()

@@ -45,3 +45,12 @@ def test_scans_without_a_workspace_that_memory_could_hold_are_unsupported(monkey
         assert status_of(lambda: plan.backward(x, x, meta(C, 1), b, b, x, **named)) == 2
     else:
         assert status_of(lambda: plan(x, x, meta(C, 1), b, b, **named)) == 2
+
+
+def test_scan_workspaces_hold_a_state_of_every_8_tokens():
+    for C, N, G in ((8192, 16, 1), (33, 5, 1), (64, 100, 4), (96, 24, 3)):
+        h = dw.dwconv_scan_create(C, N, G, "bf16", True, "silu")
+        for seqs in (1, 3):
+            for n in (0, 1, 8, 1000, 4096, 100000):
+                assert dw.dwconv_scan_workspace(h, seqs, n, True) >= 4 * (n // 8 + seqs) * C * N
+        dw.dwconv_scan_destroy(h)
