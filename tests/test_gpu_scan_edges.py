@@ -155,7 +155,7 @@ def test_scan_in_long_runs(case):
 
 
 # ---------------------------------------------------------------------------
-# workspaces
+# workspaces and streams
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("case", SCAN + LANES, ids=scan_id)
 def test_scan_workspaces_hold_what_a_call_keeps(case):
@@ -175,3 +175,86 @@ def test_scan_workspaces_hold_what_a_call_keeps(case):
             plan(*pos, state_out=torch.empty(len(lens), C, N, device=DEV), workspace=ws[256:256 + need], **named)
         torch.cuda.synchronize()
         assert (ws[:256] == 77).all() and (ws[256 + need:] == 77).all()
+
+
+def stream_calls():
+    """name: (outputs that no call has written, call(stream, outputs)); the step's cache holds
+    its states."""
+    case = ("bf16", 320, 16, 1, [700, 30], True, "silu", True, True, 0)
+    d = {k: up(v) for k, v in scan_data(case).items()}
+    plan, off, T, bf = base.plan_of(case), base.offsets_of(case[4]), 730, torch.bfloat16
+    pos = [d[k] for k in ("x", "dt", "a", "b", "c")]
+    named = dict(skip=d["skip"], dt_bias=d["bias"], gate=d["gate"])
+    cache = torch.randn(800, 320, 16, device=DEV) * 0.1
+    x, big = torch.randn(3, 400, 96, device=DEV), torch.randn(2, 9000, 48, device=DEV)
+    w, b = torch.rand(96, device=DEV), torch.rand(96, device=DEV)
+    plans = [(dw.GroupNorm(96, 32, "f32"), x, 96), (dw.GroupNorm(48, 6, "f32"), big, 48),
+             (dw.GroupNorm(48, 6, "f32", act="none"), big, 48)]
+    none = lambda *s, dtype=torch.float32: torch.full(s, float("nan"), dtype=dtype, device=DEV)  # noqa: E731
+    rows, cols = lambda: none(T, 320, dtype=bf), lambda: none(T, 1, 16, dtype=bf)  # noqa: E731
+    grads = "dx ddt da db dc dskip ddt_bias dgate dstate_in".split()
+
+    def group_fwd(s, o):
+        for (p, v, C), y in zip(plans, o):
+            p(v, w[:C], b[:C], y=y, stream=s)
+
+    def group_bwd(s, o):
+        for i, (p, v, C) in enumerate(plans):
+            p.backward(v, v, w[:C], b[:C], dx=o[3 * i], dw=o[3 * i + 1], db=o[3 * i + 2], stream=s)
+
+    return {
+        "scan forward": (lambda: [rows(), none(2, 320, 16)], lambda s, o: plan(
+            *pos, offsets=off, state_in=d["state"], y=o[0], state_out=o[1], stream=s, **named)),
+        "scan step": (lambda: [rows(), cache.clone()], lambda s, o: plan.step(*pos, o[1], y=o[0], stream=s, **named)),
+        "scan backward": (lambda: [rows(), rows(), none(320, 16), cols(), cols(), none(320), none(320), rows(), none(2, 320, 16)],
+                          lambda s, o: plan.backward(*pos, d["dy"], offsets=off, state_in=d["state"], dstate_out=d["dstate"],
+                                                     stream=s, **dict(zip(grads, o)), **named)),
+        "group forward": (lambda: [torch.full_like(v, float("nan")) for _, v, _ in plans], group_fwd),
+        "group backward": (lambda: [t for _, v, C in plans for t in (torch.full_like(v, float("nan")), none(C), none(C))],
+                           group_bwd),
+    }
+
+
+@pytest.mark.parametrize("name", ["scan forward", "scan step", "scan backward", "group forward", "group backward"])
+def test_outputs_of_calls_on_given_streams(name):
+    """Every call writes outputs of its own, of which none holds the values before: on a raw
+    handle, on two streams at once, and on a stream that is busy, of which the current one sees
+    nothing yet."""
+    say(f"[gpu] given streams {name}")
+    torch.manual_seed(3)
+    make, call = stream_calls()[name]
+    want, one, two = make(), torch.cuda.Stream(), torch.cuda.Stream()
+    call(None, want)
+    equal = lambda o: all(torch.equal(p, q) for p, q in zip(o, want))  # noqa: E731
+    sets = [make() for _ in range(3)]
+    untouched = make()
+    m = torch.ones(8192, 8192, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    assert all(torch.isfinite(t).all() for t in want) and not any(equal(o) for o in sets)
+    call(one.cuda_stream, sets[0])
+    torch.cuda.synchronize()
+    assert equal(sets[0])
+    call(one, sets[1])
+    call(two, sets[2])
+    torch.cuda.synchronize()
+    assert equal(sets[1]) and equal(sets[2])
+    for _ in range(4):  # streams that share a hardware queue with the current one are no test of this
+        given, out = torch.cuda.Stream(), make()
+        busy, saw = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(given):
+            for _ in range(100):
+                torch.mm(m, m)
+            busy.record()
+        call(given, out)
+        seen = [t.clone() for t in out]
+        saw.record()
+        torch.cuda.synchronize()
+        assert equal(out)
+        early = saw.elapsed_time(busy)
+        print(f"{name}: seen {early:.2f} ms before the given stream was free", flush=True)
+        if early > 0:
+            same = [bool((p.nan_to_num(7.0) == q.nan_to_num(7.0)).all()) for p, q in zip(seen, untouched)]
+            assert all(same), "written by another stream than the given one"
+            return
+    pytest.skip("no stream ran beside the current one")
