@@ -817,7 +817,8 @@ Sizes sizes(const dwconv_group_plan &p, const Geo &g, bool back) {
     return z;
 }
 
-// LDS of a workgroup: lanes' values, columns, two values a group
+// LDS of a workgroup: lanes' values, columns, two values a group.  At most 131080 bytes, for a
+// slice of 8191 groups of one channel, of the 160 KB that a CU has; the passes take 32 KB.
 size_t lds_bytes(const Geo &g, int V, int groups) {
     const size_t wide = (size_t)g.vpr * V;
     return (g.rpp * (wide + 4) + wide + 2 * (size_t)groups) * sizeof(float);

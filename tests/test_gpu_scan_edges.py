@@ -7,7 +7,7 @@ import depthwise_convolution_amd as dw
 import scan_reference as ref
 import test_gpu_scan as base
 from gpu_helpers import DEV, say
-from scan_cases import SCAN, scan_data, scan_id
+from scan_cases import SCAN, group_data, group_id, scan_data, scan_id
 from scan_long import LONG, long_bounds, long_data, long_id
 from depthwise_convolution_amd import seq
 from seq_reference import DTYPES, U, leaves, starts
@@ -152,6 +152,71 @@ def test_scan_in_long_runs(case):
         whole = k in ("da", "dskip", "dbias")
         want = tuple(sum(w[k][j] for w in wants) if whole else torch.cat([w[k][j] for w in wants]) for j in (0, 1))
         base.holds(v, want, k)
+
+
+# ---------------------------------------------------------------------------
+# group norm: wide slices, far means
+# ---------------------------------------------------------------------------
+# as GROUP in tests/scan_cases.py: groups in no number that divides well, so that a slice is all
+# channels and its lanes' values, columns and statistics take 64 to 128 KB of LDS
+WIDE = [
+    ("bf16", 1, 9, 8192, 1, "silu", True, 0),
+    ("bf16", 2, 9, 4099, 4099, "none", True, 0),
+    ("f16", 1, 32, 4093, 4093, "silu", True, 0),
+    ("f16", 1, 9, 6002, 3001, "relu", True, 0),
+    ("bf16", 2, 16, 8191, 8191, "silu", True, 3),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=group_id)
+def test_group_forward_of_wide_slices(case):
+    fmt, n, S, C, G, act, _, _ = case
+    assert seq.dwconv_group_workspace(dw.GroupNorm(C, G, fmt, act=act).handle, n, S, False) == 0, "not in registers"
+    base.test_group_forward(case)
+
+
+@pytest.mark.parametrize("case", WIDE, ids=group_id)
+def test_group_backward_of_wide_slices(case):
+    base.test_group_backward(case)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("fmt, mean", [("f32", 1000.0), ("f32", 30.0), ("f16", 30.0), ("bf16", 10.0)])
+@pytest.mark.parametrize("pixels", [60, 9000])
+def test_group_of_means_far_from_zero(fmt, mean, pixels, act):
+    """Means of up to 1000 deviations: x r - mean r loses what the mean itself does, and the
+    bounds have it."""
+    say(f"[gpu] group far mean {fmt} {mean} {pixels} {act}")
+    d = group_data((fmt, 2, pixels, 48, 6, act, True, 0), seed=4)
+    x = (torch.randn(2, pixels, 48, generator=torch.Generator().manual_seed(6)) + mean).to(DTYPES[fmt])
+    want = ref.group_bounds(DTYPES[fmt], x, d["w"], d["b"], 6, act, 1e-5, d["dy"])
+    plan = dw.GroupNorm(48, 6, fmt, act=act)
+    base.holds(plan(up(x), up(d["w"]), up(d["b"])), want["y"], "y")
+    for name, v in zip(("dx", "dw", "db"), plan.backward(up(x), up(d["dy"]), up(d["w"]), up(d["b"]))):
+        base.holds(v, want[name], name)
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("pixels", [60, 9000])
+def test_group_of_what_is_no_number_or_too_large(pixels, act):
+    """A NaN or infinity makes NaN of its image's group and of nothing else; deviations whose
+    squares leave fp32 have u = 0."""
+    plan, g = dw.GroupNorm(48, 6, "f32", act=act), torch.Generator().manual_seed(pixels)
+    x, dy = up(torch.randn(2, pixels, 48, generator=g)), up(torch.randn(2, pixels, 48, generator=g))
+    w, b = up(0.5 + torch.rand(48, generator=g)), up(torch.randn(48, generator=g))
+    clean = plan(x, w, b), plan.backward(x, dy, w, b)[0]
+    hit = torch.zeros_like(x, dtype=torch.bool)
+    hit[1, :, :8] = True
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        e = x.clone()
+        e[1, 7, 5] = bad
+        for got, was in zip((plan(e, w, b), plan.backward(e, dy, w, b)[0]), clean):
+            assert got[hit].isnan().all() and torch.equal(got[~hit], was[~hit]), bad
+    x[1] *= 1e20
+    y, (dx, dw_, db) = plan(x, w, b), plan.backward(x, dy, w, b)
+    zero = plan(torch.zeros_like(x), None, b)
+    assert torch.equal(y[1], zero[1]) and (dx[1] == 0).all() and torch.equal(y[0], clean[0][0])
+    assert torch.isfinite(dw_).all() and torch.isfinite(db).all()
 
 
 # ---------------------------------------------------------------------------
