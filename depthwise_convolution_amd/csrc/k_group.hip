@@ -276,12 +276,13 @@ struct Have {
     }
 };
 
-// The run's or image's mean of each group (in stat) and squares around it (in sq).
-template <class DT, int V, int TH, int K, class L>
+// The run's or image's mean of each group (in stat) and squares around it (in sq); one lane a
+// group calls seen(mean, squares), before a barrier.
+template <class DT, int V, int TH, int K, class L, class F>
 __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &ln, const Group<V> &gr,
                                         Any<DT, V> (&x)[K], int n, const Have &have, Sums<TH, V> &sum, float *stat, float *sq,
-                                        float (&mean)[V]) {
-    const float inv = 1.0f / ((float)n * (float)(s.ng > 1 ? g.cg : s.w));
+                                        float (&mean)[V], F seen) {
+    const float count = (float)n * (float)(s.ng > 1 ? g.cg : s.w);
     float v[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
@@ -290,7 +291,7 @@ __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &l
         for (int i = 0; i < V; ++i) v[i] += x[k][i];
     });
     sum.rows(v, ln, g);
-    sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { stat[j] = t * inv; });
+    sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { stat[j] = t / count; });
 #pragma unroll
     for (int i = 0; i < V; ++i) mean[i] = stat[gr.of[i]], v[i] = 0.0f;
     fresh(x);
@@ -302,7 +303,7 @@ __device__ __forceinline__ void moments(const Geo &g, const Slice &s, const L &l
         }
     });
     sum.rows(v, ln, g);
-    sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { sq[j] = t; });
+    sum.of_groups(s, g.cg, [](int, float t) { return t; }, [&](int j, float t) { sq[j] = t, seen(stat[j], t); });
     fresh(x);
 }
 
@@ -353,27 +354,42 @@ __global__ void __launch_bounds__(TH) k_fwd(Geo g, const typename DT::X *x, int6
         params(scale, w, ln.c, 1.0f);
         params(shift, b, ln.c, 0.0f);
     }
-    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
+    const float inv = 1.0f / ((float)n * (float)g.cg);
+    constexpr bool NEAR = !RUNS && sizeof(typename DT::X) == 2 && ACT != DWCONV_GROUP_ACT_RELU;
+    __shared__ int far;  // a mean of 16 deviations or more
+    if (NEAR && threadIdx.x == 0) far = 0;
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean, [&](float m, float q) {
+        if (NEAR && !(m * m < 256.0f * __builtin_fmaf(q, inv, g.eps))) far = 1;
+    });
     if (RUNS) {
         leave(g, s, stats, img, run, sl, stat, sq);
         return;
     }
-    const float inv = 1.0f / ((float)n * (float)g.cg);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
-        shift[i] = __builtin_fmaf(-mean[i], scale[i], shift[i]);
-    }
-    if (!ln.live) return;
+    for (int i = 0; i < V; ++i) scale[i] *= inverse_root(sq[gr.of[i]] * inv, g.eps);
     y += ((int64_t)img * g.S + p0 + ln.row) * ldy + ln.c;
     const int64_t step = g.rpp * ldy;
-    have.each<K>([&](int k) {
-        float o[V];
+    auto outputs = [&](auto z) {
+        if (!ln.live) return;
+        have.each<K>([&](int k) {
+            float o[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[k][i], scale[i], shift[i]);
-        activate<DT, ACT>(o);
-        ln.store(y + k * step, o, true);  // all loads of the slice are behind a barrier
-    });
+            for (int i = 0; i < V; ++i) o[i] = z(v[k][i], i);
+            activate<DT, ACT>(o);
+            ln.store(y + k * step, o, true);  // all loads of the slice are behind a barrier
+        });
+    };
+    // 16-bit data whose means are all less than 16 deviations: (x - mean) scale in one operation,
+    // off by 16 units of 2^-24 of a deviation (64 images of 56x56x128 bf16 28.2 us, with the
+    // difference taken first 30.2).  The same for the workgroup, of which two lanes may write
+    // one element; not with a rectifier, whose corner the gradients find by the difference.
+    if (NEAR && !uniform(far)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) shift[i] = __builtin_fmaf(-mean[i], scale[i], shift[i]);
+        outputs([&](float x, int i) { return __builtin_fmaf(x, scale[i], shift[i]); });
+    } else {
+        outputs([&](float x, int i) { return __builtin_fmaf(x - mean[i], scale[i], shift[i]); });
+    }
 }
 
 // Two sums over the W wavefronts that share a group, in all of their lanes.
@@ -392,7 +408,8 @@ __device__ __forceinline__ void sum_group(float &a, float &b, float *sh) {
 }
 
 // Puts the moments of a group's runs together: W wavefronts a group.  With counts n_i,
-// means m_i and squares q_i: m = sum n_i m_i / n and q = sum (q_i + n_i (m_i - m)^2).
+// means m_i and squares q_i: m = m_0 + sum n_i (m_i - m_0) / n, which is m_0 where all are
+// equal, and q = sum (q_i + n_i (m_i - m)^2).
 // out: mean and r.  part: the sums that k_both has left, or nullptr.
 template <int W>
 __global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const float2 *stats, float2 *out, float *part) {
@@ -407,9 +424,11 @@ __global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const floa
         return (float)min(g.rows, g.S - run * g.rows) * (float)(parts > 1 ? min(g.part, g.cg - part * g.part) : g.cg);
     };
     const float inv = 1.0f / ((float)g.S * (float)g.cg);
+    const float m0 = p[0].x;
     float m = 0.0f, q = 0.0f, none = 0.0f;
-    for (int i = lane; i < per; i += 64 * W) m = __builtin_fmaf(count(i) * inv, p[i].x, m);
+    for (int i = lane; i < per; i += 64 * W) m = __builtin_fmaf(count(i) * inv, p[i].x - m0, m);
     sum_group<W>(m, none, sh);
+    m += m0;
     for (int i = lane; i < per; i += 64 * W) {
         const float d = p[i].x - m;
         q += __builtin_fmaf(count(i) * d, d, p[i].y);
@@ -428,35 +447,31 @@ __global__ void __launch_bounds__(W > 4 ? W * 64 : 256) k_join(Geo g, const floa
     }
 }
 
-// A lane's channels: u = x r + off and z = x scale + shift with scale = r w.  (That the mean
-// is taken from x only after a product costs a rounding of r mean, no more than the mean's own.)
+// A lane's channels: with d = x - mean, u = d r and z = d scale + shift, scale = r w.  The
+// mean is taken from x before any product: x r - mean r would leave a rounding of mean r
+// where the deviations are nothing beside the mean (groups of one value, blank images).
 template <int V>
 struct Known {
-    float r[V], off[V], scale[V], shift[V];
+    float r[V], mean[V], scale[V], shift[V];
     Known() = default;
     // from mean and r
-    __device__ __forceinline__ void ready(const float (&mean)[V], const float *w, const float *b, int c) {
+    __device__ __forceinline__ void ready(const float *w, const float *b, int c) {
         params(scale, w, c, 1.0f);
         params(shift, b, c, 0.0f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            off[i] = -mean[i] * r[i];
-            scale[i] *= r[i];
-            shift[i] = __builtin_fmaf(-mean[i], scale[i], shift[i]);
-        }
+        for (int i = 0; i < V; ++i) scale[i] *= r[i];
     }
     template <class L>
     __device__ __forceinline__ Known(const Geo &g, const Slice &s, const L &ln, const float2 *joined, int img, const float *w,
                                      const float *b) {
         const Group<V> gr(g, s, ln);
-        float mean[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float2 m = joined[(int64_t)img * g.G + s.g0 + gr.of[i]];
             mean[i] = m.x;
             r[i] = m.y;
         }
-        ready(mean, w, b, ln.c);
+        ready(w, b, ln.c);
     }
 };
 
@@ -479,55 +494,79 @@ __global__ void __launch_bounds__(TH) k_apply(Geo g, const typename DT::X *x, in
                              [&](int u, int k) {
                                  float o[V];
 #pragma unroll
-                                 for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[u][i], kn.scale[i], kn.shift[i]);
+                                 for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(v[u][i] - kn.mean[i], kn.scale[i], kn.shift[i]);
                                  activate<DT, ACT>(o);
                                  ln.store(y + k * sy, o, apart);
                              });
 }
 
-// dz of one vector
+// x - mean: of fp16 data in one operation with the conversion, as a product with a one that the
+// compiler does not know
+template <class DT>
+struct Minus {
+    float one = 1.0f;
+    __device__ __forceinline__ Minus() {
+        if constexpr (std::is_same_v<DT, F16>) asm("" : "+s"(one));
+    }
+    __device__ __forceinline__ float operator()(float x, float mean) const {
+        if constexpr (std::is_same_v<DT, F16>) return __builtin_fmaf(x, one, -mean);
+        return x - mean;
+    }
+};
+
+// d and dz of one vector
 template <int ACT, class DT, int V>
-__device__ __forceinline__ void make_dz(float (&dz)[V], const Any<DT, V> &x, const Any<DT, V> &dy, const Known<V> &kn) {
+__device__ __forceinline__ void make_dz(float (&dz)[V], float (&d)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
+                                        const Known<V> &kn) {
     float z[V];
+    const Minus<DT> minus;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        z[i] = __builtin_fmaf(x[i], kn.scale[i], kn.shift[i]);
+        d[i] = minus(x[i], kn.mean[i]);
+        z[i] = __builtin_fmaf(d[i], kn.scale[i], kn.shift[i]);
         dz[i] = dy[i];
     }
     back_through<DT, ACT>(dz, z);
 }
 
-// A lane's share of the sums dz and dz u of one vector
+// A lane's share of the sums dz and dz d of one vector
 template <int ACT, class DT, int V>
 __device__ __forceinline__ void add_sums(float (&s1)[V], float (&s2)[V], const Any<DT, V> &x, const Any<DT, V> &dy,
                                          const Known<V> &kn) {
-    float dz[V];
-    make_dz<ACT>(dz, x, dy, kn);
+    float dz[V], d[V];
+    make_dz<ACT>(dz, d, x, dy, kn);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         s1[i] += dz[i];
-        s2[i] = __builtin_fmaf(dz[i], __builtin_fmaf(x[i], kn.r[i], kn.off[i]), s2[i]);
+        s2[i] = __builtin_fmaf(dz[i], d[i], s2[i]);
     }
 }
+// sums of dz d to those of dz u; where the squares have left fp32, r and u are 0
+template <int V>
+__device__ __forceinline__ void of_units(float (&s2)[V], const Known<V> &kn) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s2[i] = kn.r[i] == 0.0f ? 0.0f : s2[i] * kn.r[i];
+}
 
-// r (dz w - m1 - u m2) as r (dz w + x slope + rest)
+// r (dz w - m1 - u m2) as dz scale + d slope + rest
 template <int V>
 struct Grad {
-    float w[V], slope[V], rest[V];
-    __device__ __forceinline__ Grad(const Known<V> &kn, const float *pw, int c, const float (&m1)[V], const float (&m2)[V]) {
-        params(w, pw, c, 1.0f);
+    float scale[V], slope[V], rest[V];
+    __device__ __forceinline__ Grad(const Geo &g, const Known<V> &kn, const float (&m1)[V], const float (&m2)[V]) {
+        const bool one = g.cg == 1 && g.S == 1;  // nothing depends on the one value of a group
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            slope[i] = -kn.r[i] * m2[i];
-            rest[i] = -__builtin_fmaf(kn.off[i], m2[i], m1[i]);
+            scale[i] = one ? 0.0f : kn.scale[i];
+            slope[i] = one ? 0.0f : -kn.r[i] * (kn.r[i] * m2[i]);
+            rest[i] = one ? 0.0f : -kn.r[i] * m1[i];
         }
     }
     template <int ACT, class DT>
     __device__ __forceinline__ void of(float (&o)[V], const Any<DT, V> &x, const Any<DT, V> &dy, const Known<V> &kn) const {
-        float dz[V];
-        make_dz<ACT>(dz, x, dy, kn);
+        float dz[V], d[V];
+        make_dz<ACT>(dz, d, x, dy, kn);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = kn.r[i] * __builtin_fmaf(dz[i], w[i], __builtin_fmaf(x[i], slope[i], rest[i]));
+        for (int i = 0; i < V; ++i) o[i] = __builtin_fmaf(dz[i], scale[i], __builtin_fmaf(d[i], slope[i], rest[i]));
     }
 };
 
@@ -553,8 +592,7 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     take(v, x + ((int64_t)img * n + ln.row) * ldx + ln.c, g.rpp * ldx, have);
     take(d, dy + ((int64_t)img * n + ln.row) * lddy + ln.c, g.rpp * lddy, have);
     Known<V> kn;
-    float mean[V];
-    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, kn.mean, [](float, float) {});
     const float inv = 1.0f / ((float)n * (float)g.cg);
     float s1[V], s2[V];
 #pragma unroll
@@ -562,8 +600,9 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
         kn.r[i] = inverse_root(sq[gr.of[i]] * inv, g.eps);
         s1[i] = s2[i] = 0.0f;
     }
-    kn.ready(mean, w, b, ln.c);
+    kn.ready(w, b, ln.c);
     have.each<K>([&](int k) { add_sums<ACT>(s1, s2, v[k], d[k], kn); });
+    of_units(s2, kn);
     float *o = sums + (int64_t)img * 2 * g.C + s.c0;
     float m1[V], m2[V];
     __syncthreads();  // stat and sq have been read
@@ -581,7 +620,7 @@ __global__ void __launch_bounds__(TH) k_resident(Geo g, const typename DT::X *x,
     if (!ln.live) return;  // all loads of the slice are behind a barrier
     fresh(v);
     fresh(d);
-    const Grad<V> grad(kn, w, ln.c, m1, m2);
+    const Grad<V> grad(g, kn, m1, m2);
     have.each<K>([&](int k) {
         float r[V];
         grad.template of<ACT>(r, v[k], d[k], kn);
@@ -610,6 +649,7 @@ __global__ void __launch_bounds__(TH) k_sums(Geo g, const typename DT::X *x, int
     Any<DT, V> vx[U], vd[U];
     Have(g, ln, n).stream<U>([&](int u, int k) { vx[u] = Lane<DT, V>::load(x + k * sx), vd[u] = Lane<DT, V>::load(dy + k * sy); },
                              [&](int u, int) { add_sums<ACT>(s1, s2, vx[u], vd[u], kn); });
+    of_units(s2, kn);
     channel_sums<TH>(g, s, ln, sum, s1, s2, part + ((int64_t)img * g.runs + run) * 2 * g.C + s.c0);
 }
 
@@ -634,7 +674,7 @@ __global__ void __launch_bounds__(TH) k_both(Geo g, const typename DT::X *x, int
     take(v, x + ((int64_t)img * g.S + p0 + ln.row) * ldx + ln.c, g.rpp * ldx, have);
     take(d, dy + ((int64_t)img * g.S + p0 + ln.row) * lddy + ln.c, g.rpp * lddy, have);
     float mean[V], s1[V], s2[V];
-    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean);
+    moments<DT, V, TH, K>(g, s, ln, gr, v, n, have, sum, stat, sq, mean, [](float, float) {});
     leave(g, s, stats, img, run, sl, stat, sq);
 #pragma unroll
     for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.0f;
@@ -722,7 +762,7 @@ __global__ void __launch_bounds__(TH) k_dx(Geo g, const typename DT::X *x, int64
         m1[i] = m.x;
         m2[i] = m.y;
     }
-    const Grad<V> grad(kn, w, ln.c, m1, m2);
+    const Grad<V> grad(g, kn, m1, m2);
     Any<DT, V> vx[U], vd[U];
     Have(g, ln, n).stream<U>([&](int u, int k) { vx[u] = Lane<DT, V>::load(x + k * sx), vd[u] = Lane<DT, V>::load(dy + k * sy); },
                              [&](int u, int k) {

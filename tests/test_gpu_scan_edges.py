@@ -196,6 +196,44 @@ def test_group_of_means_far_from_zero(fmt, mean, pixels, act):
         base.holds(v, want[name], name)
 
 
+@pytest.mark.parametrize("act", ["none", "silu", "relu"])
+@pytest.mark.parametrize("fmt, C", [("f32", 64), ("bf16", 64), ("f16", 40), ("f32", 3), ("bf16", 5), ("f16", 1)])
+def test_group_of_one_value(fmt, C, act):
+    """A group that is one value has u = 0 whatever the value is: y = act(b), and nothing
+    depends on x or w.  (Channels in vectors, and too few for one.)"""
+    say(f"[gpu] group of one {fmt} {C} {act}")
+    g, dt = torch.Generator().manual_seed(C), DTYPES[fmt]
+    x, dy = up((torch.randn(1, 1, C, generator=g) * 5 + 20).to(dt)), up(torch.randn(1, 1, C, generator=g).to(dt))
+    w, b = up(0.5 + torch.rand(C, generator=g)), up(torch.randn(C, generator=g))
+    plan = dw.GroupNorm(C, C, fmt, act=act)
+    zero = torch.zeros_like(x)
+    assert torch.equal(plan(x, w, b), plan(zero, None, b))
+    if act != "silu":
+        assert torch.equal(plan(x, w, b)[0, 0], (b if act == "none" else b.clamp_min(0)).to(dt))
+    dx, dw_, db = plan.backward(x, dy, w, b)
+    assert (dx == 0).all() and (dw_ == 0).all()
+    assert torch.equal(db, plan.backward(zero, dy, w, b)[2])
+    if act == "none":
+        assert torch.equal(db, dy[0, 0].float())
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("pixels, C, G", [(49, 48, 6), (9000, 48, 6), (3000, 61, 61), (500, 7, 1), (20000, 256, 2)])
+def test_group_of_equal_values(pixels, C, G, act):
+    """Images without variance whose sums are exact (8 bits of bf16 times up to 2^15 values of
+    a workgroup): u = 0 to the last bit, in registers and in passes, whatever their value is."""
+    say(f"[gpu] group of equals {pixels} {C} {G} {act}")
+    g = torch.Generator().manual_seed(pixels)
+    value = (torch.randn(2, 1, G, generator=g) * 5 + 20).to(torch.bfloat16).repeat_interleave(C // G, 2)
+    x, dy = up(value.expand(2, pixels, C).contiguous()), up(torch.randn(2, pixels, C, generator=g).to(torch.bfloat16))
+    w, b = up(0.5 + torch.rand(C, generator=g)), up(torch.randn(C, generator=g))
+    plan = dw.GroupNorm(C, G, "bf16", act=act)
+    y, dw_ = plan(x, w, b), plan.backward(x, dy, w, b)[1]
+    assert torch.equal(y, plan(torch.zeros_like(x), None, b))
+    assert act != "none" or torch.equal(y, b.bfloat16().expand_as(y))
+    assert (dw_ == 0).all()
+
+
 @pytest.mark.parametrize("act", ["none", "silu"])
 @pytest.mark.parametrize("pixels", [60, 9000])
 def test_group_of_what_is_no_number_or_too_large(pixels, act):
