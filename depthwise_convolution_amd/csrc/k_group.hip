@@ -17,9 +17,10 @@
 // Resident: 64 images of 56x56x128 bf16 with silu 25 to 28 us (103 MB, 3.7 to 4.1 TB/s; 19 at
 // a copy's rate; loads, sums and stores follow each other in the one workgroup of a CU),
 // gradients of 64x56x56x96 fp16 46 and 4 for dw and db (116 MB; vector instructions: with no
-// activation 39).  In passes: 2 fp32 images of 256x256x256 84 to 91 us: moments 39, joins 4,
-// outputs 45 (reading 134 MB alone takes 42 on this card, a copy of it 50); gradients of
-// 16x112x112x61 bf16 without activation 40 to 44: sums 18, joins 8.5, dx 16.
+// activation 39).  In passes: 2 fp32 images of 256x256x256 84 to 91 us: moments 35 to 39, joins
+// 4, outputs 45 (a copy of 134 MB takes 50, a plain reading of them 21 to 29, so that the
+// moments are not at the memory's rate); gradients 157: 35, 4, sums 42, joins 4, dx 70.
+// Gradients of 16x112x112x61 bf16 without activation 40 to 43: sums 17, joins 9, dx 17.
 #include <type_traits>
 
 #include "seq_common.h"
@@ -934,6 +935,8 @@ hipError_t bwd(const dwconv_group_plan &p, const GroupArgs &a, hipStream_t st) {
     using X = typename DT::X;
     if constexpr (V > 1) {
         Geo g;
+        // 20 vectors of x and of dy are what 512 lanes have registers for: 64 fp16 images of
+        // 56x56x96 take 51 us; of 64x64x96, in passes, 73, a tenth more for an element.
         for (int least : {64, 32}) {
             if (resident(p, a.images, a.pixels, V, 256, 8, least, g)) return bwd_resident<DT, V, 256, 8, ACT>(g, a, st);
             if (resident(p, a.images, a.pixels, V, 512, 20, least, g)) return bwd_resident<DT, V, 512, 20, ACT>(g, a, st);

@@ -22,10 +22,12 @@
 //
 // Vector instructions bound all of it, an exponential (8 cycles) and four operations (4 each)
 // a state and token forward, in the gradients about 76 cycles: 16384 tokens x 8192 channels x
-// 16 states, bf16, 570 to 630 us by the card's clock (367 for those instructions at 2.14 GHz;
-// 204 for the bytes at a copy's rate; vector units 84 % busy, 92 % where sequences are
-// equally long); gradients of 4096 x 8192 600 to 640 (291 and 90).  One sequence of 5003
-// x 2048 in runs of 64: k_ends 36, k_join 11, k_out 49 us.  Sums over channels on the matrix
+// 16 states, bf16, 1.39 million cycles, of which vector units are busy 84 % (97 % where sequences
+// are equally long), 574 us at 2.41 GHz and 645 to 700 at 2.16 to 1.97, as under a profiler
+// (0.79 million for those instructions alone; 204 us for the bytes at a copy's rate); fp32 687.
+// Gradients of 4096 x 8192 1.40 million, 595 us (0.62; bytes 90, with the states and sums that
+// they keep and read again 217).  One sequence of 5003 x 2048 in runs of 64: k_ends 36, k_join
+// 11, k_out 49 us; gradients of 2048 x 2048 33, 11 and 76.  Sums over channels on the matrix
 // units, with a left operand of zeros and ones, take longer (gradients 870): an fp32 product's
 // 32 cycles add to the vector unit's time.
 #include <type_traits>
@@ -870,7 +872,10 @@ ScanGeo geometry(const dwconv_scan_plan &p, const int32_t *offsets, int seqs, in
     // tokens as give a CU six (four in the gradients).  N = 16, whole sequences and runs:
     // 16384 and 32768 channels x 2048 tokens 220 and 312 us, 246 and 479; two sequences of
     // 150 tokens, 8192 channels 29 and 38; four of 593 to 1266, 1024 channels, N = 64, 160
-    // and 142; gradients of four of 297 to 633 tokens, 4096 channels, 229 and 253.
+    // and 142; gradients of four of 297 to 633 tokens, 4096 channels, 229 and 253.  The host
+    // knows no lengths but the average: one sequence of 16000 tokens, 2048 channels, takes 248
+    // us in runs and 1690 beside fifteen of 32 tokens, whole (gradients 770, and 5470 from
+    // seven of them on).
     const int64_t blocks = (int64_t)seqs * G.nblk, want = back ? 1024 : 1536;
     const bool ragged = !back && seqs > 1 && tokens / seqs >= 512;
     if (seqs > 0 && blocks < (ragged ? 512 : 256)) {

@@ -6,9 +6,11 @@
 // lanes a channel, so that a wavefront's states are one run of memory; it walks every
 // `walkers`-th row and has the next one's loads on their way while it computes.
 //
-// 8192 channels of 16 states, bf16: one row 4.1 us, 8 rows 5.7, 32 rows 11.4, 96 rows 29
-// (107 MB, 3.7 TB/s; a large copy's rate would be 20), 192 rows 57.5.  A workgroup for every
-// row, which has nothing on its way while it computes: 13.2, 40 and 78 for 32, 96 and 192.
+// 8192 channels of 16 states, bf16, caches that change from call to call so that none is in the
+// last-level cache: one row 4.1 us, 8 rows 5.7, 32 rows 11.4, 96 rows 29 (107 MB, 3.7 TB/s; a
+// large copy's rate would be 20), 192 rows 57.5; 96 rows of one or two caches (51 MB each) 24.
+// A workgroup for every row, which has nothing on its way while it computes: 13.2, 40 and 78
+// for 32, 96 and 192.
 #include "scan_common.h"
 
 namespace dw {

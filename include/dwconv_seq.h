@@ -268,6 +268,11 @@ dwconv_status_t dwconv_norm_bwd(dwconv_norm_t p, int rows, const void *o, const 
  * number, though, infinite from d a = 88.8 on, where it makes NaN of a state of zero; that
  * of many tokens together has no such end.
  *
+ * Work is laid out by the average length, which is all that the host knows: a sequence
+ * many times longer than the others of its call is walked by few CUs where those are as
+ * many as fill the card by themselves (C / 64 or more workgroups a sequence, 256 in all).
+ * A workgroup has channels of one group: groups of fewer than 64 leave it part empty.
+ *
  * Forward, a NaN or infinity reaches no token before its own, no other sequence and,
  * but for those of b and c, no other channel.  In the gradients it may reach any
  * token of its sequence and, through db and dc, the sums over the group's channels.
