@@ -335,9 +335,10 @@ dwconv_status_t dwconv_scan_bwd(dwconv_scan_t h, const void *x, int64_t ldx, con
  *               images one behind the other; y may be x itself (with ldy == ldx)
  *   w, b        C float or NULL (ones, zeros)
  *
- * Squares around the mean are fp32 numbers: a group whose deviations' squares add up to more
- * than 3.4e38 has u = 0 and dx = 0, and where eps = 0 deviations below 1e-18 lose digits.
- * A NaN or infinity makes NaN of its image's group, in y and in dx, and of no other one.
+ * Sums over a group are fp32 numbers: a group whose deviations' squares add up to more than
+ * 3.4e38 has u = 0 and dx = 0, one whose values do is NaN, and where eps = 0 deviations
+ * below 1e-18 lose digits.  A NaN or infinity makes NaN of its image's group, in y and in
+ * dx, and of no other one.
  * ------------------------------------------------------------------------ */
 typedef enum {
     DWCONV_GROUP_ACT_NONE = 0,   /* identity                                   */

@@ -255,6 +255,9 @@ def test_group_of_what_is_no_number_or_too_large(pixels, act):
     zero = plan(torch.zeros_like(x), None, b)
     assert torch.equal(y[1], zero[1]) and (dx[1] == 0).all() and torch.equal(y[0], clean[0][0])
     assert torch.isfinite(dw_).all() and torch.isfinite(db).all()
+    x[1] = 1e38  # 60 x 8 of them add up to more than fp32 holds
+    y, dx = plan(x, w, b), plan.backward(x, dy, w, b)[0]
+    assert y[1].isnan().all() and dx[1].isnan().all() and torch.equal(y[0], clean[0][0]) and torch.equal(dx[0], clean[1][0])
 
 
 # ---------------------------------------------------------------------------
